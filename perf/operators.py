@@ -193,7 +193,7 @@ def _prepare_attn(c, g):
          "table": table.contiguous(), "lens": lens.to(torch.int32), "scale": d ** -0.5,
          "window": c["window"] or None}
     if own:
-        s["workspace"] = _package().paged_attention_workspace(n, c["h_q"], c["h_kv"], d, "cuda")
+        s["workspace"] = _package().paged_attention_workspace(c["h_q"], c["h_kv"], d, "cuda")
     return s
 
 
