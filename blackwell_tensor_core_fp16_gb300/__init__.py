@@ -28,6 +28,8 @@ __all__ = [
     "gemm_f16_sk_items", "gemm_f16_sk_item", "gemm_f16_sk_unit_of",
     "gemm_f16_half_tail_tiles", "gemm_f16_half_items", "gemm_f16_half_item",
     "exported_symbols", "VARIANTS", "STATUS",
+    "gated_delta_step", "qk_norm_rope", "rotary_table", "paged_attention",
+    "paged_attention_workspace", "check_decode_status",
 ]
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA_ERROR", 4: "TIMEOUT"}
@@ -173,6 +175,16 @@ def load():
         lib.gdn_set_scan_kernel.restype = i32
         lib.gdn_set_fault_injection.argtypes = [i32]
         lib.gdn_set_fault_injection.restype = i32
+        # the decode-step operators take their argument struct packed into bytes
+        for name in ("decode_gdn_step", "decode_qk_norm_rope", "decode_paged_attention"):
+            getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
+            getattr(lib, name).restype = i32
+        lib.decode_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+        lib.decode_paged_attention_workspace_bytes.restype = i32
+        lib.decode_last_error.argtypes = []
+        lib.decode_last_error.restype = ctypes.c_char_p
+        lib.decode_check_status.argtypes = [vp, u32p]
+        lib.decode_check_status.restype = i32
         _lib = lib
         return lib
 
@@ -362,12 +374,13 @@ def gemm_f16_ring_pos(it: int, stages: int):
 
 
 def exported_symbols(header_path: str | None = None):
-    """Names of the functions the public headers (include/gemm_f16.h, include/gdn.h) declare."""
+    """Names of the functions the public headers (include/gemm_f16.h, include/gdn.h,
+    include/decode.h) declare."""
     paths = [header_path] if header_path else _build.HEADERS
     names = set()
     for path in paths:
         text = re.sub(r"/\*.*?\*/", "", open(path).read(), flags=re.S)
-        names.update(re.findall(r"\b((?:gemm_(?:f16|mxf8)|gdn)_\w+)\s*\(", text))
+        names.update(re.findall(r"\b((?:gemm_(?:f16|mxf8)|gdn|decode)_\w+)\s*\(", text))
     return sorted(names)
 
 
@@ -728,3 +741,21 @@ def check_status(stream=None) -> None:
     rc, bits = gemm_f16_check_status(_stream_handle(stream))
     if rc != OK:
         raise GemmError(rc, f"{gemm_f16_last_error()} (bits 0x{bits:x})")
+
+
+# ---- the operators of a decode step -----------------------------------------------------------
+
+_DECODE_NAMES = frozenset((
+    "check_decode_status", "decode_check_status", "decode_gdn_step", "decode_last_error",
+    "decode_paged_attention", "decode_paged_attention_workspace_bytes", "decode_qk_norm_rope",
+    "gated_delta_step", "paged_attention", "paged_attention_workspace", "qk_norm_rope",
+    "rotary_table"))
+
+
+def __getattr__(name):
+    """The decode-step operators (decode.py, which imports torch), loaded at their first use."""
+    if name not in _DECODE_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import decode
+    value = globals()[name] = getattr(decode, name)
+    return value

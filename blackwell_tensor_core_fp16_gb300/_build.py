@@ -10,8 +10,10 @@ import tempfile
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
-HEADERS = [os.path.join(ROOT, "include", "gemm_f16.h"), os.path.join(ROOT, "include", "gdn.h")]
-SOURCES = ["gemm_f16.cu", "gdn.cu"]   # translation units, compiled in parallel
+HEADERS = [os.path.join(ROOT, "include", h) for h in ("gemm_f16.h", "gdn.h", "decode.h")]
+# translation units, compiled in parallel
+SOURCES = ["gemm_f16.cu", "gdn.cu", "decode.cu", "gdn_step.cu", "qk_norm_rope.cu",
+           "paged_attention.cu"]
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f16.so")
 
 NVCC_FLAGS = [
@@ -46,8 +48,7 @@ def is_stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/gemm_f16.cu and csrc/gdn.cu (in parallel) and link libgemm_f16.so next to
-    this file."""
+    """Compile the sources (in parallel) and link libgemm_f16.so next to this file."""
     if not force and not is_stale():
         return LIB_PATH
     tag = f"tmp{os.getpid()}"

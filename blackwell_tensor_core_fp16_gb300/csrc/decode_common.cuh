@@ -1,0 +1,84 @@
+// What the decode-step kernels share: 16-bit conversions, the programmatic-dependent-launch
+// helper, the status word's address and the error text (defined in decode.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/decode.h"
+
+namespace decode {
+
+// Stores the message for decode_last_error() and returns `code`.
+__attribute__((visibility("hidden"))) int fail(int code, const char* fmt, ...);
+__attribute__((visibility("hidden"))) void clear_error();
+
+// Address of the status word of the current device; nullptr (with the error stored) on failure.
+__attribute__((visibility("hidden"))) uint32_t* status_word();
+
+// Multiprocessors of the current device; 0 (with the error stored) on failure.
+__attribute__((visibility("hidden"))) int sm_count();
+
+// The calling device's ordinal and a per-device "done once" mark for a kernel's attributes.
+constexpr int kMaxDevices = 64;
+
+// Programmatic dependent launch: dep_wait() returns once all earlier work on the stream has
+// completed and its writes are visible; dep_launch() lets the next kernel of the stream be placed.
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                   cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+inline bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// ---- 16-bit types ------------------------------------------------------------------------------
+
+template <typename T>
+struct Half2;
+template <>
+struct Half2<__half> {
+    __device__ static float2 unpack(uint32_t x)
+    {
+        return __half22float2(*reinterpret_cast<const __half2*>(&x));
+    }
+    __device__ static uint32_t pack(float lo, float hi)
+    {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+template <>
+struct Half2<__nv_bfloat16> {
+    __device__ static float2 unpack(uint32_t x)
+    {
+        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    }
+    __device__ static uint32_t pack(float lo, float hi)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+};
+
+}  // namespace decode

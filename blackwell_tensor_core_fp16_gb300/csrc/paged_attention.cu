@@ -1,0 +1,694 @@
+// Attention of one new token per sequence over a paged key-value cache, split over the cache's
+// length and joined (C ABI in include/decode.h).
+//
+//     s_t = scale q . K_t;   o = sum_t exp(s_t - m) V_t / sum_t exp(s_t - m)
+//
+// A key and a value of head_dim d are 4 d bytes and serve h_q / h_kv query heads with 4 d flops
+// each: a few flops per byte, so the cache is read once and HBM bounds the time.  One pass: each
+// warp keeps the running maximum and sum of its tokens' exponentials (log2 domain, fp32) and the
+// unnormalised output, and results of warps and blocks are joined by their maxima.
+//
+// Work split.  An item is one (sequence, key head, up to 8 kHeadTiles of its query heads).  A tile is
+// 16 tokens per warp of an item.  All items' tiles, in order, are dealt to the blocks in equal
+// contiguous ranges, whatever the lengths: every block finds its range itself from a scan of the
+// lengths.  So a block has at most one item that began in an earlier block and one that goes on in
+// a later one; those two go to the workspace as (maximum, sum, output) and a second kernel joins
+// each item's parts in block order, the rest are written at once.  The order of every sum is fixed.
+//
+// Inside a block each warp streams its own 16-token slices through a ring of shared-memory stages
+// (16-byte cp.async, rows looked up in the page table one slice ahead, so pages may have any size
+// and the cache any strides) and needs no block barrier until an item ends; the ring runs on
+// across items.  Tokens outside the sequence are filled with zeros and not read.
+//
+// Both products put the tokens or the head dimension on the 16 rows of mma.m16n8k16 and the
+// query heads on its 8 columns, so up to 8 heads of a group cost no padding:
+//     S^T[token][head] = K Q^T,     O^T[d][head] = V^T P^T.
+// The weights P are rounded to the 16-bit type for the second product (they are at most 1, and
+// their roundings average out over the tokens); their sum is taken of the unrounded fp32 values.
+#include <cstdint>
+#include <type_traits>
+
+#include "decode_common.cuh"
+
+namespace {
+
+using namespace decode;
+
+constexpr int kSlice = 16;   // tokens of a warp's slice
+
+struct AttnParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const int32_t* table;
+    const int32_t* lens;
+    uint16_t* o;
+    float* lse;
+    uint32_t* status;
+    int4* desc;        // [blocks]: the item that goes on in later blocks
+    float2* part_ml;   // [2 * blocks][kHeads]
+    float* part_o;     // [2 * blocks][kHeads][D]
+    int64_t q_stride[2], k_stride[3], v_stride[3];
+    int64_t table_stride, max_len;
+    int32_t n, h_q, h_kv, group, head_items, pages, page_size, window;
+    float scale_log2;
+};
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p)
+{
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A sequence's tokens [start, len); len = 0 for a length the page table cannot hold.
+struct Span {
+    int start, len;
+};
+__device__ __forceinline__ Span span_of(const AttnParams& p, int i)
+{
+    int len = p.lens[i];
+    if (len < 0 || len > p.max_len) len = 0;
+    return {p.window > 0 && len > p.window ? len - p.window : 0, len};
+}
+
+// Tiles [first, last) of block c when `total` tiles are dealt to `blocks` blocks; and the block
+// that a tile is dealt to.
+__device__ __forceinline__ int first_tile(int c, int total, int blocks)
+{
+    const int each = total / blocks, more = total % blocks;
+    return c * each + min(c, more);
+}
+__device__ __forceinline__ int block_of(int tile, int total, int blocks)
+{
+    const int each = total / blocks, more = total % blocks;
+    const int big = more * (each + 1);
+    return tile < big ? tile / (each + 1) : more + (tile - big) / each;
+}
+
+// Where a warp is in the block's range of tiles.
+struct Cursor {
+    int i;              // sequence
+    int item;           // of the sequence: key head * head_items + head tile group
+    int tile;           // of the item
+    int tiles;          // of each of the sequence's items
+    Span span;
+};
+
+template <int kTileTokens>
+__device__ __forceinline__ int tiles_of(const Span& s)
+{
+    return (s.len - s.start + kTileTokens - 1) / kTileTokens;
+}
+
+template <int kTileTokens>
+__device__ __forceinline__ void advance(Cursor& c, const AttnParams& p)
+{
+    if (++c.tile < c.tiles) return;
+    c.tile = 0;
+    if (++c.item < p.h_kv * p.head_items) return;
+    c.item = 0;
+    do {
+        if (++c.i >= p.n) return;     // past the last tile: the caller stops by its count
+        c.span = span_of(p, c.i);
+        c.tiles = tiles_of<kTileTokens>(c.span);
+    } while (c.tiles == 0);
+}
+
+template <int D, int kHeadTiles>
+struct Cfg {
+    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kHeads = 8 * kHeadTiles;
+    static constexpr int kTile = kWarps * kSlice;
+    static constexpr int kStageBytes = 2 * kSlice * D * 2;    // keys, then values
+    static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
+    static constexpr int kMergeBytes = kWarps * kHeads * kMergeRow * 4;
+    static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
+    static constexpr int kRoom = 232448 - kMergeBytes - kSmallBytes;
+    static constexpr int kMaxStages = kRoom / (kWarps * kStageBytes);
+    static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes;
+    static_assert(kStages >= 2, "no room for two stages");
+};
+
+template <typename T, int D, int kHeadTiles>
+__global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
+    paged_attention_kernel(const AttnParams p)
+{
+    using C = Cfg<D, kHeadTiles>;
+    constexpr int kHeads = C::kHeads, kWarps = C::kWarps, kTile = C::kTile;
+    constexpr int kChunks = D / 8;                 // 16-byte pieces of a row
+    constexpr int kRowsPerCopy = 32 / kChunks;     // rows that one cp.async of the warp covers
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;
+    float* merge = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStageBytes);
+    float* sm_m = merge + C::kMergeBytes / 4;      // [kWarps][kHeads]
+    float* sm_l = sm_m + kWarps * kHeads;
+    int* sm_i = reinterpret_cast<int*>(sm_l + kWarps * kHeads);   // 64 words
+
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int blocks = gridDim.x, c = blockIdx.x;
+    const int items_per_seq = p.h_kv * p.head_items;
+
+    dep_launch();
+    dep_wait();
+
+    // ---- the block's range: a scan of all sequences' tiles
+    const int chunk = (p.n + C::kThreads - 1) / C::kThreads;
+    const int i_lo = min(p.n, tid * chunk), i_hi = min(p.n, i_lo + chunk);
+    int mine = 0;
+    for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += x;
+    }
+    if (lane == 31) sm_i[w] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+        if (x == w) upto += total;
+        total += sm_i[x];
+    }
+    const int t0 = first_tile(c, total, blocks), t1 = first_tile(c + 1, total, blocks);
+    if (t0 >= upto - mine && t0 < upto) {          // one thread: its sequences hold tile t0
+        int at = upto - mine;
+        for (int i = i_lo; i < i_hi; ++i) {
+            const int tiles = tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+            if (t0 < at + tiles) {
+                sm_i[32] = i;
+                sm_i[33] = t0 - at;
+                break;
+            }
+            at += tiles;
+        }
+    }
+    // sequences without tokens have no tile: their results are written here
+    for (int i = c; i < p.n; i += blocks) {
+        const int raw = p.lens[i];
+        const Span s = span_of(p, i);
+        if (tid == 0 && raw != s.len) atomicOr(p.status, DECODE_BAD_LENGTH);
+        if (s.len > 0) continue;
+        uint4* row = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * p.h_q * D);
+        for (int x = tid; x < p.h_q * (D / 8); x += C::kThreads) row[x] = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr)
+            for (int x = tid; x < p.h_q; x += C::kThreads)
+                p.lse[static_cast<int64_t>(i) * p.h_q + x] = -INFINITY;
+    }
+    if (tid == 0) p.desc[c] = make_int4(-1, 0, 0, 0);
+    if (t0 >= t1) return;
+    __syncthreads();
+
+    Cursor cur;
+    cur.i = sm_i[32];
+    cur.span = span_of(p, cur.i);
+    cur.tiles = tiles_of<kTile>(cur.span);
+    cur.item = sm_i[33] / cur.tiles;
+    cur.tile = sm_i[33] % cur.tiles;
+    Cursor pre = cur;                              // where the loads are
+    int pre_t = t0;
+
+    // ---- loads of a slice: the rows' places one slice ahead, then the copies
+    const uint32_t ring0 = smem_addr(ring) + w * C::kStages * C::kStageBytes;
+    int page = -1, off = 0;                        // lanes 0 .. 15: the place of row `lane`
+    auto look_up = [&]() {
+        page = -1;
+        if (pre_t < t1) {
+            const int pos = pre.span.start + pre.tile * kTile + w * kSlice + (lane & 15);
+            if (pos < pre.span.len) {
+                const int x = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
+                off = pos - x * p.page_size;
+                page = p.table[pre.i * p.table_stride + x];
+                if (page < 0 || page >= p.pages) {
+                    atomicOr(p.status, DECODE_BAD_PAGE);
+                    page = -1;
+                }
+            }
+        }
+    };
+    auto load = [&](int stage) {
+        if (pre_t < t1) {
+            const int kv = pre.item / p.head_items;
+            const uint16_t* kb = p.k + kv * p.k_stride[2];
+            const uint16_t* vb = p.v + kv * p.v_stride[2];
+            const uint32_t dst0 = ring0 + stage * C::kStageBytes;
+            const int ch = lane % kChunks;
+#pragma unroll
+            for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
+                const int row = x * kRowsPerCopy + lane / kChunks;
+                const int64_t pg = __shfl_sync(0xffffffffu, page, row);
+                const int64_t of = __shfl_sync(0xffffffffu, off, row);
+                const uint32_t bytes = pg >= 0 ? 16u : 0u;
+                const int64_t ko = pg >= 0 ? pg * p.k_stride[0] + of * p.k_stride[1] + ch * 8 : 0;
+                const int64_t vo = pg >= 0 ? pg * p.v_stride[0] + of * p.v_stride[1] + ch * 8 : 0;
+                const uint32_t dst = dst0 + row * (D * 2) + ((ch ^ (row & 7)) << 4);
+                cp_async16(dst, kb + ko, bytes);
+                cp_async16(dst + kSlice * D * 2, vb + vo, bytes);
+            }
+            ++pre_t;
+            advance<kTile>(pre, p);
+        }
+        cp_commit();
+        look_up();
+    };
+    look_up();
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) load(s);
+
+    // ---- the tiles
+    const int hq = (lane & 3) * 2;                 // the lane's two heads (of each head tile)
+    uint32_t qf[kHeadTiles][D / 16][2];
+    float acc[kHeadTiles][D / 16][4];
+    float m[kHeadTiles][2], l[kHeadTiles][2];
+    bool fresh = true;
+    int stage = 0;
+    for (int t = t0; t < t1; ++t) {
+        const int kv = cur.item / p.head_items, h0 = kv * p.group + (cur.item % p.head_items) * kHeads;
+        const int heads = min(kHeads, (kv + 1) * p.group - h0);
+        if (fresh) {
+            fresh = false;
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
+                const int h = x * 8 + (lane >> 2);
+                const uint16_t* row = p.q + cur.i * p.q_stride[0] + (h0 + h) * p.q_stride[1] +
+                                      (lane & 3) * 2;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    qf[x][d][0] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16) : 0u;
+                    qf[x][d][1] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16 + 8) : 0u;
+                    acc[x][d][0] = acc[x][d][1] = acc[x][d][2] = acc[x][d][3] = 0.f;
+                }
+                m[x][0] = m[x][1] = -INFINITY;
+                l[x][0] = l[x][1] = 0.f;
+            }
+        }
+        __syncwarp();
+        load((stage + C::kStages - 1) % C::kStages);
+        cp_wait<C::kStages - 1>();
+        __syncwarp();
+
+        const int pos0 = cur.span.start + cur.tile * kTile + w * kSlice;
+        if (pos0 < cur.span.len) {
+            const uint32_t ks = ring0 + stage * C::kStageBytes, vs = ks + kSlice * D * 2;
+            float s[kHeadTiles][4];
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            const int r = lane & 7, sel = lane >> 3;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t a[4];
+                ldsm4(a, ks + ((sel & 1) * 8 + r) * (D * 2) + (((2 * d + (sel >> 1)) ^ r) << 4));
+#pragma unroll
+                for (int x = 0; x < kHeadTiles; ++x) mma<T>(s[x], a, qf[x][d][0], qf[x][d][1]);
+            }
+            const bool in_lo = pos0 + (lane >> 2) < cur.span.len;
+            const bool in_hi = pos0 + (lane >> 2) + 8 < cur.span.len;
+            uint32_t pb[kHeadTiles][2];
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
+                float corr[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float& lo = s[x][e];
+                    float& hi = s[x][2 + e];
+                    lo = in_lo ? lo * p.scale_log2 : -INFINITY;
+                    hi = in_hi ? hi * p.scale_log2 : -INFINITY;
+                    float top = fmaxf(lo, hi);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    top = fmaxf(top, m[x][e]);
+                    // scores of -infinity only: any finite reference leaves their weights 0
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    corr[e] = exp2_fast(m[x][e] - ref);
+                    m[x][e] = top;
+                    lo = exp2_fast(lo - ref);
+                    hi = exp2_fast(hi - ref);
+                    l[x][e] = fmaf(l[x][e], corr[e], lo + hi);
+                }
+                if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        acc[x][d][0] *= corr[0];
+                        acc[x][d][1] *= corr[1];
+                        acc[x][d][2] *= corr[0];
+                        acc[x][d][3] *= corr[1];
+                    }
+                }
+                pb[x][0] = transpose8x8(Half2<T>::pack(s[x][0], s[x][1]));
+                pb[x][1] = transpose8x8(Half2<T>::pack(s[x][2], s[x][3]));
+            }
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                uint32_t a[4];
+                ldsm4_trans(a, vs + ((sel >> 1) * 8 + r) * (D * 2) + (((2 * d + (sel & 1)) ^ r) << 4));
+#pragma unroll
+                for (int x = 0; x < kHeadTiles; ++x) mma<T>(acc[x][d], a, pb[x][0], pb[x][1]);
+            }
+        }
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
+        // ---- the item's end, or the range's: join the warps
+        const bool item_ends = cur.tile + 1 == cur.tiles;
+        if (item_ends || t + 1 == t1) {
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float sum = l[x][e];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    if (lane < 4) {
+                        sm_m[w * kHeads + x * 8 + hq + e] = m[x][e];
+                        sm_l[w * kHeads + x * 8 + hq + e] = sum;
+                    }
+                }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int h = x * 8 + hq + e;
+                    float top = sm_m[h];
+#pragma unroll
+                    for (int y = 1; y < kWarps; ++y) top = fmaxf(top, sm_m[y * kHeads + h]);
+                    const float f = exp2_fast(m[x][e] - (top == -INFINITY ? 0.f : top));
+                    float* to = merge + (w * kHeads + h) * C::kMergeRow + (lane >> 2);
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        to[d * 16] = acc[x][d][e] * f;
+                        to[d * 16 + 8] = acc[x][d][2 + e] * f;
+                    }
+                }
+            __syncthreads();
+            const int begin = t - cur.tile;                   // the item's tiles [begin, end)
+            const int end = begin + cur.tiles;
+            const bool whole = begin >= t0 && end <= t1;
+            const int slot = 2 * c + (begin >= t0 ? 1 : 0);
+            for (int x = tid; x < heads * (D / 4); x += C::kThreads) {
+                const int h = x / (D / 4), d = x % (D / 4) * 4;
+                float top = sm_m[h];
+#pragma unroll
+                for (int y = 1; y < kWarps; ++y) top = fmaxf(top, sm_m[y * kHeads + h]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < kWarps; ++y) {
+                    sum = fmaf(sm_l[y * kHeads + h], exp2_fast(sm_m[y * kHeads + h] - ref), sum);
+                    const float4 b = *reinterpret_cast<const float4*>(
+                        merge + (y * kHeads + h) * C::kMergeRow + d);
+                    o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+                }
+                if (whole) {
+                    const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
+                    const float inv = 1.f / sum;
+                    *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
+                        Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
+                    if (d == 0 && p.lse != nullptr)
+                        p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+                } else {
+                    const int64_t row = static_cast<int64_t>(slot) * kHeads + h;
+                    *reinterpret_cast<float4*>(p.part_o + row * D + d) = o;
+                    if (d == 0) p.part_ml[row] = make_float2(top, sum);
+                }
+            }
+            if (tid == 0 && begin >= t0 && end > t1)
+                p.desc[c] = make_int4(cur.i, cur.item, block_of(end - 1, total, blocks), heads);
+            __syncthreads();
+            fresh = true;
+        }
+        advance<kTile>(cur, p);
+    }
+}
+
+// Joins the parts of the item that began in main block blockIdx.x and went on in later ones; one
+// block of the grid's y dimension per query head.  Part 0 is that block's slot 2 c + 1, the
+// others' parts are their slots 2 c'.
+constexpr int kJoinThreads = 256;
+
+template <typename T, int D, int kHeadTiles>
+__global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(const AttnParams p)
+{
+    constexpr int kHeads = 8 * kHeadTiles, kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float4 sums[kGroups][kLanes];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float part_sum[kGroups];
+    dep_launch();
+    dep_wait();
+    const int c = blockIdx.x, h = blockIdx.y;
+    const int4 item = p.desc[c];
+    if (item.x < 0 || h >= item.w) return;
+    const int parts = item.z - c + 1;
+    const int tid = threadIdx.x;
+    auto slot = [&](int x) { return static_cast<int64_t>(x == 0 ? 2 * c + 1 : 2 * (c + x)) * kHeads + h; };
+
+    float top = -INFINITY;
+    for (int x = tid; x < parts; x += kJoinThreads) top = fmaxf(top, p.part_ml[slot(x)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((tid & 31) == 0) red[tid >> 5] = top;
+    __syncthreads();
+    top = red[0];
+#pragma unroll
+    for (int x = 1; x < kJoinThreads / 32; ++x) top = fmaxf(top, red[x]);
+    const float ref = top == -INFINITY ? 0.f : top;
+
+    const int g = tid / kLanes, d = tid % kLanes;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int x = g; x < parts; x += kGroups) {
+        const float2 ml = p.part_ml[slot(x)];
+        const float f = exp2_fast(ml.x - ref);
+        const float4 b = *reinterpret_cast<const float4*>(p.part_o + slot(x) * D + d * 4);
+        o.x = fmaf(b.x, f, o.x), o.y = fmaf(b.y, f, o.y);
+        o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
+        sum = fmaf(ml.y, f, sum);
+    }
+    sums[g][d] = o;
+    if (d == 0) part_sum[g] = sum;
+    __syncthreads();
+    if (g != 0) return;
+    sum = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kGroups; ++x) {
+        sum += part_sum[x];
+        const float4 b = sums[x][d];
+        o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
+    }
+    const int64_t row = static_cast<int64_t>(item.x) * p.h_q + item.y / p.head_items * p.group +
+                        item.y % p.head_items * kHeads + h;
+    const float inv = 1.f / sum;
+    *reinterpret_cast<uint2*>(p.o + row * D + d * 4) =
+        make_uint2(Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
+    if (d == 0 && p.lse != nullptr) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+struct Layout {
+    size_t ml, o, total;
+};
+Layout layout_for(int sms, int kHeads, int64_t d)
+{
+    Layout l{};
+    size_t at = sizeof(int4) * static_cast<size_t>(sms);
+    l.ml = at = (at + 255) & ~size_t(255);
+    at += sizeof(float2) * 2 * static_cast<size_t>(sms) * kHeads;
+    l.o = at = (at + 255) & ~size_t(255);
+    l.total = at + sizeof(float) * 2 * static_cast<size_t>(sms) * kHeads * static_cast<size_t>(d);
+    return l;
+}
+
+int heads_of(int64_t group) { return group > 8 ? 16 : 8; }
+
+template <typename T, int D, int kHeadTiles>
+int run(const AttnParams& p, int64_t most_tokens, int sms, cudaStream_t stream)
+{
+    using C = Cfg<D, kHeadTiles>;
+    const int64_t per_item = (most_tokens + C::kTile - 1) / C::kTile;
+    const int64_t items = static_cast<int64_t>(p.n) * p.h_kv * p.head_items;
+    if (per_item > 0 && items >= (int64_t(1) << 31) / per_item)
+        return fail(DECODE_ERR_UNSUPPORTED, "too many tiles of the cache for one call");
+    const int64_t tiles = per_item * items;
+    const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < sms ? tiles : sms);
+    auto* kernel = paged_attention_kernel<T, D, kHeadTiles>;
+    static thread_local bool set[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && !(dev < kMaxDevices && set[dev])) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e == cudaSuccess && dev < kMaxDevices) set[dev] = true;
+    }
+    if (e == cudaSuccess)
+        e = launch(kernel, dim3(blocks), dim3(C::kThreads), C::kSmem, stream, p);
+    if (e != cudaSuccess)
+        return fail(DECODE_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
+    if (blocks == 1) return DECODE_OK;
+    e = launch(paged_attention_join_kernel<T, D, kHeadTiles>,
+               dim3(blocks, p.group < C::kHeads ? p.group : C::kHeads), dim3(kJoinThreads), 0,
+               stream, p);
+    if (e != cudaSuccess)
+        return fail(DECODE_ERR_CUDA, "paged_attention_join_kernel: %s", cudaGetErrorString(e));
+    return DECODE_OK;
+}
+
+template <typename T>
+int dispatch(const AttnParams& p, int64_t d, int64_t most, int sms, cudaStream_t s)
+{
+    const bool two = p.group > 8;
+    if (d == 64) return two ? run<T, 64, 2>(p, most, sms, s) : run<T, 64, 1>(p, most, sms, s);
+    if (d == 128) return two ? run<T, 128, 2>(p, most, sms, s) : run<T, 128, 1>(p, most, sms, s);
+    return two ? run<T, 256, 2>(p, most, sms, s) : run<T, 256, 1>(p, most, sms, s);
+}
+
+int check_heads(int64_t h_q, int64_t h_kv, int64_t d)
+{
+    if (h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0)
+        return fail(DECODE_ERR_INVALID_ARG, "%lld query heads over %lld key heads", (long long)h_q,
+                    (long long)h_kv);
+    if (d != 64 && d != 128 && d != 256)
+        return fail(DECODE_ERR_UNSUPPORTED, "head_dim %lld (64, 128 or 256)", (long long)d);
+    return DECODE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_paged_attention_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t head_dim,
+                                           size_t* bytes)
+{
+    clear_error();
+    if (bytes == nullptr) return fail(DECODE_ERR_INVALID_ARG, "bytes is null");
+    const int rc = check_heads(h_q, h_kv, head_dim);
+    if (rc != DECODE_OK) return rc;
+    const int sms = sm_count();
+    if (sms == 0) return DECODE_ERR_CUDA;
+    *bytes = layout_for(sms, heads_of(h_q / h_kv), head_dim).total;
+    return DECODE_OK;
+}
+
+int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t stream)
+{
+    clear_error();
+    if (a == nullptr) return fail(DECODE_ERR_INVALID_ARG, "args is null");
+    if (a->n < 0 || a->pages < 0 || a->page_size <= 0 || a->table_width < 0 || a->window < 0)
+        return fail(DECODE_ERR_INVALID_ARG, "negative size or no page size");
+    if (a->dtype != DECODE_F16 && a->dtype != DECODE_BF16)
+        return fail(DECODE_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
+    int rc = check_heads(a->h_q, a->h_kv, a->head_dim);
+    if (rc != DECODE_OK) return rc;
+    if (a->n == 0) return DECODE_OK;
+    if (!a->q || !a->o || !a->lens || !a->workspace ||
+        (a->table_width > 0 && a->pages > 0 && (!a->k_cache || !a->v_cache || !a->page_table)))
+        return fail(DECODE_ERR_INVALID_ARG, "null pointer");
+    if (misaligned(a->q) || misaligned(a->k_cache) || misaligned(a->v_cache) || misaligned(a->o) ||
+        misaligned(a->workspace))
+        return fail(DECODE_ERR_UNSUPPORTED, "16-bit tensors and workspace must be 16-byte aligned");
+    for (int d = 0; d < 2; ++d)
+        if (a->q_stride[d] % 8) return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
+    for (int d = 0; d < 3; ++d)
+        if (a->k_stride[d] % 8 || a->v_stride[d] % 8)
+            return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 8");
+    constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+    if (a->n > kMost || a->h_q >= (1 << 20) || a->pages > kMost || a->page_size > kMost ||
+        a->table_width > kMost)
+        return fail(DECODE_ERR_UNSUPPORTED, "problem too large for one call");
+    const int sms = sm_count();
+    if (sms == 0) return DECODE_ERR_CUDA;
+    const int64_t group = a->h_q / a->h_kv;
+    const int heads = heads_of(group);
+    const Layout l = layout_for(sms, heads, a->head_dim);
+    if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < l.total)
+        return fail(DECODE_ERR_INVALID_ARG, "workspace of %zu bytes needed", l.total);
+    // lengths are 32-bit: a table that could hold more holds no more than that (and the last
+    // tile's positions stay below 2^31)
+    int64_t max_len = a->pages == 0 ? 0 : a->page_size * a->table_width;
+    if (max_len > kMost - 1024) max_len = kMost - 1024;
+
+    AttnParams p{};
+    p.status = status_word();
+    if (p.status == nullptr) return DECODE_ERR_CUDA;
+    auto* ws = static_cast<uint8_t*>(a->workspace);
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.k = static_cast<const uint16_t*>(a->k_cache);
+    p.v = static_cast<const uint16_t*>(a->v_cache);
+    p.table = a->page_table;
+    p.lens = a->lens;
+    p.o = static_cast<uint16_t*>(a->o);
+    p.lse = a->lse;
+    p.desc = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+    p.part_o = reinterpret_cast<float*>(ws + l.o);
+    for (int d = 0; d < 2; ++d) p.q_stride[d] = a->q_stride[d];
+    for (int d = 0; d < 3; ++d) {
+        p.k_stride[d] = a->k_stride[d];
+        p.v_stride[d] = a->v_stride[d];
+    }
+    p.table_stride = a->table_stride;
+    p.max_len = max_len;
+    p.n = static_cast<int32_t>(a->n);
+    p.h_q = static_cast<int32_t>(a->h_q);
+    p.h_kv = static_cast<int32_t>(a->h_kv);
+    p.group = static_cast<int32_t>(group);
+    p.head_items = static_cast<int32_t>((group + heads - 1) / heads);
+    p.pages = static_cast<int32_t>(a->pages);
+    p.page_size = static_cast<int32_t>(a->page_size);
+    p.window = a->window > kMost ? 0 : static_cast<int32_t>(a->window);
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    const int64_t most = p.window > 0 && p.window < max_len ? p.window : max_len;
+    return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, a->head_dim, most, sms, stream)
+                                   : dispatch<__half>(p, a->head_dim, most, sms, stream);
+}
+
+}  // extern "C"
