@@ -23,8 +23,9 @@
 // Both products put the tokens or the head dimension on the 16 rows of mma.m16n8k16 and the
 // query heads on its 8 columns, so up to 8 heads of a group cost no padding:
 //     S^T[token][head] = K Q^T,     O^T[d][head] = V^T P^T.
-// The weights P are rounded to the 16-bit type for the second product (they are at most 1, and
-// their roundings average out over the tokens); their sum is taken of the unrounded fp32 values.
+// For the second product each weight is carried as two 16-bit pieces (p0 = round(p), p1 =
+// round(p - p0)): one piece would lose as much as the rounding of the result itself where few
+// tokens share the weight, and the products are not what bounds the time.
 #include <cstdint>
 #include <type_traits>
 
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
             }
             const bool in_lo = pos0 + (lane >> 2) < cur.span.len;
             const bool in_hi = pos0 + (lane >> 2) + 8 < cur.span.len;
-            uint32_t pb[kHeadTiles][2];
+            uint32_t pb[kHeadTiles][2][2];         // [piece][tokens 0 .. 7, 8 .. 15]
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
                 float corr[2];
@@ -383,15 +384,24 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
                         acc[x][d][3] *= corr[1];
                     }
                 }
-                pb[x][0] = transpose8x8(Half2<T>::pack(s[x][0], s[x][1]));
-                pb[x][1] = transpose8x8(Half2<T>::pack(s[x][2], s[x][3]));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t first = Half2<T>::pack(s[x][2 * y], s[x][2 * y + 1]);
+                    const float2 f = Half2<T>::unpack(first);
+                    pb[x][0][y] = transpose8x8(first);
+                    pb[x][1][y] = transpose8x8(
+                        Half2<T>::pack(s[x][2 * y] - f.x, s[x][2 * y + 1] - f.y));
+                }
             }
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 uint32_t a[4];
                 ldsm4_trans(a, vs + ((sel >> 1) * 8 + r) * (D * 2) + (((2 * d + (sel & 1)) ^ r) << 4));
 #pragma unroll
-                for (int x = 0; x < kHeadTiles; ++x) mma<T>(acc[x][d], a, pb[x][0], pb[x][1]);
+                for (int x = 0; x < kHeadTiles; ++x) {
+                    mma<T>(acc[x][d], a, pb[x][0][0], pb[x][0][1]);
+                    mma<T>(acc[x][d], a, pb[x][1][0], pb[x][1][1]);
+                }
             }
         }
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
