@@ -50,6 +50,19 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Copies a tensor's strides, 0 for a dimension of one element; false if one is not a multiple of
+// `of`.
+template <int N>
+bool take_strides(int64_t (&to)[N], const int64_t (&from)[N], const int64_t (&sizes)[N], int64_t of)
+{
+    bool ok = true;
+    for (int d = 0; d < N; ++d) {
+        to[d] = sizes[d] > 1 ? from[d] : 0;
+        ok = ok && to[d] % of == 0;
+    }
+    return ok;
+}
+
 inline bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
 // ---- 16-bit types ------------------------------------------------------------------------------

@@ -55,6 +55,28 @@ __device__ __forceinline__ void load_row(float (&x)[16], const uint16_t* row, in
     }
 }
 
+// Sums of d[0 .. 3] over a group of eight lanes, one row to a lane: lane l gets row l & 3, by
+// halving the rows with the lanes (4 shuffles for the 12 of four butterflies).
+__device__ __forceinline__ float sum_rows(const float (&d)[kRows], int l)
+{
+    const bool hi1 = l & 2, hi0 = l & 1;
+    const float a = (hi1 ? d[2] : d[0]) + __shfl_xor_sync(0xffffffffu, hi1 ? d[0] : d[2], 2);
+    const float b = (hi1 ? d[3] : d[1]) + __shfl_xor_sync(0xffffffffu, hi1 ? d[1] : d[3], 2);
+    const float c = (hi0 ? b : a) + __shfl_xor_sync(0xffffffffu, hi0 ? a : b, 1);
+    return c + __shfl_xor_sync(0xffffffffu, c, 4);
+}
+
+__device__ __forceinline__ float dot16(const float (&x)[16], const float (&y)[16])
+{
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        a = fmaf(x[c], y[c], a);
+        b = fmaf(x[8 + c], y[8 + c], b);
+    }
+    return a + b;
+}
+
 __device__ __forceinline__ float sum8(float x)
 {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -62,15 +84,41 @@ __device__ __forceinline__ float sum8(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 4);
 }
 
-// Block: kWarps warps, 16 value rows each, of one (sequence, value head).
-template <typename T, int kWarps>
+template <typename T>
+__device__ __forceinline__ float to_float(uint16_t x)
+{
+    return Half2<T>::unpack(x).x;
+}
+template <typename T>
+__device__ __forceinline__ uint16_t from_float(float x)
+{
+    return static_cast<uint16_t>(Half2<T>::pack(x, 0.f));
+}
+
+// Block: kWarps warps, 16 value rows each, of one (sequence, value head).  kMany: several tokens
+// a sequence; their keys, queries, values and gates are staged in shared memory kStage tokens at
+// a time, while the state's loads are in flight, so that a token costs no round trip to L2.
+constexpr int kStage = 8;
+
+struct Staged {                    // bytes of a staged token
+    int k, q, v, total;
+    __host__ __device__ Staged(int queries, int rows)
+        : k(0), q(2 * kD), v(2 * kD * (1 + queries)), total(2 * kD * (1 + queries) + 2 * rows)
+    {
+    }
+};
+
+template <typename T, int kWarps, bool kMany>
 __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams p)
 {
-    constexpr int kParts = kD / (kWarpRows * kWarps);    // blocks of a state
+    constexpr int kBlockRows = kWarpRows * kWarps;
+    constexpr int kParts = kD / kBlockRows;              // blocks of a state
+    extern __shared__ __align__(16) uint8_t smem[];
     const int item = blockIdx.x / kParts, part = blockIdx.x % kParts;
     const int i = item / p.h_v, j = item % p.h_v;
     const int lane = threadIdx.x & 31, l = lane & 7;
-    const int row0 = (part * kWarps + (threadIdx.x >> 5)) * kWarpRows + (lane >> 3) * kRows;
+    const int block_row = part * kBlockRows;
+    const int row0 = block_row + (threadIdx.x >> 5) * kWarpRows + (lane >> 3) * kRows;
 
     dep_launch();
     dep_wait();
@@ -101,52 +149,91 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
         }
 
     const uint16_t* kp = p.k + i * p.k_stride[0] + (j / p.kgroup) * p.k_stride[2];
-    const uint16_t* vp = p.v + i * p.v_stride[0] + j * p.v_stride[2] + row0;
+    const uint16_t* vp = p.v + i * p.v_stride[0] + j * p.v_stride[2];
     const uint16_t* qp = p.q + i * p.q_stride[0] +
                          static_cast<int64_t>(p.queries > 1 ? j * p.queries : j / p.qgroup) *
                              p.q_stride[2];
     const float* ap = p.alpha + i * p.alpha_stride[0] + j;
     const float* bp = p.beta + i * p.beta_stride[0] + j;
+    const int row = row0 + (l & 3);                      // the row whose sums this lane gets
 
-    for (int t = 0; t < p.tokens; ++t) {
-        float k[16];
-        load_row<T>(k, kp + t * p.k_stride[1], l);
-        const float alpha = ap[t * p.alpha_stride[1]], beta = bp[t * p.beta_stride[1]];
-        const uint2 vb = *reinterpret_cast<const uint2*>(vp + t * p.v_stride[1]);
-        const float2 v01 = Half2<T>::unpack(vb.x), v23 = Half2<T>::unpack(vb.y);
-        const float v[kRows] = {v01.x, v01.y, v23.x, v23.y};
-        float u[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float d = 0.f;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) d = fmaf(s[r][c], k[c], d);
-            u[r] = beta * (v[r] - alpha * sum8(d));
-        }
-        for (int g = 0; g < p.queries; ++g) {
-            float q[16];
-            load_row<T>(q, qp + t * p.q_stride[1] + g * p.q_stride[2], l);
-            float kq = 0.f;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) kq = fmaf(k[c], q[c], kq);
-            kq = sum8(kq);
-            float o[kRows];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                float d = 0.f;
-#pragma unroll
-                for (int c = 0; c < 16; ++c) d = fmaf(s[r][c], q[c], d);
-                o[r] = p.scale * fmaf(alpha, sum8(d), u[r] * kq);
+    const Staged at(p.queries, kBlockRows);
+    float* gates = reinterpret_cast<float*>(smem + kStage * at.total);   // [kStage][alpha, beta]
+    float* kqs = gates + 2 * kStage;                                     // [kStage][queries]
+    for (int t0 = 0; t0 < p.tokens; t0 += kMany ? kStage : 1) {
+        const int here = kMany ? min(kStage, p.tokens - t0) : 1;
+        if constexpr (kMany) {
+            if (t0 > 0) __syncthreads();
+            const int chunks = at.total / 16;            // 16-byte pieces of a token
+            for (int x = threadIdx.x; x < here * chunks; x += kWarps * 32) {
+                const int t = x / chunks, b = (x - t * chunks) * 16;
+                const uint16_t* src;
+                if (b < at.q)
+                    src = kp + (t0 + t) * p.k_stride[1] + b / 2;
+                else if (b < at.v)
+                    src = qp + (t0 + t) * p.q_stride[1] + (b - at.q) / (2 * kD) * p.q_stride[2] +
+                          (b - at.q) % (2 * kD) / 2;
+                else
+                    src = vp + (t0 + t) * p.v_stride[1] + block_row + (b - at.v) / 2;
+                *reinterpret_cast<uint4*>(smem + t * at.total + b) =
+                    *reinterpret_cast<const uint4*>(src);
             }
-            if (l == 0)
-                *reinterpret_cast<uint2*>(p.o + out0 +
-                                          (static_cast<int64_t>(t) * p.h_o + g) * kD) =
-                    make_uint2(Half2<T>::pack(o[0], o[1]), Half2<T>::pack(o[2], o[3]));
+            for (int x = threadIdx.x; x < 2 * here; x += kWarps * 32)
+                gates[x] = x & 1 ? bp[(t0 + x / 2) * p.beta_stride[1]]
+                                 : ap[(t0 + x / 2) * p.alpha_stride[1]];
+            __syncthreads();
+            // k . q of each token and query, a group of eight lanes each
+            for (int x = 0; x < here * p.queries; x += kWarps * 4) {
+                const int y = x + (threadIdx.x >> 3), z = min(y, here * p.queries - 1);
+                const int t = z / p.queries, g = z - t * p.queries;
+                const uint16_t* tok = reinterpret_cast<const uint16_t*>(smem + t * at.total);
+                float k[16], q[16];
+                load_row<T>(k, tok, l);
+                load_row<T>(q, tok + kD * (1 + g), l);
+                const float kq = sum8(dot16(k, q));
+                if (y == z && l == 0) kqs[z] = kq;
+            }
+            __syncthreads();
         }
+        for (int t = 0; t < here; ++t) {
+            const uint16_t* tok = reinterpret_cast<const uint16_t*>(smem + t * at.total);
+            float k[16], alpha, beta, v;
+            if constexpr (kMany) {
+                load_row<T>(k, tok, l);
+                alpha = gates[2 * t], beta = gates[2 * t + 1];
+                v = to_float<T>(tok[at.v / 2 + row - block_row]);
+            } else {
+                load_row<T>(k, kp, l);
+                alpha = ap[0], beta = bp[0];
+                v = to_float<T>(vp[row]);
+            }
+            float d[kRows], u[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
+            for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], k);
+            const float mine = beta * (v - alpha * sum_rows(d, l));
 #pragma unroll
-            for (int c = 0; c < 16; ++c) s[r][c] = fmaf(u[r], k[c], alpha * s[r][c]);
+            for (int r = 0; r < kRows; ++r) u[r] = __shfl_sync(0xffffffffu, mine, (lane & 24) + r);
+            for (int g = 0; g < p.queries; ++g) {
+                float q[16], kq;
+                if constexpr (kMany) {
+                    load_row<T>(q, tok + kD * (1 + g), l);
+                    kq = kqs[t * p.queries + g];
+                } else {
+                    load_row<T>(q, qp + g * p.q_stride[2], l);
+                    kq = sum8(dot16(k, q));
+                }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], q);
+                const float o = p.scale * fmaf(alpha, sum_rows(d, l), mine * kq);
+                if (l < kRows)
+                    p.o[out0 + l + (static_cast<int64_t>(t0 + t) * p.h_o + g) * kD] =
+                        from_float<T>(o);
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int c = 0; c < 16; ++c) s[r][c] = fmaf(u[r], k[c], alpha * s[r][c]);
+        }
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -154,6 +241,17 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
         for (int c = 0; c < 4; ++c)
             state[r * (kD / 4) + 8 * c] =
                 make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
+}
+
+template <typename T, int kWarps>
+cudaError_t run(const StepParams& p, int64_t items, cudaStream_t stream)
+{
+    constexpr int kBlockRows = kWarpRows * kWarps;
+    const dim3 grid(static_cast<uint32_t>(items * (kD / kBlockRows))), block(kWarps * 32);
+    if (p.tokens == 1)
+        return launch(gdn_step_kernel<T, kWarps, false>, grid, block, 0, stream, p);
+    const size_t smem = kStage * (Staged(p.queries, kBlockRows).total + 4 * (2 + p.queries));
+    return launch(gdn_step_kernel<T, kWarps, true>, grid, block, smem, stream, p);
 }
 
 }  // namespace
@@ -182,18 +280,20 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     if (misaligned(a->q) || misaligned(a->k) || misaligned(a->v) || misaligned(a->state) ||
         misaligned(a->o))
         return fail(DECODE_ERR_UNSUPPORTED, "q, k, v, state and o must be 16-byte aligned");
-    for (int d = 0; d < 3; ++d)
-        if (a->q_stride[d] % 8 || a->k_stride[d] % 8 || a->v_stride[d] % 8)
-            return fail(DECODE_ERR_UNSUPPORTED, "strides of q, k and v must be multiples of 8");
-    if (a->state_stride % 4 || (a->n_slots > 1 && a->state_stride < a->h_v * kD * kD))
+    StepParams p{};
+    if (!take_strides(p.q_stride, a->q_stride, {a->n, a->tokens, a->h_q}, 8) ||
+        !take_strides(p.k_stride, a->k_stride, {a->n, a->tokens, a->h_k}, 8) ||
+        !take_strides(p.v_stride, a->v_stride, {a->n, a->tokens, a->h_v}, 8))
+        return fail(DECODE_ERR_UNSUPPORTED, "strides of q, k and v must be multiples of 8");
+    take_strides(p.alpha_stride, a->alpha_stride, {a->n, a->tokens}, 1);
+    take_strides(p.beta_stride, a->beta_stride, {a->n, a->tokens}, 1);
+    if (a->n_slots > 1 && (a->state_stride % 4 || a->state_stride < a->h_v * kD * kD))
         return fail(DECODE_ERR_INVALID_ARG, "state_stride %lld", (long long)a->state_stride);
     constexpr int kWarps = 2;
-    const int64_t blocks = a->n * a->h_v * (kD / (kWarpRows * kWarps));
     if (a->n >= (int64_t(1) << 31) / (a->h_v * 8) || a->tokens >= (1 << 24) ||
         a->n_slots >= (int64_t(1) << 31))
         return fail(DECODE_ERR_UNSUPPORTED, "too many states or tokens for one call");
 
-    StepParams p{};
     p.status = status_word();
     if (p.status == nullptr) return DECODE_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(a->q);
@@ -204,16 +304,7 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     p.state = a->state;
     p.slots = a->slots;
     p.o = static_cast<uint16_t*>(a->o);
-    for (int d = 0; d < 3; ++d) {
-        p.q_stride[d] = a->q_stride[d];
-        p.k_stride[d] = a->k_stride[d];
-        p.v_stride[d] = a->v_stride[d];
-    }
-    for (int d = 0; d < 2; ++d) {
-        p.alpha_stride[d] = a->alpha_stride[d];
-        p.beta_stride[d] = a->beta_stride[d];
-    }
-    p.state_stride = a->state_stride;
+    p.state_stride = a->n_slots > 1 ? a->state_stride : 0;
     p.tokens = static_cast<int32_t>(a->tokens);
     p.h_v = static_cast<int32_t>(a->h_v);
     p.h_o = static_cast<int32_t>(queries > 1 ? a->h_q : a->h_v);
@@ -222,10 +313,9 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     p.queries = static_cast<int32_t>(queries);
     p.n_slots = static_cast<int32_t>(a->n_slots);
     p.scale = a->scale;
-    auto* kernel = a->dtype == DECODE_BF16 ? gdn_step_kernel<__nv_bfloat16, kWarps>
-                                           : gdn_step_kernel<__half, kWarps>;
-    const cudaError_t e = launch(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(kWarps * 32), 0,
-                                 stream, p);
+    const int64_t items = a->n * a->h_v;
+    const cudaError_t e = a->dtype == DECODE_BF16 ? run<__nv_bfloat16, kWarps>(p, items, stream)
+                                                  : run<__half, kWarps>(p, items, stream);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "gdn_step_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;

@@ -645,11 +645,13 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     if (misaligned(a->q) || misaligned(a->k_cache) || misaligned(a->v_cache) || misaligned(a->o) ||
         misaligned(a->workspace))
         return fail(DECODE_ERR_UNSUPPORTED, "16-bit tensors and workspace must be 16-byte aligned");
-    for (int d = 0; d < 2; ++d)
-        if (a->q_stride[d] % 8) return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
-    for (int d = 0; d < 3; ++d)
-        if (a->k_stride[d] % 8 || a->v_stride[d] % 8)
-            return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 8");
+    AttnParams p{};
+    if (!take_strides(p.q_stride, a->q_stride, {a->n, a->h_q}, 8))
+        return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_kv};
+    if (!take_strides(p.k_stride, a->k_stride, cs, 8) ||
+        !take_strides(p.v_stride, a->v_stride, cs, 8))
+        return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 8");
     constexpr int64_t kMost = (int64_t(1) << 31) - 1;
     if (a->n > kMost || a->h_q >= (1 << 20) || a->pages > kMost || a->page_size > kMost ||
         a->table_width > kMost)
@@ -666,7 +668,6 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     int64_t max_len = a->pages == 0 ? 0 : a->page_size * a->table_width;
     if (max_len > kMost - 1024) max_len = kMost - 1024;
 
-    AttnParams p{};
     p.status = status_word();
     if (p.status == nullptr) return DECODE_ERR_CUDA;
     auto* ws = static_cast<uint8_t*>(a->workspace);
@@ -680,12 +681,7 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     p.desc = reinterpret_cast<int4*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
     p.part_o = reinterpret_cast<float*>(ws + l.o);
-    for (int d = 0; d < 2; ++d) p.q_stride[d] = a->q_stride[d];
-    for (int d = 0; d < 3; ++d) {
-        p.k_stride[d] = a->k_stride[d];
-        p.v_stride[d] = a->v_stride[d];
-    }
-    p.table_stride = a->table_stride;
+    p.table_stride = a->n > 1 ? a->table_stride : 0;
     p.max_len = max_len;
     p.n = static_cast<int32_t>(a->n);
     p.h_q = static_cast<int32_t>(a->h_q);

@@ -20,7 +20,9 @@ namespace {
 
 using namespace decode;
 
-constexpr int kWarps = 4;
+constexpr int kUnroll = 4;       // heads a lane has in flight
+constexpr int kMaxWarps = 8;
+enum Pairing { kNone, kSplit, kInterleaved };
 
 struct NormParams {
     const uint16_t* q;
@@ -53,53 +55,97 @@ __device__ __forceinline__ void unpack8(float (&x)[8], uint4 b)
     x[4] = a2.x, x[5] = a2.y, x[6] = a3.x, x[7] = a3.y;
 }
 
-template <typename T, int kLanes, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const NormParams p)
+template <typename T, int kLanes, Pairing kPairing>
+__global__ void __launch_bounds__(kMaxWarps * 32) qk_norm_rope_kernel(const NormParams p)
 {
     constexpr int kHeads = 32 / kLanes;              // heads of a warp at a time
     const int64_t t = blockIdx.x;
     const int lane = threadIdx.x & 31, l = lane % kLanes;
+    const int warps = blockDim.x >> 5;
     const int first = (threadIdx.x >> 5) * kHeads + lane / kLanes;
     const int e = 8 * l;                             // the lane's first element
     const bool in_head = e < p.head_dim, in_rot = e < p.rot;
     const int half = p.rot / 2;
+    const int total = p.h_q + p.h_k + (p.v != nullptr ? p.h_k : 0);
 
     dep_launch();
     dep_wait();
 
+    // What the indices say is loaded first, the rows next, and the angles, which wait for the
+    // positions, after them.
+    int32_t pos[DECODE_MAX_AXES];
+    if constexpr (kPairing != kNone) {
+#pragma unroll
+        for (int x = 0; x < DECODE_MAX_AXES; ++x)
+            pos[x] = x < p.axes ? p.positions[x * p.position_stride + t] : 0;
+    }
+    int32_t slot = p.k_cache != nullptr ? p.slots[t] : -1;
+    auto row_of = [&](int h) {
+        return h < p.h_q           ? p.q + t * p.q_stride[0] + h * p.q_stride[1]
+               : h < p.h_q + p.h_k ? p.k + t * p.k_stride[0] + (h - p.h_q) * p.k_stride[1]
+                                   : p.v + t * p.v_stride[0] + (h - p.h_q - p.h_k) * p.v_stride[1];
+    };
+    uint4 in[kUnroll];
+    auto fetch = [&](int h0) {
+#pragma unroll
+        for (int x = 0; x < kUnroll; ++x) {
+            const int h = h0 + x * warps * kHeads + first;
+            in[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (in_head && h < total) in[x] = *reinterpret_cast<const uint4*>(row_of(h) + e);
+        }
+    };
+    fetch(0);
+    const bool weights = p.q_weight != nullptr || p.k_weight != nullptr;
+    uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
+    if (in_head && p.q_weight) wq = *reinterpret_cast<const uint4*>(p.q_weight + e);
+    if (in_head && p.k_weight) wk = *reinterpret_cast<const uint4*>(p.k_weight + e);
+
     // The token's angles at the lane's elements, and whether its positions lie in the table.
     bool ok = true;
-    float cs[8], sn[8];
+    constexpr int kPairs = kPairing == kInterleaved ? 4 : 8;   // pairs that the lane meets
+    float cs[kPairs], sn[kPairs];
+    if constexpr (kPairing != kNone) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) cs[c] = 1.f, sn[c] = 0.f;
-    if (p.rot > 0) {
-        int64_t pos[DECODE_MAX_AXES];
+        for (int x = 0; x < DECODE_MAX_AXES; ++x)
+            ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
 #pragma unroll
-        for (int x = 0; x < DECODE_MAX_AXES; ++x) {
-            pos[x] = x < p.axes ? p.positions[x * p.position_stride + t] : 0;
-            ok = ok && pos[x] >= 0 && pos[x] < p.table_rows;
-        }
+        for (int c = 0; c < kPairs; ++c) cs[c] = 1.f, sn[c] = 0.f;
         if (ok && in_rot) {
-            constexpr int kPairs = kInterleaved ? 4 : 8;
-            const int pair0 = kInterleaved ? e / 2 : (e < half ? e : e - half);
+            const int pair0 = kPairing == kInterleaved ? e / 2 : (e < half ? e : e - half);
+            auto axis_of = [&](int pair) {
+                int axis = 0;
 #pragma unroll
-            for (int c = 0; c < kPairs; ++c) {
-                const int pair = pair0 + c;
-                int64_t at = pos[0];
-                if (p.axes > 1) {
+                for (int x = 1; x < DECODE_MAX_AXES; ++x)
+                    axis += x < p.axes && pair >= p.section_end[x - 1];
+                return axis;
+            };
+            auto table_row = [&](int axis) {
+                int32_t at = pos[0];
 #pragma unroll
-                    for (int x = 1; x < DECODE_MAX_AXES; ++x)
-                        if (x < p.axes && pair >= p.section_end[x - 1]) at = pos[x];
+                for (int x = 1; x < DECODE_MAX_AXES; ++x) at = axis == x ? pos[x] : at;
+                return p.table + static_cast<int64_t>(at) * p.rot;
+            };
+            const int axis = axis_of(pair0);
+            if (axis == axis_of(pair0 + kPairs - 1)) {
+                // one row of the table: its pairs lie side by side
+                const float* row = table_row(axis) + pair0;
+#pragma unroll
+                for (int c = 0; c < kPairs; c += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(row + c);
+                    const float4 y = *reinterpret_cast<const float4*>(row + half + c);
+                    cs[c] = x.x, cs[c + 1] = x.y, cs[c + 2] = x.z, cs[c + 3] = x.w;
+                    sn[c] = y.x, sn[c + 1] = y.y, sn[c + 2] = y.z, sn[c + 3] = y.w;
                 }
-                const float* row = p.table + at * p.rot + pair;
-                const float co = row[0], si = row[half];
-                if constexpr (kInterleaved) {
-                    cs[2 * c] = cs[2 * c + 1] = co;
-                    sn[2 * c] = -si, sn[2 * c + 1] = si;
-                } else {
-                    cs[c] = co;
-                    sn[c] = e < half ? -si : si;
+            } else {
+#pragma unroll
+                for (int c = 0; c < kPairs; ++c) {
+                    const float* row = table_row(axis_of(pair0 + c)) + pair0 + c;
+                    cs[c] = row[0], sn[c] = row[half];
                 }
+            }
+            if (kPairing == kSplit && e < half) {
+#pragma unroll
+                for (int c = 0; c < kPairs; ++c) sn[c] = -sn[c];
             }
         }
         if (!ok && threadIdx.x == 0) atomicOr(p.status, DECODE_BAD_POSITION);
@@ -107,84 +153,99 @@ __global__ void __launch_bounds__(kWarps * 32) qk_norm_rope_kernel(const NormPar
     // The lane that holds the partners of this lane's elements (split pairing).
     const int partner = !in_rot ? lane : lane + (e < half ? half / 8 : -(half / 8));
 
-    float wq[8], wk[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) wq[c] = wk[c] = 1.f;
-    if (in_head && p.q_weight) unpack8<T>(wq, *reinterpret_cast<const uint4*>(p.q_weight + e));
-    if (in_head && p.k_weight) unpack8<T>(wk, *reinterpret_cast<const uint4*>(p.k_weight + e));
-
-    int64_t slot = -1;
-    if (p.k_cache != nullptr && ok) {
-        slot = p.slots[t];
-        if (slot < -1 || slot >= p.cache_slots) {
-            if (threadIdx.x == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
-            slot = -1;
-        }
+    if (!ok) slot = -1;
+    if (slot < -1 || slot >= p.cache_slots) {
+        if (threadIdx.x == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+        slot = -1;
     }
-    const int64_t page = slot < 0 ? 0 : static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
-    const int64_t off = slot < 0 ? 0 : slot - page * p.page_size;
+    const int32_t page = slot < 0 ? 0 : static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
+    const int32_t off = slot < 0 ? 0 : slot - page * p.page_size;
+    uint16_t* const k_row = p.k_cache == nullptr
+                                ? p.k_out + t * p.k_out_stride[0]
+                                : p.k_cache + page * p.k_cache_stride[0] + off * p.k_cache_stride[1];
+    const int64_t k_head = p.k_cache == nullptr ? p.k_out_stride[1] : p.k_cache_stride[2];
     const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
 
-    const int total = p.h_q + p.h_k + (p.v != nullptr ? p.h_k : 0);
-    // the trip count is the same for all lanes: the shuffles below need the whole warp
-    for (int h0 = 0; h0 < total; h0 += kWarps * kHeads) {
-        const int h = h0 + first;
-        const bool is_q = h < p.h_q, is_k = !is_q && h < p.h_q + p.h_k;
-        const int hh = is_q ? h : is_k ? h - p.h_q : h - p.h_q - p.h_k;
-        const bool here = in_head && h < total;
-        const uint16_t* src = is_q   ? p.q + t * p.q_stride[0] + hh * p.q_stride[1]
-                              : is_k ? p.k + t * p.k_stride[0] + hh * p.k_stride[1]
-                                     : p.v + t * p.v_stride[0] + hh * p.v_stride[1];
-        uint4 b = make_uint4(0u, 0u, 0u, 0u);
-        if (here && ok) b = *reinterpret_cast<const uint4*>(src + e);
-        float x[8];
-        unpack8<T>(x, b);
-        float f = 1.f;
-        if (p.norm != DECODE_NORM_NONE) {
-            float s = 0.f;
+    // the trip counts are the same for all lanes: the shuffles need the whole warp
+    for (int h0 = 0; h0 < total; h0 += warps * kHeads * kUnroll) {
+        if (h0 > 0) fetch(h0);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) s = fmaf(x[c], x[c], s);
+        for (int u = 0; u < kUnroll; ++u) {
+            if (h0 + u * warps * kHeads >= total) break;
+            const int h = h0 + u * warps * kHeads + first;
+            const bool is_q = h < p.h_q, is_v = h >= p.h_q + p.h_k;
+            float x[8];
+            unpack8<T>(x, in[u]);
+            float f = 1.f;
+            if (p.norm != DECODE_NORM_NONE) {
+                float s = 0.f;
 #pragma unroll
-            for (int m = 1; m < kLanes; m *= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
-            f = rsqrtf(fmaf(s, inv_d, p.eps));
+                for (int c = 0; c < 8; ++c) s = fmaf(x[c], x[c], s);
+#pragma unroll
+                for (int m = 1; m < kLanes; m *= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
+                f = rsqrtf(fmaf(s, inv_d, p.eps));
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) x[c] *= f;
+            if (weights && (is_q ? p.q_weight : p.k_weight) != nullptr) {
+                float w[8];
+                unpack8<T>(w, is_q ? wq : wk);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] *= w[c];
+            }
+            if constexpr (kPairing == kSplit) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float y = __shfl_sync(0xffffffffu, x[c], partner);
+                    x[c] = in_rot ? fmaf(x[c], cs[c], y * sn[c]) : x[c];
+                }
+            } else if constexpr (kPairing == kInterleaved) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float a = x[2 * c], b = x[2 * c + 1];
+                    x[2 * c] = in_rot ? fmaf(a, cs[c], -b * sn[c]) : a;
+                    x[2 * c + 1] = in_rot ? fmaf(b, cs[c], a * sn[c]) : b;
+                }
+            }
+            uint4 b = in[u];
+            if (!is_v) {
+                b = make_uint4(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]),
+                               Half2<T>::pack(x[4], x[5]), Half2<T>::pack(x[6], x[7]));
+                if (!ok) b = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (!in_head || h >= total) continue;
+            if (is_q)
+                *reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride[0] +
+                                          h * p.q_out_stride[1] + e) = b;
+            else if (p.k_cache == nullptr || slot >= 0)
+                *reinterpret_cast<uint4*>(
+                    (is_v ? p.v_cache + page * p.v_cache_stride[0] + off * p.v_cache_stride[1] +
+                                (h - p.h_q - p.h_k) * p.v_cache_stride[2]
+                          : k_row + (h - p.h_q) * k_head) + e) = b;
         }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = x[c] * f * (is_q ? wq[c] : wk[c]);
-        if (p.rot > 0) {
-            float y[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                y[c] = kInterleaved ? x[c ^ 1] : __shfl_sync(0xffffffffu, x[c], partner);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) x[c] = in_rot ? fmaf(x[c], cs[c], y[c] * sn[c]) : x[c];
-        }
-        uint16_t* dst = nullptr;
-        if (is_q)
-            dst = p.q_out + t * p.q_out_stride[0] + hh * p.q_out_stride[1];
-        else if (is_k && p.k_cache == nullptr)
-            dst = p.k_out + t * p.k_out_stride[0] + hh * p.k_out_stride[1];
-        else if (slot >= 0)
-            dst = is_k ? p.k_cache + page * p.k_cache_stride[0] + off * p.k_cache_stride[1] +
-                             hh * p.k_cache_stride[2]
-                       : p.v_cache + page * p.v_cache_stride[0] + off * p.v_cache_stride[1] +
-                             hh * p.v_cache_stride[2];
-        if (is_q || is_k) {
-            b = make_uint4(Half2<T>::pack(x[0], x[1]), Half2<T>::pack(x[2], x[3]),
-                           Half2<T>::pack(x[4], x[5]), Half2<T>::pack(x[6], x[7]));
-            if (!ok) b = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (here && dst != nullptr) *reinterpret_cast<uint4*>(dst + e) = b;
     }
 }
 
-template <typename T>
-void (*pick(int64_t d, bool interleaved))(NormParams)
+template <typename T, int kLanes>
+cudaError_t run(const NormParams& p, int64_t tokens, bool interleaved, cudaStream_t stream)
 {
-    if (d <= 64)
-        return interleaved ? qk_norm_rope_kernel<T, 8, true> : qk_norm_rope_kernel<T, 8, false>;
-    if (d <= 128)
-        return interleaved ? qk_norm_rope_kernel<T, 16, true> : qk_norm_rope_kernel<T, 16, false>;
-    return interleaved ? qk_norm_rope_kernel<T, 32, true> : qk_norm_rope_kernel<T, 32, false>;
+    auto* kernel = p.rot == 0    ? qk_norm_rope_kernel<T, kLanes, kNone>
+                   : interleaved ? qk_norm_rope_kernel<T, kLanes, kInterleaved>
+                                 : qk_norm_rope_kernel<T, kLanes, kSplit>;
+    // as many warps as the token's heads keep busy with kUnroll heads a lane
+    constexpr int kPass = 32 / kLanes * kUnroll;
+    const int total = p.h_q + (p.v != nullptr ? 2 : 1) * p.h_k;
+    const int warps = (total + kPass - 1) / kPass;
+    return launch(kernel, dim3(static_cast<uint32_t>(tokens)),
+                  dim3(32 * (warps < 1 ? 1 : warps > kMaxWarps ? kMaxWarps : warps)), 0, stream, p);
+}
+
+template <typename T>
+cudaError_t run(const NormParams& p, int64_t tokens, bool interleaved, cudaStream_t stream)
+{
+    return p.head_dim <= 64    ? run<T, 8>(p, tokens, interleaved, stream)
+           : p.head_dim <= 128 ? run<T, 16>(p, tokens, interleaved, stream)
+                               : run<T, 32>(p, tokens, interleaved, stream);
 }
 
 }  // namespace
@@ -235,20 +296,22 @@ extern "C" int decode_qk_norm_rope(const decode_qk_norm_rope_args* a, cudaStream
         return fail(DECODE_ERR_INVALID_ARG, "null pointer");
     if (misaligned(a->q) || misaligned(a->k) || misaligned(a->v) || misaligned(a->q_out) ||
         misaligned(a->k_out) || misaligned(a->k_cache) || misaligned(a->v_cache) ||
-        misaligned(a->q_weight) || misaligned(a->k_weight))
-        return fail(DECODE_ERR_UNSUPPORTED, "16-bit tensors must be 16-byte aligned");
-    for (int d = 0; d < 2; ++d)
-        if (a->q_stride[d] % 8 || a->k_stride[d] % 8 || (a->v && a->v_stride[d] % 8) ||
-            a->q_out_stride[d] % 8 || (!cache && a->k_out_stride[d] % 8))
-            return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
-    if (cache)
-        for (int d = 0; d < 3; ++d)
-            if (a->k_cache_stride[d] % 8 || a->v_cache_stride[d] % 8)
-                return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 8");
+        misaligned(a->q_weight) || misaligned(a->k_weight) || misaligned(a->table))
+        return fail(DECODE_ERR_UNSUPPORTED, "16-bit tensors and the table must be 16-byte aligned");
+    NormParams p{};
+    if (!take_strides(p.q_stride, a->q_stride, {a->tokens, a->h_q}, 8) ||
+        !take_strides(p.k_stride, a->k_stride, {a->tokens, a->h_k}, 8) ||
+        !take_strides(p.q_out_stride, a->q_out_stride, {a->tokens, a->h_q}, 8) ||
+        (!cache && !take_strides(p.k_out_stride, a->k_out_stride, {a->tokens, a->h_k}, 8)) ||
+        (cache && !take_strides(p.v_stride, a->v_stride, {a->tokens, a->h_k}, 8)))
+        return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_k};
+    if (cache && (!take_strides(p.k_cache_stride, a->k_cache_stride, cs, 8) ||
+                  !take_strides(p.v_cache_stride, a->v_cache_stride, cs, 8)))
+        return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 8");
     if (a->tokens >= (int64_t(1) << 31) || a->h_q + 2 * a->h_k >= (1 << 24))
         return fail(DECODE_ERR_UNSUPPORTED, "too many tokens or heads for one call");
 
-    NormParams p{};
     p.status = status_word();
     if (p.status == nullptr) return DECODE_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(a->q);
@@ -263,17 +326,6 @@ extern "C" int decode_qk_norm_rope(const decode_qk_norm_rope_args* a, cudaStream
     p.k_cache = static_cast<uint16_t*>(a->k_cache);
     p.v_cache = static_cast<uint16_t*>(a->v_cache);
     p.slots = a->slots;
-    for (int d = 0; d < 2; ++d) {
-        p.q_stride[d] = a->q_stride[d];
-        p.k_stride[d] = a->k_stride[d];
-        p.v_stride[d] = a->v_stride[d];
-        p.q_out_stride[d] = a->q_out_stride[d];
-        p.k_out_stride[d] = a->k_out_stride[d];
-    }
-    for (int d = 0; d < 3; ++d) {
-        p.k_cache_stride[d] = a->k_cache_stride[d];
-        p.v_cache_stride[d] = a->v_cache_stride[d];
-    }
     p.position_stride = a->position_stride;
     p.table_rows = a->table_rows;
     p.cache_slots = cache ? a->pages * a->page_size : 0;
@@ -287,10 +339,10 @@ extern "C" int decode_qk_norm_rope(const decode_qk_norm_rope_args* a, cudaStream
     int32_t end = 0;
     for (int x = 0; x < DECODE_MAX_AXES; ++x) p.section_end[x] = end += a->sections[x];
     p.eps = a->eps;
-    auto* kernel = a->dtype == DECODE_BF16 ? pick<__nv_bfloat16>(a->head_dim, a->interleaved != 0)
-                                           : pick<__half>(a->head_dim, a->interleaved != 0);
-    const cudaError_t e = launch(kernel, dim3(static_cast<uint32_t>(a->tokens)), dim3(kWarps * 32),
-                                 0, stream, p);
+    const bool inter = a->interleaved != 0;
+    const cudaError_t e = a->dtype == DECODE_BF16
+                              ? run<__nv_bfloat16>(p, a->tokens, inter, stream)
+                              : run<__half>(p, a->tokens, inter, stream);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "qk_norm_rope_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;

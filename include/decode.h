@@ -13,8 +13,8 @@
  * DECODE_BF16, for all of a call's 16-bit tensors); sums, norms, states and softmax statistics are
  * fp32 and each 16-bit result is rounded once.  Strides are in elements; the innermost dimension
  * (head_dim) is dense, other strides of 16-bit tensors are multiples of 8 (rows are read 16 bytes at
- * a time), and pointers are 16-byte aligned.  Inputs may have any such stride, zero included; a
- * written tensor's elements must not overlap.  Buffers belong to the caller and nothing is retained.
+ * a time), and pointers are 16-byte aligned; the stride of a dimension of one element is ignored.
+ * Inputs may have any such stride, zero included; a written tensor's elements must not overlap.  Buffers belong to the caller and nothing is retained.
  * Calls are asynchronous on `stream` in stream order, enqueue kernel launches only (no allocation,
  * copy or synchronisation; they may be recorded into a CUDA graph once one call has run on the
  * device) and use programmatic dependent launch: every kernel waits for all earlier work on the

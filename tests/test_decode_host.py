@@ -86,7 +86,7 @@ BAD, NOT = g.GDN_ERR_INVALID_ARG, g.GDN_ERR_UNSUPPORTED
     (dict(dtype=2), BAD, "dtype"), (dict(h_v=3), BAD, "layout"), (dict(h_q=3), BAD, "layout"),
     (dict(head_dim=64), NOT, "head_dim"), (dict(h_q=36), NOT, "8 query heads"),
     (dict(q=0), BAD, "null"), (dict(state=0), BAD, "null"), (dict(slots=0, n=2), BAD, "states"),
-    (dict(v=4104), NOT, "aligned"), (dict(k_stride=(0, 12, 0)), NOT, "multiples"),
+    (dict(v=4104), NOT, "aligned"), (dict(tokens=2, k_stride=(0, 12, 0)), NOT, "multiples"),
     (dict(n_slots=2, state_stride=64), BAD, "state_stride"), (dict(n=1 << 40), NOT, "too many"),
 ])
 def test_step_refusals(change, code, match):
@@ -104,8 +104,8 @@ def test_step_refusals(change, code, match):
     (dict(axes=2, sections=(-1, 33, 0, 0)), BAD, "negative section"),
     (dict(v=0), BAD, "together"), (dict(slots=0), BAD, "together"), (dict(page_size=0), BAD, "pages"),
     (dict(pages=1 << 30), BAD, "pages"), (dict(q_out=0), BAD, "null"), (dict(positions=0), BAD, "null"),
-    (dict(k=4100), NOT, "aligned"), (dict(q_stride=(4, 0)), NOT, "multiples"),
-    (dict(v_cache_stride=(0, 0, 4)), NOT, "multiples"), (dict(tokens=1 << 31), NOT, "too many"),
+    (dict(k=4100), NOT, "aligned"), (dict(tokens=2, q_stride=(4, 0)), NOT, "multiples"),
+    (dict(v_cache_stride=(4, 0, 0)), NOT, "multiples"), (dict(tokens=1 << 31), NOT, "too many"),
 ])
 def test_norm_refusals(change, code, match):
     args = pack("decode_qk_norm_rope_args", **{**NORM, **change})
@@ -117,7 +117,7 @@ def test_norm_refusals(change, code, match):
     (dict(n=-1), BAD, "negative"), (dict(page_size=0), BAD, "page size"), (dict(dtype=7), BAD, "dtype"),
     (dict(h_q=3), BAD, "query heads"), (dict(h_kv=0), BAD, "key heads"), (dict(window=-1), BAD, "neg"),
     (dict(head_dim=96), NOT, "head_dim"), (dict(q=0), BAD, "null"), (dict(workspace=0), BAD, "null"),
-    (dict(o=4104), NOT, "aligned"), (dict(q_stride=(4, 0)), NOT, "multiples"),
+    (dict(o=4104), NOT, "aligned"), (dict(q_stride=(0, 4)), NOT, "multiples"),
     (dict(k_stride=(8, 4, 8)), NOT, "multiples"), (dict(pages=1 << 31), NOT, "too large"),
 ])
 def test_attention_refusals(change, code, match):
