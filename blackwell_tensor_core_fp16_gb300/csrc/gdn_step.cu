@@ -43,15 +43,50 @@ struct StepParams {
     float scale;
 };
 
-// Elements 4 (l + 8 j) .. + 3, j = 0 .. 3, of a row of 128.
+// Pairs of fp32 values in one 64-bit register pair: fma.rn.f32x2 does two products at the issue
+// cost of one.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Elements 4 (l + 8 j) .. + 3, j = 0 .. 3, of a row of 128, as eight pairs.
 template <typename T>
-__device__ __forceinline__ void load_row(float (&x)[16], const uint16_t* row, int l)
+__device__ __forceinline__ void load_row(uint64_t (&x)[8], const uint16_t* row, int l)
 {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint2 b = *reinterpret_cast<const uint2*>(row + 4 * (l + 8 * j));
         const float2 lo = Half2<T>::unpack(b.x), hi = Half2<T>::unpack(b.y);
-        x[4 * j] = lo.x, x[4 * j + 1] = lo.y, x[4 * j + 2] = hi.x, x[4 * j + 3] = hi.y;
+        x[2 * j] = pair(lo.x, lo.y), x[2 * j + 1] = pair(hi.x, hi.y);
+    }
+}
+__device__ __forceinline__ void load_row(uint64_t (&x)[8], const float* row, int l)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(row + 4 * (l + 8 * j));
+        x[2 * j] = b.x, x[2 * j + 1] = b.y;
     }
 }
 
@@ -66,15 +101,16 @@ __device__ __forceinline__ float sum_rows(const float (&d)[kRows], int l)
     return c + __shfl_xor_sync(0xffffffffu, c, 4);
 }
 
-__device__ __forceinline__ float dot16(const float (&x)[16], const float (&y)[16])
+__device__ __forceinline__ float dot16(const uint64_t (&x)[8], const uint64_t (&y)[8])
 {
-    float a = 0.f, b = 0.f;
+    uint64_t a = mul2(x[0], y[0]), b = mul2(x[4], y[4]);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        a = fmaf(x[c], y[c], a);
-        b = fmaf(x[8 + c], y[8 + c], b);
+    for (int c = 1; c < 4; ++c) {
+        a = fma2(x[c], y[c], a);
+        b = fma2(x[4 + c], y[4 + c], b);
     }
-    return a + b;
+    const float2 p = halves(a), q = halves(b);
+    return (p.x + p.y) + (q.x + q.y);
 }
 
 __device__ __forceinline__ float sum8(float x)
@@ -97,13 +133,16 @@ __device__ __forceinline__ uint16_t from_float(float x)
 
 // Block: kWarps warps, 16 value rows each, of one (sequence, value head).  kMany: several tokens
 // a sequence; their keys, queries, values and gates are staged in shared memory kStage tokens at
-// a time, while the state's loads are in flight, so that a token costs no round trip to L2.
+// a time, converted to fp32, while the state's loads are in flight, so that a token costs neither
+// a round trip to L2 nor a conversion in every lane group.
 constexpr int kStage = 8;
 
-struct Staged {                    // bytes of a staged token
-    int k, q, v, total;
+// Floats of a staged token: its key, its queries, the block's values, (alpha, beta) and k . q.
+struct Staged {
+    int q, v, gates, kq, total;
     __host__ __device__ Staged(int queries, int rows)
-        : k(0), q(2 * kD), v(2 * kD * (1 + queries)), total(2 * kD * (1 + queries) + 2 * rows)
+        : q(kD), v(kD * (1 + queries)), gates(v + rows), kq(gates + 2),
+          total((kq + queries + 3) / 4 * 4)
     {
     }
 };
@@ -113,7 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
 {
     constexpr int kBlockRows = kWarpRows * kWarps;
     constexpr int kParts = kD / kBlockRows;              // blocks of a state
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(16) float smem[];
     const int item = blockIdx.x / kParts, part = blockIdx.x % kParts;
     const int i = item / p.h_v, j = item % p.h_v;
     const int lane = threadIdx.x & 31, l = lane & 7;
@@ -137,15 +176,16 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
         return;
     }
 
-    float4* state = reinterpret_cast<float4*>(p.state + slot * p.state_stride +
-                                              (static_cast<int64_t>(j) * kD + row0) * kD) + l;
-    float s[kRows][16];
+    ulonglong2* state =
+        reinterpret_cast<ulonglong2*>(p.state + slot * p.state_stride +
+                                      (static_cast<int64_t>(j) * kD + row0) * kD) + l;
+    uint64_t s[kRows][8];
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 x = state[r * (kD / 4) + 8 * c];
-            s[r][4 * c] = x.x, s[r][4 * c + 1] = x.y, s[r][4 * c + 2] = x.z, s[r][4 * c + 3] = x.w;
+            const ulonglong2 x = state[r * (kD / 4) + 8 * c];
+            s[r][2 * c] = x.x, s[r][2 * c + 1] = x.y;
         }
 
     const uint16_t* kp = p.k + i * p.k_stride[0] + (j / p.kgroup) * p.k_stride[2];
@@ -158,66 +198,68 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
     const int row = row0 + (l & 3);                      // the row whose sums this lane gets
 
     const Staged at(p.queries, kBlockRows);
-    float* gates = reinterpret_cast<float*>(smem + kStage * at.total);   // [kStage][alpha, beta]
-    float* kqs = gates + 2 * kStage;                                     // [kStage][queries]
     for (int t0 = 0; t0 < p.tokens; t0 += kMany ? kStage : 1) {
         const int here = kMany ? min(kStage, p.tokens - t0) : 1;
         if constexpr (kMany) {
             if (t0 > 0) __syncthreads();
-            const int chunks = at.total / 16;            // 16-byte pieces of a token
-            for (int x = threadIdx.x; x < here * chunks; x += kWarps * 32) {
-                const int t = x / chunks, b = (x - t * chunks) * 16;
+            const int pieces = at.gates / 8;             // of 8 elements, of a token
+            for (int x = threadIdx.x; x < here * pieces; x += kWarps * 32) {
+                const int t = x / pieces, c = (x - t * pieces) * 8;
                 const uint16_t* src;
-                if (b < at.q)
-                    src = kp + (t0 + t) * p.k_stride[1] + b / 2;
-                else if (b < at.v)
-                    src = qp + (t0 + t) * p.q_stride[1] + (b - at.q) / (2 * kD) * p.q_stride[2] +
-                          (b - at.q) % (2 * kD) / 2;
+                if (c < at.q)
+                    src = kp + (t0 + t) * p.k_stride[1] + c;
+                else if (c < at.v)
+                    src = qp + (t0 + t) * p.q_stride[1] + (c / kD - 1) * p.q_stride[2] + c % kD;
                 else
-                    src = vp + (t0 + t) * p.v_stride[1] + block_row + (b - at.v) / 2;
-                *reinterpret_cast<uint4*>(smem + t * at.total + b) =
-                    *reinterpret_cast<const uint4*>(src);
+                    src = vp + (t0 + t) * p.v_stride[1] + block_row + c - at.v;
+                const uint4 b = *reinterpret_cast<const uint4*>(src);
+                const float2 x0 = Half2<T>::unpack(b.x), x1 = Half2<T>::unpack(b.y),
+                             x2 = Half2<T>::unpack(b.z), x3 = Half2<T>::unpack(b.w);
+                float4* to = reinterpret_cast<float4*>(smem + t * at.total + c);
+                to[0] = make_float4(x0.x, x0.y, x1.x, x1.y);
+                to[1] = make_float4(x2.x, x2.y, x3.x, x3.y);
             }
             for (int x = threadIdx.x; x < 2 * here; x += kWarps * 32)
-                gates[x] = x & 1 ? bp[(t0 + x / 2) * p.beta_stride[1]]
-                                 : ap[(t0 + x / 2) * p.alpha_stride[1]];
+                smem[x / 2 * at.total + at.gates + (x & 1)] =
+                    x & 1 ? bp[(t0 + x / 2) * p.beta_stride[1]]
+                          : ap[(t0 + x / 2) * p.alpha_stride[1]];
             __syncthreads();
             // k . q of each token and query, a group of eight lanes each
             for (int x = 0; x < here * p.queries; x += kWarps * 4) {
                 const int y = x + (threadIdx.x >> 3), z = min(y, here * p.queries - 1);
                 const int t = z / p.queries, g = z - t * p.queries;
-                const uint16_t* tok = reinterpret_cast<const uint16_t*>(smem + t * at.total);
-                float k[16], q[16];
-                load_row<T>(k, tok, l);
-                load_row<T>(q, tok + kD * (1 + g), l);
+                float* tok = smem + t * at.total;
+                uint64_t k[8], q[8];
+                load_row(k, tok, l);
+                load_row(q, tok + at.q + kD * g, l);
                 const float kq = sum8(dot16(k, q));
-                if (y == z && l == 0) kqs[z] = kq;
+                if (y == z && l == 0) tok[at.kq + g] = kq;
             }
             __syncthreads();
         }
         for (int t = 0; t < here; ++t) {
-            const uint16_t* tok = reinterpret_cast<const uint16_t*>(smem + t * at.total);
-            float k[16], alpha, beta, v;
+            const float* tok = smem + t * at.total;
+            uint64_t k[8];
+            float alpha, beta, v;
             if constexpr (kMany) {
-                load_row<T>(k, tok, l);
-                alpha = gates[2 * t], beta = gates[2 * t + 1];
-                v = to_float<T>(tok[at.v / 2 + row - block_row]);
+                load_row(k, tok, l);
+                alpha = tok[at.gates], beta = tok[at.gates + 1];
+                v = tok[at.v + row - block_row];
             } else {
                 load_row<T>(k, kp, l);
                 alpha = ap[0], beta = bp[0];
                 v = to_float<T>(vp[row]);
             }
-            float d[kRows], u[kRows];
+            float d[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], k);
             const float mine = beta * (v - alpha * sum_rows(d, l));
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) u[r] = __shfl_sync(0xffffffffu, mine, (lane & 24) + r);
             for (int g = 0; g < p.queries; ++g) {
-                float q[16], kq;
+                uint64_t q[8];
+                float kq;
                 if constexpr (kMany) {
-                    load_row<T>(q, tok + kD * (1 + g), l);
-                    kq = kqs[t * p.queries + g];
+                    load_row(q, tok + at.q + kD * g, l);
+                    kq = tok[at.kq + g];
                 } else {
                     load_row<T>(q, qp + g * p.q_stride[2], l);
                     kq = sum8(dot16(k, q));
@@ -229,18 +271,21 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
                     p.o[out0 + l + (static_cast<int64_t>(t0 + t) * p.h_o + g) * kD] =
                         from_float<T>(o);
             }
+            const uint64_t decay = pair(alpha, alpha);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
+            for (int r = 0; r < kRows; ++r) {
+                const float ur = __shfl_sync(0xffffffffu, mine, (lane & 24) + r);
+                const uint64_t u = pair(ur, ur);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) s[r][c] = fmaf(u[r], k[c], alpha * s[r][c]);
+                for (int c = 0; c < 8; ++c) s[r][c] = fma2(u, k[c], mul2(decay, s[r][c]));
+            }
         }
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            state[r * (kD / 4) + 8 * c] =
-                make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
+            state[r * (kD / 4) + 8 * c] = make_ulonglong2(s[r][2 * c], s[r][2 * c + 1]);
 }
 
 template <typename T, int kWarps>
@@ -250,7 +295,7 @@ cudaError_t run(const StepParams& p, int64_t items, cudaStream_t stream)
     const dim3 grid(static_cast<uint32_t>(items * (kD / kBlockRows))), block(kWarps * 32);
     if (p.tokens == 1)
         return launch(gdn_step_kernel<T, kWarps, false>, grid, block, 0, stream, p);
-    const size_t smem = kStage * (Staged(p.queries, kBlockRows).total + 4 * (2 + p.queries));
+    const size_t smem = sizeof(float) * kStage * Staged(p.queries, kBlockRows).total;
     return launch(gdn_step_kernel<T, kWarps, true>, grid, block, smem, stream, p);
 }
 

@@ -51,7 +51,7 @@ struct AttnParams {
     float* part_o;     // [2 * blocks][kHeads][D]
     int64_t q_stride[2], k_stride[3], v_stride[3];
     int64_t table_stride, max_len;
-    int32_t n, h_q, h_kv, group, head_items, pages, page_size, window;
+    int32_t n, h_q, h_kv, group, head_items, pages, page_size, page_shift, window;
     float scale_log2;
 };
 
@@ -107,9 +107,12 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// A sequence's tokens [start, len); len = 0 for a length the page table cannot hold.
+// A sequence's tokens [start, len); len = 0 for a length the page table cannot hold.  Its slices
+// begin at `origin`, the start rounded down to a whole slice, so that with pages of whole slices
+// a slice lies in one page.
 struct Span {
     int start, len;
+    __device__ __forceinline__ int origin() const { return start & ~(kSlice - 1); }
 };
 __device__ __forceinline__ Span span_of(const AttnParams& p, int i)
 {
@@ -144,7 +147,7 @@ struct Cursor {
 template <int kTileTokens>
 __device__ __forceinline__ int tiles_of(const Span& s)
 {
-    return (s.len - s.start + kTileTokens - 1) / kTileTokens;
+    return (s.len - s.origin() + kTileTokens - 1) / kTileTokens;
 }
 
 template <int kTileTokens>
@@ -171,10 +174,15 @@ struct Cfg {
     static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
     static constexpr int kMergeBytes = kWarps * kHeads * kMergeRow * 4;
     static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
-    static constexpr int kRoom = 232448 - kMergeBytes - kSmallBytes;
+    // the queries stay in registers, but for the one shape whose sums leave no room for them
+    static constexpr bool kQueriesShared = D == 256 && kHeadTiles == 2;
+    static constexpr int kQueryRow = D + 8;                   // elements
+    static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 : 0;
+    static constexpr int kRoom = 232448 - kMergeBytes - kSmallBytes - kQueryBytes;
     static constexpr int kMaxStages = kRoom / (kWarps * kStageBytes);
     static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
-    static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
+                                 kQueryBytes;
     static_assert(kStages >= 2, "no room for two stages");
 };
 
@@ -192,6 +200,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
     float* sm_m = merge + C::kMergeBytes / 4;      // [kWarps][kHeads]
     float* sm_l = sm_m + kWarps * kHeads;
     int* sm_i = reinterpret_cast<int*>(sm_l + kWarps * kHeads);   // 64 words
+    uint16_t* sm_q = reinterpret_cast<uint16_t*>(sm_i + 64);      // [kHeads][kQueryRow]
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int blocks = gridDim.x, c = blockIdx.x;
@@ -257,42 +266,69 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
     Cursor pre = cur;                              // where the loads are
     int pre_t = t0;
 
-    // ---- loads of a slice: the rows' places one slice ahead, then the copies
+    // ---- loads of a slice.  Its place in the cache is looked up one slice ahead: that of its first
+    // row where pages are whole slices, else that of row `lane & 15`.
     const uint32_t ring0 = smem_addr(ring) + w * C::kStages * C::kStageBytes;
-    int page = -1, off = 0;                        // lanes 0 .. 15: the place of row `lane`
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    const bool whole_pages = p.page_size % kSlice == 0;
+    int page = 0, off = 0;
+    bool there = false;                            // the place is one of the sequence's
     auto look_up = [&]() {
-        page = -1;
-        if (pre_t < t1) {
-            const int pos = pre.span.start + pre.tile * kTile + w * kSlice + (lane & 15);
-            if (pos < pre.span.len) {
-                const int x = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
-                off = pos - x * p.page_size;
-                page = p.table[pre.i * p.table_stride + x];
-                if (page < 0 || page >= p.pages) {
-                    atomicOr(p.status, DECODE_BAD_PAGE);
-                    page = -1;
-                }
-            }
-        }
+        there = false;
+        if (pre_t >= t1) return;
+        const int pos = pre.span.origin() + pre.tile * kTile + w * kSlice +
+                        (whole_pages ? 0 : lane & 15);
+        if (pos >= pre.span.len || (!whole_pages && pos < pre.span.start)) return;
+        there = true;
+        const int x = p.page_shift >= 0
+                          ? pos >> p.page_shift
+                          : static_cast<int>(static_cast<uint32_t>(pos) /
+                                             static_cast<uint32_t>(p.page_size));
+        off = pos - x * p.page_size;
+        page = p.table[pre.i * p.table_stride + x];
     };
     auto load = [&](int stage) {
         if (pre_t < t1) {
+            if (there && (page < 0 || page >= p.pages)) {
+                atomicOr(p.status, DECODE_BAD_PAGE);
+                there = false;
+            }
             const int kv = pre.item / p.head_items;
-            const uint16_t* kb = p.k + kv * p.k_stride[2];
-            const uint16_t* vb = p.v + kv * p.v_stride[2];
-            const uint32_t dst0 = ring0 + stage * C::kStageBytes;
-            const int ch = lane % kChunks;
+            const uint16_t* kb = p.k + kv * p.k_stride[2] + ch * 8;
+            const uint16_t* vb = p.v + kv * p.v_stride[2] + ch * 8;
+            int64_t ko = !there ? 0 : page * p.k_stride[0] + off * p.k_stride[1];
+            int64_t vo = !there ? 0 : page * p.v_stride[0] + off * p.v_stride[1];
+            const uint32_t dst0 = ring0 + stage * C::kStageBytes + sub * (D * 2);
+            const int pos0 = pre.span.origin() + pre.tile * kTile + w * kSlice;
+            // rows [lo, hi) of the slice are read
+            const int lo = pre.span.start - pos0;
+            const int hi = whole_pages && !there ? 0 : pre.span.len - pos0;
+            if (whole_pages) {
+                kb += ko + sub * p.k_stride[1];
+                vb += vo + sub * p.v_stride[1];
+                const int64_t ks = kRowsPerCopy * p.k_stride[1], vs = kRowsPerCopy * p.v_stride[1];
 #pragma unroll
-            for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
-                const int row = x * kRowsPerCopy + lane / kChunks;
-                const int64_t pg = __shfl_sync(0xffffffffu, page, row);
-                const int64_t of = __shfl_sync(0xffffffffu, off, row);
-                const uint32_t bytes = pg >= 0 ? 16u : 0u;
-                const int64_t ko = pg >= 0 ? pg * p.k_stride[0] + of * p.k_stride[1] + ch * 8 : 0;
-                const int64_t vo = pg >= 0 ? pg * p.v_stride[0] + of * p.v_stride[1] + ch * 8 : 0;
-                const uint32_t dst = dst0 + row * (D * 2) + ((ch ^ (row & 7)) << 4);
-                cp_async16(dst, kb + ko, bytes);
-                cp_async16(dst + kSlice * D * 2, vb + vo, bytes);
+                for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
+                    const int row = x * kRowsPerCopy + sub;
+                    const uint32_t bytes = row >= lo && row < hi ? 16u : 0u;
+                    const uint32_t dst = dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
+                    cp_async16(dst, bytes ? kb : p.k, bytes);
+                    cp_async16(dst + kSlice * D * 2, bytes ? vb : p.v, bytes);
+                    kb += ks;
+                    vb += vs;
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
+                    const int row = x * kRowsPerCopy + sub;
+                    const int64_t k1 = __shfl_sync(0xffffffffu, ko, row);
+                    const int64_t v1 = __shfl_sync(0xffffffffu, vo, row);
+                    const bool have = __shfl_sync(0xffffffffu, there, row);
+                    const uint32_t bytes = have && row >= lo && row < hi ? 16u : 0u;
+                    const uint32_t dst = dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
+                    cp_async16(dst, kb + k1, bytes);
+                    cp_async16(dst + kSlice * D * 2, vb + v1, bytes);
+                }
             }
             ++pre_t;
             advance<kTile>(pre, p);
@@ -306,7 +342,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
 
     // ---- the tiles
     const int hq = (lane & 3) * 2;                 // the lane's two heads (of each head tile)
-    uint32_t qf[kHeadTiles][D / 16][2];
+    uint32_t qf[kHeadTiles][C::kQueriesShared ? 1 : D / 16][2];
     float acc[kHeadTiles][D / 16][4];
     float m[kHeadTiles][2], l[kHeadTiles][2];
     bool fresh = true;
@@ -316,6 +352,18 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
         const int heads = min(kHeads, (kv + 1) * p.group - h0);
         if (fresh) {
             fresh = false;
+            if constexpr (C::kQueriesShared) {
+                // (every warp has passed the barrier that ends the item before)
+                for (int x = tid; x < kHeads * kChunks; x += C::kThreads) {
+                    const int h = x / kChunks, d = x % kChunks * 8;
+                    uint4 b = make_uint4(0u, 0u, 0u, 0u);
+                    if (h < heads)
+                        b = *reinterpret_cast<const uint4*>(p.q + cur.i * p.q_stride[0] +
+                                                            (h0 + h) * p.q_stride[1] + d);
+                    *reinterpret_cast<uint4*>(sm_q + h * C::kQueryRow + d) = b;
+                }
+                __syncthreads();
+            }
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
                 const int h = x * 8 + (lane >> 2);
@@ -323,8 +371,11 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
                                       (lane & 3) * 2;
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
-                    qf[x][d][0] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16) : 0u;
-                    qf[x][d][1] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16 + 8) : 0u;
+                    if constexpr (!C::kQueriesShared) {
+                        qf[x][d][0] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16) : 0u;
+                        qf[x][d][1] =
+                            h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16 + 8) : 0u;
+                    }
                     acc[x][d][0] = acc[x][d][1] = acc[x][d][2] = acc[x][d][3] = 0.f;
                 }
                 m[x][0] = m[x][1] = -INFINITY;
@@ -336,22 +387,36 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
         cp_wait<C::kStages - 1>();
         __syncwarp();
 
-        const int pos0 = cur.span.start + cur.tile * kTile + w * kSlice;
+        const int pos0 = cur.span.origin() + cur.tile * kTile + w * kSlice;
         if (pos0 < cur.span.len) {
             const uint32_t ks = ring0 + stage * C::kStageBytes, vs = ks + kSlice * D * 2;
             float s[kHeadTiles][4];
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
             const int r = lane & 7, sel = lane >> 3;
+            [[maybe_unused]] uint32_t qs[kHeadTiles][4];
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 uint32_t a[4];
                 ldsm4(a, ks + ((sel & 1) * 8 + r) * (D * 2) + (((2 * d + (sel >> 1)) ^ r) << 4));
+                if constexpr (C::kQueriesShared) {
+                    if (d % 2 == 0) {
 #pragma unroll
-                for (int x = 0; x < kHeadTiles; ++x) mma<T>(s[x], a, qf[x][d][0], qf[x][d][1]);
+                        for (int x = 0; x < kHeadTiles; ++x)
+                            ldsm4(qs[x], smem_addr(sm_q) + (x * 8 + r) * (C::kQueryRow * 2) +
+                                             (2 * d + sel) * 16);
+                    }
+#pragma unroll
+                    for (int x = 0; x < kHeadTiles; ++x)
+                        mma<T>(s[x], a, qs[x][d % 2 * 2], qs[x][d % 2 * 2 + 1]);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kHeadTiles; ++x) mma<T>(s[x], a, qf[x][d][0], qf[x][d][1]);
+                }
             }
-            const bool in_lo = pos0 + (lane >> 2) < cur.span.len;
-            const bool in_hi = pos0 + (lane >> 2) + 8 < cur.span.len;
+            const int lo_pos = pos0 + (lane >> 2), hi_pos = lo_pos + 8;
+            const bool in_lo = lo_pos >= cur.span.start && lo_pos < cur.span.len;
+            const bool in_hi = hi_pos >= cur.span.start && hi_pos < cur.span.len;
             uint32_t pb[kHeadTiles][2][2];         // [piece][tokens 0 .. 7, 8 .. 15]
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
@@ -690,9 +755,13 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     p.head_items = static_cast<int32_t>((group + heads - 1) / heads);
     p.pages = static_cast<int32_t>(a->pages);
     p.page_size = static_cast<int32_t>(a->page_size);
+    p.page_shift = -1;                // no power of two
+    for (int x = 0; x < 31; ++x)
+        if (p.page_size == 1 << x) p.page_shift = x;
     p.window = a->window > kMost ? 0 : static_cast<int32_t>(a->window);
     p.scale_log2 = a->scale * 1.4426950408889634f;
-    const int64_t most = p.window > 0 && p.window < max_len ? p.window : max_len;
+    // tokens of a sequence's slices, the rounding of its window's start included
+    const int64_t most = p.window > 0 && p.window < max_len - kSlice ? p.window + kSlice : max_len;
     return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, a->head_dim, most, sms, stream)
                                    : dispatch<__half>(p, a->head_dim, most, sms, stream);
 }
