@@ -9,11 +9,15 @@
 // unnormalised output, and results of warps and blocks are joined by their maxima.
 //
 // Work split.  An item is one (sequence, key head, up to 8 kHeadTiles of its query heads).  A tile is
-// 16 tokens per warp of an item.  All items' tiles, in order, are dealt to the blocks in equal
-// contiguous ranges, whatever the lengths: every block finds its range itself from a scan of the
-// lengths.  So a block has at most one item that began in an earlier block and one that goes on in
-// a later one; those two go to the workspace as (maximum, sum, output) and a second kernel joins
-// each item's parts in block order, the rest are written at once.  The order of every sum is fixed.
+// 16 tokens per warp of an item.  All items' tiles, in order, are cut into equal contiguous ranges,
+// one a block, whatever the lengths: every block finds its range itself from a scan of the lengths.
+// So a block has at most one item that began in an earlier block and one that goes on in a later
+// one; those two go to the workspace as (maximum, sum, output) and a second kernel joins each
+// item's parts in block order, the rest are written at once.  The order of every sum is fixed.
+// Two blocks of four warps an SM, so that one streams while the other begins or joins an item: 64
+// sequences of up to 8192 tokens, 8 key heads of 128, take 161 us, against 175 us with one block of
+// eight warps, whose SMs were busy 78% of the time on average; ranges four times finer than the
+// GPU holds blocks, which even the SMs out, take 167 us, their blocks' beginnings cost more.
 //
 // Inside a block each warp streams its own 16-token slices through a ring of shared-memory stages
 // (16-byte cp.async, rows looked up in the page table one slice ahead, so pages may have any size
@@ -35,7 +39,10 @@ namespace {
 
 using namespace decode;
 
-constexpr int kSlice = 16;   // tokens of a warp's slice
+constexpr int kSlice = 16;       // tokens of a warp's slice
+constexpr int kResident = 2;     // blocks of an SM
+constexpr int kSharedItems = 64;     // items up to which the join takes a block a head
+constexpr int kListedItems = 1024;   // items up to which the join goes by item
 
 struct AttnParams {
     const uint16_t* q;
@@ -46,12 +53,13 @@ struct AttnParams {
     uint16_t* o;
     float* lse;
     uint32_t* status;
-    int4* desc;        // [blocks]: the item that goes on in later blocks
+    int4* split;       // by item or by its first block: (first block, -1 if in one block; last; i, item)
     float2* part_ml;   // [2 * blocks][kHeads]
     float* part_o;     // [2 * blocks][kHeads][D]
     int64_t q_stride[2], k_stride[3], v_stride[3];
     int64_t table_stride, max_len;
     int32_t n, h_q, h_kv, group, head_items, pages, page_size, page_shift, window;
+    int32_t by_item;
     float scale_log2;
 };
 
@@ -166,7 +174,7 @@ __device__ __forceinline__ void advance(Cursor& c, const AttnParams& p)
 
 template <int D, int kHeadTiles>
 struct Cfg {
-    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kWarps = D == 256 ? 2 : 4;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHeads = 8 * kHeadTiles;
     static constexpr int kTile = kWarps * kSlice;
@@ -178,7 +186,8 @@ struct Cfg {
     static constexpr bool kQueriesShared = D == 256 && kHeadTiles == 2;
     static constexpr int kQueryRow = D + 8;                   // elements
     static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 : 0;
-    static constexpr int kRoom = 232448 - kMergeBytes - kSmallBytes - kQueryBytes;
+    // (two blocks share an SM's 228 KB, of which the system takes 1 KB a block)
+    static constexpr int kRoom = 115712 - kMergeBytes - kSmallBytes - kQueryBytes;
     static constexpr int kMaxStages = kRoom / (kWarps * kStageBytes);
     static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
@@ -187,7 +196,7 @@ struct Cfg {
 };
 
 template <typename T, int D, int kHeadTiles>
-__global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
     paged_attention_kernel(const AttnParams p)
 {
     using C = Cfg<D, kHeadTiles>;
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
     uint16_t* sm_q = reinterpret_cast<uint16_t*>(sm_i + 64);      // [kHeads][kQueryRow]
 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const int blocks = gridDim.x, c = blockIdx.x;
+    const int c = blockIdx.x;
     const int items_per_seq = p.h_kv * p.head_items;
 
     dep_launch();
@@ -228,7 +237,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
         if (x == w) upto += total;
         total += sm_i[x];
     }
-    const int t0 = first_tile(c, total, blocks), t1 = first_tile(c + 1, total, blocks);
+    const int blocks = min(static_cast<int>(gridDim.x), total);   // with a tile each at least
+    const int t0 = c < blocks ? first_tile(c, total, blocks) : total;
+    const int t1 = c < blocks ? first_tile(c + 1, total, blocks) : total;
     if (t0 >= upto - mine && t0 < upto) {          // one thread: its sequences hold tile t0
         int at = upto - mine;
         for (int i = i_lo; i < i_hi; ++i) {
@@ -242,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
         }
     }
     // sequences without tokens have no tile: their results are written here
-    for (int i = c; i < p.n; i += blocks) {
+    for (int i = c; i < p.n; i += gridDim.x) {
         const int raw = p.lens[i];
         const Span s = span_of(p, i);
         if (tid == 0 && raw != s.len) atomicOr(p.status, DECODE_BAD_LENGTH);
@@ -252,8 +263,11 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
         if (p.lse != nullptr)
             for (int x = tid; x < p.h_q; x += C::kThreads)
                 p.lse[static_cast<int64_t>(i) * p.h_q + x] = -INFINITY;
+        if (p.by_item)
+            for (int x = tid; x < items_per_seq; x += C::kThreads)
+                p.split[i * items_per_seq + x] = make_int4(-1, 0, 0, 0);
     }
-    if (tid == 0) p.desc[c] = make_int4(-1, 0, 0, 0);
+    if (tid == 0 && !p.by_item) p.split[c] = make_int4(-1, 0, 0, 0);
     if (t0 >= t1) return;
     __syncthreads();
 
@@ -537,8 +551,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
                     if (d == 0) p.part_ml[row] = make_float2(top, sum);
                 }
             }
-            if (tid == 0 && begin >= t0 && end > t1)
-                p.desc[c] = make_int4(cur.i, cur.item, block_of(end - 1, total, blocks), heads);
+            if (tid == 0 && begin >= t0 && (p.by_item || !whole))
+                p.split[p.by_item ? cur.i * items_per_seq + cur.item : c] = make_int4(
+                    whole ? -1 : c, whole ? 0 : block_of(end - 1, total, blocks), cur.i, cur.item);
             __syncthreads();
             fresh = true;
         }
@@ -546,88 +561,139 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, 1)
     }
 }
 
-// Joins the parts of the item that began in main block blockIdx.x and went on in later ones; one
-// block of the grid's y dimension per query head.  Part 0 is that block's slot 2 c + 1, the
-// others' parts are their slots 2 c'.
-constexpr int kJoinThreads = 256;
+// Joins the parts of an item that went over several blocks' ranges: part 0 is its first block's slot
+// 2 c + 1, the others are their blocks' slots 2 c'.  Block x has the item listed at x.  With one
+// block an item each warp joins heads of its own; with a block (x, y) for each head, which is for
+// few items of many parts, the block's warps share the head's parts out.  It is a chain of three
+// dependent loads (the list, maxima and sums, outputs), so each is issued for all parts at once.
+constexpr int kJoinWarps = 8;
+
+// A warp's running join: its lanes hold D / 32 neighbouring outputs each.
+template <int D>
+struct Joined {
+    static constexpr int kOut = D / 32;
+    float top = -INFINITY, sum = 0.f, o[kOut] = {};
+
+    // Takes in up to 32 parts; lane x has part x's maximum and sum (-infinity, 0: none), `row` is
+    // the address of its output.
+    __device__ __forceinline__ void take(float m, float l, const float* row, int count, int lane)
+    {
+        float next = fmaxf(m, top);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, d));
+        const float ref = next == -INFINITY ? 0.f : next;
+        const float old = exp2_fast(top - ref), f = exp2_fast(m - ref);
+        top = next;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < kOut; ++e) o[e] *= old;
+        constexpr int kBatch = 8;
+        for (int x0 = 0; x0 < count; x0 += kBatch) {
+            float b[kBatch][kOut];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                // lanes past the count name part 0 again, with weight 0
+                const int at = x0 + x < count ? x0 + x : 0;
+                const float* from = reinterpret_cast<const float*>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<uint64_t>(row), at)) + lane * kOut;
+                if constexpr (kOut == 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(from);
+                    b[x][0] = v.x, b[x][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kOut; e += 4) {
+                        const float4 v = *reinterpret_cast<const float4*>(from + e);
+                        b[x][e] = v.x, b[x][e + 1] = v.y, b[x][e + 2] = v.z, b[x][e + 3] = v.w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const float w = x0 + x < count ? __shfl_sync(0xffffffffu, f, (x0 + x) & 31) : 0.f;
+                const float lx = x0 + x < count ? __shfl_sync(0xffffffffu, l, (x0 + x) & 31) : 0.f;
+                if (x0 + x < count) {
+                    sum = fmaf(lx, w, sum);
+#pragma unroll
+                    for (int e = 0; e < kOut; ++e) o[e] = fmaf(b[x][e], w, o[e]);
+                }
+            }
+        }
+    }
+};
 
 template <typename T, int D, int kHeadTiles>
-__global__ void __launch_bounds__(kJoinThreads) paged_attention_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(const AttnParams p)
 {
-    constexpr int kHeads = 8 * kHeadTiles, kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-    __shared__ float4 sums[kGroups][kLanes];
-    __shared__ float red[kJoinThreads / 32];
-    __shared__ float part_sum[kGroups];
+    constexpr int kHeads = 8 * kHeadTiles, kOut = Joined<D>::kOut;
+    __shared__ __align__(16) float sm_o[kJoinWarps][D];
+    __shared__ float2 sm_ml[kJoinWarps];
     dep_launch();
     dep_wait();
-    const int c = blockIdx.x, h = blockIdx.y;
-    const int4 item = p.desc[c];
-    if (item.x < 0 || h >= item.w) return;
-    const int parts = item.z - c + 1;
-    const int tid = threadIdx.x;
-    auto slot = [&](int x) { return static_cast<int64_t>(x == 0 ? 2 * c + 1 : 2 * (c + x)) * kHeads + h; };
+    const int4 item = p.split[blockIdx.x];
+    if (item.x < 0) return;
+    const int c = item.x, parts = item.y - c + 1;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h0 = item.w / p.head_items * p.group + item.w % p.head_items * kHeads;
+    const int heads = min(kHeads, p.group - item.w % p.head_items * kHeads);
+    const bool shared = gridDim.y > 1;
+    const int each = shared ? (parts + kJoinWarps - 1) / kJoinWarps : parts;
+    const int first = shared ? min(w * each, parts) : 0, last = min(first + each, parts);
 
-    float top = -INFINITY;
-    for (int x = tid; x < parts; x += kJoinThreads) top = fmaxf(top, p.part_ml[slot(x)].x);
+    for (int h = shared ? blockIdx.y : w; h < heads; h += shared ? gridDim.y : kJoinWarps) {
+        Joined<D> sums;
+        for (int x0 = first; x0 < last; x0 += 32) {
+            const int x = min(x0 + lane, last - 1);
+            const int64_t slot = static_cast<int64_t>(x == 0 ? 2 * c + 1 : 2 * (c + x)) * kHeads + h;
+            const float2 ml = p.part_ml[slot];
+            const bool mine = x0 + lane < last;
+            sums.take(mine ? ml.x : -INFINITY, mine ? ml.y : 0.f, p.part_o + slot * D,
+                      min(32, last - x0), lane);
+        }
+        if (shared) {
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if ((tid & 31) == 0) red[tid >> 5] = top;
-    __syncthreads();
-    top = red[0];
+            for (int e = 0; e < kOut; ++e) sm_o[w][lane * kOut + e] = sums.o[e];
+            if (lane == 0) sm_ml[w] = make_float2(sums.top, sums.sum);
+            __syncthreads();
+            if (w == 0) {
+                Joined<D> all;
+                const float2 ml = sm_ml[min(lane, kJoinWarps - 1)];
+                all.take(lane < kJoinWarps ? ml.x : -INFINITY, lane < kJoinWarps ? ml.y : 0.f,
+                         sm_o[min(lane, kJoinWarps - 1)], kJoinWarps, lane);
+                sums = all;
+            }
+            __syncthreads();
+            if (w != 0) continue;
+        }
+        const int64_t row = static_cast<int64_t>(item.z) * p.h_q + h0 + h;
+        const float inv = 1.f / sums.sum;
+        uint32_t* out = reinterpret_cast<uint32_t*>(p.o + row * D + lane * kOut);
 #pragma unroll
-    for (int x = 1; x < kJoinThreads / 32; ++x) top = fmaxf(top, red[x]);
-    const float ref = top == -INFINITY ? 0.f : top;
-
-    const int g = tid / kLanes, d = tid % kLanes;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int x = g; x < parts; x += kGroups) {
-        const float2 ml = p.part_ml[slot(x)];
-        const float f = exp2_fast(ml.x - ref);
-        const float4 b = *reinterpret_cast<const float4*>(p.part_o + slot(x) * D + d * 4);
-        o.x = fmaf(b.x, f, o.x), o.y = fmaf(b.y, f, o.y);
-        o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
-        sum = fmaf(ml.y, f, sum);
+        for (int e = 0; e < kOut; e += 2)
+            out[e / 2] = Half2<T>::pack(sums.o[e] * inv, sums.o[e + 1] * inv);
+        if (lane == 0 && p.lse != nullptr)
+            p.lse[row] = (sums.top + log2f(sums.sum)) * 0.6931471805599453f;
     }
-    sums[g][d] = o;
-    if (d == 0) part_sum[g] = sum;
-    __syncthreads();
-    if (g != 0) return;
-    sum = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int x = 0; x < kGroups; ++x) {
-        sum += part_sum[x];
-        const float4 b = sums[x][d];
-        o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
-    }
-    const int64_t row = static_cast<int64_t>(item.x) * p.h_q + item.y / p.head_items * p.group +
-                        item.y % p.head_items * kHeads + h;
-    const float inv = 1.f / sum;
-    *reinterpret_cast<uint2*>(p.o + row * D + d * 4) =
-        make_uint2(Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
-    if (d == 0 && p.lse != nullptr) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 struct Layout {
     size_t ml, o, total;
 };
-Layout layout_for(int sms, int kHeads, int64_t d)
+Layout layout_for(int sms, int heads, int64_t d)
 {
+    const size_t blocks = static_cast<size_t>(sms) * kResident;
     Layout l{};
-    size_t at = sizeof(int4) * static_cast<size_t>(sms);
+    size_t at = sizeof(int4) * (blocks > kListedItems ? blocks : kListedItems);
     l.ml = at = (at + 255) & ~size_t(255);
-    at += sizeof(float2) * 2 * static_cast<size_t>(sms) * kHeads;
+    at += sizeof(float2) * 2 * blocks * heads;
     l.o = at = (at + 255) & ~size_t(255);
-    l.total = at + sizeof(float) * 2 * static_cast<size_t>(sms) * kHeads * static_cast<size_t>(d);
+    l.total = at + sizeof(float) * 2 * blocks * heads * static_cast<size_t>(d);
     return l;
 }
 
 int heads_of(int64_t group) { return group > 8 ? 16 : 8; }
 
 template <typename T, int D, int kHeadTiles>
-int run(const AttnParams& p, int64_t most_tokens, int sms, cudaStream_t stream)
+int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
 {
     using C = Cfg<D, kHeadTiles>;
     const int64_t per_item = (most_tokens + C::kTile - 1) / C::kTile;
@@ -635,7 +701,9 @@ int run(const AttnParams& p, int64_t most_tokens, int sms, cudaStream_t stream)
     if (per_item > 0 && items >= (int64_t(1) << 31) / per_item)
         return fail(DECODE_ERR_UNSUPPORTED, "too many tiles of the cache for one call");
     const int64_t tiles = per_item * items;
-    const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < sms ? tiles : sms);
+    const int64_t most = static_cast<int64_t>(sms) * kResident;
+    const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < most ? tiles : most);
+    p.by_item = items <= kListedItems;
     auto* kernel = paged_attention_kernel<T, D, kHeadTiles>;
     static thread_local bool set[kMaxDevices] = {};
     int dev = 0;
@@ -650,8 +718,9 @@ int run(const AttnParams& p, int64_t most_tokens, int sms, cudaStream_t stream)
         return fail(DECODE_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
     if (blocks == 1) return DECODE_OK;
     e = launch(paged_attention_join_kernel<T, D, kHeadTiles>,
-               dim3(blocks, p.group < C::kHeads ? p.group : C::kHeads), dim3(kJoinThreads), 0,
-               stream, p);
+               dim3(p.by_item ? static_cast<uint32_t>(items) : blocks,
+                    items > kSharedItems ? 1 : p.group < C::kHeads ? p.group : C::kHeads),
+               dim3(kJoinWarps * 32), 0, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "paged_attention_join_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;
@@ -743,7 +812,7 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     p.lens = a->lens;
     p.o = static_cast<uint16_t*>(a->o);
     p.lse = a->lse;
-    p.desc = reinterpret_cast<int4*>(ws);
+    p.split = reinterpret_cast<int4*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
     p.part_o = reinterpret_cast<float*>(ws + l.o);
     p.table_stride = a->n > 1 ? a->table_stride : 0;
