@@ -1,4 +1,5 @@
-"""Build step for libgemm_f16.so: one nvcc invocation, sm_103a only, in-tree output."""
+"""Build step for libgemm_f16.so (nvcc, sm_103a only) and the Python module _decode.so that links to
+it (g++); in-tree output."""
 from __future__ import annotations
 
 import os
@@ -15,6 +16,9 @@ HEADERS = [os.path.join(ROOT, "include", h) for h in ("gemm_f16.h", "gdn.h", "de
 SOURCES = ["gemm_f16.cu", "gdn.cu", "decode.cu", "gdn_step.cu", "qk_norm_rope.cu",
            "paged_attention.cu"]
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f16.so")
+# the CPython module of the decode-step operators' torch entry points, linked to the library
+BINDING = "decode_binding.cpp"
+BINDING_PATH = os.path.join(PKG_DIR, "_decode.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -36,15 +40,34 @@ def _nvcc() -> str:
 
 def _sources():
     srcs = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-            if f.endswith((".cu", ".cuh", ".h"))]
+            if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     return srcs + HEADERS
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return any(os.path.getmtime(s) > t for s in _sources())
+
+
+def _binding_commands(obj: str, out: str):
+    """g++ commands that compile and link the binding against this Python and this torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(root, "include"), os.path.join(root, "include/torch/csrc/api/include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                *(x for i in include for x in ("-isystem", i)),
+                "-c", "-o", obj, os.path.join(CSRC, BINDING)]
+    link = ["g++", "-shared", "-o", out, obj, "-L" + os.path.join(root, "lib"), "-ltorch_python",
+            "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+            "-L" + PKG_DIR, "-l:libgemm_f16.so", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -62,12 +85,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
                                       text=True))
         objs.append(obj)
+    binding_obj = os.path.join(PKG_DIR, f".decode_binding.{tag}.o")
+    binding_tmp = BINDING_PATH + "." + tag
+    binding_compile, binding_link = _binding_commands(binding_obj, binding_tmp)
+    procs.append(subprocess.Popen(binding_compile, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
+                                  text=True))
     errors, logs = [], []
     for p in procs:
         out, err = p.communicate()
         logs.append(out + err)
         if p.returncode != 0:
-            errors.append(f"nvcc failed ({p.returncode}):\n{out}\n{err}")
+            errors.append(f"{p.args[0]} failed ({p.returncode}):\n{out}\n{err}")
     try:
         if errors:
             raise RuntimeError("\n".join(errors))
@@ -76,13 +104,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
                              text=True)
         if res.returncode != 0:
             raise RuntimeError(f"nvcc link failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB_PATH)
+        res = subprocess.run(binding_link, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ link failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        os.replace(binding_tmp, BINDING_PATH)
     finally:
-        for obj in objs:
+        for obj in (*objs, binding_obj):
             if os.path.exists(obj):
                 os.unlink(obj)
     if verbose:
         print("".join(logs))
-    os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
 

@@ -39,7 +39,7 @@ namespace {
 
 using namespace decode;
 
-constexpr int kSlice = 16;       // tokens of a warp's slice
+constexpr int kSub = 16;         // tokens of a matrix tile
 constexpr int kResident = 2;     // blocks of an SM
 constexpr int kSharedItems = 64;     // items up to which the join takes a block a head
 constexpr int kListedItems = 1024;   // items up to which the join goes by item
@@ -116,11 +116,11 @@ __device__ __forceinline__ float exp2_fast(float x)
 }
 
 // A sequence's tokens [start, len); len = 0 for a length the page table cannot hold.  Its slices
-// begin at `origin`, the start rounded down to a whole slice, so that with pages of whole slices
-// a slice lies in one page.
+// begin at `origin`, the start rounded down to a multiple of 16, so that where pages are multiples
+// of 16 tokens, each 16 tokens of a slice lie in one page.
 struct Span {
     int start, len;
-    __device__ __forceinline__ int origin() const { return start & ~(kSlice - 1); }
+    __device__ __forceinline__ int origin() const { return start & ~(kSub - 1); }
 };
 __device__ __forceinline__ Span span_of(const AttnParams& p, int i)
 {
@@ -177,6 +177,10 @@ struct Cfg {
     static constexpr int kWarps = D == 256 ? 2 : 4;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHeads = 8 * kHeadTiles;
+    // a slice is 8 KB at least: for short rows the look-up, the maxima and the loop cost as much as
+    // the products
+    static constexpr int kSubs = D == 64 ? 2 : 1;
+    static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
     static constexpr int kStageBytes = 2 * kSlice * D * 2;    // keys, then values
     static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
@@ -201,6 +205,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
 {
     using C = Cfg<D, kHeadTiles>;
     constexpr int kHeads = C::kHeads, kWarps = C::kWarps, kTile = C::kTile;
+    constexpr int kSlice = C::kSlice, kSubs = C::kSubs;
     constexpr int kChunks = D / 8;                 // 16-byte pieces of a row
     constexpr int kRowsPerCopy = 32 / kChunks;     // rows that one cp.async of the warp covers
     extern __shared__ __align__(128) uint8_t smem[];
@@ -280,68 +285,78 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
     Cursor pre = cur;                              // where the loads are
     int pre_t = t0;
 
-    // ---- loads of a slice.  Its place in the cache is looked up one slice ahead: that of its first
-    // row where pages are whole slices, else that of row `lane & 15`.
+    // ---- loads of a slice.  The places in the cache of its 16-token pieces are looked up one slice
+    // ahead: that of the first row where pages are multiples of 16 tokens, else that of row
+    // `lane & 15`.
     const uint32_t ring0 = smem_addr(ring) + w * C::kStages * C::kStageBytes;
     const int ch = lane % kChunks, sub = lane / kChunks;
-    const bool whole_pages = p.page_size % kSlice == 0;
-    int page = 0, off = 0;
-    bool there = false;                            // the place is one of the sequence's
+    const bool whole_pages = p.page_size % kSub == 0;
+    const int ahead = whole_pages ? 0 : lane & 15;
+    int page[kSubs], off[kSubs];
+    bool there[kSubs];                             // the place is one of the sequence's
     auto look_up = [&]() {
-        there = false;
-        if (pre_t >= t1) return;
-        const int pos = pre.span.origin() + pre.tile * kTile + w * kSlice +
-                        (whole_pages ? 0 : lane & 15);
-        if (pos >= pre.span.len || (!whole_pages && pos < pre.span.start)) return;
-        there = true;
-        const int x = p.page_shift >= 0
-                          ? pos >> p.page_shift
-                          : static_cast<int>(static_cast<uint32_t>(pos) /
-                                             static_cast<uint32_t>(p.page_size));
-        off = pos - x * p.page_size;
-        page = p.table[pre.i * p.table_stride + x];
+#pragma unroll
+        for (int y = 0; y < kSubs; ++y) {
+            there[y] = false;
+            if (pre_t >= t1) continue;
+            const int pos = pre.span.origin() + pre.tile * kTile + w * kSlice + y * kSub + ahead;
+            if (pos >= pre.span.len || (!whole_pages && pos < pre.span.start)) continue;
+            there[y] = true;
+            const int x = p.page_shift >= 0
+                              ? pos >> p.page_shift
+                              : static_cast<int>(static_cast<uint32_t>(pos) /
+                                                 static_cast<uint32_t>(p.page_size));
+            off[y] = pos - x * p.page_size;
+            page[y] = p.table[pre.i * p.table_stride + x];
+        }
     };
     auto load = [&](int stage) {
         if (pre_t < t1) {
-            if (there && (page < 0 || page >= p.pages)) {
-                atomicOr(p.status, DECODE_BAD_PAGE);
-                there = false;
-            }
             const int kv = pre.item / p.head_items;
-            const uint16_t* kb = p.k + kv * p.k_stride[2] + ch * 8;
-            const uint16_t* vb = p.v + kv * p.v_stride[2] + ch * 8;
-            int64_t ko = !there ? 0 : page * p.k_stride[0] + off * p.k_stride[1];
-            int64_t vo = !there ? 0 : page * p.v_stride[0] + off * p.v_stride[1];
-            const uint32_t dst0 = ring0 + stage * C::kStageBytes + sub * (D * 2);
-            const int pos0 = pre.span.origin() + pre.tile * kTile + w * kSlice;
-            // rows [lo, hi) of the slice are read
-            const int lo = pre.span.start - pos0;
-            const int hi = whole_pages && !there ? 0 : pre.span.len - pos0;
-            if (whole_pages) {
-                kb += ko + sub * p.k_stride[1];
-                vb += vo + sub * p.v_stride[1];
-                const int64_t ks = kRowsPerCopy * p.k_stride[1], vs = kRowsPerCopy * p.v_stride[1];
+            const uint16_t* k0 = p.k + kv * p.k_stride[2] + ch * 8;
+            const uint16_t* v0 = p.v + kv * p.v_stride[2] + ch * 8;
 #pragma unroll
-                for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
-                    const int row = x * kRowsPerCopy + sub;
-                    const uint32_t bytes = row >= lo && row < hi ? 16u : 0u;
-                    const uint32_t dst = dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
-                    cp_async16(dst, bytes ? kb : p.k, bytes);
-                    cp_async16(dst + kSlice * D * 2, bytes ? vb : p.v, bytes);
-                    kb += ks;
-                    vb += vs;
+            for (int y = 0; y < kSubs; ++y) {
+                if (there[y] && (page[y] < 0 || page[y] >= p.pages)) {
+                    atomicOr(p.status, DECODE_BAD_PAGE);
+                    there[y] = false;
                 }
-            } else {
+                const int64_t ko = !there[y] ? 0 : page[y] * p.k_stride[0] + off[y] * p.k_stride[1];
+                const int64_t vo = !there[y] ? 0 : page[y] * p.v_stride[0] + off[y] * p.v_stride[1];
+                const uint32_t dst0 =
+                    ring0 + stage * C::kStageBytes + (y * kSub + sub) * (D * 2);
+                const int pos0 = pre.span.origin() + pre.tile * kTile + w * kSlice + y * kSub;
+                // rows [lo, hi) of the 16 are read
+                const int lo = pre.span.start - pos0;
+                const int hi = whole_pages && !there[y] ? 0 : pre.span.len - pos0;
+                if (whole_pages) {
+                    const uint16_t* kb = k0 + ko + sub * p.k_stride[1];
+                    const uint16_t* vb = v0 + vo + sub * p.v_stride[1];
+                    const int64_t ks = kRowsPerCopy * p.k_stride[1], vs = kRowsPerCopy * p.v_stride[1];
 #pragma unroll
-                for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
-                    const int row = x * kRowsPerCopy + sub;
-                    const int64_t k1 = __shfl_sync(0xffffffffu, ko, row);
-                    const int64_t v1 = __shfl_sync(0xffffffffu, vo, row);
-                    const bool have = __shfl_sync(0xffffffffu, there, row);
-                    const uint32_t bytes = have && row >= lo && row < hi ? 16u : 0u;
-                    const uint32_t dst = dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
-                    cp_async16(dst, kb + k1, bytes);
-                    cp_async16(dst + kSlice * D * 2, vb + v1, bytes);
+                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
+                        const int row = x * kRowsPerCopy + sub;
+                        const uint32_t bytes = row >= lo && row < hi ? 16u : 0u;
+                        const uint32_t dst =
+                            dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
+                        cp_async16(dst, bytes ? kb : p.k, bytes);
+                        cp_async16(dst + kSlice * D * 2, bytes ? vb : p.v, bytes);
+                        kb += ks;
+                        vb += vs;
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
+                        const int row = x * kRowsPerCopy + sub;
+                        const int64_t k1 = __shfl_sync(0xffffffffu, ko, row);
+                        const int64_t v1 = __shfl_sync(0xffffffffu, vo, row);
+                        const bool have = __shfl_sync(0xffffffffu, there[y], row);
+                        const uint32_t bytes = have && row >= lo && row < hi ? 16u : 0u;
+                        const uint32_t dst =
+                            dst0 + x * kRowsPerCopy * (D * 2) + ((ch ^ (row & 7)) << 4);
+                        cp_async16(dst, k0 + k1, bytes);
+                        cp_async16(dst + kSlice * D * 2, v0 + v1, bytes);
+                    }
                 }
             }
             ++pre_t;
@@ -404,15 +419,16 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
         const int pos0 = cur.span.origin() + cur.tile * kTile + w * kSlice;
         if (pos0 < cur.span.len) {
             const uint32_t ks = ring0 + stage * C::kStageBytes, vs = ks + kSlice * D * 2;
-            float s[kHeadTiles][4];
+            float s[kHeadTiles][kSubs][4];
 #pragma unroll
-            for (int x = 0; x < kHeadTiles; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int y = 0; y < kSubs; ++y)
+                    s[x][y][0] = s[x][y][1] = s[x][y][2] = s[x][y][3] = 0.f;
             const int r = lane & 7, sel = lane >> 3;
             [[maybe_unused]] uint32_t qs[kHeadTiles][4];
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
-                uint32_t a[4];
-                ldsm4(a, ks + ((sel & 1) * 8 + r) * (D * 2) + (((2 * d + (sel >> 1)) ^ r) << 4));
                 if constexpr (C::kQueriesShared) {
                     if (d % 2 == 0) {
 #pragma unroll
@@ -420,28 +436,41 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
                             ldsm4(qs[x], smem_addr(sm_q) + (x * 8 + r) * (C::kQueryRow * 2) +
                                              (2 * d + sel) * 16);
                     }
+                }
 #pragma unroll
-                    for (int x = 0; x < kHeadTiles; ++x)
-                        mma<T>(s[x], a, qs[x][d % 2 * 2], qs[x][d % 2 * 2 + 1]);
-                } else {
+                for (int y = 0; y < kSubs; ++y) {
+                    uint32_t a[4];
+                    ldsm4(a, ks + (y * kSub + (sel & 1) * 8 + r) * (D * 2) +
+                                 (((2 * d + (sel >> 1)) ^ r) << 4));
 #pragma unroll
-                    for (int x = 0; x < kHeadTiles; ++x) mma<T>(s[x], a, qf[x][d][0], qf[x][d][1]);
+                    for (int x = 0; x < kHeadTiles; ++x) {
+                        if constexpr (C::kQueriesShared)
+                            mma<T>(s[x][y], a, qs[x][d % 2 * 2], qs[x][d % 2 * 2 + 1]);
+                        else
+                            mma<T>(s[x][y], a, qf[x][d][0], qf[x][d][1]);
+                    }
                 }
             }
-            const int lo_pos = pos0 + (lane >> 2), hi_pos = lo_pos + 8;
-            const bool in_lo = lo_pos >= cur.span.start && lo_pos < cur.span.len;
-            const bool in_hi = hi_pos >= cur.span.start && hi_pos < cur.span.len;
-            uint32_t pb[kHeadTiles][2][2];         // [piece][tokens 0 .. 7, 8 .. 15]
+            // the lane's tokens are pos0 + 8 j + lane / 4
+            bool in[2 * kSubs];
+#pragma unroll
+            for (int j = 0; j < 2 * kSubs; ++j) {
+                const int pos = pos0 + j * 8 + (lane >> 2);
+                in[j] = pos >= cur.span.start && pos < cur.span.len;
+            }
+            uint32_t pb[kHeadTiles][kSubs][2][2];  // [piece][tokens 0 .. 7, 8 .. 15]
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
                 float corr[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float& lo = s[x][e];
-                    float& hi = s[x][2 + e];
-                    lo = in_lo ? lo * p.scale_log2 : -INFINITY;
-                    hi = in_hi ? hi * p.scale_log2 : -INFINITY;
-                    float top = fmaxf(lo, hi);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 2 * kSubs; ++j) {
+                        float& v = s[x][j / 2][j % 2 * 2 + e];
+                        v = in[j] ? v * p.scale_log2 : -INFINITY;
+                        top = fmaxf(top, v);
+                    }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -450,9 +479,14 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
                     const float ref = top == -INFINITY ? 0.f : top;
                     corr[e] = exp2_fast(m[x][e] - ref);
                     m[x][e] = top;
-                    lo = exp2_fast(lo - ref);
-                    hi = exp2_fast(hi - ref);
-                    l[x][e] = fmaf(l[x][e], corr[e], lo + hi);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2 * kSubs; ++j) {
+                        float& v = s[x][j / 2][j % 2 * 2 + e];
+                        v = exp2_fast(v - ref);
+                        sum += v;
+                    }
+                    l[x][e] = fmaf(l[x][e], corr[e], sum);
                 }
                 if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
@@ -464,24 +498,28 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
                     }
                 }
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t first = Half2<T>::pack(s[x][2 * y], s[x][2 * y + 1]);
+                for (int j = 0; j < 2 * kSubs; ++j) {
+                    const float* v = s[x][j / 2] + j % 2 * 2;
+                    const uint32_t first = Half2<T>::pack(v[0], v[1]);
                     const float2 f = Half2<T>::unpack(first);
-                    pb[x][0][y] = transpose8x8(first);
-                    pb[x][1][y] = transpose8x8(
-                        Half2<T>::pack(s[x][2 * y] - f.x, s[x][2 * y + 1] - f.y));
+                    pb[x][j / 2][0][j % 2] = transpose8x8(first);
+                    pb[x][j / 2][1][j % 2] =
+                        transpose8x8(Half2<T>::pack(v[0] - f.x, v[1] - f.y));
                 }
             }
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                uint32_t a[4];
-                ldsm4_trans(a, vs + ((sel >> 1) * 8 + r) * (D * 2) + (((2 * d + (sel & 1)) ^ r) << 4));
+            for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-                for (int x = 0; x < kHeadTiles; ++x) {
-                    mma<T>(acc[x][d], a, pb[x][0][0], pb[x][0][1]);
-                    mma<T>(acc[x][d], a, pb[x][1][0], pb[x][1][1]);
+                for (int y = 0; y < kSubs; ++y) {
+                    uint32_t a[4];
+                    ldsm4_trans(a, vs + (y * kSub + (sel >> 1) * 8 + r) * (D * 2) +
+                                       (((2 * d + (sel & 1)) ^ r) << 4));
+#pragma unroll
+                    for (int x = 0; x < kHeadTiles; ++x) {
+                        mma<T>(acc[x][d], a, pb[x][y][0][0], pb[x][y][0][1]);
+                        mma<T>(acc[x][d], a, pb[x][y][1][0], pb[x][y][1][1]);
+                    }
                 }
-            }
         }
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
 
@@ -830,7 +868,7 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     p.window = a->window > kMost ? 0 : static_cast<int32_t>(a->window);
     p.scale_log2 = a->scale * 1.4426950408889634f;
     // tokens of a sequence's slices, the rounding of its window's start included
-    const int64_t most = p.window > 0 && p.window < max_len - kSlice ? p.window + kSlice : max_len;
+    const int64_t most = p.window > 0 && p.window < max_len - kSub ? p.window + kSub : max_len;
     return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, a->head_dim, most, sms, stream)
                                    : dispatch<__half>(p, a->head_dim, most, sms, stream);
 }

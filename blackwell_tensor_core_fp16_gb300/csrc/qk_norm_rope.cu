@@ -15,8 +15,12 @@
 // Norm and rotation are one linear map of a row up to its norm: with f the row's factor,
 //     y_e = f (x_e (w_e cos) + x_partner (+-w_partner sin)),
 // and the two factors in brackets are the same for all of a token's query (or key) heads.  So a
-// warp's unit of work is one token and a run of its heads of one kind: it forms the factors once
-// and spends two packed fp32 operations per pair of elements on each head.
+// warp's unit of work is one token and a run of its heads: it forms the factors once and spends
+// three packed fp32 operations per pair of elements on each head.
+//
+// A unit is a chain of dependent loads (position, then its row of the table; slot), so the warps
+// stay for the whole call and load ahead: a unit's rows and angles go to shared memory by cp.async
+// while the unit before it is in work, and the indices they need are read one unit earlier still.
 #include <cstdint>
 
 #include "decode_common.cuh"
@@ -25,8 +29,12 @@ namespace {
 
 using namespace decode;
 
-constexpr int kUnroll = 4;            // rows a lane has in flight
+constexpr int kSteps = 8;             // most groups of 32 / kLanes heads of a unit
+constexpr int kStages = 2;
 constexpr int kBlockWarps = 4;
+constexpr int kResident = 5;          // blocks of an SM
+constexpr int kStageBytes = kSteps * 512 + 1024 + 16;   // rows, angles, (valid, slot)
+constexpr int kSmem = kBlockWarps * kStages * kStageBytes;
 enum Pairing { kNone, kSplit, kInterleaved };
 
 struct NormParams {
@@ -46,8 +54,8 @@ struct NormParams {
     int64_t q_stride[2], k_stride[2], v_stride[2], q_out_stride[2], k_out_stride[2];
     int64_t k_cache_stride[3], v_cache_stride[3];
     int64_t position_stride, table_rows, cache_slots;
-    uint32_t tokens, units;                 // units of a token: q_units, k_units, and as many of v
-    int32_t q_units, k_units, steps;        // groups of heads of a unit
+    uint32_t tokens, units;                 // units of a token
+    int32_t q_steps, k_steps, all_steps, steps;   // groups of heads: of q, of k, of a token, of a unit
     int32_t h_q, h_k, head_dim, rot, axes, page_size, norm;
     int32_t section_end[DECODE_MAX_AXES];   // first pair of the next axis
     float eps;
@@ -89,155 +97,216 @@ __device__ __forceinline__ uint32_t word(const uint4& b, int c)
     return c == 0 ? b.x : c == 1 ? b.y : c == 2 ? b.z : b.w;
 }
 
-// One unit: token t, `steps` groups of 32 / kLanes heads of its queries (kind 0), keys (1) or
-// values (2), from the given group on.
-template <typename T, int kLanes, Pairing kPairing>
-__global__ void __launch_bounds__(kBlockWarps * 32, 6) qk_norm_rope_kernel(const NormParams p)
+__device__ __forceinline__ uint32_t smem_addr(const void* p)
 {
-    constexpr int kHeads = 32 / kLanes;              // heads of a warp at a time
-    const int lane = threadIdx.x & 31, l = lane % kLanes;
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A token's groups of heads in order: its queries' (kind 0), its keys' (1), its values' (2).
+template <typename T, int kLanes, Pairing kPairing>
+__global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kernel(const NormParams p)
+{
+    constexpr int kHeads = 32 / kLanes;              // heads of a group
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
+    uint8_t* const ring = smem + warp * kStages * kStageBytes;
     const int e = 8 * l;                             // the lane's first element
     const bool in_head = e < p.head_dim, in_rot = e < p.rot;
     const int half = p.rot / 2;
-    const uint32_t unit = blockIdx.x * kBlockWarps + (threadIdx.x >> 5);
-    const uint32_t t = unit / p.units, part = unit - t * p.units;
+    const int64_t all = static_cast<int64_t>(p.tokens) * p.units;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockWarps;
+    const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
+    const int partner = kPairing != kSplit || !in_rot ? lane
+                        : lane + (e < half ? half / 8 : -(half / 8));
 
     dep_launch();
     dep_wait();
-    if (t >= p.tokens) return;
-    const int kind = part < p.q_units ? 0 : part < p.q_units + p.k_units ? 1 : 2;
-    const int heads = kind == 0 ? p.h_q : p.h_k;
-    const int step0 = (part - (kind == 0 ? 0 : kind == 1 ? p.q_units : p.q_units + p.k_units)) * p.steps;
-    int h = step0 * kHeads + lane / kLanes;          // the lane's head
-    const int end = min(heads, (step0 + p.steps) * kHeads);
 
-    // What the indices say is loaded first, the rows next, and the angles, which wait for the
-    // positions, after them.
-    int32_t pos[DECODE_MAX_AXES];
-    if constexpr (kPairing != kNone) {
-#pragma unroll
-        for (int x = 0; x < DECODE_MAX_AXES; ++x)
-            pos[x] = x < p.axes ? p.positions[x * p.position_stride + t] : 0;
-    }
-    int32_t slot = p.k_cache != nullptr && kind > 0 ? p.slots[t] : 0;
+    uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
+    if (in_head && p.q_weight) wq = *reinterpret_cast<const uint4*>(p.q_weight + e);
+    if (in_head && p.k_weight) wk = *reinterpret_cast<const uint4*>(p.k_weight + e);
 
-    const int64_t* from = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
-    const uint16_t* src = (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * from[0] + h * from[1] + e;
-    const int64_t src_step = kHeads * from[1];
-    uint4 in[kUnroll];
-    auto fetch = [&]() {
+    // The unit whose loads come next, its token's indices, and its own first group.
+    int64_t ahead = static_cast<int64_t>(blockIdx.x) * kBlockWarps + warp;
+    uint32_t token = 0;
+    int part = 0;
+    int32_t pos[DECODE_MAX_AXES], slot = -1;
+    auto look = [&]() {
+        if (ahead >= all) return;
+        token = static_cast<uint32_t>(ahead) / p.units;
+        part = static_cast<int>(static_cast<uint32_t>(ahead) - token * p.units);
+        if constexpr (kPairing != kNone) {
 #pragma unroll
-        for (int x = 0; x < kUnroll; ++x) {
-            in[x] = make_uint4(0u, 0u, 0u, 0u);
-            if (in_head && h + x * kHeads < end) in[x] = *reinterpret_cast<const uint4*>(src);
-            src += src_step;
+            for (int x = 0; x < DECODE_MAX_AXES; ++x)
+                pos[x] = x < p.axes ? p.positions[x * p.position_stride + token] : 0;
         }
+        if (p.k_cache != nullptr) slot = p.slots[token];
     };
-    fetch();
-
-    const uint16_t* w = kind == 0 ? p.q_weight : p.k_weight;
-    uint4 wb = make_uint4(0u, 0u, 0u, 0u);
-    if (w != nullptr && in_head) wb = *reinterpret_cast<const uint4*>(w + e);
-
-    // The factors of the lane's elements and of their partners.
-    bool ok = true;
-    uint64_t mine[4], other[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        mine[c] = w != nullptr ? value2<T>(word(wb, c)) : pair_of(1.f, 1.f);
-    const int partner = kPairing != kSplit || !in_rot ? lane
-                        : lane + (e < half ? half / 8 : -(half / 8));
-    if constexpr (kPairing != kNone) {
-        if constexpr (kPairing == kSplit) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) other[c] = __shfl_sync(0xffffffffu, mine[c], partner);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 f = halves(mine[c]);
-                other[c] = pair_of(f.y, f.x);
+    auto load = [&](int stage) {
+        if (ahead < all) {
+            uint8_t* const to = ring + stage * kStageBytes;
+            const uint32_t rows = smem_addr(to) + lane * 16, angles = smem_addr(to) + kSteps * 512;
+            const int g0 = part * p.steps, g1 = min(g0 + p.steps, p.all_steps);
+            for (int g = g0; g < g1; ++g) {
+                const int kind = g < p.q_steps ? 0 : g < p.q_steps + p.k_steps ? 1 : 2;
+                const int h = (kind == 0   ? g
+                               : kind == 1 ? g - p.q_steps
+                                           : g - p.q_steps - p.k_steps) * kHeads + lane / kLanes;
+                const uint16_t* from = kind == 0   ? p.q + token * p.q_stride[0] + h * p.q_stride[1]
+                                       : kind == 1 ? p.k + token * p.k_stride[0] + h * p.k_stride[1]
+                                                   : p.v + token * p.v_stride[0] + h * p.v_stride[1];
+                if (in_head && h < (kind == 0 ? p.h_q : p.h_k))
+                    cp_async16(rows + (g - g0) * 512, from + e);
             }
+            bool ok = true;
+            if constexpr (kPairing != kNone) {
+#pragma unroll
+                for (int x = 0; x < DECODE_MAX_AXES; ++x)
+                    ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
+                if (!ok && lane == 0) atomicOr(p.status, DECODE_BAD_POSITION);
+                // a lane of the first head fetches the table's floats e .. e + 7: cosines or
+                // sines of the pairs pair0 .. pair0 + 7
+                if (ok && in_rot && lane < kLanes) {
+                    const int pair0 = e < half ? e : e - half;
+                    auto axis_of = [&](int pair) {
+                        int axis = 0;
+#pragma unroll
+                        for (int x = 1; x < DECODE_MAX_AXES; ++x)
+                            axis += x < p.axes && pair >= p.section_end[x - 1];
+                        return axis;
+                    };
+                    auto table_row = [&](int axis) {
+                        int32_t at = pos[0];
+#pragma unroll
+                        for (int x = 1; x < DECODE_MAX_AXES; ++x) at = axis == x ? pos[x] : at;
+                        return p.table + static_cast<int64_t>(at) * p.rot;
+                    };
+                    const int axis = axis_of(pair0);
+                    if (axis == axis_of(pair0 + 7)) {
+                        const float* row = table_row(axis) + e;
+                        cp_async16(angles + e * 4, row);
+                        cp_async16(angles + e * 4 + 16, row + 4);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            cp_async4(angles + (e + c) * 4, table_row(axis_of(pair0 + c)) + e + c);
+                    }
+                }
+            }
+            if (slot < -1 || slot >= p.cache_slots) {
+                if (lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+                slot = -1;
+            }
+            if (lane == 0)
+                *reinterpret_cast<int4*>(to + kSteps * 512 + 1024) =
+                    make_int4(ok, ok ? slot : -1, static_cast<int>(token), part);
+            ahead += stride;
         }
+        cp_commit();
+        look();
+    };
+    look();
 #pragma unroll
-        for (int x = 0; x < DECODE_MAX_AXES; ++x)
-            ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
-        if (ok && in_rot) {
-            constexpr int kPairs = kPairing == kInterleaved ? 4 : 8;   // pairs that the lane meets
-            const int pair0 = kPairing == kInterleaved ? e / 2 : (e < half ? e : e - half);
-            auto axis_of = [&](int pair) {
-                int axis = 0;
-#pragma unroll
-                for (int x = 1; x < DECODE_MAX_AXES; ++x)
-                    axis += x < p.axes && pair >= p.section_end[x - 1];
-                return axis;
-            };
-            auto table_row = [&](int axis) {
-                int32_t at = pos[0];
-#pragma unroll
-                for (int x = 1; x < DECODE_MAX_AXES; ++x) at = axis == x ? pos[x] : at;
-                return p.table + static_cast<int64_t>(at) * p.rot;
-            };
-            float cs[kPairs], sn[kPairs];
-            const int axis = axis_of(pair0);
-            if (axis == axis_of(pair0 + kPairs - 1)) {
-                // one row of the table: its pairs lie side by side
-                const float* row = table_row(axis) + pair0;
-#pragma unroll
-                for (int c = 0; c < kPairs; c += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(row + c);
-                    const float4 y = *reinterpret_cast<const float4*>(row + half + c);
-                    cs[c] = x.x, cs[c + 1] = x.y, cs[c + 2] = x.z, cs[c + 3] = x.w;
-                    sn[c] = y.x, sn[c + 1] = y.y, sn[c + 2] = y.z, sn[c + 3] = y.w;
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < kPairs; ++c) {
-                    const float* row = table_row(axis_of(pair0 + c)) + pair0 + c;
-                    cs[c] = row[0], sn[c] = row[half];
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if constexpr (kPairing == kInterleaved) {
-                    mine[c] = mul2(mine[c], pair_of(cs[c], cs[c]));
-                    other[c] = mul2(other[c], pair_of(-sn[c], sn[c]));
+    for (int s = 0; s < kStages - 1; ++s) load(s);
+
+    int stage = 0;
+    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kBlockWarps + warp; unit < all;
+         unit += stride) {
+        __syncwarp();
+        load(stage + kStages - 1 < kStages ? stage + kStages - 1 : stage - 1);
+        cp_wait<kStages - 1>();
+        __syncwarp();
+        const uint8_t* const from = ring + stage * kStageBytes;
+        const uint4* const rows = reinterpret_cast<const uint4*>(from);
+        const float* const angles = reinterpret_cast<const float*>(from + kSteps * 512);
+        const int4 head = *reinterpret_cast<const int4*>(from + kSteps * 512 + 1024);
+        const bool ok = head.x;
+        const int32_t place = head.y;
+        const uint32_t t = static_cast<uint32_t>(head.z);
+        const int32_t pg = place < 0 ? 0 : static_cast<uint32_t>(place) / static_cast<uint32_t>(p.page_size);
+        const int32_t off = place < 0 ? 0 : place - pg * p.page_size;
+        const int g0 = head.w * p.steps, g1 = min(g0 + p.steps, p.all_steps);
+
+        int have = -1;                               // the kind the factors are for
+        uint64_t mine[4], other[4];
+        uint16_t* dst = nullptr;
+        int64_t dst_step = 0;
+        int heads = 0, h = 0;
+        bool write = false;
+        for (int g = g0; g < g1; ++g) {
+            const int kind = g < p.q_steps ? 0 : g < p.q_steps + p.k_steps ? 1 : 2;
+            if (kind != have) {
+                have = kind;
+                heads = kind == 0 ? p.h_q : p.h_k;
+                h = (kind == 0   ? g
+                     : kind == 1 ? g - p.q_steps
+                                 : g - p.q_steps - p.k_steps) * kHeads + lane / kLanes;
+                // where the rows go: to q_out or k_out, or to the token's place in a cache
+                write = true;
+                if (kind == 0) {
+                    dst = p.q_out + t * p.q_out_stride[0] + h * p.q_out_stride[1];
+                    dst_step = p.q_out_stride[1] * kHeads;
+                } else if (p.k_cache == nullptr) {
+                    dst = p.k_out + t * p.k_out_stride[0] + h * p.k_out_stride[1];
+                    dst_step = p.k_out_stride[1] * kHeads;
                 } else {
-                    const float sign = e < half ? -1.f : 1.f;
-                    mine[c] = mul2(mine[c], pair_of(cs[2 * c], cs[2 * c + 1]));
-                    other[c] = mul2(other[c], pair_of(sign * sn[2 * c], sign * sn[2 * c + 1]));
+                    const int64_t* to = kind == 1 ? p.k_cache_stride : p.v_cache_stride;
+                    dst = (kind == 1 ? p.k_cache : p.v_cache) + pg * to[0] + off * to[1] + h * to[2];
+                    dst_step = to[2] * kHeads;
+                    write = place >= 0;
+                }
+                dst += e;
+                const uint4 wb = kind == 0 ? wq : wk;
+                const bool weights = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mine[c] = weights ? value2<T>(word(wb, c)) : pair_of(1.f, 1.f);
+                    if constexpr (kPairing == kSplit) {
+                        const uint32_t x = __shfl_sync(0xffffffffu, word(wb, c), partner);
+                        other[c] = weights ? value2<T>(x) : pair_of(1.f, 1.f);
+                    } else if constexpr (kPairing == kInterleaved) {
+                        const float2 f = halves(mine[c]);
+                        other[c] = pair_of(f.y, f.x);
+                    }
+                }
+                if constexpr (kPairing == kSplit) {
+                    if (in_rot) {
+                        const float* cs = angles + (e < half ? e : e - half);
+                        const float sign = e < half ? -1.f : 1.f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float2 x = *reinterpret_cast<const float2*>(cs + 2 * c);
+                            const float2 y = *reinterpret_cast<const float2*>(cs + half + 2 * c);
+                            mine[c] = mul2(mine[c], pair_of(x.x, x.y));
+                            other[c] = mul2(other[c], pair_of(sign * y.x, sign * y.y));
+                        }
+                    }
+                } else if constexpr (kPairing == kInterleaved) {
+                    if (in_rot) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float x = angles[e / 2 + c], y = angles[half + e / 2 + c];
+                            mine[c] = mul2(mine[c], pair_of(x, x));
+                            other[c] = mul2(other[c], pair_of(-y, y));
+                        }
+                    }
                 }
             }
-        }
-        if (!ok && lane == 0 && part == 0) atomicOr(p.status, DECODE_BAD_POSITION);
-    }
-
-    // Where the rows go: to q_out or k_out, or to the token's place in a cache.
-    uint16_t* dst;
-    int64_t dst_step;
-    if (kind == 0 || p.k_cache == nullptr) {
-        const int64_t* to = kind == 0 ? p.q_out_stride : p.k_out_stride;
-        dst = (kind == 0 ? p.q_out : p.k_out) + t * to[0] + h * to[1] + e;
-        dst_step = kHeads * to[1];
-    } else {
-        if (slot < -1 || slot >= p.cache_slots) {
-            if (lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
-            slot = -1;
-        }
-        if (slot < 0 || !ok) return;
-        const int32_t page = static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size);
-        const int32_t off = slot - page * p.page_size;
-        const int64_t* to = kind == 1 ? p.k_cache_stride : p.v_cache_stride;
-        dst = (kind == 1 ? p.k_cache : p.v_cache) + page * to[0] + off * to[1] + h * to[2] + e;
-        dst_step = kHeads * to[2];
-    }
-    const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
-
-    for (int s = 0; s < p.steps; s += kUnroll) {     // trip counts do not depend on the lane
-        if (s > 0) fetch();
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (s + u >= p.steps) break;
-            uint4 b = in[u];
+            uint4 b = rows[(g - g0) * 32 + lane];
             if (kind < 2) {
                 uint64_t x[4];
 #pragma unroll
@@ -248,33 +317,34 @@ __global__ void __launch_bounds__(kBlockWarps * 32, 6) qk_norm_rope_kernel(const
 #pragma unroll
                     for (int c = 1; c < 4; ++c) s2 = fma2(x[c], x[c], s2);
                     const float2 s1 = halves(s2);
-                    float sum = s1.x + s1.y;
+                    float sum = in_head ? s1.x + s1.y : 0.f;
 #pragma unroll
                     for (int m = 1; m < kLanes; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
                     f = rsqrtf(fmaf(sum, inv_d, p.eps));
                 }
                 const uint64_t ff = pair_of(f, f);
+                uint4 z;
+                if constexpr (kPairing == kSplit) z = rows[(g - g0) * 32 + partner];
                 uint32_t out[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint64_t y = mul2(x[c], mine[c]);
                     if constexpr (kPairing == kSplit) {
-                        const uint64_t z =
-                            value2<T>(__shfl_sync(0xffffffffu, word(b, c), partner));
-                        if (in_rot) y = fma2(z, other[c], y);
+                        if (in_rot) y = fma2(value2<T>(word(z, c)), other[c], y);
                     } else if constexpr (kPairing == kInterleaved) {
-                        const float2 z = halves(x[c]);
-                        if (in_rot) y = fma2(pair_of(z.y, z.x), other[c], y);
+                        const float2 v = halves(x[c]);
+                        if (in_rot) y = fma2(pair_of(v.y, v.x), other[c], y);
                     }
                     const float2 r = halves(mul2(y, ff));
                     out[c] = Half2<T>::pack(r.x, r.y);
                 }
                 b = ok ? make_uint4(out[0], out[1], out[2], out[3]) : make_uint4(0u, 0u, 0u, 0u);
             }
-            if (in_head && h < end) *reinterpret_cast<uint4*>(dst) = b;
+            if (write && in_head && h < heads) *reinterpret_cast<uint4*>(dst) = b;
             h += kHeads;
             dst += dst_step;
         }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
     }
 }
 
@@ -282,22 +352,21 @@ template <typename T, int kLanes, Pairing kPairing>
 cudaError_t run(NormParams p, int sms, cudaStream_t stream)
 {
     constexpr int kHeads = 32 / kLanes;
-    const int q_steps = (p.h_q + kHeads - 1) / kHeads, k_steps = (p.h_k + kHeads - 1) / kHeads;
+    p.q_steps = (p.h_q + kHeads - 1) / kHeads;
+    p.k_steps = (p.h_k + kHeads - 1) / kHeads;
+    p.all_steps = p.q_steps + p.k_steps * (p.v != nullptr ? 2 : 1);
     // Long units spend the least on their token's factors; shorter ones, when there would be less
-    // than a wave of them, keep the GPU full and a single token's latency low.
-    auto cut = [&](int steps) {
-        p.steps = steps;
-        p.q_units = (q_steps + steps - 1) / steps;
-        p.k_units = (k_steps + steps - 1) / steps;
-        p.units = p.q_units + p.k_units * (p.v != nullptr ? 2 : 1);
-    };
-    for (int steps = 2 * kUnroll; steps > 0; steps /= 2) {
-        cut(steps);
-        if (static_cast<int64_t>(p.tokens) * p.units >= static_cast<int64_t>(sms) * 24) break;
+    // than a unit for every warp of the GPU, keep a single token's latency low.
+    const int64_t warps = static_cast<int64_t>(sms) * kResident * kBlockWarps;
+    for (p.steps = kSteps;; p.steps /= 2) {
+        p.units = (p.all_steps + p.steps - 1) / p.steps;
+        if (p.steps == 1 || static_cast<int64_t>(p.tokens) * p.units >= warps) break;
     }
     const int64_t blocks = (static_cast<int64_t>(p.tokens) * p.units + kBlockWarps - 1) / kBlockWarps;
-    return launch(qk_norm_rope_kernel<T, kLanes, kPairing>, dim3(static_cast<uint32_t>(blocks)),
-                  dim3(kBlockWarps * 32), 0, stream, p);
+    const int64_t most = static_cast<int64_t>(sms) * kResident;
+    return launch(qk_norm_rope_kernel<T, kLanes, kPairing>,
+                  dim3(static_cast<uint32_t>(blocks < most ? blocks : most)), dim3(kBlockWarps * 32),
+                  kSmem, stream, p);
 }
 
 template <typename T, int kLanes>
