@@ -15,12 +15,14 @@
 // Norm and rotation are one linear map of a row up to its norm: with f the row's factor,
 //     y_e = f (x_e (w_e cos) + x_partner (+-w_partner sin)),
 // and the two factors in brackets are the same for all of a token's query (or key) heads.  So a
-// warp's unit of work is one token and a run of its heads: it forms the factors once and spends
-// three packed fp32 operations per pair of elements on each head.
+// warp takes a token's heads one after the other: it forms the factors once for its queries and
+// once for its keys, and spends three packed fp32 operations per pair of elements on each head.
+// (With the factors formed anew for every eight groups of heads the kernel issued twice the
+// instructions, and they bounded it.)
 //
-// A unit is a chain of dependent loads (position, then its row of the table; slot), so the warps
-// stay for the whole call and load ahead: a unit's rows and angles go to shared memory by cp.async
-// while the unit before it is in work, and the indices they need are read one unit earlier still.
+// A token is a chain of dependent loads (position, then its row of the table), so the warps stay
+// for the whole call and load ahead: rows and angles go to shared memory by cp.async, three chunks
+// of four head groups ahead of the work, and a token's indices are read one token earlier.
 #include <cstdint>
 
 #include "decode_common.cuh"
@@ -29,12 +31,13 @@ namespace {
 
 using namespace decode;
 
-constexpr int kSteps = 8;             // most groups of 32 / kLanes heads of a unit
-constexpr int kStages = 2;
-constexpr int kBlockWarps = 4;
-constexpr int kResident = 5;          // blocks of an SM
-constexpr int kStageBytes = kSteps * 512 + 1024 + 16;   // rows, angles, (valid, slot)
-constexpr int kSmem = kBlockWarps * kStages * kStageBytes;
+constexpr int kSteps = 4;             // groups of 32 / kLanes heads of a chunk
+constexpr int kStages = 4;
+constexpr int kBlockWarps = 2;
+constexpr int kResident = 8;          // blocks of an SM
+constexpr int kRowBytes = kSteps * 512;
+constexpr int kAngleBytes = 1024 + 16;   // a token's angles and (valid, slot)
+constexpr int kWarpBytes = kStages * (kRowBytes + kAngleBytes);
 enum Pairing { kNone, kSplit, kInterleaved };
 
 struct NormParams {
@@ -54,8 +57,8 @@ struct NormParams {
     int64_t q_stride[2], k_stride[2], v_stride[2], q_out_stride[2], k_out_stride[2];
     int64_t k_cache_stride[3], v_cache_stride[3];
     int64_t position_stride, table_rows, cache_slots;
-    uint32_t tokens, units;                 // units of a token
-    int32_t q_steps, k_steps, all_steps, steps;   // groups of heads: of q, of k, of a token, of a unit
+    uint32_t tokens, parts;                 // parts: warps that share a token's chunks out
+    int32_t q_chunks, k_chunks, all_chunks; // of q, of k, of a token (q, k and v)
     int32_t h_q, h_k, head_dim, rot, axes, page_size, norm;
     int32_t section_end[DECODE_MAX_AXES];   // first pair of the next axis
     float eps;
@@ -116,39 +119,35 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A token's groups of heads in order: its queries' (kind 0), its keys' (1), its values' (2).
+// A token's chunks in order: its queries' (kind 0), its keys' (1), its values' (2).
 template <typename T, int kLanes, Pairing kPairing>
 __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kernel(const NormParams p)
 {
     constexpr int kHeads = 32 / kLanes;              // heads of a group
     extern __shared__ __align__(16) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-    uint8_t* const ring = smem + warp * kStages * kStageBytes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes;
+    uint8_t* const ring = smem + (threadIdx.x >> 5) * kWarpBytes;      // [kStages][kRowBytes]
+    uint8_t* const tokens = ring + kStages * kRowBytes;                // [kStages][kAngleBytes]
     const int e = 8 * l;                             // the lane's first element
     const bool in_head = e < p.head_dim, in_rot = e < p.rot;
     const int half = p.rot / 2;
-    const int64_t all = static_cast<int64_t>(p.tokens) * p.units;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockWarps;
-    const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
     const int partner = kPairing != kSplit || !in_rot ? lane
                         : lane + (e < half ? half / 8 : -(half / 8));
+    const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
+
+    // The warp's units: (token, part) number `first`, first + step, ...
+    const uint32_t first = blockIdx.x * kBlockWarps + (threadIdx.x >> 5);
+    const uint32_t step = gridDim.x * kBlockWarps, all = p.tokens * p.parts;
 
     dep_launch();
     dep_wait();
+    if (first >= all) return;
 
-    uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
-    if (in_head && p.q_weight) wq = *reinterpret_cast<const uint4*>(p.q_weight + e);
-    if (in_head && p.k_weight) wk = *reinterpret_cast<const uint4*>(p.k_weight + e);
-
-    // The unit whose loads come next, its token's indices, and its own first group.
-    int64_t ahead = static_cast<int64_t>(blockIdx.x) * kBlockWarps + warp;
-    uint32_t token = 0;
-    int part = 0;
-    int32_t pos[DECODE_MAX_AXES], slot = -1;
+    // ---- loads: `at` is the unit and `chunk` its chunk whose loads come next
+    uint32_t at = first, token = at / p.parts;
+    int chunk = static_cast<int>(at - token * p.parts), slot_ring = 0;
+    int32_t pos[DECODE_MAX_AXES], slot = -1;         // of the token
     auto look = [&]() {
-        if (ahead >= all) return;
-        token = static_cast<uint32_t>(ahead) / p.units;
-        part = static_cast<int>(static_cast<uint32_t>(ahead) - token * p.units);
         if constexpr (kPairing != kNone) {
 #pragma unroll
             for (int x = 0; x < DECODE_MAX_AXES; ++x)
@@ -156,120 +155,116 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
         }
         if (p.k_cache != nullptr) slot = p.slots[token];
     };
+    look();
+    bool begins = true;                              // the chunk is its unit's first
     auto load = [&](int stage) {
-        if (ahead < all) {
-            uint8_t* const to = ring + stage * kStageBytes;
-            const uint32_t rows = smem_addr(to) + lane * 16, angles = smem_addr(to) + kSteps * 512;
-            const int g0 = part * p.steps, g1 = min(g0 + p.steps, p.all_steps);
-            for (int g = g0; g < g1; ++g) {
-                const int kind = g < p.q_steps ? 0 : g < p.q_steps + p.k_steps ? 1 : 2;
-                const int h = (kind == 0   ? g
-                               : kind == 1 ? g - p.q_steps
-                                           : g - p.q_steps - p.k_steps) * kHeads + lane / kLanes;
-                const uint16_t* from = kind == 0   ? p.q + token * p.q_stride[0] + h * p.q_stride[1]
-                                       : kind == 1 ? p.k + token * p.k_stride[0] + h * p.k_stride[1]
-                                                   : p.v + token * p.v_stride[0] + h * p.v_stride[1];
-                if (in_head && h < (kind == 0 ? p.h_q : p.h_k))
-                    cp_async16(rows + (g - g0) * 512, from + e);
+        if (at < all) {
+            const int kind = chunk < p.q_chunks ? 0 : chunk < p.q_chunks + p.k_chunks ? 1 : 2;
+            const int group = (kind == 0   ? chunk
+                               : kind == 1 ? chunk - p.q_chunks
+                                           : chunk - p.q_chunks - p.k_chunks) * kSteps;
+            const int h = group * kHeads + lane / kLanes, heads = kind == 0 ? p.h_q : p.h_k;
+            const int64_t* by = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
+            const uint16_t* from =
+                (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + token * by[0] + h * by[1] + e;
+            const uint32_t rows = smem_addr(ring) + stage * kRowBytes + lane * 16;
+#pragma unroll
+            for (int x = 0; x < kSteps; ++x) {
+                if (in_head && h + x * kHeads < heads) cp_async16(rows + x * 512, from);
+                from += kHeads * by[1];
             }
-            bool ok = true;
-            if constexpr (kPairing != kNone) {
+            if (begins) {
+                uint8_t* const to = tokens + slot_ring * kAngleBytes;
+                bool ok = true;
+                if constexpr (kPairing != kNone) {
 #pragma unroll
-                for (int x = 0; x < DECODE_MAX_AXES; ++x)
-                    ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
-                if (!ok && lane == 0) atomicOr(p.status, DECODE_BAD_POSITION);
-                // a lane of the first head fetches the table's floats e .. e + 7: cosines or
-                // sines of the pairs pair0 .. pair0 + 7
-                if (ok && in_rot && lane < kLanes) {
-                    const int pair0 = e < half ? e : e - half;
-                    auto axis_of = [&](int pair) {
-                        int axis = 0;
+                    for (int x = 0; x < DECODE_MAX_AXES; ++x)
+                        ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
+                    if (!ok && lane == 0) atomicOr(p.status, DECODE_BAD_POSITION);
+                    // a lane of the first head fetches the table's floats e .. e + 7: cosines or
+                    // sines of the pairs pair0 .. pair0 + 7
+                    if (ok && in_rot && lane < kLanes) {
+                        const int pair0 = e < half ? e : e - half;
+                        auto axis_of = [&](int pair) {
+                            int axis = 0;
 #pragma unroll
-                        for (int x = 1; x < DECODE_MAX_AXES; ++x)
-                            axis += x < p.axes && pair >= p.section_end[x - 1];
-                        return axis;
-                    };
-                    auto table_row = [&](int axis) {
-                        int32_t at = pos[0];
+                            for (int x = 1; x < DECODE_MAX_AXES; ++x)
+                                axis += x < p.axes && pair >= p.section_end[x - 1];
+                            return axis;
+                        };
+                        auto table_row = [&](int axis) {
+                            int32_t row = pos[0];
 #pragma unroll
-                        for (int x = 1; x < DECODE_MAX_AXES; ++x) at = axis == x ? pos[x] : at;
-                        return p.table + static_cast<int64_t>(at) * p.rot;
-                    };
-                    const int axis = axis_of(pair0);
-                    if (axis == axis_of(pair0 + 7)) {
-                        const float* row = table_row(axis) + e;
-                        cp_async16(angles + e * 4, row);
-                        cp_async16(angles + e * 4 + 16, row + 4);
-                    } else {
+                            for (int x = 1; x < DECODE_MAX_AXES; ++x) row = axis == x ? pos[x] : row;
+                            return p.table + static_cast<int64_t>(row) * p.rot;
+                        };
+                        const uint32_t angles = smem_addr(to) + e * 4;
+                        const int axis = axis_of(pair0);
+                        if (axis == axis_of(pair0 + 7)) {
+                            const float* row = table_row(axis) + e;
+                            cp_async16(angles, row);
+                            cp_async16(angles + 16, row + 4);
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            cp_async4(angles + (e + c) * 4, table_row(axis_of(pair0 + c)) + e + c);
+                            for (int c = 0; c < 8; ++c)
+                                cp_async4(angles + c * 4, table_row(axis_of(pair0 + c)) + e + c);
+                        }
                     }
                 }
+                if (slot < -1 || slot >= p.cache_slots) {
+                    if (lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+                    slot = -1;
+                }
+                if (lane == 0)
+                    *reinterpret_cast<int2*>(to + 1024) = make_int2(ok, ok ? slot : -1);
+                slot_ring = slot_ring + 1 == kStages ? 0 : slot_ring + 1;
             }
-            if (slot < -1 || slot >= p.cache_slots) {
-                if (lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
-                slot = -1;
+            chunk += p.parts;
+            begins = chunk >= p.all_chunks;
+            if (begins) {
+                at += step;
+                token = at / p.parts;
+                chunk = static_cast<int>(at - token * p.parts);
+                if (at < all) look();
             }
-            if (lane == 0)
-                *reinterpret_cast<int4*>(to + kSteps * 512 + 1024) =
-                    make_int4(ok, ok ? slot : -1, static_cast<int>(token), part);
-            ahead += stride;
         }
         cp_commit();
-        look();
     };
-    look();
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) load(s);
 
-    int stage = 0;
-    for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kBlockWarps + warp; unit < all;
-         unit += stride) {
-        __syncwarp();
-        load(stage + kStages - 1 < kStages ? stage + kStages - 1 : stage - 1);
-        cp_wait<kStages - 1>();
-        __syncwarp();
-        const uint8_t* const from = ring + stage * kStageBytes;
-        const uint4* const rows = reinterpret_cast<const uint4*>(from);
-        const float* const angles = reinterpret_cast<const float*>(from + kSteps * 512);
-        const int4 head = *reinterpret_cast<const int4*>(from + kSteps * 512 + 1024);
-        const bool ok = head.x;
-        const int32_t place = head.y;
-        const uint32_t t = static_cast<uint32_t>(head.z);
-        const int32_t pg = place < 0 ? 0 : static_cast<uint32_t>(place) / static_cast<uint32_t>(p.page_size);
-        const int32_t off = place < 0 ? 0 : place - pg * p.page_size;
-        const int g0 = head.w * p.steps, g1 = min(g0 + p.steps, p.all_steps);
-
+    // ---- the work
+    uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
+    if (in_head && p.q_weight) wq = *reinterpret_cast<const uint4*>(p.q_weight + e);
+    if (in_head && p.k_weight) wk = *reinterpret_cast<const uint4*>(p.k_weight + e);
+    int stage = 0, token_ring = 0;
+    for (uint32_t unit = first; unit < all; unit += step) {
+        const uint32_t t = unit / p.parts;
+        const uint8_t* const head = tokens + token_ring * kAngleBytes;
+        const float* const angles = reinterpret_cast<const float*>(head);
+        bool ok = true;
+        int32_t place = -1, page = 0, off = 0;
         int have = -1;                               // the kind the factors are for
         uint64_t mine[4], other[4];
-        uint16_t* dst = nullptr;
-        int64_t dst_step = 0;
-        int heads = 0, h = 0;
-        bool write = false;
-        for (int g = g0; g < g1; ++g) {
-            const int kind = g < p.q_steps ? 0 : g < p.q_steps + p.k_steps ? 1 : 2;
-            if (kind != have) {
-                have = kind;
-                heads = kind == 0 ? p.h_q : p.h_k;
-                h = (kind == 0   ? g
-                     : kind == 1 ? g - p.q_steps
-                                 : g - p.q_steps - p.k_steps) * kHeads + lane / kLanes;
-                // where the rows go: to q_out or k_out, or to the token's place in a cache
-                write = true;
-                if (kind == 0) {
-                    dst = p.q_out + t * p.q_out_stride[0] + h * p.q_out_stride[1];
-                    dst_step = p.q_out_stride[1] * kHeads;
-                } else if (p.k_cache == nullptr) {
-                    dst = p.k_out + t * p.k_out_stride[0] + h * p.k_out_stride[1];
-                    dst_step = p.k_out_stride[1] * kHeads;
-                } else {
-                    const int64_t* to = kind == 1 ? p.k_cache_stride : p.v_cache_stride;
-                    dst = (kind == 1 ? p.k_cache : p.v_cache) + pg * to[0] + off * to[1] + h * to[2];
-                    dst_step = to[2] * kHeads;
-                    write = place >= 0;
+        for (int c0 = static_cast<int>(unit - t * p.parts); c0 < p.all_chunks; c0 += p.parts) {
+            __syncwarp();
+            load(stage == 0 ? kStages - 1 : stage - 1);
+            cp_wait<kStages - 1>();
+            __syncwarp();
+            if (have < 0) {
+                const int2 x = *reinterpret_cast<const int2*>(head + 1024);
+                ok = x.x;
+                place = x.y;
+                if (place >= 0) {
+                    page = static_cast<uint32_t>(place) / static_cast<uint32_t>(p.page_size);
+                    off = place - page * p.page_size;
                 }
-                dst += e;
+            }
+            const int kind = c0 < p.q_chunks ? 0 : c0 < p.q_chunks + p.k_chunks ? 1 : 2;
+            const int group = (kind == 0   ? c0
+                               : kind == 1 ? c0 - p.q_chunks
+                                           : c0 - p.q_chunks - p.k_chunks) * kSteps;
+            if (kind != have && kind < 2) {
                 const uint4 wb = kind == 0 ? wq : wk;
                 const bool weights = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
 #pragma unroll
@@ -288,85 +283,114 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                         const float* cs = angles + (e < half ? e : e - half);
                         const float sign = e < half ? -1.f : 1.f;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float2 x = *reinterpret_cast<const float2*>(cs + 2 * c);
-                            const float2 y = *reinterpret_cast<const float2*>(cs + half + 2 * c);
+                        for (int c = 0; c < 4; c += 2) {
+                            const float4 x = *reinterpret_cast<const float4*>(cs + 2 * c);
+                            const float4 y = *reinterpret_cast<const float4*>(cs + half + 2 * c);
                             mine[c] = mul2(mine[c], pair_of(x.x, x.y));
+                            mine[c + 1] = mul2(mine[c + 1], pair_of(x.z, x.w));
                             other[c] = mul2(other[c], pair_of(sign * y.x, sign * y.y));
+                            other[c + 1] = mul2(other[c + 1], pair_of(sign * y.z, sign * y.w));
                         }
                     }
                 } else if constexpr (kPairing == kInterleaved) {
                     if (in_rot) {
+                        const float4 x = *reinterpret_cast<const float4*>(angles + e / 2);
+                        const float4 y = *reinterpret_cast<const float4*>(angles + half + e / 2);
+                        mine[0] = mul2(mine[0], pair_of(x.x, x.x));
+                        mine[1] = mul2(mine[1], pair_of(x.y, x.y));
+                        mine[2] = mul2(mine[2], pair_of(x.z, x.z));
+                        mine[3] = mul2(mine[3], pair_of(x.w, x.w));
+                        other[0] = mul2(other[0], pair_of(-y.x, y.x));
+                        other[1] = mul2(other[1], pair_of(-y.y, y.y));
+                        other[2] = mul2(other[2], pair_of(-y.z, y.z));
+                        other[3] = mul2(other[3], pair_of(-y.w, y.w));
+                    }
+                }
+            }
+            have = kind;
+
+            // where the rows go: to q_out or k_out, or to the token's place in a cache
+            const int heads = kind == 0 ? p.h_q : p.h_k;
+            int h = group * kHeads + lane / kLanes;
+            uint16_t* dst;
+            int64_t dst_step;
+            bool write = in_head;
+            if (kind == 0) {
+                dst = p.q_out + t * p.q_out_stride[0] + h * p.q_out_stride[1] + e;
+                dst_step = p.q_out_stride[1] * kHeads;
+            } else if (p.k_cache == nullptr) {
+                dst = p.k_out + t * p.k_out_stride[0] + h * p.k_out_stride[1] + e;
+                dst_step = p.k_out_stride[1] * kHeads;
+            } else {
+                const int64_t* to = kind == 1 ? p.k_cache_stride : p.v_cache_stride;
+                dst = (kind == 1 ? p.k_cache : p.v_cache) + page * to[0] + off * to[1] + h * to[2] + e;
+                dst_step = to[2] * kHeads;
+                write = write && place >= 0;
+            }
+            const uint4* const rows = reinterpret_cast<const uint4*>(ring + stage * kRowBytes);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float x = angles[e / 2 + c], y = angles[half + e / 2 + c];
-                            mine[c] = mul2(mine[c], pair_of(x, x));
-                            other[c] = mul2(other[c], pair_of(-y, y));
+            for (int s = 0; s < kSteps; ++s) {
+                if ((group + s) * kHeads >= heads) break;
+                uint4 b = rows[s * 32 + lane];
+                if (kind < 2) {
+                    uint64_t x[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) x[c] = value2<T>(word(b, c));
+                    float f = 1.f;
+                    if (p.norm != DECODE_NORM_NONE) {
+                        uint64_t s2 = mul2(x[0], x[0]);
+#pragma unroll
+                        for (int c = 1; c < 4; ++c) s2 = fma2(x[c], x[c], s2);
+                        const float2 s1 = halves(s2);
+                        float sum = in_head ? s1.x + s1.y : 0.f;
+#pragma unroll
+                        for (int m = 1; m < kLanes; m *= 2)
+                            sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                        f = rsqrtf(fmaf(sum, inv_d, p.eps));
+                    }
+                    const uint64_t ff = pair_of(f, f);
+                    [[maybe_unused]] uint4 z;
+                    if constexpr (kPairing == kSplit) z = rows[s * 32 + partner];
+                    uint32_t out[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint64_t y = mul2(x[c], mine[c]);
+                        if constexpr (kPairing == kSplit) {
+                            if (in_rot) y = fma2(value2<T>(word(z, c)), other[c], y);
+                        } else if constexpr (kPairing == kInterleaved) {
+                            const float2 v = halves(x[c]);
+                            if (in_rot) y = fma2(pair_of(v.y, v.x), other[c], y);
                         }
+                        const float2 r = halves(mul2(y, ff));
+                        out[c] = Half2<T>::pack(r.x, r.y);
                     }
+                    b = ok ? make_uint4(out[0], out[1], out[2], out[3]) : make_uint4(0u, 0u, 0u, 0u);
                 }
+                if (write && h < heads) *reinterpret_cast<uint4*>(dst) = b;
+                h += kHeads;
+                dst += dst_step;
             }
-            uint4 b = rows[(g - g0) * 32 + lane];
-            if (kind < 2) {
-                uint64_t x[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) x[c] = value2<T>(word(b, c));
-                float f = 1.f;
-                if (p.norm != DECODE_NORM_NONE) {
-                    uint64_t s2 = mul2(x[0], x[0]);
-#pragma unroll
-                    for (int c = 1; c < 4; ++c) s2 = fma2(x[c], x[c], s2);
-                    const float2 s1 = halves(s2);
-                    float sum = in_head ? s1.x + s1.y : 0.f;
-#pragma unroll
-                    for (int m = 1; m < kLanes; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                    f = rsqrtf(fmaf(sum, inv_d, p.eps));
-                }
-                const uint64_t ff = pair_of(f, f);
-                uint4 z;
-                if constexpr (kPairing == kSplit) z = rows[(g - g0) * 32 + partner];
-                uint32_t out[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint64_t y = mul2(x[c], mine[c]);
-                    if constexpr (kPairing == kSplit) {
-                        if (in_rot) y = fma2(value2<T>(word(z, c)), other[c], y);
-                    } else if constexpr (kPairing == kInterleaved) {
-                        const float2 v = halves(x[c]);
-                        if (in_rot) y = fma2(pair_of(v.y, v.x), other[c], y);
-                    }
-                    const float2 r = halves(mul2(y, ff));
-                    out[c] = Half2<T>::pack(r.x, r.y);
-                }
-                b = ok ? make_uint4(out[0], out[1], out[2], out[3]) : make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (write && in_head && h < heads) *reinterpret_cast<uint4*>(dst) = b;
-            h += kHeads;
-            dst += dst_step;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        token_ring = token_ring + 1 == kStages ? 0 : token_ring + 1;
     }
 }
 
 template <typename T, int kLanes, Pairing kPairing>
 cudaError_t run(NormParams p, int sms, cudaStream_t stream)
 {
-    constexpr int kHeads = 32 / kLanes;
-    p.q_steps = (p.h_q + kHeads - 1) / kHeads;
-    p.k_steps = (p.h_k + kHeads - 1) / kHeads;
-    p.all_steps = p.q_steps + p.k_steps * (p.v != nullptr ? 2 : 1);
-    // Long units spend the least on their token's factors; shorter ones, when there would be less
-    // than a unit for every warp of the GPU, keep a single token's latency low.
-    const int64_t warps = static_cast<int64_t>(sms) * kResident * kBlockWarps;
-    for (p.steps = kSteps;; p.steps /= 2) {
-        p.units = (p.all_steps + p.steps - 1) / p.steps;
-        if (p.steps == 1 || static_cast<int64_t>(p.tokens) * p.units >= warps) break;
-    }
-    const int64_t blocks = (static_cast<int64_t>(p.tokens) * p.units + kBlockWarps - 1) / kBlockWarps;
-    const int64_t most = static_cast<int64_t>(sms) * kResident;
+    constexpr int kPass = 32 / kLanes * kSteps;      // heads of a chunk
+    p.q_chunks = (p.h_q + kPass - 1) / kPass;
+    p.k_chunks = (p.h_k + kPass - 1) / kPass;
+    p.all_chunks = p.q_chunks + p.k_chunks * (p.v != nullptr ? 2 : 1);
+    // A warp takes whole tokens; with fewer tokens than the GPU holds warps, parts of them.
+    const int64_t most = static_cast<int64_t>(sms) * kResident, warps = most * kBlockWarps;
+    const int64_t share = warps / p.tokens;
+    p.parts = static_cast<uint32_t>(share < 1 ? 1 : share > p.all_chunks ? p.all_chunks : share);
+    const int64_t blocks = (static_cast<int64_t>(p.tokens) * p.parts + kBlockWarps - 1) / kBlockWarps;
     return launch(qk_norm_rope_kernel<T, kLanes, kPairing>,
                   dim3(static_cast<uint32_t>(blocks < most ? blocks : most)), dim3(kBlockWarps * 32),
-                  kSmem, stream, p);
+                  kBlockWarps * kWarpBytes, stream, p);
 }
 
 template <typename T, int kLanes>
