@@ -7,22 +7,22 @@
 // a copy bound by HBM, or by its launch when there are few tokens.
 //
 // Layout.  A lane holds 8 neighbouring elements (one 16-byte access), kLanes = 8, 16 or 32 lanes
-// a head (head_dim up to 64, 128, 256), so a head's sum is a few shuffles and a warp takes 32 /
-// kLanes heads at a time.  In the split pairing element e's partner lies rot / 2 elements, that is
-// rot / 16 lanes, away and comes by shuffle, still as 16-bit pairs; in the interleaved pairing it
-// is the lane's own neighbour.
+// a head (head_dim up to 64, 128, 256), so a head's sum is a few shuffles.  In the split pairing
+// element e's partner lies rot / 2 elements, that is rot / 16 lanes, away; in the interleaved
+// pairing it is the lane's own neighbour.
 //
 // Norm and rotation are one linear map of a row up to its norm: with f the row's factor,
 //     y_e = f (x_e (w_e cos) + x_partner (+-w_partner sin)),
-// and the two factors in brackets are the same for all of a token's query (or key) heads.  So a
-// warp takes a token's heads one after the other: it forms the factors once for its queries and
-// once for its keys, and spends three packed fp32 operations per pair of elements on each head.
-// (With the factors formed anew for every eight groups of heads the kernel issued twice the
-// instructions, and they bounded it.)
+// and the two factors in brackets are the same for all of a token's query (or key) heads.  So each
+// group of kLanes lanes has a token of its own and takes its heads one after the other: it forms
+// the factors once for the queries and once for the keys, and spends three packed fp32 operations
+// per pair of elements on each head.  (With the factors formed anew for every eight heads the
+// kernel issued twice the instructions, which bounded it; with a warp's groups on one token the
+// keys' few heads left lanes idle.)
 //
 // A token is a chain of dependent loads (position, then its row of the table), so the warps stay
 // for the whole call and load ahead: rows and angles go to shared memory by cp.async, three chunks
-// of four head groups ahead of the work, and a token's indices are read one token earlier.
+// of four heads ahead of the work, and the tokens' indices are read one set of tokens earlier.
 #include <cstdint>
 
 #include "decode_common.cuh"
@@ -31,12 +31,13 @@ namespace {
 
 using namespace decode;
 
-constexpr int kSteps = 4;             // groups of 32 / kLanes heads of a chunk
+constexpr int kSteps = 4;             // heads of a chunk
 constexpr int kStages = 4;
 constexpr int kBlockWarps = 2;
 constexpr int kResident = 8;          // blocks of an SM
+constexpr int kUnits = 4;             // units that a warp should have at least
 constexpr int kRowBytes = kSteps * 512;
-constexpr int kAngleBytes = 1024 + 16;   // a token's angles and (valid, slot)
+constexpr int kAngleBytes = 1024 + 32;   // the angles of a warp's tokens, and (valid, slot) of each
 constexpr int kWarpBytes = kStages * (kRowBytes + kAngleBytes);
 enum Pairing { kNone, kSplit, kInterleaved };
 
@@ -57,7 +58,7 @@ struct NormParams {
     int64_t q_stride[2], k_stride[2], v_stride[2], q_out_stride[2], k_out_stride[2];
     int64_t k_cache_stride[3], v_cache_stride[3];
     int64_t position_stride, table_rows, cache_slots;
-    uint32_t tokens, parts;                 // parts: warps that share a token's chunks out
+    uint32_t tokens, sets, parts;           // sets of a warp's tokens; warps that share a set out
     int32_t q_chunks, k_chunks, all_chunks; // of q, of k, of a token (q, k and v)
     int32_t h_q, h_k, head_dim, rot, axes, page_size, norm;
     int32_t section_end[DECODE_MAX_AXES];   // first pair of the next axis
@@ -123,11 +124,11 @@ __device__ __forceinline__ void cp_wait()
 template <typename T, int kLanes, Pairing kPairing>
 __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kernel(const NormParams p)
 {
-    constexpr int kHeads = 32 / kLanes;              // heads of a group
+    constexpr int kTokens = 32 / kLanes;             // tokens of a warp at a time: a set
     extern __shared__ __align__(16) uint8_t smem[];
-    const int lane = threadIdx.x & 31, l = lane % kLanes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, mine_at = lane / kLanes;
     uint8_t* const ring = smem + (threadIdx.x >> 5) * kWarpBytes;      // [kStages][kRowBytes]
-    uint8_t* const tokens = ring + kStages * kRowBytes;                // [kStages][kAngleBytes]
+    uint8_t* const sets = ring + kStages * kRowBytes;                  // [kStages][kAngleBytes]
     const int e = 8 * l;                             // the lane's first element
     const bool in_head = e < p.head_dim, in_rot = e < p.rot;
     const int half = p.rot / 2;
@@ -135,55 +136,59 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                         : lane + (e < half ? half / 8 : -(half / 8));
     const float inv_d = p.norm == DECODE_NORM_RMS ? 1.f / p.head_dim : 1.f;
 
-    // The warp's units: (token, part) number `first`, first + step, ...
+    // The warp's units: (set, part) number `first`, first + step, ...
     const uint32_t first = blockIdx.x * kBlockWarps + (threadIdx.x >> 5);
-    const uint32_t step = gridDim.x * kBlockWarps, all = p.tokens * p.parts;
+    const uint32_t step = gridDim.x * kBlockWarps, all = p.sets * p.parts;
 
     dep_launch();
     dep_wait();
     if (first >= all) return;
 
-    // ---- loads: `at` is the unit and `chunk` its chunk whose loads come next
+    // ---- loads: `at` is the unit and `chunk` its chunk whose loads come next, `token` the lane's
     uint32_t at = first, token = at / p.parts;
-    int chunk = static_cast<int>(at - token * p.parts), slot_ring = 0;
+    int chunk = static_cast<int>(at - token * p.parts), set_ring = 0;
+    token = token * kTokens + mine_at;
     int32_t pos[DECODE_MAX_AXES], slot = -1;         // of the token
     auto look = [&]() {
+        slot = -1;
         if constexpr (kPairing != kNone) {
 #pragma unroll
             for (int x = 0; x < DECODE_MAX_AXES; ++x)
-                pos[x] = x < p.axes ? p.positions[x * p.position_stride + token] : 0;
+                pos[x] = x < p.axes && token < p.tokens ? p.positions[x * p.position_stride + token]
+                                                        : 0;
         }
-        if (p.k_cache != nullptr) slot = p.slots[token];
+        if (p.k_cache != nullptr && token < p.tokens) slot = p.slots[token];
     };
     look();
     bool begins = true;                              // the chunk is its unit's first
     auto load = [&](int stage) {
         if (at < all) {
             const int kind = chunk < p.q_chunks ? 0 : chunk < p.q_chunks + p.k_chunks ? 1 : 2;
-            const int group = (kind == 0   ? chunk
-                               : kind == 1 ? chunk - p.q_chunks
-                                           : chunk - p.q_chunks - p.k_chunks) * kSteps;
-            const int h = group * kHeads + lane / kLanes, heads = kind == 0 ? p.h_q : p.h_k;
+            const int h = (kind == 0   ? chunk
+                           : kind == 1 ? chunk - p.q_chunks
+                                       : chunk - p.q_chunks - p.k_chunks) * kSteps;
+            const int heads = kind == 0 ? p.h_q : p.h_k;
             const int64_t* by = kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride;
             const uint16_t* from =
                 (kind == 0 ? p.q : kind == 1 ? p.k : p.v) + token * by[0] + h * by[1] + e;
             const uint32_t rows = smem_addr(ring) + stage * kRowBytes + lane * 16;
+            const bool here = in_head && token < p.tokens;
 #pragma unroll
             for (int x = 0; x < kSteps; ++x) {
-                if (in_head && h + x * kHeads < heads) cp_async16(rows + x * 512, from);
-                from += kHeads * by[1];
+                if (here && h + x < heads) cp_async16(rows + x * 512, from);
+                from += by[1];
             }
             if (begins) {
-                uint8_t* const to = tokens + slot_ring * kAngleBytes;
+                uint8_t* const to = sets + set_ring * kAngleBytes;
                 bool ok = true;
                 if constexpr (kPairing != kNone) {
 #pragma unroll
                     for (int x = 0; x < DECODE_MAX_AXES; ++x)
                         ok = ok && pos[x] >= 0 && (x >= p.axes || pos[x] < p.table_rows);
-                    if (!ok && lane == 0) atomicOr(p.status, DECODE_BAD_POSITION);
-                    // a lane of the first head fetches the table's floats e .. e + 7: cosines or
-                    // sines of the pairs pair0 .. pair0 + 7
-                    if (ok && in_rot && lane < kLanes) {
+                    if (!ok && l == 0) atomicOr(p.status, DECODE_BAD_POSITION);
+                    // the table's floats e .. e + 7: cosines or sines of the pairs pair0 ..
+                    // pair0 + 7
+                    if (ok && in_rot && here) {
                         const int pair0 = e < half ? e : e - half;
                         auto axis_of = [&](int pair) {
                             int axis = 0;
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                             for (int x = 1; x < DECODE_MAX_AXES; ++x) row = axis == x ? pos[x] : row;
                             return p.table + static_cast<int64_t>(row) * p.rot;
                         };
-                        const uint32_t angles = smem_addr(to) + e * 4;
+                        const uint32_t angles = smem_addr(to) + lane * 32;
                         const int axis = axis_of(pair0);
                         if (axis == axis_of(pair0 + 7)) {
                             const float* row = table_row(axis) + e;
@@ -212,19 +217,21 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                     }
                 }
                 if (slot < -1 || slot >= p.cache_slots) {
-                    if (lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+                    if (l == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
                     slot = -1;
                 }
-                if (lane == 0)
-                    *reinterpret_cast<int2*>(to + 1024) = make_int2(ok, ok ? slot : -1);
-                slot_ring = slot_ring + 1 == kStages ? 0 : slot_ring + 1;
+                if (l == 0)
+                    *reinterpret_cast<int2*>(to + 1024 + mine_at * 8) =
+                        make_int2(ok, ok ? slot : -1);
+                set_ring = set_ring + 1 == kStages ? 0 : set_ring + 1;
             }
             chunk += p.parts;
             begins = chunk >= p.all_chunks;
             if (begins) {
                 at += step;
-                token = at / p.parts;
-                chunk = static_cast<int>(at - token * p.parts);
+                const uint32_t set = at / p.parts;
+                chunk = static_cast<int>(at - set * p.parts);
+                token = set * kTokens + mine_at;
                 if (at < all) look();
             }
         }
@@ -237,22 +244,22 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
     uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
     if (in_head && p.q_weight) wq = *reinterpret_cast<const uint4*>(p.q_weight + e);
     if (in_head && p.k_weight) wk = *reinterpret_cast<const uint4*>(p.k_weight + e);
-    int stage = 0, token_ring = 0;
+    int stage = 0, work_ring = 0;
     for (uint32_t unit = first; unit < all; unit += step) {
-        const uint32_t t = unit / p.parts;
-        const uint8_t* const head = tokens + token_ring * kAngleBytes;
-        const float* const angles = reinterpret_cast<const float*>(head);
+        const uint32_t set = unit / p.parts, t = set * kTokens + mine_at;
+        const uint8_t* const head = sets + work_ring * kAngleBytes;
+        const float* const angles = reinterpret_cast<const float*>(head) + mine_at * kLanes * 8;
         bool ok = true;
         int32_t place = -1, page = 0, off = 0;
         int have = -1;                               // the kind the factors are for
         uint64_t mine[4], other[4];
-        for (int c0 = static_cast<int>(unit - t * p.parts); c0 < p.all_chunks; c0 += p.parts) {
+        for (int c0 = static_cast<int>(unit - set * p.parts); c0 < p.all_chunks; c0 += p.parts) {
             __syncwarp();
             load(stage == 0 ? kStages - 1 : stage - 1);
             cp_wait<kStages - 1>();
             __syncwarp();
             if (have < 0) {
-                const int2 x = *reinterpret_cast<const int2*>(head + 1024);
+                const int2 x = *reinterpret_cast<const int2*>(head + 1024 + mine_at * 8);
                 ok = x.x;
                 place = x.y;
                 if (place >= 0) {
@@ -261,9 +268,9 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                 }
             }
             const int kind = c0 < p.q_chunks ? 0 : c0 < p.q_chunks + p.k_chunks ? 1 : 2;
-            const int group = (kind == 0   ? c0
-                               : kind == 1 ? c0 - p.q_chunks
-                                           : c0 - p.q_chunks - p.k_chunks) * kSteps;
+            const int h = (kind == 0   ? c0
+                           : kind == 1 ? c0 - p.q_chunks
+                                       : c0 - p.q_chunks - p.k_chunks) * kSteps;
             if (kind != have && kind < 2) {
                 const uint4 wb = kind == 0 ? wq : wk;
                 const bool weights = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
@@ -311,26 +318,25 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
 
             // where the rows go: to q_out or k_out, or to the token's place in a cache
             const int heads = kind == 0 ? p.h_q : p.h_k;
-            int h = group * kHeads + lane / kLanes;
             uint16_t* dst;
             int64_t dst_step;
-            bool write = in_head;
+            bool write = in_head && t < p.tokens;
             if (kind == 0) {
                 dst = p.q_out + t * p.q_out_stride[0] + h * p.q_out_stride[1] + e;
-                dst_step = p.q_out_stride[1] * kHeads;
+                dst_step = p.q_out_stride[1];
             } else if (p.k_cache == nullptr) {
                 dst = p.k_out + t * p.k_out_stride[0] + h * p.k_out_stride[1] + e;
-                dst_step = p.k_out_stride[1] * kHeads;
+                dst_step = p.k_out_stride[1];
             } else {
                 const int64_t* to = kind == 1 ? p.k_cache_stride : p.v_cache_stride;
                 dst = (kind == 1 ? p.k_cache : p.v_cache) + page * to[0] + off * to[1] + h * to[2] + e;
-                dst_step = to[2] * kHeads;
+                dst_step = to[2];
                 write = write && place >= 0;
             }
             const uint4* const rows = reinterpret_cast<const uint4*>(ring + stage * kRowBytes);
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                if ((group + s) * kHeads >= heads) break;
+                if (h + s >= heads) break;
                 uint4 b = rows[s * 32 + lane];
                 if (kind < 2) {
                     uint64_t x[4];
@@ -366,28 +372,29 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                     }
                     b = ok ? make_uint4(out[0], out[1], out[2], out[3]) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (write && h < heads) *reinterpret_cast<uint4*>(dst) = b;
-                h += kHeads;
+                if (write) *reinterpret_cast<uint4*>(dst) = b;
                 dst += dst_step;
             }
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
-        token_ring = token_ring + 1 == kStages ? 0 : token_ring + 1;
+        work_ring = work_ring + 1 == kStages ? 0 : work_ring + 1;
     }
 }
 
 template <typename T, int kLanes, Pairing kPairing>
 cudaError_t run(NormParams p, int sms, cudaStream_t stream)
 {
-    constexpr int kPass = 32 / kLanes * kSteps;      // heads of a chunk
-    p.q_chunks = (p.h_q + kPass - 1) / kPass;
-    p.k_chunks = (p.h_k + kPass - 1) / kPass;
+    constexpr int kTokens = 32 / kLanes;
+    p.sets = (p.tokens + kTokens - 1) / kTokens;
+    p.q_chunks = (p.h_q + kSteps - 1) / kSteps;
+    p.k_chunks = (p.h_k + kSteps - 1) / kSteps;
     p.all_chunks = p.q_chunks + p.k_chunks * (p.v != nullptr ? 2 : 1);
-    // A warp takes whole tokens; with fewer tokens than the GPU holds warps, parts of them.
+    // A warp takes whole sets; where that would leave warps without one, or with one more than
+    // others have, parts of them.
     const int64_t most = static_cast<int64_t>(sms) * kResident, warps = most * kBlockWarps;
-    const int64_t share = warps / p.tokens;
+    const int64_t share = kUnits * warps / p.sets;
     p.parts = static_cast<uint32_t>(share < 1 ? 1 : share > p.all_chunks ? p.all_chunks : share);
-    const int64_t blocks = (static_cast<int64_t>(p.tokens) * p.parts + kBlockWarps - 1) / kBlockWarps;
+    const int64_t blocks = (static_cast<int64_t>(p.sets) * p.parts + kBlockWarps - 1) / kBlockWarps;
     return launch(qk_norm_rope_kernel<T, kLanes, kPairing>,
                   dim3(static_cast<uint32_t>(blocks < most ? blocks : most)), dim3(kBlockWarps * 32),
                   kBlockWarps * kWarpBytes, stream, p);
