@@ -6,7 +6,7 @@
 // taken of the row before its update,
 //     p = s . k,   r = s . q,   u = beta (v - alpha p),   o = scale (alpha r + u (k . q)),
 //     s <- alpha s + u k,
-// so their two reductions overlap and the row is read once.  A state is 65,536 bytes and a token
+// so their two reductions overlap (with several tokens o is taken of the row after it, below).  A state is 65,536 bytes and a token
 // adds about 1 KB to it, so the bytes of the states, read once and written once, are the floor:
 // the kernel is a copy with 6 flops per element on the way.
 //
@@ -81,15 +81,6 @@ __device__ __forceinline__ void load_row(uint64_t (&x)[8], const uint16_t* row, 
         x[2 * j] = pair(lo.x, lo.y), x[2 * j + 1] = pair(hi.x, hi.y);
     }
 }
-__device__ __forceinline__ void load_row(uint64_t (&x)[8], const float* row, int l)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(row + 4 * (l + 8 * j));
-        x[2 * j] = b.x, x[2 * j + 1] = b.y;
-    }
-}
-
 // Sums of d[0 .. 3] over a group of eight lanes, one row to a lane: lane l gets row l & 3, by
 // halving the rows with the lanes (4 shuffles for the 12 of four butterflies).
 __device__ __forceinline__ float sum_rows(const float (&d)[kRows], int l)
@@ -131,40 +122,85 @@ __device__ __forceinline__ uint16_t from_float(float x)
     return static_cast<uint16_t>(Half2<T>::pack(x, 0.f));
 }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+}
+
 // Block: kWarps warps, 16 value rows each, of one (sequence, value head).  kMany: several tokens
-// a sequence; their keys, queries, values and gates are staged in shared memory kStage tokens at
-// a time, converted to fp32, while the state's loads are in flight, so that a token costs neither
-// a round trip to L2 nor a conversion in every lane group.
+// a sequence.  Their keys, queries, values and gates are staged in shared memory kStage tokens at
+// a time, on their way before the state's slot is even known, so that a token costs no round trip
+// to L2; and a token's output is taken of the updated rows, which frees the key's registers for
+// the queries (with fewer registers more blocks hide the states' latency).
 constexpr int kStage = 8;
 
-// Floats of a staged token: its key, its queries, the block's values, (alpha, beta) and k . q.
+// Bytes of a staged token: its key, its queries, the block's values, (alpha, beta).
 struct Staged {
-    int q, v, gates, kq, total;
+    int q, v, gates, total;
     __host__ __device__ Staged(int queries, int rows)
-        : q(kD), v(kD * (1 + queries)), gates(v + rows), kq(gates + 2),
-          total((kq + queries + 3) / 4 * 4)
+        : q(2 * kD), v(2 * kD * (1 + queries)), gates(v + 2 * rows), total(gates + 16)
     {
     }
 };
 
 template <typename T, int kWarps, bool kMany>
-__global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams p)
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
+    gdn_step_kernel(const StepParams p)
 {
     constexpr int kBlockRows = kWarpRows * kWarps;
     constexpr int kParts = kD / kBlockRows;              // blocks of a state
-    extern __shared__ __align__(16) float smem[];
+    extern __shared__ __align__(16) uint8_t smem[];
     const int item = blockIdx.x / kParts, part = blockIdx.x % kParts;
     const int i = item / p.h_v, j = item % p.h_v;
     const int lane = threadIdx.x & 31, l = lane & 7;
     const int block_row = part * kBlockRows;
     const int row0 = block_row + (threadIdx.x >> 5) * kWarpRows + (lane >> 3) * kRows;
 
+    const uint16_t* kp = p.k + i * p.k_stride[0] + (j / p.kgroup) * p.k_stride[2];
+    const uint16_t* vp = p.v + i * p.v_stride[0] + j * p.v_stride[2] + block_row;
+    const uint16_t* qp = p.q + i * p.q_stride[0] +
+                         static_cast<int64_t>(p.queries > 1 ? j * p.queries : j / p.qgroup) *
+                             p.q_stride[2];
+    const float* ap = p.alpha + i * p.alpha_stride[0] + j;
+    const float* bp = p.beta + i * p.beta_stride[0] + j;
+    const int64_t out0 = (static_cast<int64_t>(i) * p.tokens * p.h_o +
+                          static_cast<int64_t>(j) * p.queries) * kD + row0;
+    const Staged at(p.queries, kBlockRows);
+    auto stage = [&](int t0) {
+        const int here = min(kStage, p.tokens - t0), pieces = at.gates / 16;
+        for (int x = threadIdx.x; x < here * pieces; x += kWarps * 32) {
+            const int t = x / pieces, b = (x - t * pieces) * 16;
+            const uint16_t* src;
+            if (b < at.q)
+                src = kp + (t0 + t) * p.k_stride[1] + b / 2;
+            else if (b < at.v)
+                src = qp + (t0 + t) * p.q_stride[1] + (b / (2 * kD) - 1) * p.q_stride[2] +
+                      b % (2 * kD) / 2;
+            else
+                src = vp + (t0 + t) * p.v_stride[1] + (b - at.v) / 2;
+            cp_async16(smem + t * at.total + b, src);
+        }
+        for (int x = threadIdx.x; x < 2 * here; x += kWarps * 32)
+            cp_async4(smem + x / 2 * at.total + at.gates + (x & 1) * 4,
+                      x & 1 ? bp + (t0 + x / 2) * p.beta_stride[1]
+                            : ap + (t0 + x / 2) * p.alpha_stride[1]);
+    };
+
     dep_launch();
     dep_wait();
     const int slot = p.slots ? p.slots[i] : i;
+    if constexpr (kMany) stage(0);
     const bool active = slot >= 0 && slot < p.n_slots;
-    const int64_t out0 = (static_cast<int64_t>(i) * p.tokens * p.h_o +
-                          static_cast<int64_t>(j) * p.queries) * kD + row0;
     if (!active) {
         if (slot != -1 && threadIdx.x == 0) atomicOr(p.status, DECODE_BAD_STATE_SLOT);
         if (l == 0)
@@ -173,6 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
                     *reinterpret_cast<uint2*>(
                         p.o + out0 + (static_cast<int64_t>(t) * p.h_o + g) * kD) =
                         make_uint2(0u, 0u);
+        if constexpr (kMany) cp_async_wait();
         return;
     }
 
@@ -187,99 +224,64 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
             const ulonglong2 x = state[r * (kD / 4) + 8 * c];
             s[r][2 * c] = x.x, s[r][2 * c + 1] = x.y;
         }
+    const int row = row0 - block_row + (l & 3);          // the row whose sums this lane gets
 
-    const uint16_t* kp = p.k + i * p.k_stride[0] + (j / p.kgroup) * p.k_stride[2];
-    const uint16_t* vp = p.v + i * p.v_stride[0] + j * p.v_stride[2];
-    const uint16_t* qp = p.q + i * p.q_stride[0] +
-                         static_cast<int64_t>(p.queries > 1 ? j * p.queries : j / p.qgroup) *
-                             p.q_stride[2];
-    const float* ap = p.alpha + i * p.alpha_stride[0] + j;
-    const float* bp = p.beta + i * p.beta_stride[0] + j;
-    const int row = row0 + (l & 3);                      // the row whose sums this lane gets
-
-    const Staged at(p.queries, kBlockRows);
-    for (int t0 = 0; t0 < p.tokens; t0 += kMany ? kStage : 1) {
-        const int here = kMany ? min(kStage, p.tokens - t0) : 1;
-        if constexpr (kMany) {
-            if (t0 > 0) __syncthreads();
-            const int pieces = at.gates / 8;             // of 8 elements, of a token
-            for (int x = threadIdx.x; x < here * pieces; x += kWarps * 32) {
-                const int t = x / pieces, c = (x - t * pieces) * 8;
-                const uint16_t* src;
-                if (c < at.q)
-                    src = kp + (t0 + t) * p.k_stride[1] + c;
-                else if (c < at.v)
-                    src = qp + (t0 + t) * p.q_stride[1] + (c / kD - 1) * p.q_stride[2] + c % kD;
-                else
-                    src = vp + (t0 + t) * p.v_stride[1] + block_row + c - at.v;
-                const uint4 b = *reinterpret_cast<const uint4*>(src);
-                const float2 x0 = Half2<T>::unpack(b.x), x1 = Half2<T>::unpack(b.y),
-                             x2 = Half2<T>::unpack(b.z), x3 = Half2<T>::unpack(b.w);
-                float4* to = reinterpret_cast<float4*>(smem + t * at.total + c);
-                to[0] = make_float4(x0.x, x0.y, x1.x, x1.y);
-                to[1] = make_float4(x2.x, x2.y, x3.x, x3.y);
-            }
-            for (int x = threadIdx.x; x < 2 * here; x += kWarps * 32)
-                smem[x / 2 * at.total + at.gates + (x & 1)] =
-                    x & 1 ? bp[(t0 + x / 2) * p.beta_stride[1]]
-                          : ap[(t0 + x / 2) * p.alpha_stride[1]];
-            __syncthreads();
-            // k . q of each token and query, a group of eight lanes each
-            for (int x = 0; x < here * p.queries; x += kWarps * 4) {
-                const int y = x + (threadIdx.x >> 3), z = min(y, here * p.queries - 1);
-                const int t = z / p.queries, g = z - t * p.queries;
-                float* tok = smem + t * at.total;
-                uint64_t k[8], q[8];
-                load_row(k, tok, l);
-                load_row(q, tok + at.q + kD * g, l);
-                const float kq = sum8(dot16(k, q));
-                if (y == z && l == 0) tok[at.kq + g] = kq;
-            }
-            __syncthreads();
-        }
-        for (int t = 0; t < here; ++t) {
-            const float* tok = smem + t * at.total;
-            uint64_t k[8];
-            float alpha, beta, v;
-            if constexpr (kMany) {
-                load_row(k, tok, l);
-                alpha = tok[at.gates], beta = tok[at.gates + 1];
-                v = tok[at.v + row - block_row];
-            } else {
-                load_row<T>(k, kp, l);
-                alpha = ap[0], beta = bp[0];
-                v = to_float<T>(vp[row]);
-            }
-            float d[kRows];
+    // s <- alpha s + u k, with u that of the lane's row
+    auto update = [&](const uint64_t (&k)[8], float alpha, float u) {
+        const uint64_t decay = pair(alpha, alpha);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], k);
-            const float mine = beta * (v - alpha * sum_rows(d, l));
-            for (int g = 0; g < p.queries; ++g) {
-                uint64_t q[8];
-                float kq;
-                if constexpr (kMany) {
-                    load_row(q, tok + at.q + kD * g, l);
-                    kq = tok[at.kq + g];
-                } else {
-                    load_row<T>(q, qp + g * p.q_stride[2], l);
-                    kq = sum8(dot16(k, q));
+        for (int r = 0; r < kRows; ++r) {
+            const float ur = __shfl_sync(0xffffffffu, u, (lane & 24) + r);
+            const uint64_t uu = pair(ur, ur);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) s[r][c] = fma2(uu, k[c], mul2(decay, s[r][c]));
+        }
+    };
+    auto product = [&](const uint64_t (&x)[8]) {
+        float d[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], x);
+        return sum_rows(d, l);
+    };
+    if constexpr (kMany) {
+        for (int t0 = 0; t0 < p.tokens; t0 += kStage) {
+            if (t0 > 0) {
+                __syncthreads();
+                stage(t0);
+            }
+            cp_async_wait();
+            __syncthreads();
+            const int here = min(kStage, p.tokens - t0);
+            for (int t = 0; t < here; ++t) {
+                const uint8_t* tok = smem + t * at.total;
+                const float2 gates = *reinterpret_cast<const float2*>(tok + at.gates);
+                uint64_t x[8];
+                load_row<T>(x, reinterpret_cast<const uint16_t*>(tok), l);
+                const float v =
+                    to_float<T>(reinterpret_cast<const uint16_t*>(tok + at.v)[row]);
+                update(x, gates.x, gates.y * (v - gates.x * product(x)));
+                for (int g = 0; g < p.queries; ++g) {
+                    load_row<T>(x, reinterpret_cast<const uint16_t*>(tok + at.q) + kD * g, l);
+                    const float o = p.scale * product(x);
+                    if (l < kRows)
+                        p.o[out0 + l + (static_cast<int64_t>(t0 + t) * p.h_o + g) * kD] =
+                            from_float<T>(o);
                 }
-#pragma unroll
-                for (int r = 0; r < kRows; ++r) d[r] = dot16(s[r], q);
-                const float o = p.scale * fmaf(alpha, sum_rows(d, l), mine * kq);
-                if (l < kRows)
-                    p.o[out0 + l + (static_cast<int64_t>(t0 + t) * p.h_o + g) * kD] =
-                        from_float<T>(o);
-            }
-            const uint64_t decay = pair(alpha, alpha);
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                const float ur = __shfl_sync(0xffffffffu, mine, (lane & 24) + r);
-                const uint64_t u = pair(ur, ur);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) s[r][c] = fma2(u, k[c], mul2(decay, s[r][c]));
             }
         }
+    } else {
+        uint64_t k[8];
+        load_row<T>(k, kp, l);
+        const float alpha = ap[0], beta = bp[0], v = to_float<T>(vp[row]);
+        const float u = beta * (v - alpha * product(k));
+        for (int g = 0; g < p.queries; ++g) {
+            uint64_t q[8];
+            load_row<T>(q, qp + g * p.q_stride[2], l);
+            const float kq = sum8(dot16(k, q));
+            const float o = p.scale * fmaf(alpha, product(q), u * kq);
+            if (l < kRows) p.o[out0 + l + static_cast<int64_t>(g) * kD] = from_float<T>(o);
+        }
+        update(k, alpha, u);
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
@@ -288,15 +290,21 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_step_kernel(const StepParams 
             state[r * (kD / 4) + 8 * c] = make_ulonglong2(s[r][2 * c], s[r][2 * c + 1]);
 }
 
-template <typename T, int kWarps>
+// Two warps a block for single tokens, so that few states spread over many SMs; four for several
+// tokens, whose staging they share (77 sequences of 4 tokens: 21.0 us, 21.7 with two).
+template <typename T>
 cudaError_t run(const StepParams& p, int64_t items, cudaStream_t stream)
 {
-    constexpr int kBlockRows = kWarpRows * kWarps;
-    const dim3 grid(static_cast<uint32_t>(items * (kD / kBlockRows))), block(kWarps * 32);
+    constexpr int kOne = 2, kSome = 4;
     if (p.tokens == 1)
-        return launch(gdn_step_kernel<T, kWarps, false>, grid, block, 0, stream, p);
-    const size_t smem = sizeof(float) * kStage * Staged(p.queries, kBlockRows).total;
-    return launch(gdn_step_kernel<T, kWarps, true>, grid, block, smem, stream, p);
+        return launch(gdn_step_kernel<T, kOne, false>,
+                      dim3(static_cast<uint32_t>(items * (kD / (kWarpRows * kOne)))),
+                      dim3(kOne * 32), 0, stream, p);
+    const size_t smem = static_cast<size_t>(p.tokens < kStage ? p.tokens : kStage) *
+                        Staged(p.queries, kWarpRows * kSome).total;
+    return launch(gdn_step_kernel<T, kSome, true>,
+                  dim3(static_cast<uint32_t>(items * (kD / (kWarpRows * kSome)))), dim3(kSome * 32),
+                  smem, stream, p);
 }
 
 }  // namespace
@@ -334,7 +342,6 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     take_strides(p.beta_stride, a->beta_stride, {a->n, a->tokens}, 1);
     if (a->n_slots > 1 && (a->state_stride % 4 || a->state_stride < a->h_v * kD * kD))
         return fail(DECODE_ERR_INVALID_ARG, "state_stride %lld", (long long)a->state_stride);
-    constexpr int kWarps = 2;
     if (a->n >= (int64_t(1) << 31) / (a->h_v * 8) || a->tokens >= (1 << 24) ||
         a->n_slots >= (int64_t(1) << 31))
         return fail(DECODE_ERR_UNSUPPORTED, "too many states or tokens for one call");
@@ -359,8 +366,8 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     p.n_slots = static_cast<int32_t>(a->n_slots);
     p.scale = a->scale;
     const int64_t items = a->n * a->h_v;
-    const cudaError_t e = a->dtype == DECODE_BF16 ? run<__nv_bfloat16, kWarps>(p, items, stream)
-                                                  : run<__half, kWarps>(p, items, stream);
+    const cudaError_t e = a->dtype == DECODE_BF16 ? run<__nv_bfloat16>(p, items, stream)
+                                                  : run<__half>(p, items, stream);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "gdn_step_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;
