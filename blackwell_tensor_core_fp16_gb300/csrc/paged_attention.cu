@@ -40,7 +40,9 @@ namespace {
 using namespace decode;
 
 constexpr int kSub = 16;         // tokens of a matrix tile
-constexpr int kResident = 2;     // blocks of an SM
+constexpr int kMostResident = 2;     // of Cfg::kResident
+constexpr int kClusterMost = 8;      // blocks of a cluster
+constexpr int kClusterTiles = 3;     // tiles of each of them
 constexpr int kSharedItems = 64;     // items up to which the join takes a block a head
 constexpr int kListedItems = 1024;   // items up to which the join goes by item
 
@@ -59,7 +61,7 @@ struct AttnParams {
     int64_t q_stride[2], k_stride[3], v_stride[3];
     int64_t table_stride, max_len;
     int32_t n, h_q, h_kv, group, head_items, pages, page_size, page_shift, window;
-    int32_t by_item;
+    int32_t by_item, join_shared;
     float scale_log2;
 };
 
@@ -113,6 +115,44 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// ---- thread-block clusters: rank, barrier and reads of another block's shared memory
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" :::
+                 "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t smem, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t address)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(address) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t address)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(address) : "memory");
+    return x;
 }
 
 // A sequence's tokens [start, len); len = 0 for a length the page table cannot hold.  Its slices
@@ -180,6 +220,7 @@ struct Cfg {
     // a slice is 8 KB at least: for short rows the look-up, the maxima and the loop cost as much as
     // the products
     static constexpr int kSubs = D == 64 ? 2 : 1;
+    static constexpr int kResident = 2;                       // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
     static constexpr int kStageBytes = 2 * kSlice * D * 2;    // keys, then values
@@ -190,8 +231,9 @@ struct Cfg {
     static constexpr bool kQueriesShared = D == 256 && kHeadTiles == 2;
     static constexpr int kQueryRow = D + 8;                   // elements
     static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 : 0;
-    // (two blocks share an SM's 228 KB, of which the system takes 1 KB a block)
-    static constexpr int kRoom = 115712 - kMergeBytes - kSmallBytes - kQueryBytes;
+    // (the blocks share an SM's 228 KB, of which the system takes 1 KB a block)
+    static constexpr int kRoom =
+        233472 / kResident - 1024 - kMergeBytes - kSmallBytes - kQueryBytes;
     static constexpr int kMaxStages = kRoom / (kWarps * kStageBytes);
     static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
@@ -199,8 +241,9 @@ struct Cfg {
     static_assert(kStages >= 2, "no room for two stages");
 };
 
-template <typename T, int D, int kHeadTiles>
-__global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
+// kCluster: one cluster an item, for few items of few tiles.
+template <typename T, int D, int kHeadTiles, bool kCluster>
+__global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTiles>::kResident)
     paged_attention_kernel(const AttnParams p)
 {
     using C = Cfg<D, kHeadTiles>;
@@ -223,65 +266,93 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
     dep_launch();
     dep_wait();
 
-    // ---- the block's range: a scan of all sequences' tiles
-    const int chunk = (p.n + C::kThreads - 1) / C::kThreads;
-    const int i_lo = min(p.n, tid * chunk), i_hi = min(p.n, i_lo + chunk);
-    int mine = 0;
-    for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(span_of(p, i)) * items_per_seq;
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += x;
-    }
-    if (lane == 31) sm_i[w] = upto;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int x = 0; x < kWarps; ++x) {
-        if (x == w) upto += total;
-        total += sm_i[x];
-    }
-    const int blocks = min(static_cast<int>(gridDim.x), total);   // with a tile each at least
-    const int t0 = c < blocks ? first_tile(c, total, blocks) : total;
-    const int t1 = c < blocks ? first_tile(c + 1, total, blocks) : total;
-    if (t0 >= upto - mine && t0 < upto) {          // one thread: its sequences hold tile t0
-        int at = upto - mine;
-        for (int i = i_lo; i < i_hi; ++i) {
-            const int tiles = tiles_of<kTile>(span_of(p, i)) * items_per_seq;
-            if (t0 < at + tiles) {
-                sm_i[32] = i;
-                sm_i[33] = t0 - at;
-                break;
-            }
-            at += tiles;
-        }
-    }
-    // sequences without tokens have no tile: their results are written here
-    for (int i = c; i < p.n; i += gridDim.x) {
-        const int raw = p.lens[i];
-        const Span s = span_of(p, i);
-        if (tid == 0 && raw != s.len) atomicOr(p.status, DECODE_BAD_LENGTH);
-        if (s.len > 0) continue;
-        uint4* row = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * p.h_q * D);
-        for (int x = tid; x < p.h_q * (D / 8); x += C::kThreads) row[x] = make_uint4(0, 0, 0, 0);
-        if (p.lse != nullptr)
-            for (int x = tid; x < p.h_q; x += C::kThreads)
-                p.lse[static_cast<int64_t>(i) * p.h_q + x] = -INFINITY;
-        if (p.by_item)
-            for (int x = tid; x < items_per_seq; x += C::kThreads)
-                p.split[i * items_per_seq + x] = make_int4(-1, 0, 0, 0);
-    }
-    if (tid == 0 && !p.by_item) p.split[c] = make_int4(-1, 0, 0, 0);
-    if (t0 >= t1) return;
-    __syncthreads();
-
     Cursor cur;
-    cur.i = sm_i[32];
-    cur.span = span_of(p, cur.i);
-    cur.tiles = tiles_of<kTile>(cur.span);
-    cur.item = sm_i[33] / cur.tiles;
-    cur.tile = sm_i[33] % cur.tiles;
+    int t0, t1, total = 0, blocks = 0;             // the block's tiles, of how many in how many blocks
+    if constexpr (kCluster) {
+        // ---- the block's range: its share of its cluster's item, whose tiles are numbered from 0
+        const int ranks = cluster_size(), item = c / ranks;
+        cur.i = item / items_per_seq;
+        cur.item = item % items_per_seq;
+        cur.span = span_of(p, cur.i);
+        cur.tiles = tiles_of<kTile>(cur.span);
+        if (cur.item == 0 && c % ranks == 0 && tid == 0 && p.lens[cur.i] != cur.span.len)
+            atomicOr(p.status, DECODE_BAD_LENGTH);
+        const int each = (cur.tiles + ranks - 1) / ranks;
+        t0 = cur.tile = min(c % ranks * each, cur.tiles);
+        t1 = min(t0 + each, cur.tiles);
+        if (cur.tiles == 0) {                      // for all of the cluster's blocks
+            if (c % ranks == 0) {
+                const int h0 = cur.item / p.head_items * p.group + cur.item % p.head_items * kHeads;
+                const int heads = min(kHeads, p.group - cur.item % p.head_items * kHeads);
+                const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0;
+                for (int x = tid; x < heads * (D / 8); x += C::kThreads)
+                    reinterpret_cast<uint4*>(p.o + row * D)[x] = make_uint4(0, 0, 0, 0);
+                if (p.lse != nullptr && tid < heads) p.lse[row + tid] = -INFINITY;
+            }
+            return;
+        }
+        // the block's maxima and sums, for its cluster (a block may have no tile)
+        if (tid < 2 * kHeads)
+            reinterpret_cast<float*>(sm_i)[tid] = tid < kHeads ? -INFINITY : 0.f;
+        __syncthreads();
+    } else {
+        // ---- the block's range: a scan of all sequences' tiles
+        const int chunk = (p.n + C::kThreads - 1) / C::kThreads;
+        const int i_lo = min(p.n, tid * chunk), i_hi = min(p.n, i_lo + chunk);
+        int mine = 0;
+        for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        if (lane == 31) sm_i[w] = upto;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+            if (x == w) upto += total;
+            total += sm_i[x];
+        }
+        blocks = min(static_cast<int>(gridDim.x), total);   // with a tile each at least
+        t0 = c < blocks ? first_tile(c, total, blocks) : total;
+        t1 = c < blocks ? first_tile(c + 1, total, blocks) : total;
+        if (t0 >= upto - mine && t0 < upto) {          // one thread: its sequences hold tile t0
+            int at = upto - mine;
+            for (int i = i_lo; i < i_hi; ++i) {
+                const int tiles = tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+                if (t0 < at + tiles) {
+                    sm_i[32] = i;
+                    sm_i[33] = t0 - at;
+                    break;
+                }
+                at += tiles;
+            }
+        }
+        // sequences without tokens have no tile: their results are written here
+        for (int i = c; i < p.n; i += gridDim.x) {
+            const int raw = p.lens[i];
+            const Span s = span_of(p, i);
+            if (tid == 0 && raw != s.len) atomicOr(p.status, DECODE_BAD_LENGTH);
+            if (s.len > 0) continue;
+            uint4* row = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * p.h_q * D);
+            for (int x = tid; x < p.h_q * (D / 8); x += C::kThreads) row[x] = make_uint4(0, 0, 0, 0);
+            if (p.lse != nullptr)
+                for (int x = tid; x < p.h_q; x += C::kThreads)
+                    p.lse[static_cast<int64_t>(i) * p.h_q + x] = -INFINITY;
+            if (p.by_item)
+                for (int x = tid; x < items_per_seq; x += C::kThreads)
+                    p.split[i * items_per_seq + x] = make_int4(-1, 0, 0, 0);
+        }
+        if (tid == 0 && !p.by_item) p.split[c] = make_int4(-1, 0, 0, 0);
+        if (t0 >= t1) return;
+        __syncthreads();
+        cur.i = sm_i[32];
+        cur.span = span_of(p, cur.i);
+        cur.tiles = tiles_of<kTile>(cur.span);
+        cur.item = sm_i[33] / cur.tiles;
+        cur.tile = sm_i[33] % cur.tiles;
+    }
     Cursor pre = cur;                              // where the loads are
     int pre_t = t0;
 
@@ -576,7 +647,14 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
                         merge + (y * kHeads + h) * C::kMergeRow + d);
                     o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
                 }
-                if (whole) {
+                if constexpr (kCluster) {
+                    // (each element of the first warp's rows is read by this thread alone)
+                    *reinterpret_cast<float4*>(merge + h * C::kMergeRow + d) = o;
+                    if (d == 0) {
+                        reinterpret_cast<float*>(sm_i)[h] = top;
+                        reinterpret_cast<float*>(sm_i)[kHeads + h] = sum;
+                    }
+                } else if (whole) {
                     const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
                     const float inv = 1.f / sum;
                     *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
@@ -589,13 +667,47 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
                     if (d == 0) p.part_ml[row] = make_float2(top, sum);
                 }
             }
-            if (tid == 0 && begin >= t0 && (p.by_item || !whole))
+            if (!kCluster && tid == 0 && begin >= t0 && (p.by_item || !whole))
                 p.split[p.by_item ? cur.i * items_per_seq + cur.item : c] = make_int4(
                     whole ? -1 : c, whole ? 0 : block_of(end - 1, total, blocks), cur.i, cur.item);
             __syncthreads();
             fresh = true;
         }
-        advance<kTile>(cur, p);
+        if (!kCluster || t + 1 < t1) advance<kTile>(cur, p);
+    }
+    if constexpr (kCluster) {
+        // ---- join the cluster's blocks, each an equal share of the elements
+        const uint32_t ranks = cluster_size(), rank = cluster_rank();
+        const int h0 = cur.item / p.head_items * p.group + cur.item % p.head_items * kHeads;
+        const int heads = min(kHeads, p.group - cur.item % p.head_items * kHeads);
+        const int each = (cur.tiles + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
+        const int used = (cur.tiles + each - 1) / each;      // blocks with a tile
+        cluster_barrier();
+        for (int x = rank * C::kThreads + tid; x < heads * (D / 4); x += ranks * C::kThreads) {
+            const int h = x / (D / 4), d = x % (D / 4) * 4;
+            float top = -INFINITY;
+            for (int y = 0; y < used; ++y)
+                top = fmaxf(top, cluster_load(cluster_address(smem_addr(sm_i + h), y)));
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int y = 0; y < used; ++y) {
+                const float f =
+                    exp2_fast(cluster_load(cluster_address(smem_addr(sm_i + h), y)) - ref);
+                const float4 b = cluster_load4(
+                    cluster_address(smem_addr(merge + h * C::kMergeRow + d), y));
+                sum = fmaf(cluster_load(cluster_address(smem_addr(sm_i + kHeads + h), y)), f, sum);
+                o.x = fmaf(b.x, f, o.x), o.y = fmaf(b.y, f, o.y);
+                o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
+            }
+            const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
+            const float inv = 1.f / sum;
+            *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
+                Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
+            if (d == 0 && p.lse != nullptr)
+                p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        cluster_barrier();                         // the others may still read this block's part
     }
 }
 
@@ -604,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, kResident)
 // block an item each warp joins heads of its own; with a block (x, y) for each head, which is for
 // few items of many parts, the block's warps share the head's parts out.  It is a chain of three
 // dependent loads (the list, maxima and sums, outputs), so each is issued for all parts at once.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;        // most warps of a block; 8 where an item has 64 parts at most
 
 // A warp's running join: its lanes hold D / 32 neighbouring outputs each.
 template <int D>
@@ -660,7 +772,7 @@ struct Joined {
 };
 
 template <typename T, int D, int kHeadTiles>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32, 1) paged_attention_join_kernel(const AttnParams p)
 {
     constexpr int kHeads = 8 * kHeadTiles, kOut = Joined<D>::kOut;
     __shared__ __align__(16) float sm_o[kJoinWarps][D];
@@ -673,11 +785,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h0 = item.w / p.head_items * p.group + item.w % p.head_items * kHeads;
     const int heads = min(kHeads, p.group - item.w % p.head_items * kHeads);
-    const bool shared = gridDim.y > 1;
-    const int each = shared ? (parts + kJoinWarps - 1) / kJoinWarps : parts;
+    const bool shared = p.join_shared;
+    const int warps = blockDim.x >> 5;
+    const int each = shared ? (parts + warps - 1) / warps : parts;
     const int first = shared ? min(w * each, parts) : 0, last = min(first + each, parts);
 
-    for (int h = shared ? blockIdx.y : w; h < heads; h += shared ? gridDim.y : kJoinWarps) {
+    for (int h = shared ? blockIdx.y : w; h < heads; h += shared ? gridDim.y : warps) {
         Joined<D> sums;
         for (int x0 = first; x0 < last; x0 += 32) {
             const int x = min(x0 + lane, last - 1);
@@ -694,9 +807,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attention_join_kernel(c
             __syncthreads();
             if (w == 0) {
                 Joined<D> all;
-                const float2 ml = sm_ml[min(lane, kJoinWarps - 1)];
-                all.take(lane < kJoinWarps ? ml.x : -INFINITY, lane < kJoinWarps ? ml.y : 0.f,
-                         sm_o[min(lane, kJoinWarps - 1)], kJoinWarps, lane);
+                const float2 ml = sm_ml[min(lane, warps - 1)];
+                all.take(lane < warps ? ml.x : -INFINITY, lane < warps ? ml.y : 0.f,
+                         sm_o[min(lane, warps - 1)], warps, lane);
                 sums = all;
             }
             __syncthreads();
@@ -718,7 +831,7 @@ struct Layout {
 };
 Layout layout_for(int sms, int heads, int64_t d)
 {
-    const size_t blocks = static_cast<size_t>(sms) * kResident;
+    const size_t blocks = static_cast<size_t>(sms) * kMostResident;
     Layout l{};
     size_t at = sizeof(int4) * (blocks > kListedItems ? blocks : kListedItems);
     l.ml = at = (at + 255) & ~size_t(255);
@@ -739,26 +852,37 @@ int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
     if (per_item > 0 && items >= (int64_t(1) << 31) / per_item)
         return fail(DECODE_ERR_UNSUPPORTED, "too many tiles of the cache for one call");
     const int64_t tiles = per_item * items;
-    const int64_t most = static_cast<int64_t>(sms) * kResident;
+    const int64_t most = static_cast<int64_t>(sms) * C::kResident;
     const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < most ? tiles : most);
     p.by_item = items <= kListedItems;
-    auto* kernel = paged_attention_kernel<T, D, kHeadTiles>;
-    static thread_local bool set[kMaxDevices] = {};
+    p.join_shared = items <= kSharedItems;
+    // Few items of few tiles: a cluster an item, which joins its blocks' parts itself (one sequence
+    // of 500 tokens, 8 key heads: 5.5 us, 7.3 with the second kernel; of 2000 tokens 8.9 and 8.7).
+    int ranks = 1;
+    if (per_item > 1 && per_item <= kClusterMost * kClusterTiles)
+        while (ranks < kClusterMost && ranks < per_item) ranks *= 2;
+    const bool cluster = ranks > 1 && items * ranks <= most;
+    auto* kernel = cluster ? paged_attention_kernel<T, D, kHeadTiles, true>
+                           : paged_attention_kernel<T, D, kHeadTiles, false>;
+    static thread_local bool set[2][kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && !(dev < kMaxDevices && set[dev])) {
+    if (e == cudaSuccess && !(dev < kMaxDevices && set[cluster][dev])) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e == cudaSuccess && dev < kMaxDevices) set[dev] = true;
+        if (e == cudaSuccess && dev < kMaxDevices) set[cluster][dev] = true;
     }
     if (e == cudaSuccess)
-        e = launch(kernel, dim3(blocks), dim3(C::kThreads), C::kSmem, stream, p);
+        e = cluster ? launch_cluster(kernel, dim3(static_cast<uint32_t>(items * ranks)),
+                                     dim3(C::kThreads), C::kSmem, stream, ranks, p)
+                    : launch(kernel, dim3(blocks), dim3(C::kThreads), C::kSmem, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
-    if (blocks == 1) return DECODE_OK;
+    if (cluster || per_item <= 1 || blocks == 1) return DECODE_OK;     // no item is cut
+    const int64_t most_parts = per_item < blocks ? per_item : blocks;
     e = launch(paged_attention_join_kernel<T, D, kHeadTiles>,
                dim3(p.by_item ? static_cast<uint32_t>(items) : blocks,
-                    items > kSharedItems ? 1 : p.group < C::kHeads ? p.group : C::kHeads),
-               dim3(kJoinWarps * 32), 0, stream, p);
+                    !p.join_shared ? 1 : p.group < C::kHeads ? p.group : C::kHeads),
+               dim3((p.join_shared && most_parts > 64 ? kJoinWarps : 8) * 32), 0, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "paged_attention_join_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;
