@@ -6,9 +6,17 @@
 // taken of the row before its update,
 //     p = s . k,   r = s . q,   u = beta (v - alpha p),   o = scale (alpha r + u (k . q)),
 //     s <- alpha s + u k,
-// so their two reductions overlap (with several tokens o is taken of the row after it, below).  A state is 65,536 bytes and a token
-// adds about 1 KB to it, so the bytes of the states, read once and written once, are the floor:
-// the kernel is a copy with 6 flops per element on the way.
+// so their two reductions overlap (with several tokens o is taken of the row after it, below).
+//
+// What bounds it.  A state is 65,536 bytes and a token adds about 1 KB to it, so with one token
+// the bytes of the states, read once and written once, are the floor: 256 sequences x 32 states
+// (1.08 GB) take 156 us, 6.9 TB/s, which is what a plain copy reaches; one sequence of 16 states
+// takes 2.6 us, its launch and two round trips to memory.  Each further token costs its 6 flops
+// per element, on packed fp32 pairs: 151 sequences x 8 states take 28.5 us with 2 tokens (84% of
+// the copy rate), 34 us with 4 and 52 us with 8, the FMA pipes about 70% busy meanwhile.  (The
+// chunked form on mma.m16n8k16 with operands in three bfloat16 pieces was built and measured: 46
+// to 48 us for 2 to 8 tokens alike, bound by its chain of dependent products; it wins from 16
+// tokens on, where the prefill belongs.)
 //
 // Layout.  Eight lanes share a row of 128 floats, lane l of them holding the float4s l, l + 8,
 // l + 16, l + 24 (each load of the eight lanes is one 128-byte line), and a lane group has four

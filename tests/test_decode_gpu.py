@@ -593,6 +593,43 @@ def test_operators_on_a_side_stream_and_in_a_graph():
     assert torch.equal(vc3.view(torch.int16), vc.view(torch.int16))
 
 
+def test_hybrid_example_decodes_what_it_would_read():
+    """The example's model: the logits of tokens answered one by one (eager and recorded) are those
+    of the same tokens read as a prompt.  The two differ by roundings to bfloat16 between the
+    operators only: some 2^-8 of the logits' size, a few times over."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.HybridModel(seed=3)
+    gen = generator(71)
+    seqs = [torch.randint(0, 1024, (length,), generator=gen).cuda() for length in (40, 25, 70)]
+    cut = [30, 15, 60]
+    slots = torch.tensor([2, 7, 4], dtype=torch.int32, device="cuda")
+    whole = [model.read(seq, 1) for seq in seqs]
+    for seq, c, slot in zip(seqs, cut, slots.tolist()):
+        model.read(seq[:c], slot)
+    lens = torch.tensor(cut, dtype=torch.int32, device="cuda")
+    token = torch.stack([seq[c] for seq, c in zip(seqs, cut)])
+    got = [model.step(token, slots, lens)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        logits = model.step(token, slots, lens)
+    for t in range(1, 10):
+        token.copy_(torch.stack([seq[c + t] for seq, c in zip(seqs, cut)]))
+        lens.add_(1)
+        graph.replay()
+        got.append(logits.clone())
+    for t, step in enumerate(got):
+        for i, (ref_logits, c) in enumerate(zip(whole, cut)):
+            want = ref_logits[c + t].float()
+            err = (step[i].float() - want).abs().max()
+            assert float(err) <= 2.0 ** -5 * float(want.abs().max()), (t, i, float(err))
+
+
 # ---- refusals -------------------------------------------------------------------------------------------
 
 def test_refusals_of_the_step():
