@@ -331,6 +331,28 @@ def test_norm_refused_indices():
             g.check_decode_status()
 
 
+def test_norm_strided_positions():
+    """Positions of several axes as a view with space between its rows."""
+    s = norm_inputs(70, 8, 2, 128, 128, 3, torch.bfloat16, seed=27)
+    wide = torch.full((6, 90), -5, dtype=torch.int32, device="cuda")
+    wide[::2, 7:77] = s["positions"]
+    s["positions"] = wide[::2, 7:77]
+    (qr, qb), (kr, kb) = norm_refs(s)
+    q, k = norm_call(s)
+    ref.assert_close(q, qr, qb, "q")
+    ref.assert_close(k, kr, kb, "k")
+
+
+@pytest.mark.parametrize("tokens,h_q,h_k,d", [(3000, 32, 8, 128), (5000, 3, 1, 64), (2500, 40, 8, 256)])
+def test_norm_many_tokens(tokens, h_q, h_k, d):
+    """Enough tokens that warps take several sets, whole or in parts; all against the reference."""
+    s = norm_inputs(tokens, h_q, h_k, d, d // 2, 2, torch.bfloat16, seed=tokens)
+    (qr, qb), (kr, kb) = norm_refs(s)
+    q, k = norm_call(s)
+    ref.assert_close(q, qr, qb, "q")
+    ref.assert_close(k, kr, kb, "k")
+
+
 def test_norm_empty_and_broadcast():
     s = norm_inputs(4, 2, 1, 128, 128, 1, torch.bfloat16, seed=26)
     t = {x: (y[:0] if x in ("q", "k", "positions") else y) for x, y in s.items()}
@@ -425,6 +447,24 @@ def test_attention_work_split(n, top):
     lens[n // 2] = top
     lens[::7] = 0 if n > 2 else top
     check_attn(attn_inputs(lens, 2, 1, 64, 16, torch.float16, seed=n), f"{n} sequences")
+
+
+def test_attention_many_items_cut_across_blocks():
+    """More items than the join lists one by one, of several tiles each, so that most blocks' ranges
+    begin and end inside items; every seventh sequence is empty."""
+    gen = generator(30)
+    lens = torch.randint(200, 700, (270,), generator=gen)
+    lens[::7] = 0
+    check_attn(attn_inputs(lens, 4, 4, 64, 16, torch.bfloat16, seed=30), "1080 items")
+
+
+def test_attention_strided_table():
+    """A page table that is a view: every other row of a wider one, some columns in."""
+    s = attn_inputs([100, 0, 333, 64], 4, 2, 128, 16, torch.bfloat16, seed=40)
+    wide = torch.full((8, s["table"].shape[1] + 5), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[::2, 3:-2] = s["table"]
+    s["table"] = wide[::2, 3:-2]
+    check_attn(s, "strided table")
 
 
 def test_attention_all_empty():
@@ -577,6 +617,15 @@ def test_operators_on_a_side_stream_and_in_a_graph():
     side.synchronize()
     for x, y in zip(got, first):
         assert torch.equal(x, y)
+    # a plain stream handle in place of torch's object, with and without a workspace kept
+    for kept in (ws, None):
+        with torch.cuda.stream(side):
+            st2, kc2, vc2 = s["state"].clone(), a["k_cache"].clone(), a["v_cache"].clone()
+        got = decode_layer(s, st2, slots, norm, kc2, vc2, places, a["table"], a["lens"], kept,
+                           stream=side.cuda_stream)
+        side.synchronize()
+        for x, y in zip(got, first):
+            assert torch.equal(x, y)
 
     st3, kc3, vc3 = s["state"].clone(), a["k_cache"].clone(), a["v_cache"].clone()
     torch.cuda.synchronize()
