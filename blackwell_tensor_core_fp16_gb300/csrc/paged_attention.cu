@@ -9,8 +9,9 @@
 // unnormalised output, and results of warps and blocks are joined by their maxima.
 //
 // Work split.  An item is one (sequence, key head, up to 8 kHeadTiles of its query heads).  A tile is
-// 16 tokens per warp of an item.  All items' tiles, in order, are cut into equal contiguous ranges,
-// one a block, whatever the lengths: every block finds its range itself from a scan of the lengths.
+// a slice (16 tokens, 32 at head_dim 64) of an item for each of a block's warps.  All items' tiles, in
+// order, are cut into equal contiguous ranges, one a block, whatever the lengths: every block finds
+// its range itself from a scan of the lengths.
 // So a block has at most one item that began in an earlier block and one that goes on in a later
 // one; those two go to the workspace as (maximum, sum, output) and a second kernel joins each
 // item's parts in block order, the rest are written at once.  The order of every sum is fixed.
@@ -18,8 +19,10 @@
 // sequences of up to 8192 tokens, 8 key heads of 128, take 161 us, against 175 us with one block of
 // eight warps, whose SMs were busy 78% of the time on average; ranges four times finer than the
 // GPU holds blocks, which even the SMs out, take 167 us, their blocks' beginnings cost more.
+// Few items of few tiles, where the second kernel's launch would show, run as one thread-block
+// cluster an item instead, whose blocks join their parts through distributed shared memory.
 //
-// Inside a block each warp streams its own 16-token slices through a ring of shared-memory stages
+// Inside a block each warp streams its own slices through a ring of shared-memory stages
 // (16-byte cp.async, rows looked up in the page table one slice ahead, so pages may have any size
 // and the cache any strides) and needs no block barrier until an item ends; the ring runs on
 // across items.  Tokens outside the sequence are filled with zeros and not read.
@@ -218,7 +221,8 @@ struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHeads = 8 * kHeadTiles;
     // a slice is 8 KB at least: for short rows the look-up, the maxima and the loop cost as much as
-    // the products
+    // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 29.5 us, 36 us with
+    // 16-token slices; more blocks an SM with fewer or smaller stages are no faster, 30 to 39 us)
     static constexpr int kSubs = D == 64 ? 2 : 1;
     static constexpr int kResident = 2;                       // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
@@ -234,8 +238,7 @@ struct Cfg {
     // (the blocks share an SM's 228 KB, of which the system takes 1 KB a block)
     static constexpr int kRoom =
         233472 / kResident - 1024 - kMergeBytes - kSmallBytes - kQueryBytes;
-    static constexpr int kMaxStages = kRoom / (kWarps * kStageBytes);
-    static constexpr int kStages = kMaxStages > 6 ? 6 : kMaxStages;
+    static constexpr int kStages = kRoom / (kWarps * kStageBytes);
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
                                  kQueryBytes;
     static_assert(kStages >= 2, "no room for two stages");
