@@ -579,6 +579,33 @@ def test_attention_far_pages():
     ref.assert_close(lse, l_ref, lb, "lse")
 
 
+def test_attention_recorded_and_replayed_on_other_lengths():
+    """Many short sequences with cut items: eager calls on a workspace full of anything, then a
+    recorded call replayed while the lengths change under it."""
+    s = attn_inputs(torch.randint(300, 500, (60,), generator=generator(41)), 8, 2, 128, 16,
+                    torch.bfloat16, seed=41)
+    full = s["lens"].clone()
+    ws = g.paged_attention_workspace(8, 2, 128)
+    args = (s["q"], s["k_cache"], s["v_cache"], s["table"], s["lens"])
+    first = check_attn(s, "eager")
+    for fill in (0, 1, 255):
+        ws.fill_(fill)
+        for _ in range(20):
+            o, lse = g.paged_attention(*args, return_lse=True, workspace=ws)
+            assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = g.paged_attention(*args, return_lse=True, workspace=ws)
+    for cut in (0, 7, 290, 3):
+        s["lens"].copy_(full - cut)
+        s["lens"][cut % 60] = 0
+        want = g.paged_attention(*args, return_lse=True)
+        for _ in range(5):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 # ---- streams, graphs ---------------------------------------------------------------------------------
 
 def decode_layer(s, step, slots, norm, kc, vc, places, table, lens, ws, **kw):
