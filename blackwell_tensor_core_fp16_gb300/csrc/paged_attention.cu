@@ -32,7 +32,10 @@
 //     S^T[token][head] = K Q^T,     O^T[d][head] = V^T P^T.
 // For the second product each weight is carried as two 16-bit pieces (p0 = round(p), p1 =
 // round(p - p0)): one piece would lose as much as the rounding of the result itself where few
-// tokens share the weight, and the products are not what bounds the time.
+// tokens share the weight, and the products are not what bounds the time.  float16's weights are
+// carried times 2^15 (and the results divided by it), which leaves them above 2^-40 of the warp's
+// largest: unscaled, weights below 2^-25 vanished, and with them a long tail beside a token that
+// takes nearly all the weight and has little to give.
 #include <cstdint>
 #include <type_traits>
 
@@ -119,6 +122,10 @@ __device__ __forceinline__ float exp2_fast(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// What the weights of the second product are multiplied by, a power of two.
+template <typename T>
+constexpr float kWeight = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
 // ---- thread-block clusters: rank, barrier and reads of another block's shared memory
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -573,12 +580,12 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
-                    const float* v = s[x][j / 2] + j % 2 * 2;
-                    const uint32_t first = Half2<T>::pack(v[0], v[1]);
+                    const float v0 = s[x][j / 2][j % 2 * 2] * kWeight<T>;
+                    const float v1 = s[x][j / 2][j % 2 * 2 + 1] * kWeight<T>;
+                    const uint32_t first = Half2<T>::pack(v0, v1);
                     const float2 f = Half2<T>::unpack(first);
                     pb[x][j / 2][0][j % 2] = transpose8x8(first);
-                    pb[x][j / 2][1][j % 2] =
-                        transpose8x8(Half2<T>::pack(v[0] - f.x, v[1] - f.y));
+                    pb[x][j / 2][1][j % 2] = transpose8x8(Half2<T>::pack(v0 - f.x, v1 - f.y));
                 }
             }
 #pragma unroll
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     }
                 } else if (whole) {
                     const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
-                    const float inv = 1.f / sum;
+                    const float inv = 1.f / kWeight<T> / sum;
                     *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
                         Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
                     if (d == 0 && p.lse != nullptr)
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
             }
             const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
-            const float inv = 1.f / sum;
+            const float inv = 1.f / kWeight<T> / sum;
             *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
                 Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
             if (d == 0 && p.lse != nullptr)
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) paged_attention_join_kerne
             if (w != 0) continue;
         }
         const int64_t row = static_cast<int64_t>(item.z) * p.h_q + h0 + h;
-        const float inv = 1.f / sums.sum;
+        const float inv = 1.f / kWeight<T> / sums.sum;
         uint32_t* out = reinterpret_cast<uint32_t*>(p.o + row * D + lane * kOut);
 #pragma unroll
         for (int e = 0; e < kOut; e += 2)

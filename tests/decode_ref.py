@@ -80,8 +80,8 @@ def qk_norm_rope(x, w, norm, eps, positions, table, sections, interleaved):
 def paged_attention(q, k_cache, v_cache, table, lens, scale, window):
     """(o, lse, o's bound, lse's bound).  A score's error is at most es = (d + 4) 4 e sum |q K|
     scale (the tensor core's fp32 sums) plus 8 e of the score itself; a weight's relative error is
-    that, 2^-20 for the exponentials, and at most U / 2 for the 16-bit pieces that carry it (float16
-    loses at most 2^-25 of the largest weight); o mixes them with |V|."""
+    that, 2^-20 for the exponentials, and at most U / 2 for the 16-bit pieces that carry it (float16's,
+    scaled by 2^15, lose at most 2^-40 of the largest weight); o mixes them with |V|."""
     dt = q.dtype
     q, kc, vc = (x.double().cpu() for x in (q, k_cache, v_cache))
     n, h_q, d = q.shape
@@ -103,7 +103,7 @@ def paged_attention(q, k_cache, v_cache, table, lens, scale, window):
             lse[i, m] = torch.logsumexp(x, 0)
             p = torch.exp(x - lse[i, m])
             o[i, m] = p @ V
-            small = 2.0 ** -25 * float(p.max()) if dt == torch.float16 else 0.0
+            small = 2.0 ** -40 * float(p.max()) if dt == torch.float16 else 0.0
             ob[i, m] = (2 * es + 2.0 ** -20 + U[dt] / 2) * (p @ V.abs()) + small * V.abs().sum(0)
             lb[i, m] = es + 2.0 ** -20 + 4 * E * abs(float(lse[i, m]))
     return o, lse, ob, lb

@@ -485,6 +485,21 @@ def test_attention_flat_and_sharp(spread):
     check_attn(s, f"spread {spread}")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_small_weights_beside_large_ones(d, dtype):
+    """Every 16 tokens one outweighs the others e^18 to 1 and has a zero value: the results are the
+    others' values."""
+    s = attn_inputs([16, 100, 3001], 4, 2, d, 16, dtype, seed=d)
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    for c, fill in (("k_cache", 0.0), ("v_cache", 3e4)):
+        s[c][~s[c].isnan()] = fill
+    s["k_cache"][:, 5, :, 0] = 18.0
+    s["v_cache"][:, 5] = 0.0
+    check_attn(s, "sinks", scale=1.0)
+
+
 def test_attention_scores_of_minus_infinity():
     """A key of -infinity masks its token, as an additive mask written into the cache would; the
     weights of the others stay."""
