@@ -16,7 +16,7 @@
 // one; those two go to the workspace as (maximum, sum, output) and a second kernel joins each
 // item's parts in block order, the rest are written at once.  The order of every sum is fixed.
 // Two blocks of four warps an SM, so that one streams while the other begins or joins an item: 64
-// sequences of up to 8192 tokens, 8 key heads of 128, take 161 us, against 175 us with one block of
+// sequences of up to 8192 tokens, 8 key heads of 128, take 160 us, against 175 us with one block of
 // eight warps, whose SMs were busy 78% of the time on average; ranges four times finer than the
 // GPU holds blocks, which even the SMs out, take 167 us, their blocks' beginnings cost more.
 // Few items of few tiles, where the second kernel's launch would show, run as one thread-block
@@ -228,7 +228,7 @@ struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHeads = 8 * kHeadTiles;
     // a slice is 8 KB at least: for short rows the look-up, the maxima and the loop cost as much as
-    // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 29.5 us, 36 us with
+    // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 28.7 us, 36 us with
     // 16-token slices; more blocks an SM with fewer or smaller stages are no faster, 30 to 39 us)
     static constexpr int kSubs = D == 64 ? 2 : 1;
     static constexpr int kResident = 2;                       // blocks of an SM
@@ -457,6 +457,24 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
     float m[kHeadTiles][2], l[kHeadTiles][2];
     bool fresh = true;
     int stage = 0;
+    // the queries of an item (their loads are on their way while the item before is joined)
+    auto load_queries = [&](const Cursor& of) {
+        const int kv = of.item / p.head_items;
+        const int first = of.item % p.head_items * kHeads, heads = min(kHeads, p.group - first);
+        const uint16_t* q0 = p.q + of.i * p.q_stride[0] + (kv * p.group + first) * p.q_stride[1] +
+                             (lane & 3) * 2;
+#pragma unroll
+        for (int x = 0; x < kHeadTiles; ++x) {
+            const int h = x * 8 + (lane >> 2);
+            const uint16_t* row = q0 + h * p.q_stride[1];
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                qf[x][d][0] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16) : 0u;
+                qf[x][d][1] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16 + 8) : 0u;
+            }
+        }
+    };
+    if constexpr (!C::kQueriesShared) load_queries(cur);
     for (int t = t0; t < t1; ++t) {
         const int kv = cur.item / p.head_items, h0 = kv * p.group + (cur.item % p.head_items) * kHeads;
         const int heads = min(kHeads, (kv + 1) * p.group - h0);
@@ -476,18 +494,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
             }
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
-                const int h = x * 8 + (lane >> 2);
-                const uint16_t* row = p.q + cur.i * p.q_stride[0] + (h0 + h) * p.q_stride[1] +
-                                      (lane & 3) * 2;
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    if constexpr (!C::kQueriesShared) {
-                        qf[x][d][0] = h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16) : 0u;
-                        qf[x][d][1] =
-                            h < heads ? *reinterpret_cast<const uint32_t*>(row + d * 16 + 8) : 0u;
-                    }
+                for (int d = 0; d < D / 16; ++d)
                     acc[x][d][0] = acc[x][d][1] = acc[x][d][2] = acc[x][d][3] = 0.f;
-                }
                 m[x][0] = m[x][1] = -INFINITY;
                 l[x][0] = l[x][1] = 0.f;
             }
@@ -606,6 +615,10 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
 
         // ---- the item's end, or the range's: join the warps
         const bool item_ends = cur.tile + 1 == cur.tiles;
+        Cursor next = cur;
+        if (!kCluster && t + 1 < t1) advance<kTile>(next, p);
+        if constexpr (!kCluster && !C::kQueriesShared)
+            if (item_ends && t + 1 < t1) load_queries(next);
         if (item_ends || t + 1 == t1) {
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x)
@@ -683,7 +696,10 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
             __syncthreads();
             fresh = true;
         }
-        if (!kCluster || t + 1 < t1) advance<kTile>(cur, p);
+        if (!kCluster)
+            cur = next;
+        else if (t + 1 < t1)
+            ++cur.tile;
     }
     if constexpr (kCluster) {
         // ---- join the cluster's blocks, each an equal share of the elements
@@ -726,7 +742,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
 // block an item each warp joins heads of its own; with a block (x, y) for each head, which is for
 // few items of many parts, the block's warps share the head's parts out.  It is a chain of three
 // dependent loads (the list, maxima and sums, outputs), so each is issued for all parts at once.
-constexpr int kJoinWarps = 16;        // most warps of a block; 8 where an item has 64 parts at most
+constexpr int kJoinWarps = 16;        // most warps of a block, else 8
 
 // A warp's running join: its lanes hold D / 32 neighbouring outputs each.
 template <int D>
@@ -866,12 +882,13 @@ int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
     const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < most ? tiles : most);
     p.by_item = items <= kListedItems;
     p.join_shared = items <= kSharedItems;
-    // Few items of few tiles: a cluster an item, which joins its blocks' parts itself (one sequence
-    // of 500 tokens, 8 key heads: 5.5 us, 7.3 with the second kernel; of 2000 tokens 8.9 and 8.7).
+    // Few items of few tiles: a cluster an item, which joins its blocks' parts itself, as large as
+    // the GPU holds for all items, up to three tiles a block (8 key heads: one sequence of 500
+    // tokens 5.5 us, 7.3 with the second kernel; 16 of up to 250 tokens 6.6 and 8.1; one of 2000
+    // with four tiles a block 8.4 and 8.2).
     int ranks = 1;
-    if (per_item > 1 && per_item <= kClusterMost * kClusterTiles)
-        while (ranks < kClusterMost && ranks < per_item) ranks *= 2;
-    const bool cluster = ranks > 1 && items * ranks <= most;
+    while (ranks < kClusterMost && ranks < per_item && items * ranks * 2 <= most) ranks *= 2;
+    const bool cluster = ranks > 1 && per_item <= ranks * kClusterTiles;
     auto* kernel = cluster ? paged_attention_kernel<T, D, kHeadTiles, true>
                            : paged_attention_kernel<T, D, kHeadTiles, false>;
     static thread_local bool set[2][kMaxDevices] = {};
@@ -889,10 +906,12 @@ int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
         return fail(DECODE_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
     if (cluster || per_item <= 1 || blocks == 1) return DECODE_OK;     // no item is cut
     const int64_t most_parts = per_item < blocks ? per_item : blocks;
+    // (blocks of 16 warps need an SM each)
+    const int64_t heads = !p.join_shared ? 1 : p.group < C::kHeads ? p.group : C::kHeads;
+    const bool wide = p.join_shared && most_parts > 64 && items * heads <= sms;
     e = launch(paged_attention_join_kernel<T, D, kHeadTiles>,
-               dim3(p.by_item ? static_cast<uint32_t>(items) : blocks,
-                    !p.join_shared ? 1 : p.group < C::kHeads ? p.group : C::kHeads),
-               dim3((p.join_shared && most_parts > 64 ? kJoinWarps : 8) * 32), 0, stream, p);
+               dim3(p.by_item ? static_cast<uint32_t>(items) : blocks, static_cast<uint32_t>(heads)),
+               dim3((wide ? kJoinWarps : 8) * 32), 0, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "paged_attention_join_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;

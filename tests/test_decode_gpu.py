@@ -449,6 +449,16 @@ def test_attention_work_split(n, top):
     check_attn(attn_inputs(lens, 2, 1, 64, 16, torch.float16, seed=n), f"{n} sequences")
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [5, 25, 60, 150])
+def test_attention_clusters_of_each_size(n, d):
+    """Short sequences: items for clusters of eight, four and two blocks, and too many for any."""
+    top = {64: 128, 128: 64, 256: 32}[d] * (8 if n == 5 else 3)
+    lens = torch.randint(0, top, (n,), generator=generator(n + d))
+    lens[0], lens[-1] = top - 1, 0
+    check_attn(attn_inputs(lens, 6, 2, d, 16, torch.bfloat16, seed=n), f"{n} sequences")
+
+
 def test_attention_many_items_cut_across_blocks():
     """More items than the join lists one by one, of several tiles each, so that most blocks' ranges
     begin and end inside items; every seventh sequence is empty."""
