@@ -300,19 +300,25 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
 
 // Two warps a block for single tokens, so that few states spread over many SMs; four for several
 // tokens, whose staging they share (77 sequences of 4 tokens: 21.0 us, 21.7 with two).
+template <typename T, int kWarps, bool kMany>
+cudaError_t run(const StepParams& p, int64_t items, int sms, size_t smem, cudaStream_t stream)
+{
+    constexpr auto kKernel = gdn_step_kernel<T, kWarps, kMany>;
+    const int64_t blocks = items * (kD / (kWarpRows * kWarps));
+    const cudaError_t e = allow_spread<kKernel>();
+    if (e != cudaSuccess) return e;
+    return launch(kKernel, dim3(static_cast<uint32_t>(blocks)), dim3(kWarps * 32),
+                  spread(smem, blocks, sms, 16 / kWarps), stream, p);
+}
+
 template <typename T>
-cudaError_t run(const StepParams& p, int64_t items, cudaStream_t stream)
+cudaError_t run(const StepParams& p, int64_t items, int sms, cudaStream_t stream)
 {
     constexpr int kOne = 2, kSome = 4;
-    if (p.tokens == 1)
-        return launch(gdn_step_kernel<T, kOne, false>,
-                      dim3(static_cast<uint32_t>(items * (kD / (kWarpRows * kOne)))),
-                      dim3(kOne * 32), 0, stream, p);
+    if (p.tokens == 1) return run<T, kOne, false>(p, items, sms, 0, stream);
     const size_t smem = static_cast<size_t>(p.tokens < kStage ? p.tokens : kStage) *
                         Staged(p.queries, kWarpRows * kSome).total;
-    return launch(gdn_step_kernel<T, kSome, true>,
-                  dim3(static_cast<uint32_t>(items * (kD / (kWarpRows * kSome)))), dim3(kSome * 32),
-                  smem, stream, p);
+    return run<T, kSome, true>(p, items, sms, smem, stream);
 }
 
 }  // namespace
@@ -355,7 +361,8 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
         return fail(DECODE_ERR_UNSUPPORTED, "too many states or tokens for one call");
 
     p.status = status_word();
-    if (p.status == nullptr) return DECODE_ERR_CUDA;
+    const int sms = sm_count();
+    if (p.status == nullptr || sms == 0) return DECODE_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(a->q);
     p.k = static_cast<const uint16_t*>(a->k);
     p.v = static_cast<const uint16_t*>(a->v);
@@ -374,8 +381,8 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     p.n_slots = static_cast<int32_t>(a->n_slots);
     p.scale = a->scale;
     const int64_t items = a->n * a->h_v;
-    const cudaError_t e = a->dtype == DECODE_BF16 ? run<__nv_bfloat16>(p, items, stream)
-                                                  : run<__half>(p, items, stream);
+    const cudaError_t e = a->dtype == DECODE_BF16 ? run<__nv_bfloat16>(p, items, sms, stream)
+                                                  : run<__half>(p, items, sms, stream);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "gdn_step_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;

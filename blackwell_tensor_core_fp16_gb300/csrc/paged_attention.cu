@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     }
                     l[x][e] = fmaf(l[x][e], corr[e], sum);
                 }
-                if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
+                {
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
                         acc[x][d][0] *= corr[0];
@@ -895,13 +895,14 @@ int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && !(dev < kMaxDevices && set[cluster][dev])) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem > kSpreadMost ? C::kSmem : kSpreadMost);
         if (e == cudaSuccess && dev < kMaxDevices) set[cluster][dev] = true;
     }
+    const int64_t grid = cluster ? items * ranks : blocks;
     if (e == cudaSuccess)
-        e = cluster ? launch_cluster(kernel, dim3(static_cast<uint32_t>(items * ranks)),
-                                     dim3(C::kThreads), C::kSmem, stream, ranks, p)
-                    : launch(kernel, dim3(blocks), dim3(C::kThreads), C::kSmem, stream, p);
+        e = launch_cluster(kernel, dim3(static_cast<uint32_t>(grid)), dim3(C::kThreads),
+                           spread(C::kSmem, grid, sms, C::kResident), stream, cluster ? ranks : 1, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "paged_attention_kernel: %s", cudaGetErrorString(e));
     if (cluster || per_item <= 1 || blocks == 1) return DECODE_OK;     // no item is cut
