@@ -21,8 +21,11 @@
 // keys' few heads left lanes idle.)
 //
 // A token is a chain of dependent loads (position, then its row of the table), so the warps stay
-// for the whole call and load ahead: rows and angles go to shared memory by cp.async, three chunks
-// of four heads ahead of the work, and the tokens' indices are read one set of tokens earlier.
+// for the whole call and load ahead: rows and angles go to shared memory by cp.async, a chunk of
+// four heads ahead of the work, and the tokens' indices are read one set of tokens earlier.  Twenty
+// warps an SM with two stages each keep as much in flight as sixteen with four and hide more of
+// the instructions' latency, which bounds tokens of few heads: 38933 tokens of 6 + 2 heads take
+// 44.8 us (46.9), 2844 of 16 + 2 heads of 256 13.4 us (18.8).
 #include <cstdint>
 
 #include "decode_common.cuh"
@@ -32,9 +35,9 @@ namespace {
 using namespace decode;
 
 constexpr int kSteps = 4;             // heads of a chunk
-constexpr int kStages = 4;
+constexpr int kStages = 2;
 constexpr int kBlockWarps = 2;
-constexpr int kResident = 8;          // blocks of an SM
+constexpr int kResident = 10;         // blocks of an SM
 constexpr int kRowBytes = kSteps * 512;
 constexpr int kAngleBytes = 1024 + 32;   // the angles of a warp's tokens, and (valid, slot) of each
 constexpr int kWarpBytes = kStages * (kRowBytes + kAngleBytes);
@@ -469,13 +472,14 @@ cudaError_t run(NormParams p, int sms, cudaStream_t stream)
     p.sets = (p.tokens + kTokens - 1) / kTokens;
     // A warp takes whole sets, or, where there are few, parts of them: the number of parts for which
     // the warp with the most work has the least, a unit costing as much as two chunks beside its own.
-    // Two neighbouring warps share a set of ten chunks or more in any case: that brings the memory
-    // from 85% of the copy rate to 94% (32768 tokens of 32 + 8 heads, keys and values to a cache:
-    // 142 and 129 us; 24 + 8 heads 118 and 109 us; nine chunks, 28 + 4 heads, 107 both ways; six, 16
-    // + 4 heads, 70 and 88 us, since there the units' own cost shows).
+    // Neighbouring warps share a set of many chunks in any case, three from nine chunks on and two
+    // for eight, since fewer tokens at a time suit the memory: 32768 tokens, keys and values to a
+    // cache, with one, two and three warps a set take 151, 128 and 127 us (32 + 8 heads, 12 chunks),
+    // 110, 105 and 100 us (28 + 4, nine), 101, 89 and 91 us (16 + 8, eight), 69, 75 and 76 us (16 +
+    // 4, six, where the units' own cost shows).
     const int64_t most = static_cast<int64_t>(sms) * kResident, warps = most * kBlockWarps;
     int64_t least = INT64_MAX;
-    for (int32_t parts = p.all_chunks >= 10 ? 2 : 1; parts <= p.all_chunks; ++parts) {
+    for (int32_t parts = p.all_chunks >= 9 ? 3 : p.all_chunks >= 8 ? 2 : 1; parts <= p.all_chunks; ++parts) {
         const int64_t rounds = (static_cast<int64_t>(p.sets) * parts + warps - 1) / warps;
         const int64_t cost = rounds * ((p.all_chunks + parts - 1) / parts + 2);
         if (cost < least) {
@@ -485,9 +489,12 @@ cudaError_t run(NormParams p, int sms, cudaStream_t stream)
         if (rounds > 8) break;       // rounding up no longer matters
     }
     const int64_t blocks = (static_cast<int64_t>(p.sets) * p.parts + kBlockWarps - 1) / kBlockWarps;
-    return launch(qk_norm_rope_kernel<T, kLanes, kPairing>,
-                  dim3(static_cast<uint32_t>(blocks < most ? blocks : most)), dim3(kBlockWarps * 32),
-                  kBlockWarps * kWarpBytes, stream, p);
+    constexpr auto kKernel = qk_norm_rope_kernel<T, kLanes, kPairing>;
+    const cudaError_t e = allow_spread<kKernel>();
+    if (e != cudaSuccess) return e;
+    return launch(kKernel, dim3(static_cast<uint32_t>(blocks < most ? blocks : most)),
+                  dim3(kBlockWarps * 32), spread(kBlockWarps * kWarpBytes, blocks, sms, kResident),
+                  stream, p);
 }
 
 template <typename T, int kLanes>
