@@ -11,7 +11,7 @@
 // What bounds it.  A state is 65,536 bytes and a token adds about 1 KB to it, so with one token
 // the bytes of the states, read once and written once, are the floor: 256 sequences x 32 states
 // (1.08 GB) take 156 us, 6.9 TB/s, which is what a plain copy reaches; one sequence of 16 states
-// takes 2.6 us, its launch and two round trips to memory.  Each further token costs its 6 flops
+// takes 2.5 us, its launch and two round trips to memory.  Each further token costs its 6 flops
 // per element, on packed fp32 pairs: 151 sequences x 8 states take 28.5 us with 2 tokens (84% of
 // the copy rate), 34 us with 4 and 52 us with 8, the FMA pipes about 70% busy meanwhile.  (The
 // chunked form on mma.m16n8k16 with operands in three bfloat16 pieces was built and measured: 46

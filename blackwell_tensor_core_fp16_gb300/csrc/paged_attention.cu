@@ -578,14 +578,14 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     }
                     l[x][e] = fmaf(l[x][e], corr[e], sum);
                 }
-                {
+                // (always: a vote whether any maximum rose costs what it saves, 6.2 us against 5.9 for 39
+                // sequences of up to 299 tokens)
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        acc[x][d][0] *= corr[0];
-                        acc[x][d][1] *= corr[1];
-                        acc[x][d][2] *= corr[0];
-                        acc[x][d][3] *= corr[1];
-                    }
+                for (int d = 0; d < D / 16; ++d) {
+                    acc[x][d][0] *= corr[0];
+                    acc[x][d][1] *= corr[1];
+                    acc[x][d][2] *= corr[0];
+                    acc[x][d][3] *= corr[1];
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
