@@ -30,9 +30,11 @@
 // Both products put the tokens or the head dimension on the 16 rows of mma.m16n8k16 and the
 // query heads on its 8 columns, so up to 8 heads of a group cost no padding:
 //     S^T[token][head] = K Q^T,     O^T[d][head] = V^T P^T.
-// For the second product each weight is carried as two 16-bit pieces (p0 = round(p), p1 =
-// round(p - p0)): one piece would lose as much as the rounding of the result itself where few
-// tokens share the weight, and the products are not what bounds the time.  float16's weights are
+// For the second product each weight is carried as 16-bit pieces, three of bfloat16 or two of
+// float16 (p0 = round(p), p1 = round(p - p0), ...), which hold its 24 bits: with two pieces of
+// bfloat16 a result that is a small difference of large terms was off by up to 2^-17 of them, and
+// the third costs no time (64 sequences of up to 8192 tokens 161 us, 37 windows 28 us, with either),
+// since the products are not what bounds it.  float16's weights are
 // carried times 2^15 (and the results divided by it), which leaves them above 2^-40 of the warp's
 // largest: unscaled, weights below 2^-25 vanished, and with them a long tail beside a token that
 // takes nearly all the weight and has little to give.
@@ -123,6 +125,10 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// 16-bit pieces of a weight in the second product: what they leave out is less than the error of
+// the exponential itself (2^-22), three of bfloat16's 8 bits nothing, two of float16's 11 2^-23.
+template <typename T>
+constexpr int kPieces = std::is_same<T, __half>::value ? 2 : 3;
 // What the weights of the second product are multiplied by, a power of two.
 template <typename T>
 constexpr float kWeight = std::is_same<T, __half>::value ? 32768.f : 1.f;
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 const int pos = pos0 + j * 8 + (lane >> 2);
                 in[j] = pos >= cur.span.start && pos < cur.span.len;
             }
-            uint32_t pb[kHeadTiles][kSubs][2][2];  // [piece][tokens 0 .. 7, 8 .. 15]
+            uint32_t pb[kHeadTiles][kSubs][kPieces<T>][2];   // [piece][tokens 0 .. 7, 8 .. 15]
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
                 float corr[2];
@@ -589,12 +595,15 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
-                    const float v0 = s[x][j / 2][j % 2 * 2] * kWeight<T>;
-                    const float v1 = s[x][j / 2][j % 2 * 2 + 1] * kWeight<T>;
-                    const uint32_t first = Half2<T>::pack(v0, v1);
-                    const float2 f = Half2<T>::unpack(first);
-                    pb[x][j / 2][0][j % 2] = transpose8x8(first);
-                    pb[x][j / 2][1][j % 2] = transpose8x8(Half2<T>::pack(v0 - f.x, v1 - f.y));
+                    float v0 = s[x][j / 2][j % 2 * 2] * kWeight<T>;
+                    float v1 = s[x][j / 2][j % 2 * 2 + 1] * kWeight<T>;
+#pragma unroll
+                    for (int c = 0; c < kPieces<T>; ++c) {
+                        const uint32_t piece = Half2<T>::pack(v0, v1);
+                        const float2 f = Half2<T>::unpack(piece);
+                        pb[x][j / 2][c][j % 2] = transpose8x8(piece);
+                        v0 -= f.x, v1 -= f.y;
+                    }
                 }
             }
 #pragma unroll
@@ -605,10 +614,10 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     ldsm4_trans(a, vs + (y * kSub + (sel >> 1) * 8 + r) * (D * 2) +
                                        (((2 * d + (sel & 1)) ^ r) << 4));
 #pragma unroll
-                    for (int x = 0; x < kHeadTiles; ++x) {
-                        mma<T>(acc[x][d], a, pb[x][y][0][0], pb[x][y][0][1]);
-                        mma<T>(acc[x][d], a, pb[x][y][1][0], pb[x][y][1][1]);
-                    }
+                    for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                        for (int c = 0; c < kPieces<T>; ++c)
+                            mma<T>(acc[x][d], a, pb[x][y][c][0], pb[x][y][c][1]);
                 }
         }
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
