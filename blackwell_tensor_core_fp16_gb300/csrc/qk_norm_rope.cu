@@ -67,36 +67,12 @@ struct NormParams {
     float eps;
 };
 
-__device__ __forceinline__ uint64_t pair_of(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 halves(uint64_t x)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // The four 32-bit words of a lane's 8 elements, and their values as pairs.
 template <typename T>
 __device__ __forceinline__ uint64_t value2(uint32_t b)
 {
     const float2 f = Half2<T>::unpack(b);
-    return pair_of(f.x, f.y);
+    return pair(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t word(const uint4& b, int c)
 {
@@ -273,13 +249,13 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                 const bool weights = (kind == 0 ? p.q_weight : p.k_weight) != nullptr;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    mine[c] = weights ? value2<T>(word(wb, c)) : pair_of(1.f, 1.f);
+                    mine[c] = weights ? value2<T>(word(wb, c)) : pair(1.f, 1.f);
                     if constexpr (kPairing == kSplit) {
                         const uint32_t x = __shfl_sync(0xffffffffu, word(wb, c), partner);
-                        other[c] = weights ? value2<T>(x) : pair_of(1.f, 1.f);
+                        other[c] = weights ? value2<T>(x) : pair(1.f, 1.f);
                     } else if constexpr (kPairing == kInterleaved) {
                         const float2 f = halves(mine[c]);
-                        other[c] = pair_of(f.y, f.x);
+                        other[c] = pair(f.y, f.x);
                     }
                 }
                 if constexpr (kPairing == kSplit) {
@@ -290,24 +266,24 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                         for (int c = 0; c < 4; c += 2) {
                             const float4 x = *reinterpret_cast<const float4*>(cs + 2 * c);
                             const float4 y = *reinterpret_cast<const float4*>(cs + half + 2 * c);
-                            mine[c] = mul2(mine[c], pair_of(x.x, x.y));
-                            mine[c + 1] = mul2(mine[c + 1], pair_of(x.z, x.w));
-                            other[c] = mul2(other[c], pair_of(sign * y.x, sign * y.y));
-                            other[c + 1] = mul2(other[c + 1], pair_of(sign * y.z, sign * y.w));
+                            mine[c] = mul2(mine[c], pair(x.x, x.y));
+                            mine[c + 1] = mul2(mine[c + 1], pair(x.z, x.w));
+                            other[c] = mul2(other[c], pair(sign * y.x, sign * y.y));
+                            other[c + 1] = mul2(other[c + 1], pair(sign * y.z, sign * y.w));
                         }
                     }
                 } else if constexpr (kPairing == kInterleaved) {
                     if (in_rot) {
                         const float4 x = *reinterpret_cast<const float4*>(angles + e / 2);
                         const float4 y = *reinterpret_cast<const float4*>(angles + half + e / 2);
-                        mine[0] = mul2(mine[0], pair_of(x.x, x.x));
-                        mine[1] = mul2(mine[1], pair_of(x.y, x.y));
-                        mine[2] = mul2(mine[2], pair_of(x.z, x.z));
-                        mine[3] = mul2(mine[3], pair_of(x.w, x.w));
-                        other[0] = mul2(other[0], pair_of(-y.x, y.x));
-                        other[1] = mul2(other[1], pair_of(-y.y, y.y));
-                        other[2] = mul2(other[2], pair_of(-y.z, y.z));
-                        other[3] = mul2(other[3], pair_of(-y.w, y.w));
+                        mine[0] = mul2(mine[0], pair(x.x, x.x));
+                        mine[1] = mul2(mine[1], pair(x.y, x.y));
+                        mine[2] = mul2(mine[2], pair(x.z, x.z));
+                        mine[3] = mul2(mine[3], pair(x.w, x.w));
+                        other[0] = mul2(other[0], pair(-y.x, y.x));
+                        other[1] = mul2(other[1], pair(-y.y, y.y));
+                        other[2] = mul2(other[2], pair(-y.z, y.z));
+                        other[3] = mul2(other[3], pair(-y.w, y.w));
                     }
                 }
             }
@@ -351,7 +327,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                             sum += __shfl_xor_sync(0xffffffffu, sum, m);
                         f = rsqrtf(fmaf(sum, inv_d, p.eps));
                     }
-                    const uint64_t ff = pair_of(f, f);
+                    const uint64_t ff = pair(f, f);
                     [[maybe_unused]] uint4 z;
                     if constexpr (kPairing == kSplit) z = rows[s * 32 + partner];
                     uint32_t out[4];
@@ -362,7 +338,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kern
                             if (in_rot) y = fma2(value2<T>(word(z, c)), other[c], y);
                         } else if constexpr (kPairing == kInterleaved) {
                             const float2 v = halves(x[c]);
-                            if (in_rot) y = fma2(pair_of(v.y, v.x), other[c], y);
+                            if (in_rot) y = fma2(pair(v.y, v.x), other[c], y);
                         }
                         const float2 r = halves(mul2(y, ff));
                         out[c] = Half2<T>::pack(r.x, r.y);
@@ -454,7 +430,7 @@ __global__ void __launch_bounds__(kPlainWarps * 32) qk_norm_kernel(const NormPar
             uint32_t out[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint64_t y = mul2(x[c], pair_of(f, f));
+                uint64_t y = mul2(x[c], pair(f, f));
                 if (w != nullptr) y = mul2(y, value2<T>(word(wb, c)));
                 const float2 r = halves(y);
                 out[c] = Half2<T>::pack(r.x, r.y);
