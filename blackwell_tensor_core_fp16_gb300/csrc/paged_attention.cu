@@ -237,6 +237,9 @@ struct Cfg {
     // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 28.7 us, 36 us with
     // 16-token slices; more blocks an SM with fewer or smaller stages are no faster, 30 to 39 us)
     static constexpr int kSubs = D == 64 ? 2 : 1;
+    // sums of a slice's products: with one head tile of 256 the weights' lower pieces take turns with
+    // the first in a sum of their own (200001 tokens 75.1 us, 77.8 in one sum; other shapes no gain)
+    static constexpr int kSums = D == 256 && kHeadTiles == 1 ? 2 : 1;
     static constexpr int kResident = 2;                       // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
@@ -447,7 +450,10 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 }
             }
             ++pre_t;
-            advance<kTile>(pre, p);
+            if constexpr (kCluster)
+                ++pre.tile;
+            else
+                advance<kTile>(pre, p);
         }
         cp_commit();
         look_up();
@@ -555,9 +561,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 in[j] = pos >= cur.span.start && pos < cur.span.len;
             }
             uint32_t pb[kHeadTiles][kSubs][kPieces<T>][2];   // [piece][tokens 0 .. 7, 8 .. 15]
+            float corr[kHeadTiles][2];
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
-                float corr[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float top = -INFINITY;
@@ -573,7 +579,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     top = fmaxf(top, m[x][e]);
                     // scores of -infinity only: any finite reference leaves their weights 0
                     const float ref = top == -INFINITY ? 0.f : top;
-                    corr[e] = exp2_fast(m[x][e] - ref);
+                    corr[x][e] = exp2_fast(m[x][e] - ref);
                     m[x][e] = top;
                     float sum = 0.f;
 #pragma unroll
@@ -582,16 +588,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                         v = exp2_fast(v - ref);
                         sum += v;
                     }
-                    l[x][e] = fmaf(l[x][e], corr[e], sum);
-                }
-                // (always: a vote whether any maximum rose costs what it saves, 6.2 us against 5.9 for 39
-                // sequences of up to 299 tokens)
-#pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    acc[x][d][0] *= corr[0];
-                    acc[x][d][1] *= corr[1];
-                    acc[x][d][2] *= corr[0];
-                    acc[x][d][3] *= corr[1];
+                    l[x][e] = fmaf(l[x][e], corr[x][e], sum);
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
@@ -606,19 +603,46 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     }
                 }
             }
+            // The slice's products are summed on their own and added to the rescaled sums: a matrix
+            // product cuts its sum's last bits off, and over a long axis on one running sum the
+            // losses add up.  (Rescaling always: a vote whether any maximum rose costs what it
+            // saves, 6.2 us against 5.9 for 39 sequences of up to 299 tokens.)
+            constexpr int kAtOnce = 2;             // blocks of 16 elements whose sums take turns
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d)
+            for (int d0 = 0; d0 < D / 16; d0 += kAtOnce) {
+                float o[kAtOnce][kHeadTiles][C::kSums][4] = {};
 #pragma unroll
                 for (int y = 0; y < kSubs; ++y) {
-                    uint32_t a[4];
-                    ldsm4_trans(a, vs + (y * kSub + (sel >> 1) * 8 + r) * (D * 2) +
-                                       (((2 * d + (sel & 1)) ^ r) << 4));
+                    uint32_t a[kAtOnce][4];
+#pragma unroll
+                    for (int z = 0; z < kAtOnce; ++z)
+                        ldsm4_trans(a[z], vs + (y * kSub + (sel >> 1) * 8 + r) * (D * 2) +
+                                              (((2 * (d0 + z) + (sel & 1)) ^ r) << 4));
+#pragma unroll
+                    for (int c = 0; c < kPieces<T>; ++c)
+#pragma unroll
+                        for (int z = 0; z < kAtOnce; ++z)
+#pragma unroll
+                            for (int x = 0; x < kHeadTiles; ++x)
+                                mma<T>(o[z][x][c > 0 ? C::kSums - 1 : 0], a[z], pb[x][y][c][0],
+                                       pb[x][y][c][1]);
+                }
+#pragma unroll
+                for (int z = 0; z < kAtOnce; ++z)
 #pragma unroll
                     for (int x = 0; x < kHeadTiles; ++x)
 #pragma unroll
-                        for (int c = 0; c < kPieces<T>; ++c)
-                            mma<T>(acc[x][d], a, pb[x][y][c][0], pb[x][y][c][1]);
-                }
+                        for (int e = 0; e < 4; e += 2) {
+                            float* const sum = acc[x][d0 + z] + e;
+                            float2 add = make_float2(o[z][x][0][e], o[z][x][0][e + 1]);
+                            if constexpr (C::kSums == 2)
+                                add.x += o[z][x][1][e], add.y += o[z][x][1][e + 1];
+                            const float2 f = halves(fma2(pair(sum[0], sum[1]),
+                                                         pair(corr[x][0], corr[x][1]),
+                                                         pair(add.x, add.y)));
+                            sum[0] = f.x, sum[1] = f.y;
+                        }
+            }
         }
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
 

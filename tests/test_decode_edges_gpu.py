@@ -61,3 +61,29 @@ def test_attention_weights_keep_their_bits(lens, d, h_q, h_kv, dtype):
                                return_lse=True)
     ref.assert_close(o, o_ref, torch.full_like(o_ref, 24 * ref.E * 3.0), "o")
     ref.assert_close(lse, l_ref, 24 * ref.E * (1 + l_ref.abs()), "lse")
+
+
+@DTYPES
+def test_attention_long_sums_lose_nothing(dtype):
+    """A sequence a block, so that each warp adds up hundreds of slices, of values whose second half
+    undoes the first: the result is 0, and what is left of it is what the running sums lost.  With
+    P the sum of p |V| each of 512 additions rounds a sum of P / 4 on average by e at most, and a
+    slice's matrix products lose 12 e of their own sum: 144 e P in all.  (A running sum in the
+    matrix products, six of them a slice, loses about 0.75 e of P / 4 with each: 576 e P.)"""
+    n = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    page, d, length = 64, 64, 65536
+    gen = generator(101)
+    half = torch.zeros(length // 2, d)
+    half[:, 0] = torch.where(torch.arange(length // 2) % 16 == 0, 0.0,
+                             -torch.randint(1, 64, (length // 2,), generator=gen) / 64.0)
+    size = torch.randint(64, 128, (d,), generator=gen) / 32.0
+    value = torch.where(half[:, :1] == 0, 0.0, size)
+    cache = [torch.cat(x).view(-1, page, 1, d).to(dtype).cuda()
+             for x in ((half, half), (value, -value))]
+    q = torch.zeros(n, 1, d)
+    q[..., 0] = 2 + torch.randint(0, 64, (n, 1), generator=gen) / 32.0
+    table = torch.arange(length // page, dtype=torch.int32, device="cuda").expand(n, -1)
+    lens = torch.full((n,), length, dtype=torch.int32, device="cuda")
+    o = g.paged_attention(q.to(dtype).cuda(), *cache, table, lens, scale=0.25)
+    ref.assert_close(o, torch.zeros(n, 1, d, dtype=torch.float64),
+                     (144 * ref.E * size.double()).expand(n, 1, d), "o")
