@@ -31,7 +31,7 @@
 // query heads on its 8 columns, so up to 8 heads of a group cost no padding:
 //     S^T[token][head] = K Q^T,     O^T[d][head] = V^T P^T.
 // For the second product each weight is carried as 16-bit pieces, three of bfloat16 or two of
-// float16 (p0 = round(p), p1 = round(p - p0), ...), which hold its 24 bits: with two pieces of
+// float16 (each takes from p what the ones before left of it), which hold its 24 bits: with two pieces of
 // bfloat16 a result that is a small difference of large terms was off by up to 2^-17 of them, and
 // the third costs no time (64 sequences of up to 8192 tokens 161 us, 37 windows 28 us, with either),
 // since the products are not what bounds it.  float16's weights are
@@ -132,6 +132,37 @@ constexpr int kPieces = std::is_same<T, __half>::value ? 2 : 3;
 // What the weights of the second product are multiplied by, a power of two.
 template <typename T>
 constexpr float kWeight = std::is_same<T, __half>::value ? 32768.f : 1.f;
+
+// Takes piece c off a pair of weights.  An infinite value must come out infinite, so no piece of a
+// weight above 0 may be 0 or below it where it meets one.  bfloat16: each piece but the last is cut
+// off just below what is left of the weight (the product with 1 - 2^-23 takes a bit or two off), so
+// that some of it always stays for the next; the three still hold all 24 bits.  float16, whose
+// pieces run out of range first: the first piece is above 0, and the second's sums are cleared of
+// infinities, below.
+template <typename T>
+__device__ __forceinline__ uint32_t take_piece(float& v0, float& v1, int c)
+{
+    if constexpr (std::is_same<T, __half>::value) {
+        constexpr float kLeast = 5.9604645e-8f;          // 2^-24, the smallest number above 0
+        const float f0 = c == 0 && v0 > 0.f && v0 < kLeast ? kLeast : v0;
+        const float f1 = c == 0 && v1 > 0.f && v1 < kLeast ? kLeast : v1;
+        const uint32_t piece = Half2<T>::pack(f0, f1);
+        const float2 f = Half2<T>::unpack(piece);
+        v0 -= f.x, v1 -= f.y;
+        return piece;
+    } else {
+        if (c + 1 == kPieces<T>) return Half2<T>::pack(v0, v1);
+        const uint32_t b0 = __float_as_uint(v0 * 0.99999988f), b1 = __float_as_uint(v1 * 0.99999988f);
+        v0 -= __uint_as_float(b0 & 0xffff0000u), v1 -= __uint_as_float(b1 & 0xffff0000u);
+        return __byte_perm(b0, b1, 0x7632);
+    }
+}
+
+// x, or a finite number for an infinity or NaN.
+__device__ __forceinline__ float finite(float x)
+{
+    return fminf(fmaxf(x, -3.402823466e38f), 3.402823466e38f);
+}
 
 // ---- thread-block clusters: rank, barrier and reads of another block's shared memory
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -237,9 +268,12 @@ struct Cfg {
     // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 28.7 us, 36 us with
     // 16-token slices; more blocks an SM with fewer or smaller stages are no faster, 30 to 39 us)
     static constexpr int kSubs = D == 64 ? 2 : 1;
-    // sums of a slice's products: with one head tile of 256 the weights' lower pieces take turns with
-    // the first in a sum of their own (200001 tokens 75.1 us, 77.8 in one sum; other shapes no gain)
-    static constexpr int kSums = D == 256 && kHeadTiles == 1 ? 2 : 1;
+    // the weights' lower pieces have sums of their own: with one head tile of 256, where they take
+    // turns with the first piece's (bfloat16, 200001 tokens: 75.1 us, 77.8 in one sum; other shapes
+    // no gain), and for float16, whose lower pieces' sums are cleared of infinities
+    template <typename T>
+    static constexpr int kSums =
+        (D == 256 && kHeadTiles == 1) || std::is_same<T, __half>::value ? 2 : 1;
     static constexpr int kResident = 2;                       // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
@@ -595,12 +629,8 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     float v0 = s[x][j / 2][j % 2 * 2] * kWeight<T>;
                     float v1 = s[x][j / 2][j % 2 * 2 + 1] * kWeight<T>;
 #pragma unroll
-                    for (int c = 0; c < kPieces<T>; ++c) {
-                        const uint32_t piece = Half2<T>::pack(v0, v1);
-                        const float2 f = Half2<T>::unpack(piece);
-                        pb[x][j / 2][c][j % 2] = transpose8x8(piece);
-                        v0 -= f.x, v1 -= f.y;
-                    }
+                    for (int c = 0; c < kPieces<T>; ++c)
+                        pb[x][j / 2][c][j % 2] = transpose8x8(take_piece<T>(v0, v1, c));
                 }
             }
             // The slice's products are summed on their own and added to the rescaled sums: a matrix
@@ -610,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
             constexpr int kAtOnce = 2;             // blocks of 16 elements whose sums take turns
 #pragma unroll
             for (int d0 = 0; d0 < D / 16; d0 += kAtOnce) {
-                float o[kAtOnce][kHeadTiles][C::kSums][4] = {};
+                float o[kAtOnce][kHeadTiles][C::template kSums<T>][4] = {};
 #pragma unroll
                 for (int y = 0; y < kSubs; ++y) {
                     uint32_t a[kAtOnce][4];
@@ -624,7 +654,7 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                         for (int z = 0; z < kAtOnce; ++z)
 #pragma unroll
                             for (int x = 0; x < kHeadTiles; ++x)
-                                mma<T>(o[z][x][c > 0 ? C::kSums - 1 : 0], a[z], pb[x][y][c][0],
+                                mma<T>(o[z][x][c > 0 ? C::template kSums<T> - 1 : 0], a[z], pb[x][y][c][0],
                                        pb[x][y][c][1]);
                 }
 #pragma unroll
@@ -635,8 +665,11 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                         for (int e = 0; e < 4; e += 2) {
                             float* const sum = acc[x][d0 + z] + e;
                             float2 add = make_float2(o[z][x][0][e], o[z][x][0][e + 1]);
-                            if constexpr (C::kSums == 2)
+                            if constexpr (std::is_same<T, __half>::value) {
+                                add.x += finite(o[z][x][1][e]), add.y += finite(o[z][x][1][e + 1]);
+                            } else if constexpr (C::template kSums<T> == 2) {
                                 add.x += o[z][x][1][e], add.y += o[z][x][1][e + 1];
+                            }
                             const float2 f = halves(fma2(pair(sum[0], sum[1]),
                                                          pair(corr[x][0], corr[x][1]),
                                                          pair(add.x, add.y)));

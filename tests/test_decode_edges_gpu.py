@@ -87,3 +87,70 @@ def test_attention_long_sums_lose_nothing(dtype):
     o = g.paged_attention(q.to(dtype).cuda(), *cache, table, lens, scale=0.25)
     ref.assert_close(o, torch.zeros(n, 1, d, dtype=torch.float64),
                      (144 * ref.E * size.double()).expand(n, 1, d), "o")
+
+
+# ---- attention: infinities --------------------------------------------------------------------------
+
+def on_split_path(s, to=4096):
+    """The same call with a page table so wide that no cluster takes it (entries past a sequence's
+    pages are not read)."""
+    n, width = s["table"].shape
+    wide = torch.full((n, width + to // int(s["k_cache"].shape[1])), 2 ** 31 - 1, dtype=torch.int32,
+                      device="cuda")
+    wide[:, :width] = s["table"]
+    return dict(s, table=wide)
+
+
+def assert_as_defined(o, o_ref, bound, where):
+    """Infinities and NaN where the definition has them, the rest within its bound."""
+    x = o.double().cpu()
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(x), kind(o_ref)), f"{where}: {kind.__name__}"
+    rest = o_ref.isfinite()
+    ref.assert_close(o.cpu()[rest], o_ref[rest], bound[rest], where)
+
+
+@DTYPES
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (16, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_infinite_values(d, h_q, h_kv, dtype):
+    """An infinite cached value makes its element of the results infinite, whatever its weight and
+    its sign, two of opposite signs NaN, and nothing else changes; short sequences and long ones, on clusters
+    and on the split path, joined and not."""
+    s = attn_inputs([1, 40, 300, 3000, 9], h_q, h_kv, d, 16, dtype, seed=d + h_q)
+    place = lambda i, t: (s["table"][i, t // 16].long(), t % 16, 0)     # noqa: E731
+    inf = float("inf")
+    s["v_cache"][place(0, 0)][3], s["v_cache"][place(0, 0)][4] = inf, -inf
+    for i, t in ((1, 39), (2, 150), (3, 2999)):
+        s["v_cache"][place(i, t)][0] = inf
+        s["v_cache"][place(i, t)][1] = -inf
+        s["v_cache"][place(i, t)][2] = inf
+        s["v_cache"][place(i, t - 20)][2] = -inf
+    for case in (s, on_split_path(s)):
+        o_ref, l_ref, ob, lb = ref.paged_attention(case["q"], case["k_cache"], case["v_cache"],
+                                                   case["table"], case["lens"], d ** -0.5, None)
+        o, lse = g.paged_attention(case["q"], case["k_cache"], case["v_cache"], case["table"],
+                                   case["lens"], return_lse=True)
+        assert int(o_ref.isinf().sum()) == 8 * h_q // h_kv and int(o_ref.isnan().sum()) == 3 * h_q // h_kv
+        assert_as_defined(o, o_ref, ob, "o")
+        ref.assert_close(lse, l_ref, lb, "lse")
+
+
+@DTYPES
+def test_attention_infinite_values_of_small_weight(dtype):
+    """Weights of 2^-60 and 2^-100 of the largest still carry an infinite value."""
+    s = attn_inputs([1000, 33], 8, 2, 64, 16, dtype, seed=7)
+    s["q"].zero_()
+    s["q"][..., 0] = 1.0
+    s["k_cache"][~s["k_cache"].isnan()] = 0.0
+    for i, t, score in ((0, 5, -41.5), (0, 700, -69.5), (1, 20, -69.5)):
+        at = (s["table"][i, t // 16].long(), t % 16)
+        s["k_cache"][at][:, 0] = score
+        s["v_cache"][at][:, 9 + t % 2] = float("-inf")
+    for case in (s, on_split_path(s)):
+        o_ref, _, ob, _ = ref.paged_attention(case["q"], case["k_cache"], case["v_cache"],
+                                              case["table"], case["lens"], 1.0, None)
+        o = g.paged_attention(case["q"], case["k_cache"], case["v_cache"], case["table"],
+                              case["lens"], scale=1.0)
+        assert int(o_ref.isneginf().sum()) == 3 * 8
+        assert_as_defined(o, o_ref, ob, "o")
