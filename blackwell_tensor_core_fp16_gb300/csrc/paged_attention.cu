@@ -158,6 +158,19 @@ __device__ __forceinline__ uint32_t take_piece(float& v0, float& v1, int c)
     }
 }
 
+// What a row's sums are multiplied by, from the sum of its weights: 0 where every score is
+// -infinity; and two of its elements, which are then 0 whatever the values hold.
+template <typename T>
+__device__ __forceinline__ float factor_of(float sum)
+{
+    return sum == 0.f ? 0.f : 1.f / kWeight<T> / sum;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t result(float x, float y, float factor)
+{
+    return factor == 0.f ? 0u : Half2<T>::pack(x * factor, y * factor);
+}
+
 // x, or a finite number for an infinity or NaN.
 __device__ __forceinline__ float finite(float x)
 {
@@ -745,9 +758,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                     }
                 } else if (whole) {
                     const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
-                    const float inv = 1.f / kWeight<T> / sum;
+                    const float inv = factor_of<T>(sum);
                     *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
-                        Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
+                        result<T>(o.x, o.y, inv), result<T>(o.z, o.w, inv));
                     if (d == 0 && p.lse != nullptr)
                         p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
                 } else {
@@ -793,9 +806,9 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
                 o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
             }
             const int64_t row = static_cast<int64_t>(cur.i) * p.h_q + h0 + h;
-            const float inv = 1.f / kWeight<T> / sum;
+            const float inv = factor_of<T>(sum);
             *reinterpret_cast<uint2*>(p.o + row * D + d) = make_uint2(
-                Half2<T>::pack(o.x * inv, o.y * inv), Half2<T>::pack(o.z * inv, o.w * inv));
+                result<T>(o.x, o.y, inv), result<T>(o.z, o.w, inv));
             if (d == 0 && p.lse != nullptr)
                 p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
         }
@@ -908,11 +921,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 1) paged_attention_join_kerne
             if (w != 0) continue;
         }
         const int64_t row = static_cast<int64_t>(item.z) * p.h_q + h0 + h;
-        const float inv = 1.f / kWeight<T> / sums.sum;
+        const float inv = factor_of<T>(sums.sum);
         uint32_t* out = reinterpret_cast<uint32_t*>(p.o + row * D + lane * kOut);
 #pragma unroll
         for (int e = 0; e < kOut; e += 2)
-            out[e / 2] = Half2<T>::pack(sums.o[e] * inv, sums.o[e + 1] * inv);
+            out[e / 2] = result<T>(sums.o[e], sums.o[e + 1], inv);
         if (lane == 0 && p.lse != nullptr)
             p.lse[row] = (sums.top + log2f(sums.sum)) * 0.6931471805599453f;
     }

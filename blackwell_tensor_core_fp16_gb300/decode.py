@@ -158,9 +158,10 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, scale: float | None =
     q [n, h_q, d] float16 or bfloat16, d 64, 128 or 256; k_cache, v_cache [pages, page_size, h_kv,
     d] of the same type (any strides with a dense last dimension); page_table [n, width] int32:
     token t lies in page ``page_table[i, t // page_size]``; lens [n] int32.  scale: default
-    d ** -0.5.  A sequence of length 0 gives zeros and lse -inf.  Returns o [n, h_q, d], or (o,
-    lse [n, h_q] float32) with ``return_lse``.  ``workspace``: from ``paged_attention_workspace``;
-    None takes one from torch's allocator for the call."""
+    d ** -0.5.  A sequence of length 0, or all of whose scores are -infinity, gives zeros and lse
+    -inf.  Returns o [n, h_q, d], or (o, lse [n, h_q] float32) with ``return_lse``.
+    ``workspace``: from ``paged_attention_workspace``; None takes one from torch's allocator for the
+    call."""
     return _decode.paged_attention(q, k_cache, v_cache, page_table, lens, scale, window, return_lse,
                                    out, workspace, stream)
 

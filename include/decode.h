@@ -169,7 +169,8 @@ int decode_qk_norm_rope(const decode_qk_norm_rope_args* args, cudaStream_t strea
  *
  *     s_t = scale q . K_t;   lse = log sum_t exp(s_t);   o = sum_t exp(s_t - lse) V_t
  *
- * A sequence of length 0 gives o = 0 and lse = -infinity.
+ * A sequence of length 0 gives o = 0 and lse = -infinity, and so does a query whose every score is
+ * -infinity.
  *
  *   q             [n][h_q][head_dim], strides of the first two dimensions
  *   k_cache, v_cache     [pages][page_size][h_kv][head_dim], strides of the first three

@@ -154,3 +154,29 @@ def test_attention_infinite_values_of_small_weight(dtype):
                               case["lens"], scale=1.0)
         assert int(o_ref.isneginf().sum()) == 3 * 8
         assert_as_defined(o, o_ref, ob, "o")
+
+
+@DTYPES
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("h_q,h_kv", [(4, 2), (16, 1)])
+def test_attention_every_score_minus_infinity(h_q, h_kv, d, dtype):
+    """A sequence whose every score is -infinity has the result of an empty one, whatever its values
+    hold, beside sequences that go on as ever: in clusters, in blocks of their own, and joined."""
+    s = attn_inputs([1, 40, 40, 300, 3000, 3000, 17], h_q, h_kv, d, 16, dtype, seed=d + h_q)
+    s["q"].abs_().clamp_(min=0.01)
+    for i in (0, 2, 5):
+        tok = torch.arange(int(s["lens"][i]), device="cuda")
+        pg = s["table"][i].long()[tok // 16]
+        s["k_cache"][pg, tok % 16, :, 1] = float("-inf")
+        s["v_cache"][pg[0], 0, :, 0] = float("inf")
+    kept = [1, 3, 4, 6]
+    for case in (s, on_split_path(s)):
+        o_ref, l_ref, ob, lb = ref.paged_attention(case["q"][kept], case["k_cache"],
+                                                   case["v_cache"], case["table"][kept],
+                                                   case["lens"][kept], d ** -0.5, None)
+        o, lse = g.paged_attention(case["q"], case["k_cache"], case["v_cache"], case["table"],
+                                   case["lens"], return_lse=True)
+        for i in (0, 2, 5):
+            assert bool((o[i] == 0).all()) and bool((lse[i] == float("-inf")).all()), i
+        ref.assert_close(o[kept], o_ref, ob, "o")
+        ref.assert_close(lse[kept], l_ref, lb, "lse")
