@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/decode.h"
+#include "overlap.h"
 
 namespace decode {
 
@@ -99,6 +100,14 @@ bool take_strides(int64_t (&to)[N], const int64_t (&from)[N], const int64_t (&si
         ok = ok && to[d] % of == 0;
     }
     return ok;
+}
+
+// Refuses a call in which a written operand shares memory with another one.
+inline int refuse_shared(std::initializer_list<Operand> written, std::initializer_list<Operand> read)
+{
+    const char *one = nullptr, *other = nullptr;
+    if (!find_shared(written, read, one, other)) return DECODE_OK;
+    return fail(DECODE_ERR_INVALID_ARG, "%s shares memory with %s", one, other);
 }
 
 inline bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }

@@ -333,6 +333,24 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
         a->n_slots >= (int64_t(1) << 31))
         return fail(DECODE_ERR_UNSUPPORTED, "too many states or tokens for one call");
 
+    // the blocks of a state read all of its q and k while others write their rows of o (of v each
+    // reads just the rows that it writes)
+    const int64_t h_o = queries > 1 ? a->h_q : a->h_v;
+    const int64_t dense[3] = {a->tokens * h_o * kD, h_o * kD, kD};
+    const int64_t gates[3] = {a->n, a->tokens, a->h_v};
+    const int64_t alpha[3] = {p.alpha_stride[0], p.alpha_stride[1], 1};
+    const int64_t beta[3] = {p.beta_stride[0], p.beta_stride[1], 1};
+    const int shared = refuse_shared(
+        {{"o", a->o, 2, kD, {a->n, a->tokens, h_o}, dense, "v"},
+         {"state", a->state, 4, a->h_v * kD * kD, {a->n_slots}, {a->state_stride}}},
+        {{"q", a->q, 2, kD, {a->n, a->tokens, a->h_q}, p.q_stride},
+         {"k", a->k, 2, kD, {a->n, a->tokens, a->h_k}, p.k_stride},
+         {"v", a->v, 2, kD, {a->n, a->tokens, a->h_v}, p.v_stride},
+         {"alpha", a->alpha, 4, 1, gates, alpha},
+         {"beta", a->beta, 4, 1, gates, beta},
+         {"slots", a->slots, 4, a->n}});
+    if (shared != DECODE_OK) return shared;
+
     p.status = status_word();
     const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return DECODE_ERR_CUDA;
@@ -347,7 +365,7 @@ extern "C" int decode_gdn_step(const decode_gdn_step_args* a, cudaStream_t strea
     p.state_stride = a->n_slots > 1 ? a->state_stride : 0;
     p.tokens = static_cast<int32_t>(a->tokens);
     p.h_v = static_cast<int32_t>(a->h_v);
-    p.h_o = static_cast<int32_t>(queries > 1 ? a->h_q : a->h_v);
+    p.h_o = static_cast<int32_t>(h_o);
     p.kgroup = static_cast<int32_t>(a->h_v / a->h_k);
     p.qgroup = a->h_q == a->h_k ? p.kgroup : 1;
     p.queries = static_cast<int32_t>(queries);

@@ -1068,6 +1068,19 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     const Layout l = layout_for(sms, heads, a->head_dim);
     if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < l.total)
         return fail(DECODE_ERR_INVALID_ARG, "workspace of %zu bytes needed", l.total);
+    // (an item's queries are in registers or shared memory, in all of its blocks, before its results
+    // are written)
+    const int64_t d = a->head_dim, sizes[2] = {a->n, a->h_q}, dense[2] = {a->h_q * d, d};
+    const int shared = refuse_shared(
+        {{"o", a->o, 2, d, sizes, dense, "q"},
+         {"lse", a->lse, 4, a->n * a->h_q},
+         {"workspace", a->workspace, 1, static_cast<int64_t>(l.total)}},
+        {{"q", a->q, 2, d, sizes, p.q_stride},
+         {"k_cache", a->k_cache, 2, d, cs, p.k_stride},
+         {"v_cache", a->v_cache, 2, d, cs, p.v_stride},
+         {"page_table", a->page_table, 4, a->table_width, {a->n}, {a->table_stride}},
+         {"lens", a->lens, 4, a->n}});
+    if (shared != DECODE_OK) return shared;
     // lengths are 32-bit: a table that could hold more holds no more than that (and the last
     // tile's positions stay below 2^31)
     int64_t max_len = a->pages == 0 ? 0 : a->page_size * a->table_width;

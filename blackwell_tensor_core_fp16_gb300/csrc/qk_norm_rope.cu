@@ -563,6 +563,24 @@ extern "C" int decode_qk_norm_rope(const decode_qk_norm_rope_args* a, cudaStream
         a->tokens >= (int64_t(1) << 31) / (a->h_q + 2 * a->h_k))
         return fail(DECODE_ERR_UNSUPPORTED, "too many tokens or heads for one call");
 
+    // (a head of q or k is read by the lanes that write it, before they do)
+    const int64_t d = a->head_dim, q_sizes[2] = {a->tokens, a->h_q}, k_sizes[2] = {a->tokens, a->h_k};
+    const int shared = refuse_shared(
+        {{"q_out", a->q_out, 2, d, q_sizes, p.q_out_stride, "q"},
+         {"k_out", cache ? nullptr : a->k_out, 2, d, k_sizes, p.k_out_stride, "k"},
+         {"k_cache", a->k_cache, 2, d, cs, p.k_cache_stride},
+         {"v_cache", a->v_cache, 2, d, cs, p.v_cache_stride}},
+        {{"q", a->q, 2, d, q_sizes, p.q_stride},
+         {"k", a->k, 2, d, k_sizes, p.k_stride},
+         {"v", a->v, 2, d, k_sizes, p.v_stride},
+         {"q_weight", a->q_weight, 2, d},
+         {"k_weight", a->k_weight, 2, d},
+         {"positions", a->rot > 0 ? a->positions : nullptr, 4, a->tokens, {a->axes},
+          {a->position_stride}},
+         {"table", a->table, 4, a->table_rows * a->rot},
+         {"slots", a->slots, 4, a->tokens}});
+    if (shared != DECODE_OK) return shared;
+
     p.status = status_word();
     const int sms = sm_count();
     if (p.status == nullptr || sms == 0) return DECODE_ERR_CUDA;

@@ -99,7 +99,8 @@ def gated_delta_step(q, k, v, alpha, beta, state, scale: float, slots=None, out=
     beta [n, tokens, h_v] float32; state [slots, h_v, 128, 128] float32, updated in place, in the
     layout of ``gated_delta_rule``'s final_state; slots [n] int32 or None for 0 .. n - 1.  Heads as
     in ``gated_delta_rule``.  A sequence with slot -1 is inactive: its output is zero and no state
-    changes.  No two sequences may share a slot.  Returns o [n, tokens, max(h_q, h_v), 128]."""
+    changes.  No two sequences may share a slot.  Returns o [n, tokens, max(h_q, h_v), 128]; ``out``
+    may be ``v`` itself but share no other memory with the operands."""
     return _decode.gated_delta_step(q, k, v, alpha, beta, state, scale, slots, out, stream)
 
 
@@ -129,7 +130,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: flo
     With ``k_cache`` and ``v_cache`` [pages, page_size, h_k, d] (any strides with a dense last
     dimension), ``v`` [tokens, h_k, d] and ``slots`` int32 [tokens] (page * page_size + offset, or -1
     for none) the keys and values go to the cache and only q is returned in the pair (q, None);
-    else the pair is (q, k).  ``q_out`` and ``k_out`` may be ``q`` and ``k`` themselves."""
+    else the pair is (q, k).  ``q_out`` and ``k_out`` may be ``q`` and ``k`` themselves; what is written
+    may share no other memory with the operands."""
     if norm not in DECODE_NORMS:
         raise ValueError(f"norm must be one of {sorted(DECODE_NORMS)}")
     return _decode.qk_norm_rope(q, k, q_weight, k_weight, DECODE_NORMS[norm], eps, positions, rotary,
@@ -161,7 +163,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, scale: float | None =
     d ** -0.5.  A sequence of length 0, or all of whose scores are -infinity, gives zeros and lse
     -inf.  Returns o [n, h_q, d], or (o, lse [n, h_q] float32) with ``return_lse``.
     ``workspace``: from ``paged_attention_workspace``; None takes one from torch's allocator for the
-    call."""
+    call.  ``out`` may be ``q`` itself; what is written may share no other memory with the operands."""
     return _decode.paged_attention(q, k_cache, v_cache, page_table, lens, scale, window, return_lse,
                                    out, workspace, stream)
 

@@ -14,16 +14,19 @@
  * fp32 and each 16-bit result is rounded once.  Strides are in elements; the innermost dimension
  * (head_dim) is dense, other strides of 16-bit tensors are multiples of 8 (rows are read 16 bytes at
  * a time), and pointers are 16-byte aligned; the stride of a dimension of one element is ignored.
- * Inputs may have any such stride, zero included; a written tensor's elements must not overlap.  Buffers belong to the caller and nothing is retained.
+ * Inputs may have any such stride, zero included; a written tensor's elements must not overlap, and
+ * a written tensor that shares memory with another operand is refused, but where an operation says
+ * that it may be an input itself.  Buffers belong to the caller and nothing is retained.
  * Calls are asynchronous on `stream` in stream order, enqueue kernel launches only (no allocation,
  * copy or synchronisation; they may be recorded into a CUDA graph once one call has run on the
  * device) and use programmatic dependent launch: every kernel waits for all earlier work on the
  * stream before it touches memory.  An empty problem (no sequence, no token) does nothing.
  *
  * Errors: DECODE_ERR_INVALID_ARG (null pointer, negative size, head counts that form no group,
- * unknown dtype or option, workspace too small), DECODE_ERR_UNSUPPORTED (head_dim, strides or
- * alignment the kernels do not have, a problem too large for one launch), DECODE_ERR_CUDA (a launch
- * failed).  Nothing is enqueued on an error; decode_last_error() says why.
+ * unknown dtype or option, workspace too small, operands that share memory),
+ * DECODE_ERR_UNSUPPORTED (head_dim, strides or alignment the kernels do not have, a problem too large
+ * for one launch), DECODE_ERR_CUDA (a launch failed).  Nothing is enqueued on an error;
+ * decode_last_error() says why.
  *
  * Indices that live in device memory (state slots, cache slots, positions, page numbers, lengths)
  * cannot be checked on the host.  The kernels check each one: an index outside its range touches no
@@ -76,7 +79,8 @@ extern "C" {
  *                 inactive sequence: no state is touched and its outputs are zero.  A slot outside
  *                 the pool is refused the same way and reported.  No two sequences of a call may
  *                 share a slot.
- *   o             [n][tokens][h_o][128], dense, 16 bits (written; h_o = max(h_q, h_v))
+ *   o             [n][tokens][h_o][128], dense, 16 bits (written; h_o = max(h_q, h_v)).  It may be v
+ *                 itself where that has the same shape and is dense
  */
 typedef struct {
     const void* q;
@@ -177,7 +181,7 @@ int decode_qk_norm_rope(const decode_qk_norm_rope_args* args, cudaStream_t strea
  *   page_table    int32 [n][table_width], table_stride between rows; entries past a sequence's
  *                 length are not read
  *   lens          int32 [n]
- *   o             [n][h_q][head_dim], dense, 16 bits (written)
+ *   o             [n][h_q][head_dim], dense, 16 bits (written).  It may be q itself where that is dense
  *   lse           float [n][h_q], dense, or NULL (written)
  *   workspace     decode_paged_attention_workspace_bytes() bytes, 16-byte aligned; it needs no
  *                 initialisation, and calls that may overlap on the GPU need one each

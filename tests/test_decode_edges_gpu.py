@@ -8,8 +8,8 @@ import torch
 
 import blackwell_tensor_core_fp16_gb300 as g
 import decode_ref as ref
-from test_decode_gpu import (attn_inputs, cuda_library, generator, no_refusals_left,  # noqa: F401
-                             normal)
+from test_decode_gpu import (attn_inputs, cache_pair, cuda_library, generator,  # noqa: F401
+                             no_refusals_left, norm_call, norm_inputs, normal, step_inputs)
 
 pytestmark = pytest.mark.gpu
 DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
@@ -180,3 +180,150 @@ def test_attention_every_score_minus_infinity(h_q, h_kv, d, dtype):
             assert bool((o[i] == 0).all()) and bool((lse[i] == float("-inf")).all()), i
         ref.assert_close(o[kept], o_ref, ob, "o")
         ref.assert_close(lse[kept], l_ref, lb, "lse")
+
+
+# ---- operands that share memory ---------------------------------------------------------------------
+
+def test_step_refuses_outputs_that_share_memory():
+    s, slots = step_inputs(3, 2, 2, 2, 2, torch.bfloat16, seed=70)
+    args = [s[x] for x in ("q", "k", "v", "alpha", "beta", "state")]
+    before = {x: y.clone() for x, y in s.items()}
+
+    def refused(out=None, **change):
+        with pytest.raises(g.GemmError, match="shares memory"):
+            g.gated_delta_step(*(change.get(x, y) for x, y in zip(
+                ("q", "k", "v", "alpha", "beta", "state"), args)), 0.5, slots, out=out)
+
+    refused(out=s["q"])
+    refused(out=s["k"])
+    flat = torch.zeros(3 * 2 * 2 * 128 + 128, dtype=torch.bfloat16, device="cuda")
+    shape = (3, 2, 2, 128)
+    refused(out=flat[:-128].view(shape), q=flat[128:].view(shape))
+    refused(out=flat[:-128].view(shape), v=flat[128:].view(shape))
+    half = s["state"].view(torch.bfloat16).flatten()
+    refused(out=half[:3 * 2 * 2 * 128].view(shape))
+    refused(v=half[:3 * 2 * 2 * 128].view(shape))
+    refused(beta=s["state"].flatten()[:12].view(3, 2, 2))
+    torch.cuda.synchronize()
+    for x, y in before.items():
+        assert torch.equal(s[x], y), x
+
+
+@pytest.mark.parametrize("tokens", [1, 4, 11])
+def test_step_writes_over_its_values(tokens):
+    """``out`` may be ``v`` itself, and lie beside the inputs in one buffer."""
+    s, slots = step_inputs(5, tokens, 4, 4, 4, torch.float16, seed=71)
+    args = [s[x] for x in ("q", "k", "v", "alpha", "beta")]
+    state = s["state"].clone()
+    want = g.gated_delta_step(*args, state, 0.5, slots)
+    again = s["state"].clone()
+    v = s["v"].clone()
+    got = g.gated_delta_step(*args[:2], v, *args[3:], again, 0.5, slots, out=v)
+    assert got.data_ptr() == v.data_ptr()
+    assert torch.equal(got, want) and torch.equal(again, state)
+    both = torch.zeros(2, 5, tokens, 4, 128, dtype=torch.float16, device="cuda")
+    both[0] = s["q"]
+    again = s["state"].clone()
+    got = g.gated_delta_step(both[0], *args[1:], again, 0.5, slots, out=both[1])
+    assert torch.equal(got, want) and torch.equal(again, state)
+
+
+def test_norm_refuses_outputs_that_share_memory():
+    s = norm_inputs(6, 2, 2, 128, 128, 1, torch.bfloat16, seed=72)
+    kc, vc = cache_pair(2, 8, 2, 128, torch.bfloat16, "tokens")
+    slots = torch.arange(6, dtype=torch.int32, device="cuda")
+    before = {x: s[x].clone() for x in ("q", "k", "v", "rotary", "positions", "q_weight")}
+
+    def refused(**kw):
+        with pytest.raises(g.GemmError, match="shares memory"):
+            g.qk_norm_rope(**{**dict(q=s["q"], k=s["k"], q_weight=s["q_weight"],
+                                     k_weight=s["k_weight"], positions=s["positions"],
+                                     rotary=s["rotary"]), **kw})
+
+    refused(q_out=s["k"])
+    refused(k_out=s["q"])
+    refused(q_out=s["q"], k_out=s["q"])
+    same = torch.zeros(6, 2, 128, dtype=torch.bfloat16, device="cuda")
+    refused(q_out=same, k_out=same)
+    packed = torch.zeros(7, 2, 128, dtype=torch.bfloat16, device="cuda")
+    refused(q=packed[1:], q_out=packed[:6])                    # q shifted by a token
+    wide = torch.zeros(6, 5, 128, dtype=torch.bfloat16, device="cuda")
+    refused(q=wide[:, :2], k=wide[:, 2:4], q_out=wide[:, 1:3])  # heads of both
+    cache = dict(v=s["v"], k_cache=kc, v_cache=vc, slots=slots)
+    refused(**{**cache, "v_cache": kc})
+    refused(**{**cache, "q": kc[0, :6]})
+    refused(**{**cache, "v": vc[1, 2:]})
+    refused(**cache, q_out=vc[0, :6])
+    refused(**{**cache, "slots": kc.view(torch.int32).flatten()[:6]})
+    torch.cuda.synchronize()
+    assert bool(kc.isnan().all()) and bool(vc.isnan().all())
+    for x, y in before.items():
+        assert torch.equal(s[x], y), x
+
+
+@pytest.mark.parametrize("layout", ["one buffer", "heads beside each other", "pages beside each other"])
+def test_norm_takes_caches_and_projections_that_only_lie_between_each_other(layout):
+    """Views that interleave without sharing an element are no overlap: a projection's queries,
+    keys and values normed in place, and the two caches as parts of one tensor."""
+    tokens, h_q, h_k, d = 9, 4, 2, 64
+    s = norm_inputs(tokens, h_q, h_k, d, d, 1, torch.bfloat16, seed=73)
+    if layout == "one buffer":
+        kc, vc = torch.zeros(2, 3, 4, h_k, d, dtype=torch.bfloat16, device="cuda")
+    elif layout == "heads beside each other":
+        both = torch.zeros(3, 4, h_k, 2 * d, dtype=torch.bfloat16, device="cuda")
+        kc, vc = both[..., :d], both[..., d:]
+    else:
+        both = torch.zeros(3, h_k, 2, 4, d, dtype=torch.bfloat16, device="cuda")
+        kc, vc = both[:, :, 0].transpose(1, 2), both[:, :, 1].transpose(1, 2)
+    packed = torch.cat([s["q"], s["k"], s["v"]], 1)
+    q, k, v = packed[:, :h_q], packed[:, h_q:h_q + h_k], packed[:, h_q + h_k:]
+    slots = torch.randperm(12, generator=generator(74))[:tokens].to(torch.int32).cuda()
+    want_q, want_k = norm_call(s)
+    got, _ = g.qk_norm_rope(q, k, s["q_weight"], s["k_weight"], positions=s["positions"],
+                            rotary=s["rotary"], v=v, k_cache=kc, v_cache=vc, slots=slots, q_out=q)
+    assert torch.equal(packed[:, :h_q], want_q) and got.data_ptr() == packed.data_ptr()
+    at = slots.long()
+    assert torch.equal(kc[at // 4, at % 4], want_k)
+    assert torch.equal(vc[at // 4, at % 4], s["v"])
+
+
+def test_attention_refuses_outputs_that_share_memory():
+    s = attn_inputs([50, 60, 300], 4, 2, 128, 16, torch.bfloat16, seed=75)
+    kept = {x: y.clone() for x, y in s.items()}
+
+    def refused(**kw):
+        with pytest.raises(g.GemmError, match="shares memory"):
+            g.paged_attention(**{**dict(q=s["q"], k_cache=s["k_cache"], v_cache=s["v_cache"],
+                                        page_table=s["table"], lens=s["lens"]), **kw})
+
+    refused(out=s["v_cache"].flatten()[:3 * 4 * 128].view(3, 4, 128))
+    refused(out=s["k_cache"].flatten()[-3 * 4 * 128:].view(3, 4, 128))
+    flat = torch.zeros(4 * 4 * 128, dtype=torch.bfloat16, device="cuda")
+    refused(q=flat[128:128 * 13].view(3, 4, 128), out=flat[:128 * 12].view(3, 4, 128))
+    size = g.paged_attention_workspace(4, 2, 128).numel()
+    room = torch.zeros(size + 8192, dtype=torch.uint8, device="cuda")
+    refused(workspace=room, out=room[:3072].view(torch.bfloat16).view(3, 4, 128))
+    refused(workspace=room, q=room[4096:4096 + 3072].view(torch.bfloat16).view(3, 4, 128))
+    torch.cuda.synchronize()
+    for x, y in kept.items():
+        assert torch.equal(s[x].view(torch.uint8), y.view(torch.uint8)), x    # (NaN among them)
+    # what lies behind the bytes that a workspace needs is not part of it
+    out = room[size + 256:size + 256 + 3072].view(torch.bfloat16).view(3, 4, 128)
+    assert out.data_ptr() % 16 == 0
+    got = g.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["table"], s["lens"], out=out,
+                            workspace=room)
+    assert torch.equal(got, g.paged_attention(s["q"], s["k_cache"], s["v_cache"], s["table"],
+                                              s["lens"]))
+
+
+@pytest.mark.parametrize("h_q,h_kv,d", [(4, 2, 128), (16, 1, 256), (12, 12, 64)])
+@pytest.mark.parametrize("lens", [[50, 0, 300, 5000], [100] * 200, [33]], ids=["few", "many", "one"])
+def test_attention_writes_over_its_queries(lens, h_q, h_kv, d):
+    """``out`` may be ``q`` itself: a query is read before its result is written."""
+    s = attn_inputs(lens, h_q, h_kv, d, 16, torch.bfloat16, seed=76)
+    for case in (s, on_split_path(s)):
+        args = [case[x] for x in ("k_cache", "v_cache", "table", "lens")]
+        want = g.paged_attention(case["q"], *args)
+        q = case["q"].clone()
+        got = g.paged_attention(q, *args, out=q)
+        assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
