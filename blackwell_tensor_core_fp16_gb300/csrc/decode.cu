@@ -10,6 +10,26 @@ namespace {
 thread_local std::string t_error;
 __device__ uint32_t d_status;
 
+// Reads and clears a status word in one step, so that a bit that another stream sets meanwhile
+// is either in `to` or still in the word.
+__global__ void take_status_kernel(uint32_t* word, uint32_t* to) { *to = atomicExch(word, 0u); }
+
+// A word of pinned host memory, one for each thread.
+struct HostWord {
+    uint32_t* p = nullptr;
+    ~HostWord()
+    {
+        if (p != nullptr) cudaFreeHost(p);
+    }
+    cudaError_t get(uint32_t*& to)
+    {
+        cudaError_t e = cudaSuccess;
+        if (p == nullptr) e = cudaHostAlloc(reinterpret_cast<void**>(&p), sizeof(*p), cudaHostAllocPortable);
+        to = p;
+        return e;
+    }
+};
+
 }  // namespace
 
 namespace decode {
@@ -70,14 +90,28 @@ int decode_check_status(cudaStream_t stream, uint32_t* bits)
     decode::clear_error();
     if (bits == nullptr) return decode::fail(DECODE_ERR_INVALID_ARG, "bits is null");
     *bits = 0;
+    // the word of the stream's device, which is made current meanwhile
+    int before = 0, dev = 0;
+    cudaError_t e = cudaGetDevice(&before);
+    if (e == cudaSuccess) e = cudaStreamGetDevice(stream, &dev);
+    if (e == cudaSuccess && dev != before) e = cudaSetDevice(dev);
+    if (e != cudaSuccess)
+        return decode::fail(DECODE_ERR_CUDA, "the stream's device: %s", cudaGetErrorString(e));
+    static thread_local HostWord host;
+    uint32_t* taken = nullptr;
     uint32_t* word = decode::status_word();
-    if (word == nullptr) return DECODE_ERR_CUDA;
-    cudaError_t e = cudaMemcpyAsync(bits, word, sizeof(*bits), cudaMemcpyDeviceToHost, stream);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-    if (e == cudaSuccess && *bits != 0) {
-        e = cudaMemsetAsync(word, 0, sizeof(*word), stream);
+    if (word != nullptr) {
+        e = host.get(taken);
+        if (e == cudaSuccess) {
+            *taken = 0;
+            take_status_kernel<<<1, 1, 0, stream>>>(word, taken);
+            e = cudaGetLastError();
+        }
         if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+        if (e == cudaSuccess) *bits = *taken;
     }
+    if (dev != before) cudaSetDevice(before);
+    if (word == nullptr) return DECODE_ERR_CUDA;
     if (e != cudaSuccess)
         return decode::fail(DECODE_ERR_CUDA, "reading the status word: %s", cudaGetErrorString(e));
     return DECODE_OK;

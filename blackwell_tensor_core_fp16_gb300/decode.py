@@ -169,12 +169,17 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, scale: float | None =
 
 
 def check_decode_status(stream=None) -> None:
-    """Synchronise ``stream`` and raise GemmError if a kernel of this module refused an index
-    since the last check."""
+    """Synchronise ``stream`` and raise GemmError if a kernel of this module refused an index on the
+    stream's device since the last check there.  A device's streams and threads share the record,
+    and a refusal is reported to whichever check comes first after it."""
     if stream is None:
         stream = torch.cuda.current_stream()
-    rc, bits = decode_check_status(
-        int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
+    if hasattr(stream, "cuda_stream"):
+        # (a default stream's handle does not say whose it is)
+        with torch.cuda.device(stream.device):
+            rc, bits = decode_check_status(int(stream.cuda_stream))
+    else:
+        rc, bits = decode_check_status(int(stream))
     if rc != DECODE_OK:
         raise GemmError(rc, decode_last_error())
     if bits:

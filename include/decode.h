@@ -222,9 +222,10 @@ int decode_paged_attention_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t he
 /* The message of the calling thread's last failed decode_* call ("" if none). */
 const char* decode_last_error(void);
 
-/* Waits for `stream`, then reads and clears the current device's status word into *bits (0: no
- * index was refused since the last read).  Returns DECODE_OK, or DECODE_ERR_CUDA if the stream
- * reported an error. */
+/* Waits for `stream`, then reads and clears the status word of the stream's device into *bits (0: no
+ * index was refused since the last read).  A device has one word for all streams and threads, and
+ * a refusal is reported to whichever check comes first after it.  Returns DECODE_OK, or
+ * DECODE_ERR_CUDA if the stream reported an error. */
 int decode_check_status(cudaStream_t stream, uint32_t* bits);
 
 #ifdef __cplusplus

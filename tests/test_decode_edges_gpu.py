@@ -327,3 +327,64 @@ def test_attention_writes_over_its_queries(lens, h_q, h_kv, d):
         q = case["q"].clone()
         got = g.paged_attention(q, *args, out=q)
         assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
+# ---- the record of refused indices ------------------------------------------------------------------
+
+def test_status_of_concurrent_checks_is_never_lost():
+    """While one thread checks over and over, another's call on a stream of its own refuses a slot:
+    it is reported by a check during the call or by the one after it, though each first check has
+    an older refusal, of a position, to report and clear."""
+    import threading
+    step, slots = step_inputs(2, 1, 1, 1, 1, torch.bfloat16, seed=80)
+    slots[1] = 99
+    norm = norm_inputs(4, 1, 1, 64, 64, 1, torch.bfloat16, seed=81)
+    norm["positions"][2] = -7
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g.check_decode_status()
+
+    def bits_now(stream):
+        rc, bits = g.decode_check_status(stream.cuda_stream)
+        assert rc == 0
+        return bits
+
+    here = torch.cuda.current_stream()
+    for turn in range(300):
+        # a bit is up before the other thread starts, so that the first check has something to clear
+        norm_call(norm)
+        here.synchronize()
+        seen = []
+        go = threading.Event()
+
+        def refuse():
+            go.wait()
+            for _ in range(turn % 7):
+                pass
+            g.gated_delta_step(*(step[x] for x in ("q", "k", "v", "alpha", "beta", "state")), 0.5, slots,
+                               stream=side)
+
+        other = threading.Thread(target=refuse)
+        other.start()
+        go.set()
+        for _ in range(3):
+            seen.append(bits_now(here))
+        other.join()
+        side.synchronize()
+        seen.append(bits_now(side))
+        assert sum(x & 4 for x in seen) == 4 and any(x & 1 for x in seen), (turn, seen)
+    assert bits_now(here) == 0
+
+
+def test_status_is_that_of_the_streams_device():
+    """A stream's own device's record is read, whichever device is current, and the current device
+    stays."""
+    step, slots = step_inputs(2, 1, 1, 1, 1, torch.bfloat16, seed=82)
+    slots[0] = -5
+    for stream in (torch.cuda.Stream(), torch.cuda.default_stream()):
+        g.gated_delta_step(*(step[x] for x in ("q", "k", "v", "alpha", "beta", "state")), 0.5, slots,
+                           stream=stream)
+        with pytest.raises(g.GemmError, match="state slot"):
+            g.check_decode_status(stream)
+        g.check_decode_status(stream.cuda_stream)
+        assert torch.cuda.current_device() == 0
