@@ -1,12 +1,17 @@
 """Build step for libgemm_f16.so (nvcc, sm_103a only) and the Python module _decode.so that links to
-it (g++); in-tree output."""
+it (g++, where torch is installed); in-tree output."""
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
+import sysconfig
 import tempfile
+import warnings
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -16,9 +21,11 @@ HEADERS = [os.path.join(ROOT, "include", h) for h in ("gemm_f16.h", "gdn.h", "de
 SOURCES = ["gemm_f16.cu", "gdn.cu", "decode.cu", "gdn_step.cu", "qk_norm_rope.cu",
            "paged_attention.cu"]
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f16.so")
-# the CPython module of the decode-step operators' torch entry points, linked to the library
+# the CPython module of the decode-step operators' torch entry points, linked to the library, and
+# beside it the Python and torch that it was compiled for
 BINDING = "decode_binding.cpp"
 BINDING_PATH = os.path.join(PKG_DIR, "_decode.so")
+BINDING_ABI = BINDING_PATH + ".abi"
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -44,17 +51,41 @@ def _sources():
     return srcs + HEADERS
 
 
+def _stale(path: str, sources) -> bool:
+    return not os.path.exists(path) or \
+        any(os.path.getmtime(s) > os.path.getmtime(path) for s in sources)
+
+
+def binding_abi():
+    """The Python and torch that the binding is compiled for; None without torch, where there is no
+    binding.  (Does not import torch, which takes seconds.)"""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "of no version"
+    return f"{sysconfig.get_config_var('SOABI')}, torch {version}"
+
+
+def _binding_stale() -> bool:
+    abi = binding_abi()
+    if abi is None:
+        return False
+    try:
+        with open(BINDING_ABI) as f:
+            made_for = f.read()
+    except OSError:
+        made_for = None
+    return made_for != abi or _stale(BINDING_PATH, _sources())
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return any(os.path.getmtime(s) > t for s in _sources())
+    return _stale(LIB_PATH, _sources()) or _binding_stale()
 
 
 def _binding_commands(obj: str, out: str):
     """g++ commands that compile and link the binding against this Python and this torch."""
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
@@ -71,48 +102,67 @@ def _binding_commands(obj: str, out: str):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the sources (in parallel) and link libgemm_f16.so next to this file."""
+    """Compile the sources (in parallel) and link libgemm_f16.so next to this file, and _decode.so
+    where there is a torch to compile it for.  A binding that does not compile leaves the
+    library usable: a RuntimeWarning says why, and the operators that need it raise."""
     if not force and not is_stale():
         return LIB_PATH
     tag = f"tmp{os.getpid()}"
     compile_flags = [f for f in NVCC_FLAGS if f != "-shared"]
-    procs, objs = [], []
-    for src in SOURCES:
+    library = force or _stale(LIB_PATH, _sources())
+    abi = binding_abi()
+    commands, objs = [], []
+    for src in SOURCES if library else ():
         obj = os.path.join(PKG_DIR, f".{os.path.splitext(src)[0]}.{tag}.o")
         cmd = [_nvcc(), *compile_flags, "-c", "-o", obj, os.path.join(CSRC, src)]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        procs.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                      text=True))
+        commands.append(cmd)
         objs.append(obj)
     binding_obj = os.path.join(PKG_DIR, f".decode_binding.{tag}.o")
-    binding_tmp = BINDING_PATH + "." + tag
-    binding_compile, binding_link = _binding_commands(binding_obj, binding_tmp)
-    procs.append(subprocess.Popen(binding_compile, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                  text=True))
-    errors, logs = [], []
-    for p in procs:
-        out, err = p.communicate()
-        logs.append(out + err)
-        if p.returncode != 0:
-            errors.append(f"{p.args[0]} failed ({p.returncode}):\n{out}\n{err}")
+    tmp, binding_tmp = LIB_PATH + "." + tag, BINDING_PATH + "." + tag
+    made, logs = (*objs, binding_obj, tmp, binding_tmp), []
+
+    def run(cmd):
+        """(what went wrong, or None) of a command."""
+        try:
+            p = subprocess.run(cmd, capture_output=True, text=True)
+        except OSError as e:
+            return f"{cmd[0]}: {e}"
+        logs.append(p.stdout + p.stderr)
+        return f"{cmd[0]} failed ({p.returncode}):\n{p.stdout}\n{p.stderr}" if p.returncode else None
+
+    def compile_binding():
+        """(what went wrong or None, the command that links)."""
+        try:
+            compile_, link = _binding_commands(binding_obj, binding_tmp)
+        except (ImportError, OSError, RuntimeError) as e:
+            return str(e), None
+        return run(compile_), link
+
     try:
+        with ThreadPoolExecutor(len(commands) + 1) as pool:
+            binding = pool.submit(compile_binding) if abi is not None else None
+            errors = [e for e in pool.map(run, commands) if e]
+        if not errors and library:
+            errors = [e for e in [run([_nvcc(), *NVCC_FLAGS, "-o", tmp, *objs])] if e]
         if errors:
             raise RuntimeError("\n".join(errors))
-        tmp = LIB_PATH + "." + tag
-        res = subprocess.run([_nvcc(), *NVCC_FLAGS, "-o", tmp, *objs], capture_output=True,
-                             text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc link failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, LIB_PATH)
-        res = subprocess.run(binding_link, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"g++ link failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
-        os.replace(binding_tmp, BINDING_PATH)
+        if library:
+            os.replace(tmp, LIB_PATH)
+        if binding is not None:
+            error, link = binding.result()
+            error = error or run(link)
+            if error:
+                warnings.warn(f"{BINDING_PATH} is not built: {error}", RuntimeWarning)
+            else:
+                os.replace(binding_tmp, BINDING_PATH)
+                with open(BINDING_ABI, "w") as f:
+                    f.write(abi)
     finally:
-        for obj in (*objs, binding_obj):
-            if os.path.exists(obj):
-                os.unlink(obj)
+        for path in made:
+            if os.path.exists(path):
+                os.unlink(path)
     if verbose:
         print("".join(logs))
     return LIB_PATH
