@@ -182,6 +182,120 @@ def test_attention_every_score_minus_infinity(h_q, h_kv, d, dtype):
         ref.assert_close(lse[kept], l_ref, lb, "lse")
 
 
+# ---- attention: both paths of every shape -----------------------------------------------------------
+
+def path_of(case, **kw):
+    """(the results, "cluster" or "split", whether an item was cut) of a call: a cluster leaves the
+    workspace alone, the split path lists its items at its beginning and puts the parts of cut ones
+    behind the list."""
+    h_q, d = case["q"].shape[1:]
+    ws = g.paged_attention_workspace(h_q, case["k_cache"].shape[2], d)
+    ws.fill_(0xA5)
+    got = g.paged_attention(case["q"], case["k_cache"], case["v_cache"], case["table"],
+                            case["lens"], return_lse=True, workspace=ws, **kw)
+    touched = ws != 0xA5
+    return got, "split" if bool(touched.any()) else "cluster", bool(touched[16384:].any())
+
+
+def check_on(case, path, cut=None, window=None):
+    d = case["q"].shape[-1]
+    o_ref, l_ref, ob, lb = ref.paged_attention(case["q"], case["k_cache"], case["v_cache"],
+                                               case["table"], case["lens"], d ** -0.5, window)
+    (o, lse), taken, was_cut = path_of(case, window=window)
+    assert taken == path and cut in (None, was_cut)
+    ref.assert_close(lse, l_ref, lb, "lse")
+    ref.assert_close(o, o_ref, ob, "o")
+
+
+def mixed_lengths(n, seed):
+    """Empty, short and long sequences in no order."""
+    gen = generator(seed)
+    lens = torch.randint(1, 260, (n,), generator=gen)
+    lens[::9] = 0
+    lens[4::11] = torch.randint(500, 2500, (len(lens[4::11]),), generator=gen)
+    return lens
+
+
+@DTYPES
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("h_q,h_kv", [(9, 1), (20, 1), (40, 2), (16, 2), (3, 1)])
+def test_attention_heads_on_the_split_path(h_q, h_kv, d, dtype):
+    """Groups of up to 24 query heads a key head, two items a key head among them, with blocks that
+    take several whole items and items that several blocks take."""
+    s = attn_inputs(mixed_lengths(110, h_q + d), h_q, h_kv, d, 16, dtype, seed=h_q + d)
+    check_on(on_split_path(s), "split", cut=True)
+
+
+@pytest.mark.parametrize("h_q,h_kv", [(16, 1), (40, 2)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attention_whole_items_of_many_heads(d, h_q, h_kv):
+    """More short sequences than blocks: a block's items follow one another, with queries of their
+    own, and few are cut."""
+    gen = generator(d)
+    lens = torch.randint(0, 60, (620,), generator=gen)
+    s = attn_inputs(lens, h_q, h_kv, d, 16, torch.bfloat16, seed=d)
+    check_on(on_split_path(s), "split")
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("h_q,h_kv", [(16, 1), (8, 1)])
+def test_attention_one_long_sequence_of_many_heads(d, h_q, h_kv):
+    s = attn_inputs([30011], h_q, h_kv, d, 16, torch.float16, seed=d)
+    check_on(s, "split", cut=True)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16),
+                                     (256, torch.bfloat16)], ids=["64", "128", "256"])
+@pytest.mark.parametrize("window", [None, 1, 37, 333])
+@pytest.mark.parametrize("page", [1, 7, 20, 48, 100])
+def test_attention_pages_and_windows_on_the_split_path(page, window, d, dtype):
+    """Pages that end inside a slice, with a window that starts inside one; what lies before the
+    window is NaN."""
+    s = attn_inputs(mixed_lengths(160, page + d), 6, 2, d, page, dtype, seed=page + d)
+    if window:
+        for i, length in enumerate(s["lens"].tolist()):
+            tok = torch.arange(max(0, length - window), device="cuda")
+            at = (s["table"][i].long()[tok // page], tok % page)
+            s["k_cache"][at], s["v_cache"][at] = float("nan"), float("nan")
+    check_on(on_split_path(s), "split", window=window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [20, 64])
+def test_attention_pages_and_windows_on_clusters(page, d):
+    """The same for few short sequences, which run as clusters."""
+    s = attn_inputs([170, 0, 211, 33], 6, 2, d, page, torch.bfloat16, seed=page + d, spare=0)
+    check_on(s, "cluster")
+    for i, before in ((0, 20), (2, 61)):
+        tok = torch.arange(before, device="cuda")
+        at = (s["table"][i].long()[tok // page], tok % page)
+        s["k_cache"][at], s["v_cache"][at] = float("nan"), float("nan")
+    check_on(s, "cluster", window=150)
+
+
+@pytest.mark.parametrize("h_q,h_kv,d", [(4, 2, 128), (16, 1, 256), (16, 2, 64)])
+def test_attention_refused_lengths_and_pages_on_the_split_path(h_q, h_kv, d):
+    lens = mixed_lengths(40, 5)
+    s = on_split_path(attn_inputs(lens, h_q, h_kv, d, 16, torch.bfloat16, seed=37))
+    width = s["table"].shape[1]
+    for bad in (width * 16 + 1, -1, 2 ** 31 - 1):
+        t = dict(s, lens=s["lens"].clone())
+        t["lens"][4] = bad                         # the reference takes such a length as 0 too
+        check_on(t, "split")
+        with pytest.raises(g.GemmError, match="length"):
+            g.check_decode_status()
+    whole, _, _ = path_of(s)
+    for bad in (-1, int(s["k_cache"].shape[0]), 2 ** 31 - 1):
+        t = dict(s, table=s["table"].clone())
+        t["table"][4, 2] = bad
+        (o, _), taken, _ = path_of(t)
+        assert taken == "split"
+        kept = [i for i in range(40) if i != 4]
+        assert torch.equal(o[kept], whole[0][kept])
+        with pytest.raises(g.GemmError, match="page"):
+            g.check_decode_status()
+
+
 # ---- operands that share memory ---------------------------------------------------------------------
 
 def test_step_refuses_outputs_that_share_memory():
