@@ -9,7 +9,8 @@ import torch
 import blackwell_tensor_core_fp16_gb300 as g
 import decode_ref as ref
 from test_decode_gpu import (attn_inputs, cache_pair, cuda_library, generator,  # noqa: F401
-                             no_refusals_left, norm_call, norm_inputs, normal, step_inputs)
+                             no_refusals_left, norm_call, norm_inputs, norm_refs, normal,
+                             step_inputs)
 
 pytestmark = pytest.mark.gpu
 DTYPES = pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
@@ -294,6 +295,91 @@ def test_attention_refused_lengths_and_pages_on_the_split_path(h_q, h_kv, d):
         assert torch.equal(o[kept], whole[0][kept])
         with pytest.raises(g.GemmError, match="page"):
             g.check_decode_status()
+
+
+# ---- norm without rotation, and the cache under many tokens -----------------------------------------
+
+@pytest.mark.parametrize("norm", ["rms", "l2", "none"])
+@pytest.mark.parametrize("weights", [True, False])
+@pytest.mark.parametrize("d", [64, 96, 128, 256])
+def test_norm_kinds_without_rotation(d, norm, weights):
+    s = norm_inputs(9, 5, 2, d, 0, 1, torch.float16, seed=100 + d, weights=weights)
+    s["q"][3] = 0                                  # a head of zeros stays zero
+    (qr, qb), (kr, kb) = norm_refs(s, norm=norm, eps=1e-5)
+    q, k = norm_call(s, norm=norm, eps=1e-5)
+    ref.assert_close(q, qr, qb, "q")
+    ref.assert_close(k, kr, kb, "k")
+    assert bool((q[3] == 0).all())
+
+
+def check_cache(kc, vc, s, slots, written, k_ref, where):
+    """Both caches hold the tokens of `written` at their slots, values bit for bit, and nothing
+    else."""
+    page = kc.shape[1]
+    kr, kb = k_ref
+    at = slots[written].long().cuda()
+    ref.assert_close(kc[at // page, at % page], kr[written], kb[written], f"{where}: keys")
+    assert torch.equal(vc[at // page, at % page].view(torch.int16), s["v"][written].view(torch.int16))
+    rest = torch.ones(kc.shape[:2], dtype=torch.bool, device="cuda")
+    rest[at // page, at % page] = False
+    assert bool(kc[rest].isnan().all()) and bool(vc[rest].isnan().all()), f"{where}: other places"
+
+
+@DTYPES
+@pytest.mark.parametrize("layout", ["tokens", "heads", "both"])
+@pytest.mark.parametrize("page", [1, 16, 20])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norm_into_the_cache_without_rotation(d, page, layout, dtype):
+    """Active, inactive and refused slots; the refused ones are reported."""
+    tokens = 37
+    s = norm_inputs(tokens, 6, 3, d, 0, 1, dtype, seed=101)
+    s["v"][5, 1, 3] = float("nan")                 # values are copied bit for bit
+    pages = -(-tokens // page) + 2
+    slots = torch.randperm(pages * page, generator=generator(102))[:tokens].to(torch.int32)
+    slots[4] = -1
+    (qr, qb), k_ref = norm_refs(s)
+    for bad in (None, pages * page, -2, 2 ** 31 - 1):
+        kc, vc = cache_pair(pages, page, 3, d, dtype, layout)
+        at = slots.clone()
+        if bad is not None:
+            at[11] = bad
+        q, k = norm_call(s, v=s["v"], k_cache=kc, v_cache=vc, slots=at.cuda())
+        assert k is None
+        ref.assert_close(q, qr, qb, "q")
+        check_cache(kc, vc, s, at, [t for t in range(tokens) if t != 4 and (t != 11 or bad is None)],
+                    k_ref, f"slot {bad}")
+        if bad is not None:
+            with pytest.raises(g.GemmError, match="cache slot"):
+                g.check_decode_status()
+        g.check_decode_status()
+
+
+@pytest.mark.parametrize("rot", ["all", "some", "none"])
+@pytest.mark.parametrize("tokens,h_q,h_k,d,page", [(3000, 32, 8, 128, 16), (3001, 32, 8, 128, 20),
+                                                   (9000, 3, 1, 64, 20), (2500, 16, 2, 256, 64)])
+def test_norm_of_many_tokens_into_the_cache(tokens, h_q, h_k, d, page, rot):
+    """Warps take several sets of tokens, whole and in parts, each with a position and a slot of its
+    own; inactive tokens and refused slots and positions lie scattered among them."""
+    rot = {"all": d, "some": d // 4, "none": 0}[rot]
+    s = norm_inputs(tokens, h_q, h_k, d, rot, 1, torch.bfloat16, seed=tokens + rot)
+    pages = -(-tokens // page) + 3
+    slots = torch.randperm(pages * page, generator=generator(103))[:tokens].to(torch.int32)
+    slots[5::97] = -1
+    slots[7::301] = pages * page
+    lost = set(range(5, tokens, 97)) | set(range(7, tokens, 301))
+    zeros = []
+    (qr, qb), k_ref = norm_refs(s)
+    if rot:
+        zeros = list(range(11, tokens, 211))
+        s["positions"][zeros] = 300                # the table has 300 rows
+    kc, vc = cache_pair(pages, page, h_k, d, torch.bfloat16, "tokens")
+    q, _ = norm_call(s, v=s["v"], k_cache=kc, v_cache=vc, slots=slots.cuda())
+    with pytest.raises(g.GemmError, match="cache slot.*position" if rot else "cache slot"):
+        g.check_decode_status()
+    kept = [t for t in range(tokens) if t not in set(zeros)]
+    ref.assert_close(q[kept], qr[kept], qb[kept], "q")
+    assert bool((q[zeros] == 0).all())
+    check_cache(kc, vc, s, slots, [t for t in kept if t not in lost], k_ref, "cache")
 
 
 # ---- operands that share memory ---------------------------------------------------------------------
