@@ -316,14 +316,17 @@ PyObject* qk_norm_rope(PyObject* const* args)
             const int64_t count = list == nullptr ? -1 : PySequence_Fast_GET_SIZE(list);
             int64_t sum = 0;
             const bool fits = count == a.axes && count >= 1 && count <= DECODE_MAX_AXES;
+            bool small = true;                     // the struct holds 32 bits of each
             for (int64_t x = 0; fits && x < count; ++x) {
                 const int64_t pairs = PyLong_AsLongLong(PySequence_Fast_GET_ITEM(list, x));
                 a.sections[x] = static_cast<int32_t>(pairs);
-                sum += pairs;
+                small = small && a.sections[x] == pairs;
+                sum += a.sections[x];
             }
             Py_XDECREF(list);
             if (PyErr_Occurred()) throw python_error();
             if (!fits) refuse("positions of 1 to 4 axes need as many sections");
+            if (!small) refuse("a section of more pairs than any head holds");
             if (sum != a.rot / 2)
                 refuse("sections of " + std::to_string(sum) + " pairs do not hold rot / 2 = " +
                        std::to_string(a.rot / 2));

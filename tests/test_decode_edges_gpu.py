@@ -382,6 +382,13 @@ def test_norm_of_many_tokens_into_the_cache(tokens, h_q, h_k, d, page, rot):
     check_cache(kc, vc, s, slots, [t for t in kept if t not in lost], k_ref, "cache")
 
 
+def test_norm_refuses_sections_past_32_bits():
+    s = norm_inputs(4, 2, 1, 128, 128, 2, torch.bfloat16, seed=104)
+    for sections in ((2 ** 32 + 32, 32 - 2 ** 32), (2 ** 32 + 32, 32), (2 ** 31, 64 - 2 ** 31)):
+        with pytest.raises(ValueError, match="section"):
+            norm_call(dict(s, sections=sections))
+
+
 # ---- operands that share memory ---------------------------------------------------------------------
 
 def test_step_refuses_outputs_that_share_memory():
