@@ -23,7 +23,7 @@ __attribute__((visibility("hidden"))) uint32_t* status_word();
 // Multiprocessors of the current device; 0 (with the error stored) on failure.
 __attribute__((visibility("hidden"))) int sm_count();
 
-// The calling device's ordinal and a per-device "done once" mark for a kernel's attributes.
+// Devices for which a thread keeps what it has looked up or set once.
 constexpr int kMaxDevices = 64;
 
 // Programmatic dependent launch: dep_wait() returns once all earlier work on the stream has

@@ -23,7 +23,6 @@ import torch
 from . import GemmError, _build, load
 
 DECODE_OK, DECODE_ERR_INVALID_ARG, DECODE_ERR_UNSUPPORTED, DECODE_ERR_CUDA = 0, 1, 2, 3
-DECODE_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 DECODE_NORMS = {"none": 0, "rms": 1, "l2": 2}
 DECODE_STATUS = {1: "a state slot outside the pool", 2: "a cache slot outside the cache",
                  4: "a position outside the rotary table",
