@@ -103,21 +103,6 @@ __device__ __forceinline__ uint16_t from_float(float x)
     return static_cast<uint16_t>(Half2<T>::pack(x, 0.f));
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-}
-
 // Block: kWarps warps, 16 value rows each, of one (sequence, value head).  kMany: several tokens
 // a sequence.  Their keys, queries, values and gates are staged in shared memory kStage tokens at
 // a time, on their way before the state's slot is even known, so that a token costs no round trip
@@ -159,6 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     const Staged at(p.queries, kBlockRows);
     auto stage = [&](int t0) {
         const int here = min(kStage, p.tokens - t0), pieces = at.gates / 16;
+        const uint32_t dst = smem_addr(smem);
         for (int x = threadIdx.x; x < here * pieces; x += kWarps * 32) {
             const int t = x / pieces, b = (x - t * pieces) * 16;
             const uint16_t* src;
@@ -169,12 +155,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
                       b % (2 * kD) / 2;
             else
                 src = vp + (t0 + t) * p.v_stride[1] + (b - at.v) / 2;
-            cp_async16(smem + t * at.total + b, src);
+            cp_async16(dst + t * at.total + b, src);
         }
         for (int x = threadIdx.x; x < 2 * here; x += kWarps * 32)
-            cp_async4(smem + x / 2 * at.total + at.gates + (x & 1) * 4,
+            cp_async4(dst + x / 2 * at.total + at.gates + (x & 1) * 4,
                       x & 1 ? bp + (t0 + x / 2) * p.beta_stride[1]
                             : ap + (t0 + x / 2) * p.alpha_stride[1]);
+        cp_commit();
     };
 
     dep_launch();
@@ -190,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
                     *reinterpret_cast<uint2*>(
                         p.o + out0 + (static_cast<int64_t>(t) * p.h_o + g) * kD) =
                         make_uint2(0u, 0u);
-        if constexpr (kMany) cp_async_wait();
+        if constexpr (kMany) cp_wait<0>();
         return;
     }
 
@@ -230,7 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
                 __syncthreads();
                 stage(t0);
             }
-            cp_async_wait();
+            cp_wait<0>();
             __syncthreads();
             const int here = min(kStage, p.tokens - t0);
             for (int t = 0; t < here; ++t) {

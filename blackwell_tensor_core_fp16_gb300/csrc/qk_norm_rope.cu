@@ -79,25 +79,6 @@ __device__ __forceinline__ uint32_t word(const uint4& b, int c)
     return c == 0 ? b.x : c == 1 ? b.y : c == 2 ? b.z : b.w;
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p)
-{
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A token's chunks in order: its queries' (kind 0), its keys' (1), its values' (2).
 template <typename T, int kLanes, Pairing kPairing>
 __global__ void __launch_bounds__(kBlockWarps * 32, kResident) qk_norm_rope_kernel(const NormParams p)
