@@ -66,8 +66,9 @@ constexpr size_t kSpreadMost = kSmShared / 2 - 1024 + 256;
 
 // Shared memory for `blocks` blocks, fewer than the GPU holds (`resident` an SM): so much that an SM
 // takes no more of them than an even spread gives it, and leaves room for the next kernel's first
-// ones.  Without it some SMs fill up while others stay idle: 7740 tokens of 8 + 1 heads of 64 took
-// 8.6 us in the norm's kernel, 7.6 with it; 208 sequences of 5 tokens 10.3 us in the step's, 8.9.
+// ones.  Without it some SMs fill up while others stay idle: 7740 tokens of 8 + 1 heads of 64 take
+// 7.3 us in the norm's kernel, 6.4 with it; 208 sequences of 5 tokens, one state each, 8.3 us in the
+// step's, 6.9.
 inline size_t spread(size_t smem, int64_t blocks, int sms, int resident)
 {
     const int64_t each = (blocks + sms - 1) / sms;

@@ -11,12 +11,14 @@
 // What bounds it.  A state is 65,536 bytes and a token adds about 1 KB to it, so with one token
 // the bytes of the states, read once and written once, are the floor: 256 sequences x 32 states
 // (1.08 GB) take 156 us, 6.9 TB/s, which is what a plain copy reaches; one sequence of 16 states
-// takes 2.5 us, its launch and two round trips to memory.  Each further token costs its 6 flops
-// per element, on packed fp32 pairs: 151 sequences x 8 states take 28.5 us with 2 tokens (84% of
-// the copy rate), 34 us with 4 and 52 us with 8, the FMA pipes about 70% busy meanwhile.  (The
-// chunked form on mma.m16n8k16 with operands in three bfloat16 pieces was built and measured: 46
-// to 48 us for 2 to 8 tokens alike, bound by its chain of dependent products; it wins from 16
-// tokens on, where the prefill belongs.)
+// takes 2.7 us, its launch and two round trips to memory.  Each further token is a chain: a product
+// of the rows with k, four shuffles, u, the rows' update, a product with q, four shuffles.  151
+// sequences x 8 states with two queries each take 27.7 us with 2 tokens (86% of the copy rate),
+// 34.2 us with 4 and 51.8 us with 8, issue slots 56% and FMA pipes 52% busy meanwhile at 14 warps
+// an SM; 77 sequences x 4 tokens, two queries, take 19.4 us, issue slots 48% and FMA pipes 45%
+// busy, the SMs 78% of the time.  (The chunked form on mma.m16n8k16 with operands in three bfloat16
+// pieces was built and measured: 46 to 48 us for 2 to 8 tokens alike, bound by its chain of
+// dependent products; it wins from 16 tokens on, where the prefill belongs.)
 //
 // Layout.  Eight lanes share a row of 128 floats, lane l of them holding the float4s l, l + 8,
 // l + 16, l + 24 (each load of the eight lanes is one 128-byte line), and a lane group has four
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
 }
 
 // Two warps a block for single tokens, so that few states spread over many SMs; four for several
-// tokens, whose staging they share (77 sequences of 4 tokens: 21.0 us, 21.7 with two).
+// tokens, whose staging they share (77 sequences of 4 tokens: 19.4 us, 21.3 with two).
 template <typename T, int kWarps, bool kMany>
 cudaError_t run(const StepParams& p, int64_t items, int sms, size_t smem, cudaStream_t stream)
 {

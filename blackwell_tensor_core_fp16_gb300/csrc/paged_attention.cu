@@ -16,9 +16,10 @@
 // one; those two go to the workspace as (maximum, sum, output) and a second kernel joins each
 // item's parts in block order, the rest are written at once.  The order of every sum is fixed.
 // Two blocks of four warps an SM, so that one streams while the other begins or joins an item: 64
-// sequences of up to 8192 tokens, 8 key heads of 128, take 160 us, against 175 us with one block of
-// eight warps, whose SMs were busy 78% of the time on average; ranges four times finer than the
-// GPU holds blocks, which even the SMs out, take 167 us, their blocks' beginnings cost more.
+// sequences of up to 8192 tokens, 8 key heads of 128, take 158 us (6.1 TB/s, 90% of what a copy
+// reaches; the SMs are busy 91% of the time on average), against 175 us with one block of
+// eight warps, whose SMs were busy 78% of the time; ranges four times finer than the
+// GPU holds blocks, which even the SMs out, took 167 us, their blocks' beginnings cost more.
 // Few items of few tiles, where the second kernel's launch would show, run as one thread-block
 // cluster an item instead, whose blocks join their parts through distributed shared memory.
 //
@@ -33,11 +34,11 @@
 // For the second product each weight is carried as 16-bit pieces, three of bfloat16 or two of
 // float16 (each takes from p what the ones before left of it), which hold its 24 bits: with two pieces of
 // bfloat16 a result that is a small difference of large terms was off by up to 2^-17 of them, and
-// the third costs no time (64 sequences of up to 8192 tokens 161 us, 37 windows 28 us, with either),
-// since the products are not what bounds it.  float16's weights are
-// carried times 2^15 (and the results divided by it), which leaves them above 2^-40 of the warp's
-// largest: unscaled, weights below 2^-25 vanished, and with them a long tail beside a token that
-// takes nearly all the weight and has little to give.
+// the third costs no time (64 sequences of up to 8192 tokens 161 us, one of 200001 tokens 74.6 us,
+// with either), since the products are not what bounds it.  float16's weights are carried times
+// 2^15 (and the results divided by it), which leaves them above 2^-40 of the warp's largest:
+// unscaled, weights below 2^-25 vanished, and with them a long tail beside a token that takes
+// nearly all the weight and has little to give.
 #include <cstdint>
 #include <type_traits>
 
@@ -263,12 +264,13 @@ struct Cfg {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kHeads = 8 * kHeadTiles;
     // a slice is 8 KB at least: for short rows the look-up, the maxima and the loop cost as much as
-    // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 28.7 us, 36 us with
-    // 16-token slices; more blocks an SM with fewer or smaller stages are no faster, 30 to 39 us)
+    // the products (37 sequences with a window of 1000 tokens, 12 key heads of 64: 30.6 us, 39.3 us
+    // with 16-token slices; more blocks an SM with fewer or smaller stages were no faster)
     static constexpr int kSubs = D == 64 ? 2 : 1;
     // the weights' lower pieces have sums of their own: with one head tile of 256, where they take
-    // turns with the first piece's (bfloat16, 200001 tokens: 75.1 us, 77.8 in one sum; other shapes
-    // no gain), and for float16, whose lower pieces' sums are cleared of infinities
+    // turns with the first piece's (bfloat16, 200001 tokens: 75.1 us, 77.9 in one sum; other shapes
+    // no gain), and for float16, whose lower pieces' sums are cleared of infinities (37 windows of
+    // 1000 tokens, 12 key heads of 64: 28.5 us, 27.9 without that)
     template <typename T>
     static constexpr int kSums =
         (D == 256 && kHeadTiles == 1) || std::is_same<T, __half>::value ? 2 : 1;
@@ -633,8 +635,8 @@ __global__ void __launch_bounds__(Cfg<D, kHeadTiles>::kThreads, Cfg<D, kHeadTile
             }
             // The slice's products are summed on their own and added to the rescaled sums: a matrix
             // product cuts its sum's last bits off, and over a long axis on one running sum the
-            // losses add up.  (Rescaling always: a vote whether any maximum rose costs what it
-            // saves, 6.2 us against 5.9 for 39 sequences of up to 299 tokens.)
+            // losses add up (one sequence of 200001 tokens: 27 of 12288 results rounded otherwise
+            // than the formula's in 64 bits, 16 since; 74.6 us then, 75.6 since)
             constexpr int kAtOnce = 2;             // blocks of 16 elements whose sums take turns
 #pragma unroll
             for (int d0 = 0; d0 < D / 16; d0 += kAtOnce) {
@@ -948,8 +950,10 @@ int run(AttnParams p, int64_t most_tokens, int sms, cudaStream_t stream)
     p.join_shared = items <= kSharedItems;
     // Few items of few tiles: a cluster an item, which joins its blocks' parts itself, as large as
     // the GPU holds for all items, up to three tiles a block (8 key heads: one sequence of 500
-    // tokens 5.5 us, 7.3 with the second kernel; 16 of up to 250 tokens 6.6 and 8.1; one of 2000
-    // with four tiles a block 8.4 and 8.2).
+    // tokens 5.7 us, 8.1 with the second kernel; 16 of up to 250 tokens 7.2 and 8.6; one of 1500
+    // 7.5 and 8.8; with four tiles a block, one of 2000 took as long either way).  The lengths being on the device, the page table's width
+    // stands for the longest (with a window, the window): short sequences under a table made for
+    // long ones take the second kernel.
     int ranks = 1;
     while (ranks < kClusterMost && ranks < per_item && items * ranks * 2 <= most) ranks *= 2;
     const bool cluster = ranks > 1 && per_item <= ranks * kClusterTiles;

@@ -162,7 +162,8 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, scale: float | None =
     d ** -0.5.  A sequence of length 0, or all of whose scores are -infinity, gives zeros and lse
     -inf.  Returns o [n, h_q, d], or (o, lse [n, h_q] float32) with ``return_lse``.
     ``workspace``: from ``paged_attention_workspace``; None takes one from torch's allocator for the
-    call.  ``out`` may be ``q`` itself; what is written may share no other memory with the operands."""
+    call.  A page table no wider than the lengths need lets a few short sequences run in one launch.
+    ``out`` may be ``q`` itself; what is written may share no other memory with the operands."""
     return _decode.paged_attention(q, k_cache, v_cache, page_table, lens, scale, window, return_lse,
                                    out, workspace, stream)
 
