@@ -29,7 +29,8 @@ __all__ = [
     "gemm_f16_half_tail_tiles", "gemm_f16_half_items", "gemm_f16_half_item",
     "exported_symbols", "VARIANTS", "STATUS",
     "gated_delta_step", "qk_norm_rope", "rotary_table", "paged_attention",
-    "paged_attention_workspace", "check_decode_status",
+    "paged_attention_workspace", "check_decode_status", "quantize_cache", "dequantize_cache",
+    "paged_attention_fp8", "paged_attention_fp8_workspace", "linear_w4", "quantize_weight_w4",
 ]
 
 STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA_ERROR", 4: "TIMEOUT"}
@@ -176,11 +177,15 @@ def load():
         lib.gdn_set_fault_injection.argtypes = [i32]
         lib.gdn_set_fault_injection.restype = i32
         # the decode-step operators take their argument struct packed into bytes
-        for name in ("decode_gdn_step", "decode_qk_norm_rope", "decode_paged_attention"):
+        for name in ("decode_gdn_step", "decode_qk_norm_rope", "decode_paged_attention",
+                     "decode_quantize_cache", "decode_dequantize_cache",
+                     "decode_paged_attention_fp8", "decode_linear_w4"):
             getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
             getattr(lib, name).restype = i32
-        lib.decode_paged_attention_workspace_bytes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
-        lib.decode_paged_attention_workspace_bytes.restype = i32
+        for name in ("decode_paged_attention_workspace_bytes",
+                     "decode_paged_attention_fp8_workspace_bytes"):
+            getattr(lib, name).argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
+            getattr(lib, name).restype = i32
         lib.decode_last_error.argtypes = []
         lib.decode_last_error.restype = ctypes.c_char_p
         lib.decode_check_status.argtypes = [vp, u32p]
@@ -746,9 +751,12 @@ def check_status(stream=None) -> None:
 # ---- the operators of a decode step -----------------------------------------------------------
 
 _DECODE_NAMES = frozenset((
-    "check_decode_status", "decode_check_status", "decode_gdn_step", "decode_last_error",
-    "decode_paged_attention", "decode_paged_attention_workspace_bytes", "decode_qk_norm_rope",
-    "gated_delta_step", "paged_attention", "paged_attention_workspace", "qk_norm_rope",
+    "check_decode_status", "decode_check_status", "decode_dequantize_cache", "decode_gdn_step",
+    "decode_last_error", "decode_linear_w4", "decode_paged_attention", "decode_paged_attention_fp8",
+    "decode_paged_attention_fp8_workspace_bytes", "decode_paged_attention_workspace_bytes",
+    "decode_qk_norm_rope", "decode_quantize_cache", "dequantize_cache", "gated_delta_step",
+    "linear_w4", "paged_attention", "paged_attention_fp8", "paged_attention_fp8_workspace",
+    "paged_attention_workspace", "qk_norm_rope", "quantize_cache", "quantize_weight_w4",
     "rotary_table"))
 
 

@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 HEADERS = [os.path.join(ROOT, "include", h) for h in ("gemm_f16.h", "gdn.h", "decode.h")]
 # translation units, compiled in parallel
 SOURCES = ["gemm_f16.cu", "gdn.cu", "decode.cu", "gdn_step.cu", "qk_norm_rope.cu",
-           "paged_attention.cu"]
+           "paged_attention.cu", "cache_fp8.cu", "paged_attention_fp8.cu", "linear_w4.cu"]
 LIB_PATH = os.path.join(PKG_DIR, "libgemm_f16.so")
 # the CPython module of the decode-step operators' torch entry points, linked to the library, and
 # beside it the Python and torch that it was compiled for

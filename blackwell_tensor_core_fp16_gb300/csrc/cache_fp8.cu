@@ -1,0 +1,406 @@
+// The write to a paged cache of E4M3 codes with an E8M0 scale for each block of tokens and head, and
+// its reading back (C ABI and formulas in include/decode.h).
+//
+// Both move every element once, 3 bytes of it, and do a dozen operations on it: HBM bounds them.
+//
+// Write.  A block's scale needs the largest of its new elements before the first code is known, and
+// its other codes may have to follow, so one warp takes a block, of one head of the keys or of the
+// values, as a whole: the block's first new token in the call (its leader, found from the slots
+// beside it) stands for it.  The rows wait in registers while the maximum is taken (16 or 32 tokens;
+// of larger blocks the rest is read again, from a cache), nothing else is shared between warps, and no
+// order of blocks matters.  A scale being a power of two, x * 2^(127 - e) is exact and only the
+// conversion rounds, and codes that follow keep their bits but for those that become subnormal.
+#include <cstdint>
+#include <type_traits>
+
+#include "fp8.cuh"
+
+namespace {
+
+using namespace decode;
+
+constexpr int kWarps = 8;
+constexpr int kWindow = 16;           // most tokens of a block of threads; half the lanes that see slots
+
+// A cache's two tensors (keys, values), and where its places are.
+struct CacheParams {
+    uint8_t* codes[2];
+    uint8_t* scales[2];
+    int64_t code_stride[2][3], scale_stride[2][3];
+    const int32_t* slots;
+    uint32_t* status;
+    int32_t tokens, heads, page_size, page_shift, block, block_shift, places;
+};
+struct QuantizeParams : CacheParams {
+    const uint16_t* x[2];
+    int64_t x_stride[2][2];
+    int32_t window, per;              // tokens of a block of threads; its warps that share a token
+};
+struct DequantizeParams : CacheParams {
+    uint16_t* y[2];
+    int64_t y_stride[2][2];
+    int32_t units, at_once;           // 16-element units of a token; tokens of a block of threads
+    uint32_t magic;                   // ceil(2^32 / units)
+};
+
+template <typename T>
+constexpr uint32_t kInfinity = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+
+template <typename T>
+__device__ __forceinline__ float from_bits(uint32_t bits)
+{
+    return Half2<T>::unpack(bits).x;
+}
+
+// The larger of each half, of numbers without their sign.
+__device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t x)
+{
+    return __vmaxu2(top, x & 0x7fff7fffu);
+}
+// x with zeros for infinities and NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
+{
+    const uint32_t lo = x & 0x7fffu, hi = x >> 16 & 0x7fffu;
+    return (lo < kInfinity<T> ? lo : 0u) | (hi < kInfinity<T> ? hi << 16 : 0u);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) quantize_cache_kernel(const QuantizeParams p)
+{
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes;     // a row's lanes; rows of one load
+    constexpr int kHold = D == 256 ? 16 : 8;               // loads that wait in registers
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int combo = blockIdx.y * p.per + w % p.per, phase = w / p.per, phases = kWarps / p.per;
+    if (combo >= 2 * p.heads || phase >= phases) return;
+    const int kv = combo >= p.heads, head = combo - kv * p.heads;
+    dep_launch();
+    dep_wait();
+
+    // lane x sees the slot of token t0 + x, from the one before the window on
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.window - 1;
+    const int64_t t = t0 + lane;
+    const int slot = t >= 0 && t < p.tokens ? p.slots[t] : -1;
+    const int before = __shfl_up_sync(kAll, slot, 1);
+    const bool mine = lane > 0 && lane <= p.window;
+    const bool valid = slot >= 0 && slot < p.places;
+    const bool after_one = lane > 0 && before >= 0 && before < p.places;
+    const int in_block = valid ? slot - divide(slot, p.block, p.block_shift) * p.block : 0;
+    const bool goes_on = valid && after_one && slot == before + 1 && in_block > 0;
+    const bool disordered = valid && after_one && !goes_on &&
+                            divide(slot, p.block, p.block_shift) ==
+                                divide(before, p.block, p.block_shift);
+    if (combo == 0 && phase == 0 && mine && (disordered || (!valid && slot != -1)))
+        atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+    uint32_t leaders = __ballot_sync(kAll, mine && valid && !goes_on && !disordered);
+
+    for (int nth = 0; leaders != 0; ++nth, leaders &= leaders - 1) {
+        if (nth % phases != phase) continue;
+        const int lead = __ffs(leaders) - 1;
+        const int place = __shfl_sync(kAll, slot, lead), first = __shfl_sync(kAll, in_block, lead);
+        const int most = p.block - first;
+        const int64_t token = t0 + lead;
+        // the run: how many tokens of the block follow
+        uint32_t apart = __ballot_sync(kAll, lane > lead && (slot != place + lane - lead ||
+                                                             lane - lead >= most));
+        int run = apart != 0 ? __ffs(apart) - 1 - lead : 32 - lead;
+        while (apart == 0 && run < most) {
+            const int64_t next = token + run + lane;
+            const int s = next < p.tokens ? p.slots[next] : -1;
+            apart = __ballot_sync(kAll, s != place + run + lane || run + lane >= most);
+            run += apart != 0 ? __ffs(apart) - 1 : 32;
+        }
+
+        const int page = divide(place, p.page_size, p.page_shift), offset = place - page * p.page_size;
+        uint8_t* const scale = p.scales[kv] + page * p.scale_stride[kv][0] +
+                               divide(offset, p.block, p.block_shift) * p.scale_stride[kv][1] +
+                               head * p.scale_stride[kv][2];
+        const int older = first > 0 ? *scale : 0;
+        const int ch = lane % kLanes, sub = lane / kLanes;
+        const uint16_t* const x =
+            p.x[kv] + token * p.x_stride[kv][0] + head * p.x_stride[kv][1] + ch * 8;
+        uint4 row[kHold];
+        auto load = [&](int from) {
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int r = from + i * kRows + sub;
+                row[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < run) row[i] = *reinterpret_cast<const uint4*>(x + r * p.x_stride[kv][0]);
+            }
+        };
+        constexpr int kChunk = kHold * kRows;
+        const int last = (run - 1) / kChunk * kChunk;
+        uint32_t top = 0;
+        for (int from = 0; from <= last; from += kChunk) {
+            load(from);
+#pragma unroll
+            for (int i = 0; i < kHold; ++i)
+                top = larger(larger(larger(larger(top, row[i].x), row[i].y), row[i].z), row[i].w);
+        }
+        top = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
+        const bool odd = top >= kInfinity<T>;              // an infinity or NaN: rarely
+        if (odd) {
+            top = 0;
+            for (int from = 0; from <= last; from += kChunk) {
+                load(from);
+#pragma unroll
+                for (int i = 0; i < kHold; ++i) {
+                    top = larger(larger(top, finite_or_zero<T>(row[i].x)), finite_or_zero<T>(row[i].y));
+                    top = larger(larger(top, finite_or_zero<T>(row[i].z)), finite_or_zero<T>(row[i].w));
+                }
+            }
+            top = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
+        }
+        // 448 = 1.75 * 2^8
+        const uint32_t bits = __float_as_uint(from_bits<T>(top));
+        const int need = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u));
+        const int e = max(need, older);
+        if (lane == 0) *scale = static_cast<uint8_t>(e);
+
+        uint8_t* const codes = p.codes[kv] + page * p.code_stride[kv][0] +
+                               offset * p.code_stride[kv][1] + head * p.code_stride[kv][2] + ch * 8;
+        const float by = power_of(254 - e);
+        for (int from = last; from >= 0; from -= kChunk) {
+            if (from != last) load(from);                  // (the last are still there)
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int r = from + i * kRows + sub;
+                uint32_t out[2];
+                const uint32_t in[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 a = Half2<T>::unpack(in[2 * h]), b = Half2<T>::unpack(in[2 * h + 1]);
+                    float2 za = make_float2(0.f, 0.f), zb = za;
+                    if (odd) {                             // x * 0: NaN for an infinity
+                        za = make_float2(a.x * 0.f, a.y * 0.f);
+                        zb = make_float2(b.x * 0.f, b.y * 0.f);
+                        a.x = fmaf(a.x, by, za.x), a.y = fmaf(a.y, by, za.y);
+                        b.x = fmaf(b.x, by, zb.x), b.y = fmaf(b.y, by, zb.y);
+                    } else {
+                        a.x *= by, a.y *= by, b.x *= by, b.y *= by;
+                    }
+                    out[h] = codes_of(a.x, a.y) | codes_of(b.x, b.y) << 16;
+                }
+                if (r < run)
+                    *reinterpret_cast<uint2*>(codes + r * p.code_stride[kv][1]) =
+                        make_uint2(out[0], out[1]);
+            }
+        }
+        // the block's other codes follow a scale that grew (a factor below 2^-126 takes any to 0, as 0 does)
+        if (e > older && first > 0) {
+            const float down = e - older < 127 ? power_of(127 + older - e) : 0.f;
+            for (int r = sub - first; r < most; r += kRows) {
+                if (r >= 0 && r < run) continue;
+                uint2* const at = reinterpret_cast<uint2*>(codes + r * p.code_stride[kv][1]);
+                const uint2 old = *at;
+                uint32_t in[2] = {old.x, old.y};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
+                    const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
+                    in[h] = codes_of(a.x * down, a.y * down) | codes_of(b.x * down, b.y * down) << 16;
+                }
+                *at = make_uint2(in[0], in[1]);
+            }
+        }
+    }
+}
+
+// A thread takes units of 16 neighbouring elements, four at a time so that their chains of slot,
+// code and store run beside each other.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) dequantize_cache_kernel(const DequantizeParams p)
+{
+    constexpr int kUnits = 4;
+    dep_launch();
+    dep_wait();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.at_once;
+    const int here = static_cast<int>(min(static_cast<int64_t>(p.at_once), p.tokens - t0)) * p.units;
+    for (int u0 = threadIdx.x; u0 < here; u0 += 256 * kUnits) {
+        uint4 codes[kUnits];
+        int e[kUnits];
+        uint16_t* to[kUnits];
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = u0 + i * 256;
+            to[i] = nullptr;
+            if (u >= here) continue;
+            const int t = p.at_once == 1 ? 0 : static_cast<int>(__umulhi(u, p.magic));
+            int rest = u - t * p.units;
+            const int kv = rest >= p.units / 2;
+            rest -= kv * (p.units / 2);
+            const int head = rest / (D / 16), ch = rest % (D / 16);
+            const int slot = p.slots[t0 + t];
+            to[i] = p.y[kv] + (t0 + t) * p.y_stride[kv][0] + head * p.y_stride[kv][1] + ch * 16;
+            codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            e[i] = 127;
+            if (slot >= 0 && slot < p.places) {
+                const int page = divide(slot, p.page_size, p.page_shift);
+                const int offset = slot - page * p.page_size;
+                codes[i] = *reinterpret_cast<const uint4*>(
+                    p.codes[kv] + page * p.code_stride[kv][0] + offset * p.code_stride[kv][1] +
+                    head * p.code_stride[kv][2] + ch * 16);
+                e[i] = p.scales[kv][page * p.scale_stride[kv][0] +
+                                    divide(offset, p.block, p.block_shift) * p.scale_stride[kv][1] +
+                                    head * p.scale_stride[kv][2]];
+            } else if (slot != -1 && kv == 0 && rest == 0) {
+                atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            if (to[i] == nullptr) continue;
+            const float by = scale_of(e[i]);
+            const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+            uint32_t out[8];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
+                const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
+                out[2 * h] = Half2<T>::pack(a.x * by, a.y * by);
+                out[2 * h + 1] = Half2<T>::pack(b.x * by, b.y * by);
+            }
+            reinterpret_cast<uint4*>(to[i])[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            reinterpret_cast<uint4*>(to[i])[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        }
+    }
+}
+
+template <typename T, int D>
+int quantize(const QuantizeParams& p, cudaStream_t stream)
+{
+    const int64_t windows = (static_cast<int64_t>(p.tokens) + p.window - 1) / p.window;
+    const int groups = (2 * p.heads + p.per - 1) / p.per;
+    const cudaError_t e = launch(quantize_cache_kernel<T, D>, dim3(static_cast<uint32_t>(windows), groups),
+                                 dim3(kWarps * 32), 0, stream, p);
+    if (e != cudaSuccess)
+        return fail(DECODE_ERR_CUDA, "quantize_cache_kernel: %s", cudaGetErrorString(e));
+    return DECODE_OK;
+}
+
+template <typename T, int D>
+int dequantize(const DequantizeParams& p, cudaStream_t stream)
+{
+    const int64_t blocks = (static_cast<int64_t>(p.tokens) + p.at_once - 1) / p.at_once;
+    const cudaError_t e = launch(dequantize_cache_kernel<T, D>, dim3(static_cast<uint32_t>(blocks)),
+                                 dim3(256), 0, stream, p);
+    if (e != cudaSuccess)
+        return fail(DECODE_ERR_CUDA, "dequantize_cache_kernel: %s", cudaGetErrorString(e));
+    return DECODE_OK;
+}
+
+// The checks of both calls; fills in what their parameters share.  Args: either argument struct.
+template <typename Args>
+int take_cache(CacheParams& p, int64_t (&half_stride)[2][2], const Args* a)
+{
+    if (a->dtype != DECODE_F16 && a->dtype != DECODE_BF16)
+        return fail(DECODE_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
+    if (a->tokens < 0) return fail(DECODE_ERR_INVALID_ARG, "negative size");
+    const int rc = check_cache(a->pages, a->page_size, a->block_size, a->h_k, a->head_dim);
+    if (rc != DECODE_OK || a->tokens == 0) return rc;
+    if (!a->k || !a->v || !a->slots || (a->pages > 0 && (!a->k_cache || !a->v_cache || !a->k_scale ||
+                                                         !a->v_scale)))
+        return fail(DECODE_ERR_INVALID_ARG, "null pointer");
+    if (misaligned(a->k) || misaligned(a->v) || misaligned(a->k_cache) || misaligned(a->v_cache))
+        return fail(DECODE_ERR_UNSUPPORTED, "keys, values and codes must be 16-byte aligned");
+    const int64_t rows[2] = {a->tokens, a->h_k};
+    if (!take_strides(half_stride[0], a->k_stride, rows, 8) ||
+        !take_strides(half_stride[1], a->v_stride, rows, 8))
+        return fail(DECODE_ERR_UNSUPPORTED, "strides of k and v must be multiples of 8");
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_k};
+    const int64_t ss[3] = {a->pages, a->page_size / a->block_size, a->h_k};
+    if (!take_strides(p.code_stride[0], a->k_cache_stride, cs, 16) ||
+        !take_strides(p.code_stride[1], a->v_cache_stride, cs, 16))
+        return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 16");
+    take_strides(p.scale_stride[0], a->k_scale_stride, ss, 1);
+    take_strides(p.scale_stride[1], a->v_scale_stride, ss, 1);
+    constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+    if (a->tokens > kMost - 64 || a->h_k > (1 << 15) || a->pages > kMost / a->page_size)
+        return fail(DECODE_ERR_UNSUPPORTED, "too many tokens, heads or places for one call");
+    p.codes[0] = static_cast<uint8_t*>(const_cast<void*>(static_cast<const void*>(a->k_cache)));
+    p.codes[1] = static_cast<uint8_t*>(const_cast<void*>(static_cast<const void*>(a->v_cache)));
+    p.scales[0] = static_cast<uint8_t*>(const_cast<void*>(static_cast<const void*>(a->k_scale)));
+    p.scales[1] = static_cast<uint8_t*>(const_cast<void*>(static_cast<const void*>(a->v_scale)));
+    p.slots = a->slots;
+    p.tokens = static_cast<int32_t>(a->tokens);
+    p.heads = static_cast<int32_t>(a->h_k);
+    p.page_size = static_cast<int32_t>(a->page_size);
+    p.page_shift = shift_of(a->page_size);
+    p.block = a->block_size;
+    p.block_shift = shift_of(a->block_size);
+    p.places = static_cast<int32_t>(a->pages * a->page_size);
+    return DECODE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_quantize_cache(const decode_quantize_cache_args* a, cudaStream_t stream)
+{
+    clear_error();
+    if (a == nullptr) return fail(DECODE_ERR_INVALID_ARG, "args is null");
+    QuantizeParams p{};
+    const int rc = take_cache(p, p.x_stride, a);
+    if (rc != DECODE_OK || a->tokens == 0) return rc;
+    const int64_t d = a->head_dim, rows[2] = {a->tokens, a->h_k};
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_k};
+    const int64_t ss[3] = {a->pages, a->page_size / a->block_size, a->h_k};
+    const int shared = refuse_shared({{"k_cache", a->k_cache, 1, d, cs, p.code_stride[0]},
+                                      {"v_cache", a->v_cache, 1, d, cs, p.code_stride[1]},
+                                      {"k_scale", a->k_scale, 1, 1, ss, p.scale_stride[0]},
+                                      {"v_scale", a->v_scale, 1, 1, ss, p.scale_stride[1]}},
+                                     {{"k", a->k, 2, d, rows, p.x_stride[0]},
+                                      {"v", a->v, 2, d, rows, p.x_stride[1]},
+                                      {"slots", a->slots, 4, a->tokens}});
+    if (shared != DECODE_OK) return shared;
+    const int sms = sm_count();
+    p.status = status_word();
+    if (sms == 0 || p.status == nullptr) return DECODE_ERR_CUDA;
+    p.x[0] = static_cast<const uint16_t*>(a->k);
+    p.x[1] = static_cast<const uint16_t*>(a->v);
+    p.per = 2 * p.heads < kWarps ? 2 * p.heads : kWarps;
+    // few tokens: each may be a block's only one, and has warps of its own
+    p.window = static_cast<int64_t>(p.tokens) * 2 * p.heads <= sms * 64 ? 1 : kWindow;
+    const bool bf16 = a->dtype == DECODE_BF16;
+    if (d == 64) return bf16 ? quantize<__nv_bfloat16, 64>(p, stream) : quantize<__half, 64>(p, stream);
+    if (d == 128)
+        return bf16 ? quantize<__nv_bfloat16, 128>(p, stream) : quantize<__half, 128>(p, stream);
+    return bf16 ? quantize<__nv_bfloat16, 256>(p, stream) : quantize<__half, 256>(p, stream);
+}
+
+int decode_dequantize_cache(const decode_dequantize_cache_args* a, cudaStream_t stream)
+{
+    clear_error();
+    if (a == nullptr) return fail(DECODE_ERR_INVALID_ARG, "args is null");
+    DequantizeParams p{};
+    const int rc = take_cache(p, p.y_stride, a);
+    if (rc != DECODE_OK || a->tokens == 0) return rc;
+    const int64_t d = a->head_dim, rows[2] = {a->tokens, a->h_k};
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_k};
+    const int64_t ss[3] = {a->pages, a->page_size / a->block_size, a->h_k};
+    const int shared = refuse_shared({{"k", a->k, 2, d, rows, p.y_stride[0]},
+                                      {"v", a->v, 2, d, rows, p.y_stride[1]}},
+                                     {{"k_cache", a->k_cache, 1, d, cs, p.code_stride[0]},
+                                      {"v_cache", a->v_cache, 1, d, cs, p.code_stride[1]},
+                                      {"k_scale", a->k_scale, 1, 1, ss, p.scale_stride[0]},
+                                      {"v_scale", a->v_scale, 1, 1, ss, p.scale_stride[1]},
+                                      {"slots", a->slots, 4, a->tokens}});
+    if (shared != DECODE_OK) return shared;
+    p.status = status_word();
+    if (p.status == nullptr) return DECODE_ERR_CUDA;
+    p.y[0] = static_cast<uint16_t*>(a->k);
+    p.y[1] = static_cast<uint16_t*>(a->v);
+    p.units = static_cast<int32_t>(2 * a->h_k * d / 16);
+    p.at_once = p.units < 1024 ? 1024 / p.units : 1;
+    p.magic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.units - 1) / p.units);
+    const bool bf16 = a->dtype == DECODE_BF16;
+    if (d == 64)
+        return bf16 ? dequantize<__nv_bfloat16, 64>(p, stream) : dequantize<__half, 64>(p, stream);
+    if (d == 128)
+        return bf16 ? dequantize<__nv_bfloat16, 128>(p, stream) : dequantize<__half, 128>(p, stream);
+    return bf16 ? dequantize<__nv_bfloat16, 256>(p, stream) : dequantize<__half, 256>(p, stream);
+}
+
+}  // extern "C"

@@ -41,6 +41,8 @@ const char* name_of(ScalarType t)
     case ScalarType::BFloat16: return "torch.bfloat16";
     case ScalarType::Float: return "torch.float32";
     case ScalarType::Int: return "torch.int32";
+    case ScalarType::Byte: return "torch.uint8";
+    case ScalarType::Float8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
     }
 }
@@ -459,6 +461,246 @@ PyObject* paged_attention(PyObject* const* args)
     return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
 
+// The codes and scales of an 8-bit cache [pages, page_size, heads, d] with scales [pages, blocks, heads]:
+// their sizes and strides in `a`, which has the same fields in every operator's arguments.
+struct Cache {
+    int64_t pages, page_size;
+    int32_t block;
+    Cache(PyObject* k_cache, PyObject* k_scale)
+    {
+        const Tensor &kc = tensor(k_cache, "k_cache"), &ks = tensor(k_scale, "k_scale");
+        if (kc.dim() != 4 || ks.dim() != 3)
+            refuse("the caches must be [pages, page_size, heads, d], the scales [pages, blocks, heads]");
+        pages = kc.size(0), page_size = kc.size(1);
+        const int64_t blocks = ks.size(1);
+        if (blocks < 1 || page_size % blocks != 0 || page_size / blocks > INT32_MAX)
+            refuse(std::to_string(blocks) + " scales do not share pages of " + std::to_string(page_size) +
+                   " tokens out");
+        block = static_cast<int32_t>(page_size / blocks);
+    }
+    // the codes of keys or values (E4M3, or their bytes), and their scales
+    void take(PyObject* cache, const char* name, PyObject* scale, const char* scale_name,
+              const at::Device& dev, int64_t heads, int64_t d, int64_t (&stride)[3],
+              int64_t (&scale_stride)[3], bool written) const
+    {
+        const Tensor &c = tensor(cache, name), &s = tensor(scale, scale_name);
+        check(c, name, c.scalar_type() == ScalarType::Byte ? ScalarType::Byte : ScalarType::Float8_e4m3fn,
+              dev, {pages, page_size, heads, d});
+        check(s, scale_name, ScalarType::Byte, dev, {pages, page_size / block, heads});
+        strides(c, name, stride);
+        for (int x = 0; x < 3; ++x) scale_stride[x] = s.stride(x);
+        if (!written) return;
+        separate(c, name);
+        separate(s.unsqueeze(3), scale_name);
+    }
+};
+
+// quantize_cache(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream)
+PyObject* quantize_cache(PyObject* const* args)
+{
+    const Tensor &k = tensor(args[0], "k"), &v = tensor(args[1], "v"), &slots = tensor(args[6], "slots");
+    decode_quantize_cache_args a{};
+    a.dtype = half_dtype(k);
+    if (k.dim() != 3) refuse("k and v must be [tokens, heads, head_dim]");
+    const auto dev = k.device();
+    a.tokens = k.size(0), a.h_k = k.size(1), a.head_dim = k.size(2);
+    check(v, "v", k.scalar_type(), dev, {a.tokens, a.h_k, a.head_dim});
+    strides(k, "k", a.k_stride);
+    strides(v, "v", a.v_stride);
+    const Cache cache(args[2], args[4]);
+    a.pages = cache.pages, a.page_size = cache.page_size, a.block_size = cache.block;
+    cache.take(args[2], "k_cache", args[4], "k_scale", dev, a.h_k, a.head_dim, a.k_cache_stride,
+               a.k_scale_stride, true);
+    cache.take(args[3], "v_cache", args[5], "v_scale", dev, a.h_k, a.head_dim, a.v_cache_stride,
+               a.v_scale_stride, true);
+    check(slots, "slots", ScalarType::Int, dev, {a.tokens});
+    contiguous(slots, "slots");
+    const Where on(args[7], dev);
+    a.k = source(k), a.v = source(v), a.slots = source<int32_t>(slots);
+    a.k_cache = pointer(THPVariable_Unpack(args[2])), a.v_cache = pointer(THPVariable_Unpack(args[3]));
+    a.k_scale = pointer(THPVariable_Unpack(args[4])), a.v_scale = pointer(THPVariable_Unpack(args[5]));
+    ok(decode_quantize_cache(&a, on.get()));
+    Py_RETURN_NONE;
+}
+
+// dequantize_cache(k_cache, v_cache, k_scale, v_scale, slots, float16, k_out, v_out, stream)
+PyObject* dequantize_cache(PyObject* const* args)
+{
+    const Tensor &kc = tensor(args[0], "k_cache"), &slots = tensor(args[4], "slots");
+    decode_dequantize_cache_args a{};
+    if (!kc.is_cuda()) refuse("operands must be CUDA tensors");
+    const auto dev = kc.device();
+    const Cache cache(args[0], args[2]);
+    a.pages = cache.pages, a.page_size = cache.page_size, a.block_size = cache.block;
+    a.h_k = kc.size(2), a.head_dim = kc.size(3);
+    cache.take(args[0], "k_cache", args[2], "k_scale", dev, a.h_k, a.head_dim, a.k_cache_stride,
+               a.k_scale_stride, false);
+    cache.take(args[1], "v_cache", args[3], "v_scale", dev, a.h_k, a.head_dim, a.v_cache_stride,
+               a.v_scale_stride, false);
+    if (slots.dim() != 1) refuse("slots must be [tokens]");
+    a.tokens = slots.size(0);
+    check(slots, "slots", ScalarType::Int, dev, {a.tokens});
+    contiguous(slots, "slots");
+    const bool half = truth(args[5]);
+    a.dtype = half ? DECODE_F16 : DECODE_BF16;
+    const ScalarType type = half ? ScalarType::Half : ScalarType::BFloat16;
+    for (const int x : {6, 7}) {
+        if (args[x] == Py_None) continue;
+        const char* name = x == 6 ? "k_out" : "v_out";
+        const Tensor& t = tensor(args[x], name);
+        check(t, name, type, dev, {a.tokens, a.h_k, a.head_dim});
+        strides(t, name, x == 6 ? a.k_stride : a.v_stride);
+        separate(t, name);
+    }
+    const Where on(args[8], dev);
+    Tensor out[2];
+    for (int x = 0; x < 2; ++x) {
+        if (args[6 + x] != Py_None) {
+            out[x] = THPVariable_Unpack(args[6 + x]);
+            continue;
+        }
+        out[x] = empty({a.tokens, a.h_k, a.head_dim}, type, dev);
+        auto& stride = x == 0 ? a.k_stride : a.v_stride;
+        stride[0] = a.h_k * a.head_dim, stride[1] = a.head_dim;
+    }
+    a.k_cache = source(kc), a.v_cache = source(THPVariable_Unpack(args[1]));
+    a.k_scale = source(THPVariable_Unpack(args[2])), a.v_scale = source(THPVariable_Unpack(args[3]));
+    a.slots = source<int32_t>(slots);
+    a.k = pointer(out[0]), a.v = pointer(out[1]);
+    ok(decode_dequantize_cache(&a, on.get()));
+    return Py_BuildValue("NN", THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
+}
+
+// paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale, window, sinks,
+//                     return_lse, out, workspace, stream)
+PyObject* paged_attention_fp8(PyObject* const* args)
+{
+    const Tensor &q = tensor(args[0], "q"), &kc = tensor(args[1], "k_cache"),
+                 &table = tensor(args[5], "page_table"), &lens = tensor(args[6], "lens");
+    decode_paged_attention_fp8_args a{};
+    a.dtype = half_dtype(q);
+    if (q.dim() != 3 || kc.dim() != 4 || table.dim() != 2)
+        refuse("q must be [n, h_q, d], the caches [pages, page_size, h_kv, d] and page_table "
+               "[n, width]");
+    const auto dev = q.device();
+    const ScalarType half = q.scalar_type();
+    const int64_t d = q.size(2);
+    a.n = q.size(0), a.h_q = q.size(1), a.head_dim = d;
+    const Cache cache(args[1], args[3]);
+    a.pages = cache.pages, a.page_size = cache.page_size, a.block_size = cache.block;
+    a.h_kv = kc.size(2), a.table_width = table.size(1);
+    cache.take(args[1], "k_cache", args[3], "k_scale", dev, a.h_kv, d, a.k_stride, a.k_scale_stride, false);
+    cache.take(args[2], "v_cache", args[4], "v_scale", dev, a.h_kv, d, a.v_stride, a.v_scale_stride, false);
+    check(table, "page_table", ScalarType::Int, dev, {a.n, a.table_width});
+    check(lens, "lens", ScalarType::Int, dev, {a.n});
+    contiguous(lens, "lens");
+    strides(q, "q", a.q_stride);
+    int64_t table_stride[1];
+    strides(table, "page_table", table_stride);
+    a.table_stride = table_stride[0];
+    a.scale = args[7] == Py_None ? 1.0f / std::sqrt(static_cast<float>(d))
+                                 : static_cast<float>(number(args[7]));
+    a.sinks = integer(args[9]);
+    if (a.sinks < 0) refuse("sinks must be at least 0");
+    if (args[8] != Py_None) {
+        a.window = integer(args[8]);
+        if (a.window < 1) refuse("window must be at least 1");
+    } else if (a.sinks > 0) {
+        refuse("sinks come with a window");
+    }
+    if (args[11] != Py_None) {
+        check(tensor(args[11], "out"), "out", half, dev, {a.n, a.h_q, d});
+        contiguous(tensor(args[11], "out"), "out");
+    }
+    if (args[12] != Py_None) {
+        const Tensor& w = tensor(args[12], "workspace");
+        if (w.device() != dev || !w.is_contiguous())
+            refuse("workspace must be a contiguous tensor on " + dev.str());
+    }
+    const Where on(args[13], dev);
+    const Tensor out = args[11] != Py_None ? THPVariable_Unpack(args[11])
+                                           : empty({a.n, a.h_q, d}, half, dev);
+    Tensor lse, workspace;
+    if (truth(args[10])) {
+        lse = empty({a.n, a.h_q}, ScalarType::Float, dev);
+        a.lse = pointer<float>(lse);
+    }
+    if (args[12] != Py_None) {
+        workspace = THPVariable_Unpack(args[12]);
+    } else {
+        size_t bytes = 0;
+        ok(decode_paged_attention_fp8_workspace_bytes(a.h_q, a.h_kv, d, &bytes));
+        workspace = empty({static_cast<int64_t>(bytes)}, ScalarType::Byte, dev);
+    }
+    a.q = source(q), a.k_cache = source(kc), a.v_cache = source(THPVariable_Unpack(args[2]));
+    a.k_scale = source(THPVariable_Unpack(args[3])), a.v_scale = source(THPVariable_Unpack(args[4]));
+    a.page_table = source<int32_t>(table), a.lens = source<int32_t>(lens);
+    a.o = pointer(out);
+    a.workspace = pointer(workspace);
+    a.workspace_bytes = static_cast<int64_t>(workspace.nbytes());
+    ok(decode_paged_attention_fp8(&a, on.get()));
+    if (!lse.defined()) return THPVariable_Wrap(out);
+    return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
+}
+
+// linear_w4(x, codes, scales, group, zeros, bias, activation, out, stream)
+PyObject* linear_w4(PyObject* const* args)
+{
+    const Tensor &x = tensor(args[0], "x"), &codes = tensor(args[1], "codes"),
+                 &scales = tensor(args[2], "scales");
+    decode_linear_w4_args a{};
+    a.dtype = half_dtype(x);
+    if (x.dim() != 2 || codes.dim() != 2) refuse("x must be [tokens, K] and codes [N, K / 2]");
+    const auto dev = x.device();
+    const ScalarType half = x.scalar_type();
+    a.m = x.size(0), a.k = x.size(1), a.n = codes.size(0);
+    a.group = integer(args[3]);
+    if (a.group < 1) refuse("group must be at least 1");
+    if (a.k % 2 != 0) refuse("K must be even");
+    const int64_t groups = a.k / a.group + (a.k % a.group != 0);
+    int64_t stride[1];
+    auto row_stride = [&](const Tensor& t, const char* name) {
+        strides(t, name, stride);
+        return stride[0];
+    };
+    check(codes, "codes", ScalarType::Byte, dev, {a.n, a.k / 2});
+    check(scales, "scales", half, dev, {a.n, groups});
+    a.x_stride = row_stride(x, "x");
+    a.code_stride = row_stride(codes, "codes");
+    a.scale_stride = row_stride(scales, "scales");
+    if (args[4] != Py_None) {
+        const Tensor& zeros = tensor(args[4], "zeros");
+        check(zeros, "zeros", ScalarType::Byte, dev, {a.n, groups});
+        a.zero_stride = row_stride(zeros, "zeros");
+        a.zeros = source(zeros);
+    }
+    if (args[5] != Py_None) {
+        const Tensor& bias = tensor(args[5], "bias");
+        check(bias, "bias", half, dev, {a.n});
+        contiguous(bias, "bias");
+        a.bias = source(bias);
+    }
+    a.activation = static_cast<int32_t>(integer(args[6]));
+    if (args[7] != Py_None) {
+        const Tensor& out = tensor(args[7], "out");
+        check(out, "out", half, dev, {a.m, a.n});
+        a.y_stride = row_stride(out, "out");
+        separate(out, "out");
+    }
+    const Where on(args[8], dev);
+    Tensor out;
+    if (args[7] != Py_None) {
+        out = THPVariable_Unpack(args[7]);
+    } else {
+        out = empty({a.m, a.n}, half, dev);
+        a.y_stride = a.n;
+    }
+    a.x = source(x), a.codes = source(codes), a.scales = source(scales);
+    a.y = pointer(out);
+    ok(decode_linear_w4(&a, on.get()));
+    return THPVariable_Wrap(out);
+}
+
 // The Python entry: a fixed number of positional arguments (decode.py has the signatures), and every
 // C++ exception turned into Python's.
 template <PyObject* (*kFunction)(PyObject* const*), Py_ssize_t kArguments>
@@ -484,6 +726,12 @@ PyMethodDef methods[] = {
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(entry<qk_norm_rope, 17>), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(entry<paged_attention, 11>), METH_FASTCALL,
      nullptr},
+    {"quantize_cache", reinterpret_cast<PyCFunction>(entry<quantize_cache, 8>), METH_FASTCALL, nullptr},
+    {"dequantize_cache", reinterpret_cast<PyCFunction>(entry<dequantize_cache, 9>), METH_FASTCALL,
+     nullptr},
+    {"paged_attention_fp8", reinterpret_cast<PyCFunction>(entry<paged_attention_fp8, 14>), METH_FASTCALL,
+     nullptr},
+    {"linear_w4", reinterpret_cast<PyCFunction>(entry<linear_w4, 9>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_decode", nullptr, -1, methods,

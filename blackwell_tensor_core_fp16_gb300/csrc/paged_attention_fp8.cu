@@ -1,0 +1,652 @@
+// Attention of one new token per sequence over a paged cache of E4M3 codes with an E8M0 scale for each
+// block of tokens and head, with a sliding window and first tokens that stay visible (C ABI in
+// include/decode.h):
+//
+//     s_t = scale q . K_t;   o = sum_t exp(s_t - m) V_t / sum_t exp(s_t - m)
+//
+// The split of the work over the blocks, the ring of stages and the joins are those of the 16-bit
+// cache (paged_attention.cu).  A key and a value take 2 d bytes here, half of that, for the same
+// products, and their codes have to become 16-bit numbers on the way: the cache is still read once and
+// HBM bounds the time, but with less room for instructions.  What differs:
+//
+// Codes become float16, which holds every one exactly, after they have come to the registers.
+// ldmatrix moves pairs of bytes: of keys a lane gets four neighbouring elements of a token's row, which
+// are taken as two steps' operands (the queries' elements are dealt to steps in the same order), of
+// values, transposed, two tokens' two neighbouring elements, whose bytes a permutation sorts by
+// element; rows r and r + 8 of a tile stand for elements 2 r and 2 r + 1.
+//
+// Scales are read for each token of a slice (a byte each of keys and values), a slice ahead, and wait
+// beside its stage as numbers, so blocks may have any size.  A key's scale multiplies its scores.  A
+// value's goes into its weight: times 2^15 over the slice's largest scale, by which the slice's sums
+// are multiplied when they are added to the running ones, so a weight fits float16 whatever the scales.
+// It is carried as two float16 pieces, 22 bits, which leave out less than 2^-22 of it or 2^-40 of the
+// slice's largest.
+//
+// bfloat16 queries become float16 too, each head's divided by a power of two that brings its largest
+// element between 2^14 and 2^15: no bit is lost of elements above 2^-31 of the largest, and of smaller
+// ones less than 2^-38 of it.
+//
+// With a window the seen tokens are two ranges.  They are laid one after the other on one axis of rows,
+// the first tokens' range rounded up and the window's start down to 16, so that 16 rows lie in one
+// range, and the axis is cut into tiles as any other.
+#include <type_traits>
+
+#include "fp8.cuh"
+#include "paged_common.cuh"
+
+namespace {
+
+using namespace decode;
+
+struct Fp8Params : SplitParams {
+    const uint16_t* q;
+    const uint8_t* k;
+    const uint8_t* v;
+    const uint8_t* scale[2];           // keys', values'
+    const int32_t* table;
+    int64_t q_stride[2], k_stride[3], v_stride[3], scale_stride[2][3];
+    int64_t table_stride;
+    int32_t pages, page_size, page_shift, block, block_shift, window, sinks;
+    float scale_log2;
+};
+
+// A sequence's seen tokens: t < first and start <= t < len; len = 0 for a length the page table cannot
+// hold.  Row r of the axis is token r below `edge` and token r + gap from there on.
+struct Fp8Span {
+    int start, len, first, edge, gap;
+    __device__ __forceinline__ int rows() const { return len - gap; }
+    __device__ __forceinline__ int token(int row) const { return row < edge ? row : row + gap; }
+    __device__ __forceinline__ bool seen(int t) const { return t < len && (t >= start || t < first); }
+};
+__device__ __forceinline__ Fp8Span span_of(const Fp8Params& p, int i)
+{
+    Fp8Span s;
+    s.len = p.lens[i];
+    if (s.len < 0 || s.len > p.max_len) s.len = 0;
+    s.start = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
+    s.first = min(p.sinks, s.start);
+    s.edge = (s.first + kSub - 1) & ~(kSub - 1);
+    const int origin = s.start & ~(kSub - 1);
+    s.gap = max(origin - s.edge, 0);               // none where the ranges' 16 rows meet
+    return s;
+}
+
+template <int D, int kTiles>
+struct Fp8Cfg {
+    static constexpr int kD = D, kHeadTiles = kTiles;
+    static constexpr int kWarps = D == 256 && kTiles == 2 ? 2 : 4;   // (the join needs room by them)
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kHeads = 8 * kHeadTiles;
+    static constexpr int kSubs = 256 / D;                     // a slice is 8 KB
+    template <typename T>
+    static constexpr int kShift = 0;                          // (the sums carry no factor)
+    static constexpr bool kRowPairs = true;
+    static constexpr int kResident = 2;                       // blocks of an SM
+    static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
+    static constexpr int kTile = kWarps * kSlice;
+    static constexpr int kScaleBytes = (2 * kSlice + 4) * 4;  // keys', values', the values' largest
+    static constexpr int kCodeBytes = 2 * kSlice * D;         // keys, then values
+    static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+    static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
+    static constexpr int kMergeBytes = kWarps * kHeads * kMergeRow * 4;
+    static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
+    // the queries stay in registers, but for the one shape whose sums leave no room for them
+    static constexpr bool kQueriesShared = D == 256 && kTiles == 2;
+    static constexpr int kQueryRow = D + 16;                  // elements
+    static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 + kHeads * 4 : 0;
+    // (the blocks share an SM's 228 KB, of which the system takes 1 KB a block)
+    static constexpr int kRoom =
+        233472 / kResident - 1024 - kMergeBytes - kSmallBytes - kQueryBytes;
+    static constexpr int kMostStages = kRoom / (kWarps * kStageBytes);
+    static constexpr int kStages = kMostStages < 4 ? kMostStages : 4;
+    static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
+                                 kQueryBytes;
+    static_assert(kStages >= 2, "no room for two stages");
+    // where a 16-byte piece of a row lies, so that 8 rows' pieces lie in 8 different bank groups
+    __device__ static __forceinline__ int place(int row, int piece)
+    {
+        return row * D + ((piece ^ (D == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+    }
+};
+
+// kCluster: one cluster an item, for few items of few tiles.
+template <typename T, int D, int kHeadTiles, bool kCluster>
+__global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHeadTiles>::kResident)
+    paged_attention_fp8_kernel(const Fp8Params p)
+{
+    using C = Fp8Cfg<D, kHeadTiles>;
+    using H = __half;                              // what codes, queries and weights become
+    constexpr int kHeads = C::kHeads, kWarps = C::kWarps, kTile = C::kTile;
+    constexpr int kSlice = C::kSlice, kSubs = C::kSubs;
+    constexpr int kChunks = D / 16;                // 16-byte pieces of a row
+    constexpr int kRowsPerCopy = 32 / kChunks;     // rows that one cp.async of the warp covers
+    constexpr uint32_t kAll = 0xffffffffu;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* ring = smem;
+    float* merge = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStageBytes);
+    float* sm_m = merge + C::kMergeBytes / 4;      // [kWarps][kHeads]
+    float* sm_l = sm_m + kWarps * kHeads;
+    int* sm_i = reinterpret_cast<int*>(sm_l + kWarps * kHeads);   // 64 words
+    uint16_t* sm_q = reinterpret_cast<uint16_t*>(sm_i + 64);      // [kHeads][kQueryRow]
+    float* sm_q_scale = reinterpret_cast<float*>(sm_q + kHeads * C::kQueryRow);   // [kHeads]
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+
+    dep_launch();
+    dep_wait();
+
+    Cursor<Fp8Span> cur;
+    Range r;
+    if constexpr (kCluster) {
+        if (!cluster_range<C>(p, cur, r, sm_i)) return;
+    } else {
+        if (!block_range<C>(p, cur, r, sm_i)) return;
+    }
+    const int t0 = r.t0, t1 = r.t1;
+    Cursor<Fp8Span> pre = cur;                     // where the loads are
+    int pre_t = t0;
+
+    // ---- loads of a slice.  The places in the cache of its 16-row pieces are looked up one slice
+    // ahead: that of the first row where pages are multiples of 16 tokens, else that of row
+    // `lane & 15`.
+    uint8_t* const mine = ring + w * C::kStages * C::kCodeBytes;
+    const uint32_t ring0 = smem_addr(mine);
+    float* const scales0 = reinterpret_cast<float*>(ring + kWarps * C::kStages * C::kCodeBytes +
+                                                    w * C::kStages * C::kScaleBytes);
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    const bool whole_pages = p.page_size % kSub == 0;
+    const int ahead = whole_pages ? 0 : lane & 15;
+    int page[kSubs], off[kSubs];
+    bool there[kSubs];                             // the place is one of the sequence's
+    auto look_up = [&]() {
+#pragma unroll
+        for (int y = 0; y < kSubs; ++y) {
+            there[y] = false;
+            if (pre_t >= t1) continue;
+            const int row = pre.tile * kTile + w * kSlice + y * kSub;
+            const int pos = pre.span.token(row) + ahead;
+            if (row >= pre.span.rows() || pos >= pre.span.len || (!whole_pages && !pre.span.seen(pos)))
+                continue;
+            there[y] = true;
+            const int x = divide(pos, p.page_size, p.page_shift);
+            off[y] = pos - x * p.page_size;
+            page[y] = p.table[pre.i * p.table_stride + x];
+        }
+    };
+    // The scales of a slice: lanes 0 to 15 read a piece's keys', the others its values'.  They are on
+    // their way while the lane goes on and are put down (as what a score is multiplied by, and as
+    // 2^15 over the largest) at the next load.
+    int scale_byte[kSubs], scale_stage = -1;
+    uint32_t scale_seen = 0;
+    auto put_scales = [&]() {
+        if (scale_stage < 0) return;
+        int largest = 0;
+#pragma unroll
+        for (int y = 0; y < kSubs; ++y)
+            if (lane >= kSub && (scale_seen >> y & 1)) largest = max(largest, scale_byte[y]);
+        largest = __reduce_max_sync(kAll, largest);
+        float* const to = scales0 + scale_stage * (C::kScaleBytes / 4);
+#pragma unroll
+        for (int y = 0; y < kSubs; ++y) {
+            const int e = scale_byte[y];
+            float f = 0.f;                         // of an unseen token
+            if (scale_seen >> y & 1) {
+                if (lane < kSub)
+                    f = scale_of(e) * p.scale_log2;
+                else
+                    f = e == 255 ? NAN : largest - e < 142 ? power_of(142 - largest + e) : 0.f;
+            }
+            to[(lane < kSub ? 0 : kSlice - kSub) + y * kSub + lane] = f;
+        }
+        if (lane == 0) to[2 * kSlice] = power_of(largest - 15);
+    };
+    auto load = [&](int stage) {
+        put_scales();
+        scale_stage = -1;
+        if (pre_t < t1) {
+            const int kv = pre.item / p.head_items;
+            const uint8_t* k0 = p.k + kv * p.k_stride[2] + ch * 16;
+            const uint8_t* v0 = p.v + kv * p.v_stride[2] + ch * 16;
+            scale_stage = stage;
+            scale_seen = 0;
+#pragma unroll
+            for (int y = 0; y < kSubs; ++y) {
+                if (there[y] && (page[y] < 0 || page[y] >= p.pages)) {
+                    atomicOr(p.status, DECODE_BAD_PAGE);
+                    there[y] = false;
+                }
+                const int row0 = pre.tile * kTile + w * kSlice + y * kSub;
+                const int pos0 = pre.span.token(row0);
+                const int of = lane >= kSub;       // the tensor whose scale the lane reads
+                scale_byte[y] = 0;
+                if (there[y] && pre.span.seen(pos0 + (lane & 15))) {
+                    const int o = off[y] + (whole_pages ? lane & 15 : 0);
+                    scale_byte[y] = p.scale[of][page[y] * p.scale_stride[of][0] +
+                                                divide(o, p.block, p.block_shift) * p.scale_stride[of][1] +
+                                                kv * p.scale_stride[of][2]];
+                    scale_seen |= 1u << y;
+                }
+                const int64_t ko = !there[y] ? 0 : page[y] * p.k_stride[0] + off[y] * p.k_stride[1];
+                const int64_t vo = !there[y] ? 0 : page[y] * p.v_stride[0] + off[y] * p.v_stride[1];
+                const uint32_t dst0 = ring0 + stage * C::kCodeBytes;
+                if (whole_pages) {
+                    const uint8_t* kb = k0 + ko + sub * p.k_stride[1];
+                    const uint8_t* vb = v0 + vo + sub * p.v_stride[1];
+                    const int64_t ks = kRowsPerCopy * p.k_stride[1], vs = kRowsPerCopy * p.v_stride[1];
+#pragma unroll
+                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
+                        const int row = x * kRowsPerCopy + sub;
+                        const uint32_t bytes = there[y] && pre.span.seen(pos0 + row) ? 16u : 0u;
+                        const uint32_t dst = dst0 + C::place(y * kSub + row, ch);
+                        cp_async16(dst, bytes ? kb : p.k, bytes);
+                        cp_async16(dst + kSlice * D, bytes ? vb : p.v, bytes);
+                        kb += ks;
+                        vb += vs;
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
+                        const int row = x * kRowsPerCopy + sub;
+                        const int64_t k1 = __shfl_sync(kAll, ko, row);
+                        const int64_t v1 = __shfl_sync(kAll, vo, row);
+                        const bool have = __shfl_sync(kAll, there[y], row);
+                        const uint32_t bytes = have ? 16u : 0u;
+                        const uint32_t dst = dst0 + C::place(y * kSub + row, ch);
+                        cp_async16(dst, bytes ? k0 + k1 : p.k, bytes);
+                        cp_async16(dst + kSlice * D, bytes ? v0 + v1 : p.v, bytes);
+                    }
+                }
+            }
+            ++pre_t;
+            if constexpr (kCluster)
+                ++pre.tile;
+            else
+                advance<kTile>(pre, p);
+        }
+        cp_commit();
+        look_up();
+    };
+    look_up();
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) load(s);
+
+    // ---- the tiles
+    constexpr int kOwn = C::kQueriesShared ? 1 : kHeadTiles;      // head tiles of queries in registers
+    uint32_t qf[kOwn][D / 16][2];
+    float q_scale[kHeadTiles][2];                  // what the lane's two heads' queries were divided by
+    float acc[kHeadTiles][D / 16][4];
+    float m[kHeadTiles][2], l[kHeadTiles][2];
+    bool fresh = true;
+    int stage = 0;
+    // the queries of an item's head tile x: of 16 elements a lane holds four neighbouring ones of head
+    // lane / 4
+    auto load_queries = [&](const Cursor<Fp8Span>& of, int x, uint32_t (&f)[D / 16][2]) {
+        const int kv = of.item / p.head_items;
+        const int first = of.item % p.head_items * kHeads, heads = min(kHeads, p.group - first);
+        const int h = x * 8 + (lane >> 2);
+        const uint16_t* row = p.q + of.i * p.q_stride[0] +
+                              (kv * p.group + first + h) * p.q_stride[1] + (lane & 3) * 4;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const uint2 b = h < heads ? *reinterpret_cast<const uint2*>(row + d * 16)
+                                      : make_uint2(0u, 0u);
+            f[d][0] = b.x;
+            f[d][1] = b.y;
+        }
+    };
+    // makes them float16; what head lane / 4 was divided by
+    auto convert_queries = [&](uint32_t (&f)[D / 16][2]) {
+        if constexpr (std::is_same<T, __half>::value) return 1.f;
+        uint32_t top = 0;                          // the largest exponent of a finite element
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t lo = f[d][e] >> 7 & 0xffu, hi = f[d][e] >> 23 & 0xffu;
+                top = max(top, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
+            }
+        top = max(top, __shfl_xor_sync(kAll, top, 1));
+        top = max(top, __shfl_xor_sync(kAll, top, 2));
+        const int up = min(268 - static_cast<int>(top), 253);
+        const float by = power_of(up);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float2 v = Half2<T>::unpack(f[d][e]);
+                f[d][e] = Half2<H>::pack(v.x * by, v.y * by);
+            }
+        return power_of(254 - up);
+    };
+    auto begin_item = [&]() {
+        if constexpr (C::kQueriesShared) {
+            // (every warp has passed the barrier that ends the item before)
+            for (int x = w; x < kHeadTiles; x += kWarps) {
+                load_queries(cur, x, qf[0]);
+                const float back = convert_queries(qf[0]);
+                uint16_t* row = sm_q + (x * 8 + (lane >> 2)) * C::kQueryRow + (lane & 3) * 4;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+                    *reinterpret_cast<uint2*>(row + d * 16) = make_uint2(qf[0][d][0], qf[0][d][1]);
+                if (lane % 4 == 0) sm_q_scale[x * 8 + (lane >> 2)] = back;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) q_scale[x][e] = sm_q_scale[x * 8 + (lane & 3) * 2 + e];
+        } else {
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
+                const float back = convert_queries(qf[x]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    q_scale[x][e] = std::is_same<T, H>::value
+                                        ? 1.f
+                                        : __shfl_sync(kAll, back, ((lane & 3) * 2 + e) * 4);
+            }
+        }
+    };
+    auto load_all_queries = [&](const Cursor<Fp8Span>& of) {
+        if constexpr (!C::kQueriesShared)
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) load_queries(of, x, qf[x]);
+    };
+    load_all_queries(cur);
+    for (int t = t0; t < t1; ++t) {
+        if (fresh) {
+            fresh = false;
+            begin_item();
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+                    acc[x][d][0] = acc[x][d][1] = acc[x][d][2] = acc[x][d][3] = 0.f;
+                m[x][0] = m[x][1] = -INFINITY;
+                l[x][0] = l[x][1] = 0.f;
+            }
+        }
+        __syncwarp();
+        load((stage + C::kStages - 1) % C::kStages);
+        cp_wait<C::kStages - 1>();
+        __syncwarp();
+
+        const int row0 = cur.tile * kTile + w * kSlice;
+        if (row0 < cur.span.rows()) {
+            const uint32_t ks = ring0 + stage * C::kCodeBytes, vs = ks + kSlice * D;
+            const float* const scales = scales0 + stage * (C::kScaleBytes / 4);
+            const int sel = lane >> 3;
+            float s[kHeadTiles][kSubs][4];
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int y = 0; y < kSubs; ++y)
+                    s[x][y][0] = s[x][y][1] = s[x][y][2] = s[x][y][3] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 16; d += 2) {
+                [[maybe_unused]] uint2 qs[2][kHeadTiles];
+                if constexpr (C::kQueriesShared) {
+#pragma unroll
+                    for (int z = 0; z < 2; ++z)
+#pragma unroll
+                        for (int x = 0; x < kHeadTiles; ++x)
+                            qs[z][x] = *reinterpret_cast<const uint2*>(
+                                sm_q + (x * 8 + (lane >> 2)) * C::kQueryRow + (d + z) * 16 +
+                                (lane & 3) * 4);
+                }
+#pragma unroll
+                for (int y = 0; y < kSubs; ++y) {
+                    uint32_t two[4];               // rows 0 .. 7 and 8 .. 15 of elements d, of d + 1
+                    ldsm4(two, ks + C::place(y * kSub + (lane & 15), d + (sel >> 1)));
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t a[4] = {codes_to_half2(two[2 * z]), codes_to_half2(two[2 * z + 1]),
+                                               codes_to_half2(two[2 * z] >> 16),
+                                               codes_to_half2(two[2 * z + 1] >> 16)};
+#pragma unroll
+                        for (int x = 0; x < kHeadTiles; ++x) {
+                            if constexpr (C::kQueriesShared)
+                                mma<H>(s[x][y], a, qs[z][x].x, qs[z][x].y);
+                            else
+                                mma<H>(s[x][y], a, qf[x][d + z][0], qf[x][d + z][1]);
+                        }
+                    }
+                }
+            }
+            // the lane's rows are row0 + 8 j + lane / 4
+            bool in[2 * kSubs];
+            float k_scale[2 * kSubs], v_scale[2 * kSubs];
+#pragma unroll
+            for (int j = 0; j < 2 * kSubs; ++j) {
+                const int row = row0 + j * 8 + (lane >> 2);
+                in[j] = cur.span.seen(cur.span.token(row));
+                k_scale[j] = scales[j * 8 + (lane >> 2)];
+                v_scale[j] = scales[kSlice + j * 8 + (lane >> 2)];
+            }
+            const float slice_scale = scales[2 * kSlice];
+            uint32_t pb[kHeadTiles][kSubs][2][2];  // [piece][rows 0 .. 7, 8 .. 15]
+            float corr[kHeadTiles][2];
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 2 * kSubs; ++j) {
+                        float& v = s[x][j / 2][j % 2 * 2 + e];
+                        v = in[j] ? v * q_scale[x][e] * k_scale[j] : -INFINITY;
+                        top = fmaxf(top, v);
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
+                    top = fmaxf(top, m[x][e]);
+                    // scores of -infinity only: any finite reference leaves their weights 0
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    corr[x][e] = exp2_fast(m[x][e] - ref);
+                    m[x][e] = top;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 2 * kSubs; ++j) {
+                        float& v = s[x][j / 2][j % 2 * 2 + e];
+                        v = exp2_fast(v - ref);
+                        sum += v;
+                        v *= v_scale[j];
+                    }
+                    l[x][e] = fmaf(l[x][e], corr[x][e], sum);
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * kSubs; ++j) {
+                    const float v0 = s[x][j / 2][j % 2 * 2], v1 = s[x][j / 2][j % 2 * 2 + 1];
+                    const uint32_t piece = Half2<H>::pack(v0, v1);
+                    const float2 f = Half2<H>::unpack(piece);
+                    pb[x][j / 2][0][j % 2] = transpose8x8(piece);
+                    pb[x][j / 2][1][j % 2] = transpose8x8(Half2<H>::pack(v0 - f.x, v1 - f.y));
+                }
+            }
+            // a slice's products are summed on their own and added to the rescaled sums: a matrix
+            // product cuts its sum's last bits off, which would add up over a long axis
+#pragma unroll
+            for (int d = 0; d < D / 16; d += 2) {
+                float o[2][kHeadTiles][4] = {};
+#pragma unroll
+                for (int y = 0; y < kSubs; ++y) {
+                    uint32_t two[4];               // tokens 0 .. 7 and 8 .. 15 of elements d, of d + 1
+                    ldsm4_trans(two, vs + C::place(y * kSub + (lane & 15), d + (sel >> 1)));
+                    uint32_t a[2][4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const uint32_t sorted = __byte_perm(two[z], 0u, 0x3120);
+                        a[z / 2][z % 2 * 2] = codes_to_half2(sorted);
+                        a[z / 2][z % 2 * 2 + 1] = codes_to_half2(sorted >> 16);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+#pragma unroll
+                            for (int x = 0; x < kHeadTiles; ++x)
+                                mma<H>(o[z][x], a[z], pb[x][y][c][0], pb[x][y][c][1]);
+                }
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float* const sum = acc[x][d + z] + e;
+                            const uint64_t old = mul2(pair(sum[0], sum[1]), pair(corr[x][0], corr[x][1]));
+                            const float2 f = halves(fma2(pair(o[z][x][e], o[z][x][e + 1]),
+                                                         pair(slice_scale, slice_scale), old));
+                            sum[0] = f.x, sum[1] = f.y;
+                        }
+            }
+        }
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
+        // ---- the item's end, or the range's: join the warps (the next item's queries are on their way)
+        const bool item_ends = cur.tile + 1 == cur.tiles;
+        Cursor<Fp8Span> next = cur;
+        if (!kCluster && t + 1 < t1) advance<kTile>(next, p);
+        if (!kCluster && item_ends && t + 1 < t1) load_all_queries(next);
+        if (item_ends || t + 1 == t1) {
+            join_warps<T, C, kCluster>(p, cur, r, t, acc, m, l, merge, sm_m, sm_l, sm_i);
+            fresh = true;
+        }
+        if (!kCluster)
+            cur = next;
+        else if (t + 1 < t1)
+            ++cur.tile;
+    }
+    if constexpr (kCluster) join_cluster<T, C>(p, cur, merge, sm_i);
+}
+
+template <typename T, int D, int kHeadTiles>
+int run(const Fp8Params& p, int64_t most_tokens, int sms, cudaStream_t stream)
+{
+    return launch_attention<T, Fp8Cfg<D, kHeadTiles>,
+                            paged_attention_fp8_kernel<T, D, kHeadTiles, false>,
+                            paged_attention_fp8_kernel<T, D, kHeadTiles, true>>(p, most_tokens, sms,
+                                                                               stream);
+}
+
+template <typename T>
+int dispatch(const Fp8Params& p, int64_t d, int64_t most, int sms, cudaStream_t s)
+{
+    const bool two = p.group > 8;
+    if (d == 64) return two ? run<T, 64, 2>(p, most, sms, s) : run<T, 64, 1>(p, most, sms, s);
+    if (d == 128) return two ? run<T, 128, 2>(p, most, sms, s) : run<T, 128, 1>(p, most, sms, s);
+    return two ? run<T, 256, 2>(p, most, sms, s) : run<T, 256, 1>(p, most, sms, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int decode_paged_attention_fp8_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t head_dim,
+                                               size_t* bytes)
+{
+    clear_error();
+    if (bytes == nullptr) return fail(DECODE_ERR_INVALID_ARG, "bytes is null");
+    const int rc = check_heads(h_q, h_kv, head_dim);
+    if (rc != DECODE_OK) return rc;
+    const int sms = sm_count();
+    if (sms == 0) return DECODE_ERR_CUDA;
+    *bytes = layout_for(sms, heads_of(h_q / h_kv), head_dim).total;
+    return DECODE_OK;
+}
+
+int decode_paged_attention_fp8(const decode_paged_attention_fp8_args* a, cudaStream_t stream)
+{
+    clear_error();
+    if (a == nullptr) return fail(DECODE_ERR_INVALID_ARG, "args is null");
+    if (a->n < 0 || a->table_width < 0 || a->window < 0 || a->sinks < 0)
+        return fail(DECODE_ERR_INVALID_ARG, "negative size");
+    if (a->dtype != DECODE_F16 && a->dtype != DECODE_BF16)
+        return fail(DECODE_ERR_INVALID_ARG, "unknown dtype %d", a->dtype);
+    int rc = check_heads(a->h_q, a->h_kv, a->head_dim);
+    if (rc == DECODE_OK) rc = check_cache(a->pages, a->page_size, a->block_size, a->h_kv, a->head_dim);
+    if (rc != DECODE_OK || a->n == 0) return rc;
+    if (!a->q || !a->o || !a->lens || !a->workspace ||
+        (a->table_width > 0 && a->pages > 0 &&
+         (!a->k_cache || !a->v_cache || !a->k_scale || !a->v_scale || !a->page_table)))
+        return fail(DECODE_ERR_INVALID_ARG, "null pointer");
+    if (misaligned(a->q) || misaligned(a->k_cache) || misaligned(a->v_cache) || misaligned(a->o) ||
+        misaligned(a->workspace))
+        return fail(DECODE_ERR_UNSUPPORTED, "16-bit tensors, codes and workspace must be 16-byte aligned");
+    Fp8Params p{};
+    if (!take_strides(p.q_stride, a->q_stride, {a->n, a->h_q}, 8))
+        return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
+    const int64_t cs[3] = {a->pages, a->page_size, a->h_kv};
+    const int64_t ss[3] = {a->pages, a->page_size / a->block_size, a->h_kv};
+    if (!take_strides(p.k_stride, a->k_stride, cs, 16) ||
+        !take_strides(p.v_stride, a->v_stride, cs, 16))
+        return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 16");
+    take_strides(p.scale_stride[0], a->k_scale_stride, ss, 1);
+    take_strides(p.scale_stride[1], a->v_scale_stride, ss, 1);
+    constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+    if (a->n > kMost || a->h_q >= (1 << 20) || a->table_width > kMost)
+        return fail(DECODE_ERR_UNSUPPORTED, "problem too large for one call");
+    const int sms = sm_count();
+    if (sms == 0) return DECODE_ERR_CUDA;
+    const int64_t group = a->h_q / a->h_kv;
+    const int heads = heads_of(group);
+    const Layout l = layout_for(sms, heads, a->head_dim);
+    if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < l.total)
+        return fail(DECODE_ERR_INVALID_ARG, "workspace of %zu bytes needed", l.total);
+    // (an item's queries are in registers, in all of its blocks, before its results are written)
+    const int64_t d = a->head_dim, sizes[2] = {a->n, a->h_q}, dense[2] = {a->h_q * d, d};
+    const int shared = refuse_shared(
+        {{"o", a->o, 2, d, sizes, dense, "q"},
+         {"lse", a->lse, 4, a->n * a->h_q},
+         {"workspace", a->workspace, 1, static_cast<int64_t>(l.total)}},
+        {{"q", a->q, 2, d, sizes, p.q_stride},
+         {"k_cache", a->k_cache, 1, d, cs, p.k_stride},
+         {"v_cache", a->v_cache, 1, d, cs, p.v_stride},
+         {"k_scale", a->k_scale, 1, 1, ss, p.scale_stride[0]},
+         {"v_scale", a->v_scale, 1, 1, ss, p.scale_stride[1]},
+         {"page_table", a->page_table, 4, a->table_width, {a->n}, {a->table_stride}},
+         {"lens", a->lens, 4, a->n}});
+    if (shared != DECODE_OK) return shared;
+    // lengths are 32-bit: a table that could hold more holds no more than that (and the last
+    // tile's positions stay below 2^31)
+    int64_t max_len = a->pages == 0 ? 0 : a->page_size * a->table_width;
+    if (max_len > kMost - 1024) max_len = kMost - 1024;
+
+    p.status = status_word();
+    if (p.status == nullptr) return DECODE_ERR_CUDA;
+    auto* ws = static_cast<uint8_t*>(a->workspace);
+    p.q = static_cast<const uint16_t*>(a->q);
+    p.k = static_cast<const uint8_t*>(a->k_cache);
+    p.v = static_cast<const uint8_t*>(a->v_cache);
+    p.scale[0] = static_cast<const uint8_t*>(a->k_scale);
+    p.scale[1] = static_cast<const uint8_t*>(a->v_scale);
+    p.table = a->page_table;
+    p.lens = a->lens;
+    p.o = static_cast<uint16_t*>(a->o);
+    p.lse = a->lse;
+    p.split = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + l.ml);
+    p.part_o = reinterpret_cast<float*>(ws + l.o);
+    p.table_stride = a->n > 1 ? a->table_stride : 0;
+    p.max_len = max_len;
+    p.n = static_cast<int32_t>(a->n);
+    p.h_q = static_cast<int32_t>(a->h_q);
+    p.h_kv = static_cast<int32_t>(a->h_kv);
+    p.group = static_cast<int32_t>(group);
+    p.head_items = static_cast<int32_t>((group + heads - 1) / heads);
+    p.pages = static_cast<int32_t>(a->pages);
+    p.page_size = static_cast<int32_t>(a->page_size);
+    p.page_shift = shift_of(a->page_size);
+    p.block = static_cast<int32_t>(a->block_size);
+    p.block_shift = shift_of(a->block_size);
+    p.window = a->window > kMost ? 0 : static_cast<int32_t>(a->window);
+    p.sinks = a->sinks > max_len ? static_cast<int32_t>(max_len) : static_cast<int32_t>(a->sinks);
+    p.scale_log2 = a->scale * 1.4426950408889634f;
+    // rows of a sequence's axis: window and first tokens, each rounded to 16 rows
+    const int64_t seen = static_cast<int64_t>(p.window) + p.sinks + 2 * kSub;
+    const int64_t most = p.window > 0 && seen < max_len ? seen : max_len;
+    return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, a->head_dim, most, sms, stream)
+                                   : dispatch<__half>(p, a->head_dim, most, sms, stream);
+}
+
+}  // extern "C"

@@ -5,7 +5,10 @@ tokens.
 * ``gated_delta_step``: the gated delta rule token by token on a pool of states;
 * ``qk_norm_rope``: norm and position rotation of queries and keys, with the write of keys and
   values into a paged cache;
-* ``paged_attention``: attention of one new token per sequence over that cache.
+* ``paged_attention``: attention of one new token per sequence over that cache;
+* ``quantize_cache``, ``dequantize_cache``, ``paged_attention_fp8``: the same on a cache of 8-bit codes
+  with a scale for each block of tokens and head, which takes half the memory and time;
+* ``linear_w4``: a linear layer with 4-bit weights (``quantize_weight_w4`` makes them).
 
 The torch entry points check shapes, types and devices on the host and raise ``ValueError``, or
 ``GemmError`` with the library's message where the C call refuses.  They are asynchronous on
@@ -20,11 +23,12 @@ import struct
 
 import torch
 
-from . import GemmError, _build, load
+from . import ACTIVATIONS, GemmError, _build, load
 
 DECODE_OK, DECODE_ERR_INVALID_ARG, DECODE_ERR_UNSUPPORTED, DECODE_ERR_CUDA = 0, 1, 2, 3
 DECODE_NORMS = {"none": 0, "rms": 1, "l2": 2}
-DECODE_STATUS = {1: "a state slot outside the pool", 2: "a cache slot outside the cache",
+DECODE_STATUS = {1: "a state slot outside the pool",
+                 2: "a cache slot outside the cache, or out of its block's order",
                  4: "a position outside the rotary table",
                  8: "a sequence length its page table cannot hold",
                  16: "a page number outside the cache"}
@@ -33,6 +37,10 @@ DECODE_STATUS = {1: "a state slot outside the pool", 2: "a cache slot outside th
 GDN_STEP_ARGS = struct.Struct("=8Q7q9q4qqif")
 QK_NORM_ROPE_ARGS = struct.Struct("=12Q9q10q6qq4iiiif")
 PAGED_ATTENTION_ARGS = struct.Struct("=8Qq9q2q6qif")
+QUANTIZE_CACHE_ARGS = struct.Struct("=7Q5q4q6q6qii")
+DEQUANTIZE_CACHE_ARGS = struct.Struct("=7Q5q4q6q6qii")
+PAGED_ATTENTION_FP8_ARGS = struct.Struct("=10Qq10q2q6q6qqif")
+LINEAR_W4_ARGS = struct.Struct("=6Q4q5qii")
 
 
 # ---- the C ABI, one Python function per C function (args: the packed struct) ---------------------
@@ -55,6 +63,30 @@ def decode_paged_attention_workspace_bytes(h_q: int, h_kv: int, head_dim: int) -
     if rc != DECODE_OK:
         raise GemmError(rc, decode_last_error())
     return out.value
+
+
+def decode_quantize_cache(args: bytes, stream: int = 0) -> int:
+    return load().decode_quantize_cache(args, stream)
+
+
+def decode_dequantize_cache(args: bytes, stream: int = 0) -> int:
+    return load().decode_dequantize_cache(args, stream)
+
+
+def decode_paged_attention_fp8(args: bytes, stream: int = 0) -> int:
+    return load().decode_paged_attention_fp8(args, stream)
+
+
+def decode_paged_attention_fp8_workspace_bytes(h_q: int, h_kv: int, head_dim: int) -> int:
+    out = ctypes.c_size_t(0)
+    rc = load().decode_paged_attention_fp8_workspace_bytes(h_q, h_kv, head_dim, ctypes.byref(out))
+    if rc != DECODE_OK:
+        raise GemmError(rc, decode_last_error())
+    return out.value
+
+
+def decode_linear_w4(args: bytes, stream: int = 0) -> int:
+    return load().decode_linear_w4(args, stream)
 
 
 def decode_last_error() -> str:
@@ -166,6 +198,103 @@ def paged_attention(q, k_cache, v_cache, page_table, lens, scale: float | None =
     ``out`` may be ``q`` itself; what is written may share no other memory with the operands."""
     return _decode.paged_attention(q, k_cache, v_cache, page_table, lens, scale, window, return_lse,
                                    out, workspace, stream)
+
+
+def quantize_cache(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None) -> None:
+    """Write keys and values to their places in a paged cache of E4M3 codes with one E8M0 scale for
+    each block of tokens and head: a code c under the scale e stands for c * 2^(e - 127).  For each block
+    and head that new tokens go to, keys and values each on their own,
+
+        need = the least e >= 0 with |x| <= 448 * 2^(e - 127) for all finite new elements x
+        e'   = need, or max(need, e) where the block holds older tokens, of scale e
+        c    = e4m3(x * 2^(127 - e')),   and where e' > e, of its other codes e4m3(c * 2^(e - e'))
+
+    k, v [tokens, h_k, d] float16 or bfloat16, d 64, 128 or 256 (views of a packed projection are fine);
+    k_cache, v_cache [pages, page_size, h_k, d] float8_e4m3fn or uint8 (strides multiples of 16, a dense
+    last dimension); k_scale, v_scale [pages, blocks, h_k] uint8: blocks of page_size / blocks tokens.
+    slots int32 [tokens]: page * page_size + offset, or -1 for none.
+
+    A block's tokens fill it from its first place on, over any number of calls: what lies below a
+    call's first place in a block are older tokens, what lies above is nothing.  In a call they follow
+    one another in the order of their places, without a gap; neighbours that do not are refused
+    (``check_decode_status``), and tokens of one block that are apart leave it undefined.  An infinity
+    or NaN is held as NaN."""
+    _decode.quantize_cache(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream)
+
+
+def dequantize_cache(k_cache, v_cache, k_scale, v_scale, slots, dtype=torch.bfloat16, k_out=None,
+                     v_out=None, stream=None):
+    """The keys and values that a cache of ``quantize_cache`` holds at ``slots`` (int32 [tokens]),
+    rounded once to ``dtype`` (float16 or bfloat16): a pair of tensors [tokens, h_k, d].  Slot -1 gives
+    zeros.  ``k_out`` and ``v_out`` may have any strides with a dense last dimension; they may share
+    no memory with each other or the operands."""
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("dtype must be float16 or bfloat16")
+    return _decode.dequantize_cache(k_cache, v_cache, k_scale, v_scale, slots,
+                                    dtype == torch.float16, k_out, v_out, stream)
+
+
+def paged_attention_fp8_workspace(h_q: int, h_kv: int, head_dim: int, device="cuda"):
+    """A workspace for ``paged_attention_fp8``, as ``paged_attention_workspace`` makes one."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        size = decode_paged_attention_fp8_workspace_bytes(h_q, h_kv, head_dim)
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens,
+                        scale: float | None = None, window: int | None = None, sinks: int = 0,
+                        return_lse: bool = False, out=None, workspace=None, stream=None):
+    """``paged_attention`` over a cache of ``quantize_cache``: the same operands, results and refusals,
+    with the values that the codes stand for.  With a ``window`` the first ``sinks`` tokens stay
+    visible beside the last ``window``.  ``workspace``: from ``paged_attention_fp8_workspace``; None takes
+    one from torch's allocator for the call."""
+    return _decode.paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale,
+                                       window, sinks, return_lse, out, workspace, stream)
+
+
+def quantize_weight_w4(W, group: int = 128, zeros: bool = True):
+    """The operands of ``linear_w4`` nearest to W [N, K] float16 or bfloat16, K even, each group of
+    ``group`` neighbouring columns of a row (the last may be shorter) on its own: (codes, scales,
+    zeros).  With ``zeros`` a group's range, stretched to hold 0, is dealt to the codes 0 .. 15;
+    without, its largest magnitude to 7 either side of 8, and None takes the zeros' place."""
+    if W.dim() != 2 or W.dtype not in (torch.float16, torch.bfloat16) or W.shape[1] % 2 or group < 1:
+        raise ValueError("W must be a float16 or bfloat16 matrix with an even number of columns")
+    n, k = W.shape
+    groups = -(-k // group)
+    w = torch.nn.functional.pad(W.float(), (0, groups * group - k)).view(n, groups, group)
+    if zeros:
+        low, high = w.amin(-1).clamp(max=0), w.amax(-1).clamp(min=0)
+        scale = ((high - low) / 15).to(W.dtype)
+        by = scale.float().clamp(min=torch.finfo(W.dtype).tiny)
+        zero = torch.round(-low / by).clamp(0, 15)
+    else:
+        scale = (w.abs().amax(-1) / 7).to(W.dtype)
+        by = scale.float().clamp(min=torch.finfo(W.dtype).tiny)
+        zero = torch.full_like(by, 8)
+    code = torch.round(w / by[..., None] + zero[..., None]).clamp(0, 15).to(torch.uint8)
+    code = code.view(n, groups * group)[:, :k]
+    return (code[:, 0::2] | code[:, 1::2] << 4).contiguous(), scale, \
+        zero.to(torch.uint8) if zeros else None
+
+
+def linear_w4(x, codes, scales, group: int = 128, zeros=None, bias=None, activation: str = "none",
+              out=None, stream=None):
+    """act(x @ W.T + bias) with 4-bit weights, for few tokens:
+
+        W[j, c] = scales[j, c // group] * (code[j, c] - zeros[j, c // group])
+
+    x [tokens, K] float16 or bfloat16; codes uint8 [N, K / 2]: column 2 c in byte c's lower half, column
+    2 c + 1 in its upper; scales [N, ceil(K / group)] of x's type; zeros uint8 of the same shape, or None
+    for 8 everywhere; bias [N] of x's type.  K and group are multiples of 32.  Rows of all but bias may
+    be strided (x by multiples of 8, codes of 16 elements).  No weight is rounded: groups' sums and their
+    scaling are fp32.  activation: "none", "relu" or "gelu".  Returns [tokens, N] in x's type.
+
+    Reading the weights bounds the time of up to some 32 tokens; for many more, 16-bit weights and
+    ``linear`` are faster."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return _decode.linear_w4(x, codes, scales, group, zeros, bias, ACTIVATIONS[activation], out, stream)
 
 
 def check_decode_status(stream=None) -> None:

@@ -8,8 +8,14 @@
  *   decode_qk_norm_rope     the norm of each query and key head and the position rotation in one
  *                           pass, with the write of keys and values into a paged cache
  *   decode_paged_attention  attention of one new token per sequence over the paged cache
+ *   decode_quantize_cache   the write of keys and values to a paged cache of 8-bit codes with a scale
+ *                           for each block of tokens and head
+ *   decode_dequantize_cache the reading back of such a cache
+ *   decode_paged_attention_fp8   attention of one new token per sequence over it, with a sliding
+ *                           window and first tokens that stay visible
+ *   decode_linear_w4        a linear layer of few tokens with 4-bit weights and group scales
  *
- * Common to all three.  16-bit tensors are float16 or bfloat16 (`dtype`, one of DECODE_F16 and
+ * Common to all of them.  16-bit tensors are float16 or bfloat16 (`dtype`, one of DECODE_F16 and
  * DECODE_BF16, for all of a call's 16-bit tensors); sums, norms, states and softmax statistics are
  * fp32 and each 16-bit result is rounded once.  Strides are in elements; the innermost dimension
  * (head_dim) is dense, other strides of 16-bit tensors are multiples of 8 (rows are read 16 bytes at
@@ -54,10 +60,10 @@ extern "C" {
 
 /* Bits of the status word. */
 #define DECODE_BAD_STATE_SLOT 1u  /* decode_gdn_step: a slot of no state */
-#define DECODE_BAD_CACHE_SLOT 2u  /* decode_qk_norm_rope: a slot outside the cache */
+#define DECODE_BAD_CACHE_SLOT 2u  /* a slot outside the cache, or out of its block's order */
 #define DECODE_BAD_POSITION 4u    /* decode_qk_norm_rope: a position outside the table */
-#define DECODE_BAD_LENGTH 8u      /* decode_paged_attention: a length its page table cannot hold */
-#define DECODE_BAD_PAGE 16u       /* decode_paged_attention: a page outside the cache */
+#define DECODE_BAD_LENGTH 8u      /* an attention: a length its page table cannot hold */
+#define DECODE_BAD_PAGE 16u       /* an attention: a page outside the cache */
 
 /* ---- the gated delta rule, token by token ------------------------------------------------------
  *
@@ -220,6 +226,139 @@ int decode_paged_attention(const decode_paged_attention_args* args, cudaStream_t
 /* Workspace bytes for these heads on the current device, whatever the lengths and the batch. */
 int decode_paged_attention_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t head_dim,
                                            size_t* bytes);
+
+/* ---- a paged cache of 8-bit codes ---------------------------------------------------------------
+ *
+ * Keys and values as E4M3 codes [pages][page_size][h_k][head_dim] with one E8M0 scale for each block
+ * of block_size tokens and each head, [pages][page_size / block_size][h_k]: a code c in a block of
+ * scale e stands for c * 2^(e - 127), and e = 255 for NaN.  block_size divides page_size; head_dim is
+ * 64, 128 or 256; strides of the codes are multiples of 16, of the scales any.
+ *
+ * decode_quantize_cache writes tokens' keys and values to their places.  For each block and head
+ * that new tokens go to, keys and values each on their own:
+ *
+ *     need = the least e >= 0 with |x| <= 448 * 2^(e - 127) for all finite new elements x
+ *     e'   = need, or max(need, e) where the block holds older tokens, of scale e
+ *     c    = e4m3(x * 2^(127 - e')) of the new elements, rounded to nearest even
+ *     c'   = e4m3(c * 2^(e - e')) of the block's other codes, where it holds older tokens and e' > e
+ *
+ * so a token that is larger than those before it costs them at most the codes below E4M3's
+ * smallest normal number.  Where a block's new tokens begin says what it holds: the places below
+ * hold older tokens, those above nothing (a block whose first place is written begins anew).  An infinity or NaN becomes the code NaN, counts for no
+ * scale and touches no other element.
+ *
+ *   k, v          [tokens][h_k][head_dim], strides of the first two dimensions
+ *   slots         int32 [tokens]: the token's place, page * page_size + offset, or -1 for none.  A
+ *                 block's tokens follow one another in the call, in the order of their places without
+ *                 a gap; one that is next to a token of its block and not in that order is refused
+ *                 with those that continue it and reported, as is a slot outside the cache: neither is
+ *                 written.  Tokens of one block that are apart leave its contents undefined.
+ *
+ * decode_dequantize_cache gathers tokens: k and v [tokens][h_k][head_dim] receive c * 2^(e - 127), rounded
+ * once to 16 bits.  Slot -1 gives zeros, and so does one outside the cache, which is reported.
+ */
+typedef struct {
+    const void* k;
+    const void* v;
+    void* k_cache;
+    void* v_cache;
+    void* k_scale;
+    void* v_scale;
+    const int32_t* slots;
+    int64_t tokens, h_k, head_dim, pages, page_size;
+    int64_t k_stride[2], v_stride[2];                       /* token, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];           /* page, offset, head */
+    int64_t k_scale_stride[3], v_scale_stride[3];           /* page, block, head */
+    int32_t dtype, block_size;
+} decode_quantize_cache_args;
+
+int decode_quantize_cache(const decode_quantize_cache_args* args, cudaStream_t stream);
+
+typedef struct {
+    const void* k_cache;
+    const void* v_cache;
+    const void* k_scale;
+    const void* v_scale;
+    const int32_t* slots;
+    void* k;
+    void* v;
+    int64_t tokens, h_k, head_dim, pages, page_size;
+    int64_t k_stride[2], v_stride[2];                       /* token, head */
+    int64_t k_cache_stride[3], v_cache_stride[3];           /* page, offset, head */
+    int64_t k_scale_stride[3], v_scale_stride[3];           /* page, block, head */
+    int32_t dtype, block_size;                              /* dtype: of k and v */
+} decode_dequantize_cache_args;
+
+int decode_dequantize_cache(const decode_dequantize_cache_args* args, cudaStream_t stream);
+
+/* decode_paged_attention over such a cache: everything said there holds, with the values that the
+ * codes stand for, and with a window the first `sinks` tokens stay visible: a sequence's seen tokens
+ * are t < sinks and lens[i] - window <= t < lens[i] (window == 0: all, and sinks is ignored).  A
+ * scale or code that stands for NaN reaches the results of its block's or token's head; those of
+ * unseen tokens reach none.  The workspace is its own: decode_paged_attention_fp8_workspace_bytes().
+ */
+typedef struct {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const void* k_scale;
+    const void* v_scale;
+    const int32_t* page_table;
+    const int32_t* lens;
+    void* o;
+    float* lse;
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t n, h_q, h_kv, head_dim, pages, page_size, table_width, table_stride, window, sinks;
+    int64_t q_stride[2];                                    /* sequence, head */
+    int64_t k_stride[3], v_stride[3];                       /* page, offset, head */
+    int64_t k_scale_stride[3], v_scale_stride[3];           /* page, block, head */
+    int64_t block_size;
+    int32_t dtype;
+    float scale;
+} decode_paged_attention_fp8_args;
+
+int decode_paged_attention_fp8(const decode_paged_attention_fp8_args* args, cudaStream_t stream);
+
+int decode_paged_attention_fp8_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t head_dim,
+                                               size_t* bytes);
+
+/* ---- a linear layer with 4-bit weights ----------------------------------------------------------
+ *
+ *     y[i][j] = act(bias[j] + sum_g scales[j][g] sum_{c in g} x[i][c] (code[j][c] - zeros[j][g]))
+ *
+ * with g over the groups of `group` neighbouring columns (the last may be shorter).  Differences of
+ * codes are exact in the tensor cores' 16 bits, sums are fp32 and so are the scales' products: y is
+ * rounded once.  Made for few tokens, whose time is that of reading the weights.
+ *
+ *   x             [m][k], 16 bits, x_stride (a multiple of 8) between rows
+ *   codes         [n][k / 2] bytes, code_stride (a multiple of 16) between rows: byte c holds column
+ *                 2 c in its lower and 2 c + 1 in its upper half
+ *   scales        [n][groups], of x's type, scale_stride between rows; groups = ceil(k / group)
+ *   zeros         bytes [n][groups] of 0 .. 15, zero_stride between rows, or NULL: 8 everywhere.
+ *                 (of a larger byte the lower half counts)
+ *   bias          [n], of x's type, dense, or NULL
+ *   y             [m][n], of x's type, y_stride between rows (written)
+ *
+ * k and group are multiples of 32.  With k == 0 the sums are 0.
+ */
+#define DECODE_ACT_NONE 0
+#define DECODE_ACT_RELU 1
+#define DECODE_ACT_GELU 2     /* x Phi(x), in its exact form */
+
+typedef struct {
+    const void* x;
+    const void* codes;
+    const void* scales;
+    const void* zeros;
+    const void* bias;
+    void* y;
+    int64_t m, n, k, group;
+    int64_t x_stride, code_stride, scale_stride, zero_stride, y_stride;
+    int32_t dtype, activation;
+} decode_linear_w4_args;
+
+int decode_linear_w4(const decode_linear_w4_args* args, cudaStream_t stream);
 
 /* ---- common ------------------------------------------------------------------------------------ */
 
