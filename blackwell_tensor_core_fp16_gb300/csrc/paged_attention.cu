@@ -45,6 +45,8 @@ namespace {
 
 using namespace decode;
 
+constexpr int kMostResident = 2;     // of Cfg::kResident
+
 struct AttnParams : SplitParams {
     const uint16_t* q;
     const uint16_t* k;
@@ -102,13 +104,13 @@ struct Span {
     int start, len;
     __device__ __forceinline__ int origin() const { return start & ~(kSub - 1); }
     __device__ __forceinline__ int rows() const { return len - origin(); }
+    __device__ __forceinline__ static Span of(const AttnParams& p, int i)
+    {
+        int len = p.lens[i];
+        if (len < 0 || len > p.max_len) len = 0;
+        return {p.window > 0 && len > p.window ? len - p.window : 0, len};
+    }
 };
-__device__ __forceinline__ Span span_of(const AttnParams& p, int i)
-{
-    int len = p.lens[i];
-    if (len < 0 || len > p.max_len) len = 0;
-    return {p.window > 0 && len > p.window ? len - p.window : 0, len};
-}
 
 template <int D, int kTiles>
 struct Cfg {
@@ -135,7 +137,9 @@ struct Cfg {
     static constexpr int kTile = kWarps * kSlice;
     static constexpr int kStageBytes = 2 * kSlice * D * 2;    // keys, then values
     static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
-    static constexpr int kMergeBytes = kWarps * kHeads * kMergeRow * 4;
+    static constexpr int kMergeWarp = kHeads * kMergeRow;
+    static constexpr int kMergeBytes = kWarps * kMergeWarp * 4;
+    __device__ static __forceinline__ int merge_at(int h, int d) { return h * kMergeRow + d; }
     static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
     // the queries stay in registers, but for the one shape whose sums leave no room for them
     static constexpr bool kQueriesShared = D == 256 && kHeadTiles == 2;
@@ -502,7 +506,7 @@ int decode_paged_attention_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t he
     if (rc != DECODE_OK) return rc;
     const int sms = sm_count();
     if (sms == 0) return DECODE_ERR_CUDA;
-    *bytes = layout_for(sms, heads_of(h_q / h_kv), head_dim).total;
+    *bytes = layout_for(sms, kMostResident, heads_of(h_q / h_kv), head_dim).total;
     return DECODE_OK;
 }
 
@@ -538,7 +542,7 @@ int decode_paged_attention(const decode_paged_attention_args* a, cudaStream_t st
     if (sms == 0) return DECODE_ERR_CUDA;
     const int64_t group = a->h_q / a->h_kv;
     const int heads = heads_of(group);
-    const Layout l = layout_for(sms, heads, a->head_dim);
+    const Layout l = layout_for(sms, kMostResident, heads, a->head_dim);
     if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < l.total)
         return fail(DECODE_ERR_INVALID_ARG, "workspace of %zu bytes needed", l.total);
     // (an item's queries are in registers or shared memory, in all of its blocks, before its results

@@ -15,8 +15,8 @@
 // values, transposed, two tokens' two neighbouring elements, whose bytes a permutation sorts by
 // element; rows r and r + 8 of a tile stand for elements 2 r and 2 r + 1.
 //
-// Scales are read for each token of a slice (a byte each of keys and values), a slice ahead, and wait
-// beside its stage as numbers, so blocks may have any size.  A key's scale multiplies its scores.  A
+// Scales are read for each token of a slice (a byte each of keys and values) with its rows and wait
+// beside its stage, so blocks may have any size.  A key's scale multiplies its scores.  A
 // value's goes into its weight: times 2^15 over the slice's largest scale, by which the slice's sums
 // are multiplied when they are added to the running ones, so a weight fits float16 whatever the scales.
 // It is carried as two float16 pieces, 22 bits, which leave out less than 2^-22 of it or 2^-40 of the
@@ -29,6 +29,7 @@
 // With a window the seen tokens are two ranges.  They are laid one after the other on one axis of rows,
 // the first tokens' range rounded up and the window's start down to 16, so that 16 rows lie in one
 // range, and the axis is cut into tiles as any other.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -38,15 +39,19 @@ namespace {
 
 using namespace decode;
 
+constexpr int kMostResident = 3;     // of Fp8Cfg::kResident
+
 struct Fp8Params : SplitParams {
     const uint16_t* q;
     const uint8_t* k;
     const uint8_t* v;
     const uint8_t* scale[2];           // keys', values'
     const int32_t* table;
-    int64_t q_stride[2], k_stride[3], v_stride[3], scale_stride[2][3];
-    int64_t table_stride;
+    int64_t q_stride[2], table_stride;
+    int64_t head_stride[2], scale_head_stride[2];
+    uint32_t stride[2][2], scale_stride[2][2];     // page, offset; page, block
     int32_t pages, page_size, page_shift, block, block_shift, window, sinks;
+    int32_t same;                      // the strides of keys' and values' codes and scales are the same
     float scale_log2;
 };
 
@@ -57,19 +62,34 @@ struct Fp8Span {
     __device__ __forceinline__ int rows() const { return len - gap; }
     __device__ __forceinline__ int token(int row) const { return row < edge ? row : row + gap; }
     __device__ __forceinline__ bool seen(int t) const { return t < len && (t >= start || t < first); }
+    __device__ __forceinline__ static Fp8Span of(const Fp8Params& p, int i)
+    {
+        Fp8Span s;
+        s.len = p.lens[i];
+        if (s.len < 0 || s.len > p.max_len) s.len = 0;
+        s.start = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
+        s.first = min(p.sinks, s.start);
+        s.edge = (s.first + kSub - 1) & ~(kSub - 1);
+        const int origin = s.start & ~(kSub - 1);
+        s.gap = max(origin - s.edge, 0);           // none where the ranges' 16 rows meet
+        return s;
+    }
 };
-__device__ __forceinline__ Fp8Span span_of(const Fp8Params& p, int i)
-{
-    Fp8Span s;
-    s.len = p.lens[i];
-    if (s.len < 0 || s.len > p.max_len) s.len = 0;
-    s.start = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
-    s.first = min(p.sinks, s.start);
-    s.edge = (s.first + kSub - 1) & ~(kSub - 1);
-    const int origin = s.start & ~(kSub - 1);
-    s.gap = max(origin - s.edge, 0);               // none where the ranges' 16 rows meet
-    return s;
-}
+
+// What a warp needs of it for each tile: how many rows, and the first from which on all are seen.
+struct Fp8Rows {
+    int len, gap, clear;
+    __device__ __forceinline__ int rows() const { return len - gap; }
+    __device__ __forceinline__ bool all_seen(int row, int count) const
+    {
+        return row >= clear && row + count <= rows();
+    }
+    __device__ __forceinline__ static Fp8Rows of(const Fp8Params& p, int i)
+    {
+        const Fp8Span s = Fp8Span::of(p, i);
+        return {s.len, s.gap, s.start - s.gap};
+    }
+};
 
 template <int D, int kTiles>
 struct Fp8Cfg {
@@ -81,19 +101,22 @@ struct Fp8Cfg {
     template <typename T>
     static constexpr int kShift = 0;                          // (the sums carry no factor)
     static constexpr bool kRowPairs = true;
-    static constexpr int kResident = 2;                       // blocks of an SM
+    static constexpr int kResident = D <= 128 && kTiles == 1 ? 3 : 2;   // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
-    static constexpr int kScaleBytes = (2 * kSlice + 4) * 4;  // keys', values', the values' largest
+    static constexpr int kPer = kSlice > 32 ? kSlice / 32 : 1;     // tokens of a slice by lane
+    static constexpr int kScaleBytes = kPer * 64;             // 2 bytes a token: key's, value's
     static constexpr int kCodeBytes = 2 * kSlice * D;         // keys, then values
     static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
-    static constexpr int kMergeRow = D + 4;                   // floats; the pad spreads the banks
-    static constexpr int kMergeBytes = kWarps * kHeads * kMergeRow * 4;
+    // Warps are joined through the stages whose slices they have just done, where there is room: each
+    // head's elements, 16 at a time in an order of the head's own that spreads the banks (else a pad).
+    static constexpr bool kMergeInRing = kHeads * D * 4 <= kCodeBytes;
     static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
     // the queries stay in registers, but for the one shape whose sums leave no room for them
     static constexpr bool kQueriesShared = D == 256 && kTiles == 2;
     static constexpr int kQueryRow = D + 16;                  // elements
     static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 + kHeads * 4 : 0;
+    static constexpr int kMergeBytes = kMergeInRing ? 0 : kWarps * kHeads * (D + 4) * 4;
     // (the blocks share an SM's 228 KB, of which the system takes 1 KB a block)
     static constexpr int kRoom =
         233472 / kResident - 1024 - kMergeBytes - kSmallBytes - kQueryBytes;
@@ -102,6 +125,11 @@ struct Fp8Cfg {
     static constexpr int kSmem = kWarps * kStages * kStageBytes + kMergeBytes + kSmallBytes +
                                  kQueryBytes;
     static_assert(kStages >= 2, "no room for two stages");
+    static constexpr int kMergeWarp = kMergeInRing ? kStages * kCodeBytes / 4 : kHeads * (D + 4);   // floats
+    __device__ static __forceinline__ int merge_at(int h, int d)
+    {
+        return kMergeInRing ? h * D + (d ^ (h >> 1 & 3) << 4) : h * (D + 4) + d;
+    }
     // where a 16-byte piece of a row lies, so that 8 rows' pieces lie in 8 different bank groups
     __device__ static __forceinline__ int place(int row, int piece)
     {
@@ -123,8 +151,10 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
     constexpr uint32_t kAll = 0xffffffffu;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* ring = smem;
-    float* merge = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStageBytes);
-    float* sm_m = merge + C::kMergeBytes / 4;      // [kWarps][kHeads]
+    float* merge = reinterpret_cast<float*>(
+        smem + (C::kMergeInRing ? 0 : kWarps * C::kStages * C::kStageBytes));
+    float* sm_m = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kStageBytes +
+                                           C::kMergeBytes);       // [kWarps][kHeads]
     float* sm_l = sm_m + kWarps * kHeads;
     int* sm_i = reinterpret_cast<int*>(sm_l + kWarps * kHeads);   // 64 words
     uint16_t* sm_q = reinterpret_cast<uint16_t*>(sm_i + 64);      // [kHeads][kQueryRow]
@@ -134,7 +164,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
     dep_launch();
     dep_wait();
 
-    Cursor<Fp8Span> cur;
+    Cursor<Fp8Rows> cur;
     Range r;
     if constexpr (kCluster) {
         if (!cluster_range<C>(p, cur, r, sm_i)) return;
@@ -142,117 +172,104 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
         if (!block_range<C>(p, cur, r, sm_i)) return;
     }
     const int t0 = r.t0, t1 = r.t1;
-    Cursor<Fp8Span> pre = cur;                     // where the loads are
+    Cursor<Fp8Span> pre = {cur.i, cur.item, cur.tile, cur.tiles, Fp8Span::of(p, cur.i)};   // of the loads
     int pre_t = t0;
 
-    // ---- loads of a slice.  The places in the cache of its 16-row pieces are looked up one slice
-    // ahead: that of the first row where pages are multiples of 16 tokens, else that of row
-    // `lane & 15`.
-    uint8_t* const mine = ring + w * C::kStages * C::kCodeBytes;
-    const uint32_t ring0 = smem_addr(mine);
-    float* const scales0 = reinterpret_cast<float*>(ring + kWarps * C::kStages * C::kCodeBytes +
-                                                    w * C::kStages * C::kScaleBytes);
+    // ---- loads of a slice.  Lane x takes care of token x of it (and x + 32, if it has as many): it looks
+    // its page up one slice ahead and its scales, and names its rows to the lanes that copy them.
+    constexpr int kPer = C::kPer;
+    const uint32_t ring0 = smem_addr(ring + w * C::kStages * C::kCodeBytes);
+    uint16_t* const scales0 = reinterpret_cast<uint16_t*>(ring + kWarps * C::kStages * C::kCodeBytes +
+                                                          w * C::kStages * C::kScaleBytes) + lane;
     const int ch = lane % kChunks, sub = lane / kChunks;
-    const bool whole_pages = p.page_size % kSub == 0;
-    const int ahead = whole_pages ? 0 : lane & 15;
-    int page[kSubs], off[kSubs];
-    bool there[kSubs];                             // the place is one of the sequence's
+    int page[kPer], off[kPer];
+    bool there[kPer];                              // the token is one that is seen
     auto look_up = [&]() {
 #pragma unroll
-        for (int y = 0; y < kSubs; ++y) {
+        for (int y = 0; y < kPer; ++y) {
             there[y] = false;
             if (pre_t >= t1) continue;
-            const int row = pre.tile * kTile + w * kSlice + y * kSub;
-            const int pos = pre.span.token(row) + ahead;
-            if (row >= pre.span.rows() || pos >= pre.span.len || (!whole_pages && !pre.span.seen(pos)))
-                continue;
+            const int row = pre.tile * kTile + w * kSlice + y * 32 + (lane & (kSlice - 1));
+            const int pos = pre.span.token(row);
+            if (row >= pre.span.rows() || !pre.span.seen(pos)) continue;
             there[y] = true;
             const int x = divide(pos, p.page_size, p.page_shift);
             off[y] = pos - x * p.page_size;
             page[y] = p.table[pre.i * p.table_stride + x];
         }
     };
-    // The scales of a slice: lanes 0 to 15 read a piece's keys', the others its values'.  They are on
-    // their way while the lane goes on and are put down (as what a score is multiplied by, and as
-    // 2^15 over the largest) at the next load.
-    int scale_byte[kSubs], scale_stage = -1;
-    uint32_t scale_seen = 0;
-    auto put_scales = [&]() {
-        if (scale_stage < 0) return;
-        int largest = 0;
-#pragma unroll
-        for (int y = 0; y < kSubs; ++y)
-            if (lane >= kSub && (scale_seen >> y & 1)) largest = max(largest, scale_byte[y]);
-        largest = __reduce_max_sync(kAll, largest);
-        float* const to = scales0 + scale_stage * (C::kScaleBytes / 4);
-#pragma unroll
-        for (int y = 0; y < kSubs; ++y) {
-            const int e = scale_byte[y];
-            float f = 0.f;                         // of an unseen token
-            if (scale_seen >> y & 1) {
-                if (lane < kSub)
-                    f = scale_of(e) * p.scale_log2;
-                else
-                    f = e == 255 ? NAN : largest - e < 142 ? power_of(142 - largest + e) : 0.f;
-            }
-            to[(lane < kSub ? 0 : kSlice - kSub) + y * kSub + lane] = f;
-        }
-        if (lane == 0) to[2 * kSlice] = power_of(largest - 15);
-    };
+    // (the scales are on their way while the warp goes on, and are put beside their stage at the next
+    // load)
+    uint32_t scale_byte[2][kPer];
+    int scale_stage = -1;
     auto load = [&](int stage) {
-        put_scales();
+        if (scale_stage >= 0) {
+#pragma unroll
+            for (int y = 0; y < kPer; ++y)
+                scales0[scale_stage * (C::kScaleBytes / 2) + y * 32] =
+                    static_cast<uint16_t>(scale_byte[0][y] | scale_byte[1][y] << 8);
+        }
         scale_stage = -1;
         if (pre_t < t1) {
             const int kv = pre.item / p.head_items;
-            const uint8_t* k0 = p.k + kv * p.k_stride[2] + ch * 16;
-            const uint8_t* v0 = p.v + kv * p.v_stride[2] + ch * 16;
             scale_stage = stage;
-            scale_seen = 0;
+            bool all = true;
 #pragma unroll
-            for (int y = 0; y < kSubs; ++y) {
-                if (there[y] && (page[y] < 0 || page[y] >= p.pages)) {
+            for (int y = 0; y < kPer; ++y) {
+                scale_byte[0][y] = scale_byte[1][y] = 0;
+                if (there[y] && static_cast<uint32_t>(page[y]) >= static_cast<uint32_t>(p.pages)) {
                     atomicOr(p.status, DECODE_BAD_PAGE);
                     there[y] = false;
                 }
-                const int row0 = pre.tile * kTile + w * kSlice + y * kSub;
-                const int pos0 = pre.span.token(row0);
-                const int of = lane >= kSub;       // the tensor whose scale the lane reads
-                scale_byte[y] = 0;
-                if (there[y] && pre.span.seen(pos0 + (lane & 15))) {
-                    const int o = off[y] + (whole_pages ? lane & 15 : 0);
-                    scale_byte[y] = p.scale[of][page[y] * p.scale_stride[of][0] +
-                                                divide(o, p.block, p.block_shift) * p.scale_stride[of][1] +
-                                                kv * p.scale_stride[of][2]];
-                    scale_seen |= 1u << y;
+                all = all && there[y];
+                if (!there[y]) continue;
+                uint64_t from = 0;
+#pragma unroll
+                for (int of = 0; of < 2; ++of) {
+                    if (of == 0 || !p.same)
+                        from = kv * p.scale_head_stride[of] +
+                               static_cast<uint64_t>(static_cast<uint32_t>(page[y])) * p.scale_stride[of][0] +
+                               static_cast<uint64_t>(static_cast<uint32_t>(
+                                   divide(off[y], p.block, p.block_shift))) * p.scale_stride[of][1];
+                    scale_byte[of][y] = p.scale[of][from];
                 }
-                const int64_t ko = !there[y] ? 0 : page[y] * p.k_stride[0] + off[y] * p.k_stride[1];
-                const int64_t vo = !there[y] ? 0 : page[y] * p.v_stride[0] + off[y] * p.v_stride[1];
-                const uint32_t dst0 = ring0 + stage * C::kCodeBytes;
-                if (whole_pages) {
-                    const uint8_t* kb = k0 + ko + sub * p.k_stride[1];
-                    const uint8_t* vb = v0 + vo + sub * p.v_stride[1];
-                    const int64_t ks = kRowsPerCopy * p.k_stride[1], vs = kRowsPerCopy * p.v_stride[1];
+            }
+            all = __all_sync(kAll, all);
+            // where the codes of the lane's own tokens lie
+            uint64_t at[kPer];
+            auto locate = [&](int of) {
 #pragma unroll
-                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
-                        const int row = x * kRowsPerCopy + sub;
-                        const uint32_t bytes = there[y] && pre.span.seen(pos0 + row) ? 16u : 0u;
-                        const uint32_t dst = dst0 + C::place(y * kSub + row, ch);
-                        cp_async16(dst, bytes ? kb : p.k, bytes);
-                        cp_async16(dst + kSlice * D, bytes ? vb : p.v, bytes);
-                        kb += ks;
-                        vb += vs;
-                    }
-                } else {
+                for (int y = 0; y < kPer; ++y)
+                    at[y] = !there[y] ? 0
+                                      : kv * p.head_stride[of] +
+                                            static_cast<uint64_t>(static_cast<uint32_t>(page[y])) *
+                                                p.stride[of][0] +
+                                            static_cast<uint64_t>(static_cast<uint32_t>(off[y])) *
+                                                p.stride[of][1];
+            };
+            const uint32_t dst0 = ring0 + stage * C::kCodeBytes;
+            if (all && p.same) {
+                locate(0);
 #pragma unroll
-                    for (int x = 0; x < kSub / kRowsPerCopy; ++x) {
-                        const int row = x * kRowsPerCopy + sub;
-                        const int64_t k1 = __shfl_sync(kAll, ko, row);
-                        const int64_t v1 = __shfl_sync(kAll, vo, row);
-                        const bool have = __shfl_sync(kAll, there[y], row);
-                        const uint32_t bytes = have ? 16u : 0u;
-                        const uint32_t dst = dst0 + C::place(y * kSub + row, ch);
-                        cp_async16(dst, bytes ? k0 + k1 : p.k, bytes);
-                        cp_async16(dst + kSlice * D, bytes ? v0 + v1 : p.v, bytes);
+                for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
+                    const int row = x * kRowsPerCopy + sub;
+                    const uint64_t from =
+                        __shfl_sync(kAll, at[x * kRowsPerCopy / 32], row & 31) + ch * 16;
+                    const uint32_t dst = dst0 + C::place(row, ch);
+                    cp_async16(dst, p.k + from);
+                    cp_async16(dst + kSlice * D, p.v + from);
+                }
+            } else {
+                for (int of = 0; of < 2; ++of) {
+                    locate(of);
+                    const uint8_t* const base = of ? p.v : p.k;
+#pragma unroll
+                    for (int x = 0; x < kSlice / kRowsPerCopy; ++x) {
+                        const int row = x * kRowsPerCopy + sub, y = x * kRowsPerCopy / 32;
+                        const uint64_t from = __shfl_sync(kAll, at[y], row & 31) + ch * 16;
+                        const uint32_t bytes = __shfl_sync(kAll, there[y], row & 31) ? 16u : 0u;
+                        cp_async16(dst0 + of * kSlice * D + C::place(row, ch),
+                                   bytes ? base + from : base, bytes);
                     }
                 }
             }
@@ -272,14 +289,13 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
     // ---- the tiles
     constexpr int kOwn = C::kQueriesShared ? 1 : kHeadTiles;      // head tiles of queries in registers
     uint32_t qf[kOwn][D / 16][2];
-    float q_scale[kHeadTiles][2];                  // what the lane's two heads' queries were divided by
+    float q_scale[kOwn][2];                        // what the lane's two heads' queries were divided by
     float acc[kHeadTiles][D / 16][4];
     float m[kHeadTiles][2], l[kHeadTiles][2];
     bool fresh = true;
-    int stage = 0;
     // the queries of an item's head tile x: of 16 elements a lane holds four neighbouring ones of head
     // lane / 4
-    auto load_queries = [&](const Cursor<Fp8Span>& of, int x, uint32_t (&f)[D / 16][2]) {
+    auto load_queries = [&](const Cursor<Fp8Rows>& of, int x, uint32_t (&f)[D / 16][2]) {
         const int kv = of.item / p.head_items;
         const int first = of.item % p.head_items * kHeads, heads = min(kHeads, p.group - first);
         const int h = x * 8 + (lane >> 2);
@@ -330,10 +346,6 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                 if (lane % 4 == 0) sm_q_scale[x * 8 + (lane >> 2)] = back;
             }
             __syncthreads();
-#pragma unroll
-            for (int x = 0; x < kHeadTiles; ++x)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) q_scale[x][e] = sm_q_scale[x * 8 + (lane & 3) * 2 + e];
         } else {
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             }
         }
     };
-    auto load_all_queries = [&](const Cursor<Fp8Span>& of) {
+    auto load_all_queries = [&](const Cursor<Fp8Rows>& of) {
         if constexpr (!C::kQueriesShared)
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) load_queries(of, x, qf[x]);
@@ -365,6 +377,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                 l[x][0] = l[x][1] = 0.f;
             }
         }
+        const int stage = (t - t0) % C::kStages;
         __syncwarp();
         load((stage + C::kStages - 1) % C::kStages);
         cp_wait<C::kStages - 1>();
@@ -372,31 +385,16 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
 
         const int row0 = cur.tile * kTile + w * kSlice;
         if (row0 < cur.span.rows()) {
+            // the lane's piece of rows `lane & 15`, of which there are two a load: piece d lies at d ^ it
             const uint32_t ks = ring0 + stage * C::kCodeBytes, vs = ks + kSlice * D;
-            const float* const scales = scales0 + stage * (C::kScaleBytes / 4);
-            const int sel = lane >> 3;
+            const uint32_t at = C::place(lane & 15, lane >> 4);
             float s[kHeadTiles][kSubs][4];
 #pragma unroll
-            for (int x = 0; x < kHeadTiles; ++x)
-#pragma unroll
-                for (int y = 0; y < kSubs; ++y)
-                    s[x][y][0] = s[x][y][1] = s[x][y][2] = s[x][y][3] = 0.f;
-#pragma unroll
             for (int d = 0; d < D / 16; d += 2) {
-                [[maybe_unused]] uint2 qs[2][kHeadTiles];
-                if constexpr (C::kQueriesShared) {
-#pragma unroll
-                    for (int z = 0; z < 2; ++z)
-#pragma unroll
-                        for (int x = 0; x < kHeadTiles; ++x)
-                            qs[z][x] = *reinterpret_cast<const uint2*>(
-                                sm_q + (x * 8 + (lane >> 2)) * C::kQueryRow + (d + z) * 16 +
-                                (lane & 3) * 4);
-                }
 #pragma unroll
                 for (int y = 0; y < kSubs; ++y) {
                     uint32_t two[4];               // rows 0 .. 7 and 8 .. 15 of elements d, of d + 1
-                    ldsm4(two, ks + C::place(y * kSub + (lane & 15), d + (sel >> 1)));
+                    ldsm4(two, ks + (at ^ d << 4) + y * kSub * D);
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const uint32_t a[4] = {codes_to_half2(two[2 * z]), codes_to_half2(two[2 * z + 1]),
@@ -404,42 +402,77 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                                                codes_to_half2(two[2 * z + 1] >> 16)};
 #pragma unroll
                         for (int x = 0; x < kHeadTiles; ++x) {
+                            uint2 b;
                             if constexpr (C::kQueriesShared)
-                                mma<H>(s[x][y], a, qs[z][x].x, qs[z][x].y);
+                                b = *reinterpret_cast<const uint2*>(
+                                    sm_q + (x * 8 + (lane >> 2)) * C::kQueryRow + (d + z) * 16 +
+                                    (lane & 3) * 4);
                             else
-                                mma<H>(s[x][y], a, qf[x][d + z][0], qf[x][d + z][1]);
+                                b = make_uint2(qf[x][d + z][0], qf[x][d + z][1]);
+                            if (d + z == 0)
+                                mma_first<H>(s[x][y], a, b.x, b.y);
+                            else
+                                mma<H>(s[x][y], a, b.x, b.y);
                         }
                     }
                 }
             }
-            // the lane's rows are row0 + 8 j + lane / 4
-            bool in[2 * kSubs];
-            float k_scale[2 * kSubs], v_scale[2 * kSubs];
+            // the scales of the lane's token, and of its rows, row0 + 8 j + lane / 4
+            float k_scale[2 * kSubs], v_scale[2 * kSubs], slice_scale;
+            {
+                uint32_t two[kPer], largest = 0;
+                float kf[kPer], vf[kPer];
 #pragma unroll
-            for (int j = 0; j < 2 * kSubs; ++j) {
-                const int row = row0 + j * 8 + (lane >> 2);
-                in[j] = cur.span.seen(cur.span.token(row));
-                k_scale[j] = scales[j * 8 + (lane >> 2)];
-                v_scale[j] = scales[kSlice + j * 8 + (lane >> 2)];
+                for (int y = 0; y < kPer; ++y) {
+                    two[y] = scales0[stage * (C::kScaleBytes / 2) + y * 32];
+                    largest = max(largest, two[y] >> 8);
+                }
+                largest = __reduce_max_sync(kAll, largest);
+                slice_scale = power_of(static_cast<int>(largest) - 15);
+#pragma unroll
+                for (int y = 0; y < kPer; ++y) {
+                    const int e = two[y] >> 8, below = static_cast<int>(largest) - e;
+                    kf[y] = scale_of(two[y] & 0xffu) * p.scale_log2;
+                    vf[y] = e == 255 ? NAN : below < 142 ? power_of(142 - below) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * kSubs; ++j) {
+                    k_scale[j] = __shfl_sync(kAll, kf[j / 4 % kPer], (j * 8 + (lane >> 2)) & 31);
+                    v_scale[j] = __shfl_sync(kAll, vf[j / 4 % kPer], (j * 8 + (lane >> 2)) & 31);
+                }
             }
-            const float slice_scale = scales[2 * kSlice];
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                for (int j = 0; j < 2 * kSubs; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[x][j / 2][j % 2 * 2 + e] *= k_scale[j];
+            if (!cur.span.all_seen(row0, kSlice)) {
+                const Fp8Span span = Fp8Span::of(p, cur.i);
+#pragma unroll
+                for (int j = 0; j < 2 * kSubs; ++j)
+                    if (!span.seen(span.token(row0 + j * 8 + (lane >> 2)))) {
+#pragma unroll
+                        for (int x = 0; x < kHeadTiles; ++x)
+                            s[x][j / 2][j % 2 * 2] = s[x][j / 2][j % 2 * 2 + 1] = -INFINITY;
+                    }
+            }
             uint32_t pb[kHeadTiles][kSubs][2][2];  // [piece][rows 0 .. 7, 8 .. 15]
             float corr[kHeadTiles][2];
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    const float by = !C::kQueriesShared               ? q_scale[C::kQueriesShared ? 0 : x][e]
+                                     : std::is_same<T, H>::value      ? 1.f
+                                                                      : sm_q_scale[x * 8 + (lane & 3) * 2 + e];
                     float top = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 2 * kSubs; ++j) {
-                        float& v = s[x][j / 2][j % 2 * 2 + e];
-                        v = in[j] ? v * q_scale[x][e] * k_scale[j] : -INFINITY;
-                        top = fmaxf(top, v);
-                    }
+                    for (int j = 0; j < 2 * kSubs; ++j) top = fmaxf(top, s[x][j / 2][j % 2 * 2 + e]);
                     top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
-                    top = fmaxf(top, m[x][e]);
+                    top = fmaxf(top * by, m[x][e]);
                     // scores of -infinity only: any finite reference leaves their weights 0
                     const float ref = top == -INFINITY ? 0.f : top;
                     corr[x][e] = exp2_fast(m[x][e] - ref);
@@ -448,7 +481,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
 #pragma unroll
                     for (int j = 0; j < 2 * kSubs; ++j) {
                         float& v = s[x][j / 2][j % 2 * 2 + e];
-                        v = exp2_fast(v - ref);
+                        v = exp2_fast(fmaf(v, by, -ref));
                         sum += v;
                         v *= v_scale[j];
                     }
@@ -467,55 +500,73 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             // product cuts its sum's last bits off, which would add up over a long axis
 #pragma unroll
             for (int d = 0; d < D / 16; d += 2) {
-                float o[2][kHeadTiles][4] = {};
+                // (two pieces of 16 elements beside each other, but for the shape with the most sums)
+                constexpr int kBeside = C::kQueriesShared ? 1 : 2;
+                float o[kBeside][kHeadTiles][4];
+                uint32_t two[4];                   // tokens 0 .. 7 and 8 .. 15 of elements d, of d + 1
 #pragma unroll
-                for (int y = 0; y < kSubs; ++y) {
-                    uint32_t two[4];               // tokens 0 .. 7 and 8 .. 15 of elements d, of d + 1
-                    ldsm4_trans(two, vs + C::place(y * kSub + (lane & 15), d + (sel >> 1)));
-                    uint32_t a[2][4];
+                for (int z0 = 0; z0 < 2; z0 += kBeside) {
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const uint32_t sorted = __byte_perm(two[z], 0u, 0x3120);
-                        a[z / 2][z % 2 * 2] = codes_to_half2(sorted);
-                        a[z / 2][z % 2 * 2 + 1] = codes_to_half2(sorted >> 16);
+                    for (int y = 0; y < kSubs; ++y) {
+                        static_assert(kBeside == 2 || kSubs == 1, "loaded once");
+                        if (z0 == 0) ldsm4_trans(two, vs + (at ^ d << 4) + y * kSub * D);
+                        uint32_t a[kBeside][4];
+#pragma unroll
+                        for (int z = 0; z < 2 * kBeside; ++z) {
+                            const uint32_t sorted = __byte_perm(two[2 * z0 + z], 0u, 0x3120);
+                            a[z / 2][z % 2 * 2] = codes_to_half2(sorted);
+                            a[z / 2][z % 2 * 2 + 1] = codes_to_half2(sorted >> 16);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int z = 0; z < kBeside; ++z)
+#pragma unroll
+                                for (int x = 0; x < kHeadTiles; ++x) {
+                                    if (y + c == 0)
+                                        mma_first<H>(o[z][x], a[z], pb[x][y][c][0], pb[x][y][c][1]);
+                                    else
+                                        mma<H>(o[z][x], a[z], pb[x][y][c][0], pb[x][y][c][1]);
+                                }
                     }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int z = 0; z < kBeside; ++z)
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
+                        for (int x = 0; x < kHeadTiles; ++x)
 #pragma unroll
-                            for (int x = 0; x < kHeadTiles; ++x)
-                                mma<H>(o[z][x], a[z], pb[x][y][c][0], pb[x][y][c][1]);
+                            for (int e = 0; e < 4; e += 2) {
+                                float* const sum = acc[x][d + z0 + z] + e;
+                                const uint64_t old =
+                                    mul2(pair(sum[0], sum[1]), pair(corr[x][0], corr[x][1]));
+                                const float2 f = halves(fma2(pair(o[z][x][e], o[z][x][e + 1]),
+                                                             pair(slice_scale, slice_scale), old));
+                                sum[0] = f.x, sum[1] = f.y;
+                            }
                 }
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int x = 0; x < kHeadTiles; ++x)
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            float* const sum = acc[x][d + z] + e;
-                            const uint64_t old = mul2(pair(sum[0], sum[1]), pair(corr[x][0], corr[x][1]));
-                            const float2 f = halves(fma2(pair(o[z][x][e], o[z][x][e + 1]),
-                                                         pair(slice_scale, slice_scale), old));
-                            sum[0] = f.x, sum[1] = f.y;
-                        }
             }
         }
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
 
-        // ---- the item's end, or the range's: join the warps (the next item's queries are on their way)
+        // ---- the item's end, or the range's: join the warps (the next item's queries are on their way).
+        // The stage just done is free until the next load; a cluster's blocks, which have nothing more
+        // to load, use the first.
         const bool item_ends = cur.tile + 1 == cur.tiles;
-        Cursor<Fp8Span> next = cur;
-        if (!kCluster && t + 1 < t1) advance<kTile>(next, p);
-        if (!kCluster && item_ends && t + 1 < t1) load_all_queries(next);
+        [[maybe_unused]] Cursor<Fp8Rows> next = cur;
+        if constexpr (!kCluster && !C::kQueriesShared) {
+            if (t + 1 < t1) advance<kTile>(next, p);
+            if (item_ends && t + 1 < t1) load_all_queries(next);
+        }
         if (item_ends || t + 1 == t1) {
-            join_warps<T, C, kCluster>(p, cur, r, t, acc, m, l, merge, sm_m, sm_l, sm_i);
+            float* const to = merge + (C::kMergeInRing && !kCluster ? stage * (C::kCodeBytes / 4) : 0);
+            join_warps<T, C, kCluster>(p, cur, r, t, acc, m, l, to, sm_m, sm_l, sm_i);
             fresh = true;
         }
-        if (!kCluster)
+        if constexpr (kCluster) {
+            if (t + 1 < t1) ++cur.tile;
+        } else if constexpr (C::kQueriesShared) {
+            if (t + 1 < t1) advance<kTile>(cur, p);
+        } else {
             cur = next;
-        else if (t + 1 < t1)
-            ++cur.tile;
+        }
     }
     if constexpr (kCluster) join_cluster<T, C>(p, cur, merge, sm_i);
 }
@@ -551,7 +602,7 @@ int decode_paged_attention_fp8_workspace_bytes(int64_t h_q, int64_t h_kv, int64_
     if (rc != DECODE_OK) return rc;
     const int sms = sm_count();
     if (sms == 0) return DECODE_ERR_CUDA;
-    *bytes = layout_for(sms, heads_of(h_q / h_kv), head_dim).total;
+    *bytes = layout_for(sms, kMostResident, heads_of(h_q / h_kv), head_dim).total;
     return DECODE_OK;
 }
 
@@ -578,11 +629,24 @@ int decode_paged_attention_fp8(const decode_paged_attention_fp8_args* a, cudaStr
         return fail(DECODE_ERR_UNSUPPORTED, "strides must be multiples of 8");
     const int64_t cs[3] = {a->pages, a->page_size, a->h_kv};
     const int64_t ss[3] = {a->pages, a->page_size / a->block_size, a->h_kv};
-    if (!take_strides(p.k_stride, a->k_stride, cs, 16) ||
-        !take_strides(p.v_stride, a->v_stride, cs, 16))
+    int64_t stride[2][3], scale_stride[2][3];
+    if (!take_strides(stride[0], a->k_stride, cs, 16) || !take_strides(stride[1], a->v_stride, cs, 16))
         return fail(DECODE_ERR_UNSUPPORTED, "cache strides must be multiples of 16");
-    take_strides(p.scale_stride[0], a->k_scale_stride, ss, 1);
-    take_strides(p.scale_stride[1], a->v_scale_stride, ss, 1);
+    take_strides(scale_stride[0], a->k_scale_stride, ss, 1);
+    take_strides(scale_stride[1], a->v_scale_stride, ss, 1);
+    for (int of = 0; of < 2; ++of) {
+        for (int x = 0; x < 2; ++x) {
+            if (stride[of][x] < 0 || stride[of][x] > UINT32_MAX || scale_stride[of][x] < 0 ||
+                scale_stride[of][x] > UINT32_MAX)
+                return fail(DECODE_ERR_UNSUPPORTED, "strides of pages, tokens and blocks must be below 2^32");
+            p.stride[of][x] = static_cast<uint32_t>(stride[of][x]);
+            p.scale_stride[of][x] = static_cast<uint32_t>(scale_stride[of][x]);
+        }
+        p.head_stride[of] = stride[of][2];
+        p.scale_head_stride[of] = scale_stride[of][2];
+    }
+    p.same = std::equal(stride[0], stride[0] + 3, stride[1]) &&
+             std::equal(scale_stride[0], scale_stride[0] + 3, scale_stride[1]);
     constexpr int64_t kMost = (int64_t(1) << 31) - 1;
     if (a->n > kMost || a->h_q >= (1 << 20) || a->table_width > kMost)
         return fail(DECODE_ERR_UNSUPPORTED, "problem too large for one call");
@@ -590,7 +654,7 @@ int decode_paged_attention_fp8(const decode_paged_attention_fp8_args* a, cudaStr
     if (sms == 0) return DECODE_ERR_CUDA;
     const int64_t group = a->h_q / a->h_kv;
     const int heads = heads_of(group);
-    const Layout l = layout_for(sms, heads, a->head_dim);
+    const Layout l = layout_for(sms, kMostResident, heads, a->head_dim);
     if (a->workspace_bytes < 0 || static_cast<size_t>(a->workspace_bytes) < l.total)
         return fail(DECODE_ERR_INVALID_ARG, "workspace of %zu bytes needed", l.total);
     // (an item's queries are in registers, in all of its blocks, before its results are written)
@@ -600,10 +664,10 @@ int decode_paged_attention_fp8(const decode_paged_attention_fp8_args* a, cudaStr
          {"lse", a->lse, 4, a->n * a->h_q},
          {"workspace", a->workspace, 1, static_cast<int64_t>(l.total)}},
         {{"q", a->q, 2, d, sizes, p.q_stride},
-         {"k_cache", a->k_cache, 1, d, cs, p.k_stride},
-         {"v_cache", a->v_cache, 1, d, cs, p.v_stride},
-         {"k_scale", a->k_scale, 1, 1, ss, p.scale_stride[0]},
-         {"v_scale", a->v_scale, 1, 1, ss, p.scale_stride[1]},
+         {"k_cache", a->k_cache, 1, d, cs, stride[0]},
+         {"v_cache", a->v_cache, 1, d, cs, stride[1]},
+         {"k_scale", a->k_scale, 1, 1, ss, scale_stride[0]},
+         {"v_scale", a->v_scale, 1, 1, ss, scale_stride[1]},
          {"page_table", a->page_table, 4, a->table_width, {a->n}, {a->table_stride}},
          {"lens", a->lens, 4, a->n}});
     if (shared != DECODE_OK) return shared;

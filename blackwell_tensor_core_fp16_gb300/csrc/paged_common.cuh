@@ -12,7 +12,6 @@
 namespace decode {
 
 constexpr int kSub = 16;         // tokens of a matrix tile
-constexpr int kMostResident = 2;     // of Cfg::kResident
 constexpr int kClusterMost = 8;      // blocks of a cluster
 constexpr int kClusterTiles = 3;     // tiles of each of them
 constexpr int kSharedItems = 64;     // items up to which the join takes a block a head
@@ -60,6 +59,21 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The first product of a sum: c = a b.
+template <typename T>
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -136,7 +150,7 @@ __device__ __forceinline__ int block_of(int tile, int total, int blocks)
 
 // Where a warp is in the block's range of tiles.  Span, an attention's own, says which of a
 // sequence's tokens are seen: rows() of them are dealt to tiles, none where len is 0, and
-// span_of(parameters, sequence) makes it.
+// Span::of(parameters, sequence) makes it.
 template <typename Span>
 struct Cursor {
     int i;              // sequence
@@ -161,7 +175,7 @@ __device__ __forceinline__ void advance(Cursor<Span>& c, const P& p)
     c.item = 0;
     do {
         if (++c.i >= p.n) return;     // past the last tile: the caller stops by its count
-        c.span = span_of(p, c.i);
+        c.span = Span::of(p, c.i);
         c.tiles = tiles_of<kTileTokens>(c.span);
     } while (c.tiles == 0);
 }
@@ -182,7 +196,7 @@ __device__ __forceinline__ bool cluster_range(const P& p, Cursor<Span>& cur, Ran
     const int ranks = cluster_size(), item = c / ranks;
     cur.i = item / items_per_seq;
     cur.item = item % items_per_seq;
-    cur.span = span_of(p, cur.i);
+    cur.span = Span::of(p, cur.i);
     cur.tiles = tiles_of<C::kTile>(cur.span);
     if (cur.item == 0 && c % ranks == 0 && tid == 0 && p.lens[cur.i] != cur.span.len)
         atomicOr(p.status, DECODE_BAD_LENGTH);
@@ -217,7 +231,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     const int chunk = (p.n + C::kThreads - 1) / C::kThreads;
     const int i_lo = min(p.n, tid * chunk), i_hi = min(p.n, i_lo + chunk);
     int mine = 0;
-    for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+    for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(Span::of(p, i)) * items_per_seq;
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -237,7 +251,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     if (r.t0 >= upto - mine && r.t0 < upto) {          // one thread: its sequences hold tile r.t0
         int at = upto - mine;
         for (int i = i_lo; i < i_hi; ++i) {
-            const int tiles = tiles_of<kTile>(span_of(p, i)) * items_per_seq;
+            const int tiles = tiles_of<kTile>(Span::of(p, i)) * items_per_seq;
             if (r.t0 < at + tiles) {
                 sm_i[32] = i;
                 sm_i[33] = r.t0 - at;
@@ -249,7 +263,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     // sequences without tokens have no tile: their results are written here
     for (int i = c; i < p.n; i += gridDim.x) {
         const int raw = p.lens[i];
-        const Span s = span_of(p, i);
+        const Span s = Span::of(p, i);
         if (tid == 0 && raw != s.len) atomicOr(p.status, DECODE_BAD_LENGTH);
         if (s.len > 0) continue;
         uint4* row = reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * p.h_q * D);
@@ -265,14 +279,15 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     if (r.t0 >= r.t1) return false;
     __syncthreads();
     cur.i = sm_i[32];
-    cur.span = span_of(p, cur.i);
+    cur.span = Span::of(p, cur.i);
     cur.tiles = tiles_of<kTile>(cur.span);
     cur.item = sm_i[33] / cur.tiles;
     cur.tile = sm_i[33] % cur.tiles;
     return true;
 }
 
-// An item's end at tile t, or the range's: joins the warps' sums of their own tiles.  acc[x][d] are the
+// An item's end at tile t, or the range's: joins the warps' sums of their own tiles, through kMergeWarp
+// floats of `merge` for each warp, where element d of head h lies at merge_at(h, d).  acc[x][d] are the
 // products of 16 elements and a head tile as the matrix instruction leaves them, whose row r stands for
 // element r, or (kRowPairs) rows r and r + 8 for elements 2 r and 2 r + 1.  Ends with a barrier.
 template <typename T, typename C, bool kCluster, typename Span, typename P>
@@ -310,15 +325,15 @@ __device__ __forceinline__ void join_warps(const P& p, const Cursor<Span>& cur, 
 #pragma unroll
             for (int y = 1; y < kWarps; ++y) top = fmaxf(top, sm_m[y * kHeads + h]);
             const float f = exp2_fast(m[x][e] - (top == -INFINITY ? 0.f : top));
-            float* to = merge + (w * kHeads + h) * C::kMergeRow;
+            float* to = merge + w * C::kMergeWarp;
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 if constexpr (C::kRowPairs) {
-                    *reinterpret_cast<float2*>(to + d * 16 + (lane >> 2) * 2) =
+                    *reinterpret_cast<float2*>(to + C::merge_at(h, d * 16 + (lane >> 2) * 2)) =
                         make_float2(acc[x][d][e] * f, acc[x][d][2 + e] * f);
                 } else {
-                    to[d * 16 + (lane >> 2)] = acc[x][d][e] * f;
-                    to[d * 16 + (lane >> 2) + 8] = acc[x][d][2 + e] * f;
+                    to[C::merge_at(h, d * 16 + (lane >> 2))] = acc[x][d][e] * f;
+                    to[C::merge_at(h, d * 16 + (lane >> 2) + 8)] = acc[x][d][2 + e] * f;
                 }
             }
         }
@@ -339,12 +354,12 @@ __device__ __forceinline__ void join_warps(const P& p, const Cursor<Span>& cur, 
         for (int y = 0; y < kWarps; ++y) {
             sum = fmaf(sm_l[y * kHeads + h], exp2_fast(sm_m[y * kHeads + h] - ref), sum);
             const float4 b = *reinterpret_cast<const float4*>(
-                merge + (y * kHeads + h) * C::kMergeRow + d);
+                merge + y * C::kMergeWarp + C::merge_at(h, d));
             o.x += b.x, o.y += b.y, o.z += b.z, o.w += b.w;
         }
         if constexpr (kCluster) {
             // (each element of the first warp's rows is read by this thread alone)
-            *reinterpret_cast<float4*>(merge + h * C::kMergeRow + d) = o;
+            *reinterpret_cast<float4*>(merge + C::merge_at(h, d)) = o;
             if (d == 0) {
                 reinterpret_cast<float*>(sm_i)[h] = top;
                 reinterpret_cast<float*>(sm_i)[kHeads + h] = sum;
@@ -393,7 +408,7 @@ __device__ __forceinline__ void join_cluster(const P& p, const Cursor<Span>& cur
             const float f =
                 exp2_fast(cluster_load(cluster_address(smem_addr(sm_i + h), y)) - ref);
             const float4 b = cluster_load4(
-                cluster_address(smem_addr(merge + h * C::kMergeRow + d), y));
+                cluster_address(smem_addr(merge + C::merge_at(h, d)), y));
             sum = fmaf(cluster_load(cluster_address(smem_addr(sm_i + kHeads + h), y)), f, sum);
             o.x = fmaf(b.x, f, o.x), o.y = fmaf(b.y, f, o.y);
             o.z = fmaf(b.z, f, o.z), o.w = fmaf(b.w, f, o.w);
@@ -526,9 +541,10 @@ static __global__ void __launch_bounds__(kJoinWarps * 32, 1) paged_attention_joi
 struct Layout {
     size_t ml, o, total;
 };
-inline Layout layout_for(int sms, int heads, int64_t d)
+// (resident: the most blocks of an SM that any shape of the kernel has)
+inline Layout layout_for(int sms, int resident, int heads, int64_t d)
 {
-    const size_t blocks = static_cast<size_t>(sms) * kMostResident;
+    const size_t blocks = static_cast<size_t>(sms) * resident;
     Layout l{};
     size_t at = sizeof(int4) * (blocks > kListedItems ? blocks : kListedItems);
     l.ml = at = (at + 255) & ~size_t(255);

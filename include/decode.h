@@ -295,7 +295,8 @@ int decode_dequantize_cache(const decode_dequantize_cache_args* args, cudaStream
  * codes stand for, and with a window the first `sinks` tokens stay visible: a sequence's seen tokens
  * are t < sinks and lens[i] - window <= t < lens[i] (window == 0: all, and sinks is ignored).  A
  * scale or code that stands for NaN reaches the results of its block's or token's head; those of
- * unseen tokens reach none.  The workspace is its own: decode_paged_attention_fp8_workspace_bytes().
+ * unseen tokens reach none.  Strides of pages, offsets and blocks are below 2^32.  The workspace is its
+ * own: decode_paged_attention_fp8_workspace_bytes().
  */
 typedef struct {
     const void* q;
