@@ -103,6 +103,19 @@ bool take_strides(int64_t (&to)[N], const int64_t (&from)[N], const int64_t (&si
     return ok;
 }
 
+// Division by a number that is often a power of two (shift >= 0), for 0 <= x < 2^31.
+__device__ __forceinline__ int divide(int x, int by, int shift)
+{
+    return shift >= 0 ? x >> shift
+                      : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(by));
+}
+inline int shift_of(int64_t x)
+{
+    for (int s = 0; s < 31; ++s)
+        if (x == int64_t(1) << s) return s;
+    return -1;
+}
+
 // Refuses a call in which a written operand shares memory with another one.
 inline int refuse_shared(std::initializer_list<Operand> written, std::initializer_list<Operand> read)
 {
@@ -166,6 +179,50 @@ template <int N>
 __device__ __forceinline__ void cp_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- thread-block clusters: rank, barrier and reads of another block's shared memory
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_id()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" :::
+                 "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t smem, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t address)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(address) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t address)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(address) : "memory");
+    return x;
 }
 
 // ---- pairs -----------------------------------------------------------------------------------------

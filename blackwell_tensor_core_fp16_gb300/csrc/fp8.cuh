@@ -28,19 +28,6 @@ __device__ __forceinline__ float power_of(int e)
 // What a scale stands for.
 __device__ __forceinline__ float scale_of(int e) { return e == 255 ? NAN : power_of(e); }
 
-// Division by a number that is often a power of two (shift >= 0), for 0 <= x < 2^31.
-__device__ __forceinline__ int divide(int x, int by, int shift)
-{
-    return shift >= 0 ? x >> shift
-                      : static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(by));
-}
-inline int shift_of(int64_t x)
-{
-    for (int s = 0; s < 31; ++s)
-        if (x == int64_t(1) << s) return s;
-    return -1;
-}
-
 // What is wrong with a cache's sizes; DECODE_OK if nothing is.
 inline int check_cache(int64_t pages, int64_t page_size, int64_t block, int64_t heads, int64_t d)
 {

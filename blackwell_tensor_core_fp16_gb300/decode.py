@@ -31,7 +31,7 @@ DECODE_STATUS = {1: "a state slot outside the pool",
                  2: "a cache slot outside the cache, or out of its block's order",
                  4: "a position outside the rotary table",
                  8: "a sequence length its page table cannot hold",
-                 16: "a page number outside the cache"}
+                 16: "a page number outside the cache", 32: "a copy that took too long"}
 
 # The argument structs of include/decode.h, field by field (no padding on either side).
 GDN_STEP_ARGS = struct.Struct("=8Q7q9q4qqif")

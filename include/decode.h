@@ -64,6 +64,8 @@ extern "C" {
 #define DECODE_BAD_POSITION 4u    /* decode_qk_norm_rope: a position outside the table */
 #define DECODE_BAD_LENGTH 8u      /* an attention: a length its page table cannot hold */
 #define DECODE_BAD_PAGE 16u       /* an attention: a page outside the cache */
+#define DECODE_TIMED_OUT 32u      /* decode_linear_w4: a copy took longer than two seconds, and the call's
+                                     results are undefined */
 
 /* ---- the gated delta rule, token by token ------------------------------------------------------
  *
@@ -341,7 +343,8 @@ int decode_paged_attention_fp8_workspace_bytes(int64_t h_q, int64_t h_kv, int64_
  *   bias          [n], of x's type, dense, or NULL
  *   y             [m][n], of x's type, y_stride between rows (written)
  *
- * k and group are multiples of 32.  With k == 0 the sums are 0.
+ * k and group are multiples of 32; codes, scales and zeros span less than 2^32 bytes or elements each.
+ * With k == 0 the sums are 0.
  */
 #define DECODE_ACT_NONE 0
 #define DECODE_ACT_RELU 1
