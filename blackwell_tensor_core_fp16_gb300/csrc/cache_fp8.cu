@@ -39,7 +39,7 @@ struct QuantizeParams : CacheParams {
 struct DequantizeParams : CacheParams {
     uint16_t* y[2];
     int64_t y_stride[2][2];
-    int32_t units, at_once;           // 16-element units of a token; tokens of a block of threads
+    int32_t units, at_once;           // 8-element units of a token; tokens of a block of threads
     uint32_t magic;                   // ceil(2^32 / units)
 };
 
@@ -52,10 +52,21 @@ __device__ __forceinline__ float from_bits(uint32_t bits)
     return Half2<T>::unpack(bits).x;
 }
 
-// The larger of each half, of numbers without their sign.
+// The larger magnitude of each half (with some sign); NaN counts for nothing.
+template <typename T>
 __device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t x)
 {
-    return __vmaxu2(top, x & 0x7fff7fffu);
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(x));
+    else
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(x));
+    return r;
+}
+// The larger of the halves' magnitudes, over the warp.
+__device__ __forceinline__ uint32_t largest(uint32_t top)
+{
+    return __reduce_max_sync(0xffffffffu, max(top & 0x7fffu, top >> 16 & 0x7fffu));
 }
 // x with zeros for infinities and NaN.
 template <typename T>
@@ -65,16 +76,22 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
     return (lo < kInfinity<T> ? lo : 0u) | (hi < kInfinity<T> ? hi << 16 : 0u);
 }
 
+// (A warp that takes the keys' block and the values' has twice the rows on their way: 32768 tokens of 8
+// heads of 128 40 us, 46 with a warp for each.  At 256 there are no registers for both.)
+template <int D>
+constexpr int kKinds = D == 256 ? 1 : 2;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) quantize_cache_kernel(const QuantizeParams p)
+__global__ void __launch_bounds__(kWarps * 32, 2) quantize_cache_kernel(const QuantizeParams p)
 {
+    constexpr int kBoth = kKinds<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;     // a row's lanes; rows of one load
     constexpr int kHold = D == 256 ? 16 : 8;               // loads that wait in registers
     constexpr uint32_t kAll = 0xffffffffu;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int combo = blockIdx.y * p.per + w % p.per, phase = w / p.per, phases = kWarps / p.per;
-    if (combo >= 2 * p.heads || phase >= phases) return;
-    const int kv = combo >= p.heads, head = combo - kv * p.heads;
+    if (combo >= 2 / kBoth * p.heads || phase >= phases) return;
+    const int kv0 = combo >= p.heads, head = combo - kv0 * p.heads;
     dep_launch();
     dep_wait();
 
@@ -113,86 +130,117 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_cache_kernel(const Quant
         }
 
         const int page = divide(place, p.page_size, p.page_shift), offset = place - page * p.page_size;
-        uint8_t* const scale = p.scales[kv] + page * p.scale_stride[kv][0] +
-                               divide(offset, p.block, p.block_shift) * p.scale_stride[kv][1] +
-                               head * p.scale_stride[kv][2];
-        const int older = first > 0 ? *scale : 0;
+        const int block = divide(offset, p.block, p.block_shift);
         const int ch = lane % kLanes, sub = lane / kLanes;
-        const uint16_t* const x =
-            p.x[kv] + token * p.x_stride[kv][0] + head * p.x_stride[kv][1] + ch * 8;
-        uint4 row[kHold];
+        uint8_t* scale[kBoth];
+        const uint16_t* x[kBoth];
+        uint8_t* codes[kBoth];
+        int older[kBoth];
+#pragma unroll
+        for (int y = 0; y < kBoth; ++y) {
+            const int kv = kv0 + y;
+            scale[y] = p.scales[kv] + page * p.scale_stride[kv][0] + block * p.scale_stride[kv][1] +
+                       head * p.scale_stride[kv][2];
+            older[y] = first > 0 ? *scale[y] : 0;
+            x[y] = p.x[kv] + token * p.x_stride[kv][0] + head * p.x_stride[kv][1] + ch * 8;
+            codes[y] = p.codes[kv] + page * p.code_stride[kv][0] + offset * p.code_stride[kv][1] +
+                       head * p.code_stride[kv][2] + ch * 8;
+        }
+        uint4 row[kBoth][kHold];
         auto load = [&](int from) {
 #pragma unroll
-            for (int i = 0; i < kHold; ++i) {
-                const int r = from + i * kRows + sub;
-                row[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < run) row[i] = *reinterpret_cast<const uint4*>(x + r * p.x_stride[kv][0]);
-            }
+            for (int y = 0; y < kBoth; ++y)
+#pragma unroll
+                for (int i = 0; i < kHold; ++i) {
+                    const int r = from + i * kRows + sub;
+                    row[y][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < run)
+                        row[y][i] = *reinterpret_cast<const uint4*>(x[y] + r * p.x_stride[kv0 + y][0]);
+                }
         };
         constexpr int kChunk = kHold * kRows;
         const int last = (run - 1) / kChunk * kChunk;
-        uint32_t top = 0;
+        uint32_t top[kBoth] = {};
         for (int from = 0; from <= last; from += kChunk) {
             load(from);
 #pragma unroll
-            for (int i = 0; i < kHold; ++i)
-                top = larger(larger(larger(larger(top, row[i].x), row[i].y), row[i].z), row[i].w);
+            for (int y = 0; y < kBoth; ++y)
+#pragma unroll
+                for (int i = 0; i < kHold; ++i)
+                    top[y] = larger<T>(larger<T>(top[y], row[y][i].x), row[y][i].y),
+                    top[y] = larger<T>(larger<T>(top[y], row[y][i].z), row[y][i].w);
         }
-        top = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
-        const bool odd = top >= kInfinity<T>;              // an infinity or NaN: rarely
+        bool odd = false;                                  // an infinity or NaN: rarely
+#pragma unroll
+        for (int y = 0; y < kBoth; ++y) {
+            top[y] = largest(top[y]);
+            odd = odd || top[y] >= kInfinity<T>;
+        }
         if (odd) {
-            top = 0;
+#pragma unroll
+            for (int y = 0; y < kBoth; ++y) top[y] = 0;
             for (int from = 0; from <= last; from += kChunk) {
                 load(from);
 #pragma unroll
-                for (int i = 0; i < kHold; ++i) {
-                    top = larger(larger(top, finite_or_zero<T>(row[i].x)), finite_or_zero<T>(row[i].y));
-                    top = larger(larger(top, finite_or_zero<T>(row[i].z)), finite_or_zero<T>(row[i].w));
-                }
+                for (int y = 0; y < kBoth; ++y)
+#pragma unroll
+                    for (int i = 0; i < kHold; ++i) {
+                        const uint4& b = row[y][i];
+                        top[y] = larger<T>(larger<T>(top[y], finite_or_zero<T>(b.x)), finite_or_zero<T>(b.y));
+                        top[y] = larger<T>(larger<T>(top[y], finite_or_zero<T>(b.z)), finite_or_zero<T>(b.w));
+                    }
             }
-            top = __reduce_max_sync(kAll, max(top & 0xffffu, top >> 16));
+#pragma unroll
+            for (int y = 0; y < kBoth; ++y)
+                top[y] = largest(top[y]);
         }
-        // 448 = 1.75 * 2^8
-        const uint32_t bits = __float_as_uint(from_bits<T>(top));
-        const int need = max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u));
-        const int e = max(need, older);
-        if (lane == 0) *scale = static_cast<uint8_t>(e);
-
-        uint8_t* const codes = p.codes[kv] + page * p.code_stride[kv][0] +
-                               offset * p.code_stride[kv][1] + head * p.code_stride[kv][2] + ch * 8;
-        const float by = power_of(254 - e);
+        int e[kBoth];
+#pragma unroll
+        for (int y = 0; y < kBoth; ++y) {
+            // 448 = 1.75 * 2^8
+            const uint32_t bits = __float_as_uint(from_bits<T>(top[y]));
+            const int need =
+                max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u));
+            e[y] = max(need, older[y]);
+            if (lane == 0) *scale[y] = static_cast<uint8_t>(e[y]);
+        }
         for (int from = last; from >= 0; from -= kChunk) {
             if (from != last) load(from);                  // (the last are still there)
 #pragma unroll
-            for (int i = 0; i < kHold; ++i) {
-                const int r = from + i * kRows + sub;
-                uint32_t out[2];
-                const uint32_t in[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+            for (int y = 0; y < kBoth; ++y) {
+                const float by = power_of(254 - e[y]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float2 a = Half2<T>::unpack(in[2 * h]), b = Half2<T>::unpack(in[2 * h + 1]);
-                    float2 za = make_float2(0.f, 0.f), zb = za;
-                    if (odd) {                             // x * 0: NaN for an infinity
-                        za = make_float2(a.x * 0.f, a.y * 0.f);
-                        zb = make_float2(b.x * 0.f, b.y * 0.f);
-                        a.x = fmaf(a.x, by, za.x), a.y = fmaf(a.y, by, za.y);
-                        b.x = fmaf(b.x, by, zb.x), b.y = fmaf(b.y, by, zb.y);
-                    } else {
-                        a.x *= by, a.y *= by, b.x *= by, b.y *= by;
+                for (int i = 0; i < kHold; ++i) {
+                    if (from + i * kRows >= run) break;    // (for all lanes)
+                    const int r = from + i * kRows + sub;
+                    uint32_t out[2];
+                    const uint32_t in[4] = {row[y][i].x, row[y][i].y, row[y][i].z, row[y][i].w};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2 a = Half2<T>::unpack(in[2 * h]), b = Half2<T>::unpack(in[2 * h + 1]);
+                        if (odd) {                         // x * 0: NaN for an infinity
+                            a.x = fmaf(a.x, by, a.x * 0.f), a.y = fmaf(a.y, by, a.y * 0.f);
+                            b.x = fmaf(b.x, by, b.x * 0.f), b.y = fmaf(b.y, by, b.y * 0.f);
+                        } else {
+                            a = halves(mul2(pair(a.x, a.y), pair(by, by)));
+                            b = halves(mul2(pair(b.x, b.y), pair(by, by)));
+                        }
+                        out[h] = codes_of(a.x, a.y) | codes_of(b.x, b.y) << 16;
                     }
-                    out[h] = codes_of(a.x, a.y) | codes_of(b.x, b.y) << 16;
+                    if (r < run)
+                        *reinterpret_cast<uint2*>(codes[y] + r * p.code_stride[kv0 + y][1]) =
+                            make_uint2(out[0], out[1]);
                 }
-                if (r < run)
-                    *reinterpret_cast<uint2*>(codes + r * p.code_stride[kv][1]) =
-                        make_uint2(out[0], out[1]);
             }
         }
         // the block's other codes follow a scale that grew (a factor below 2^-126 takes any to 0, as 0 does)
-        if (e > older && first > 0) {
-            const float down = e - older < 127 ? power_of(127 + older - e) : 0.f;
+#pragma unroll
+        for (int y = 0; y < kBoth; ++y) {
+            if (e[y] <= older[y] || first == 0) continue;
+            const float down = e[y] - older[y] < 127 ? power_of(127 + older[y] - e[y]) : 0.f;
             for (int r = sub - first; r < most; r += kRows) {
                 if (r >= 0 && r < run) continue;
-                uint2* const at = reinterpret_cast<uint2*>(codes + r * p.code_stride[kv][1]);
+                uint2* const at = reinterpret_cast<uint2*>(codes[y] + r * p.code_stride[kv0 + y][1]);
                 const uint2 old = *at;
                 uint32_t in[2] = {old.x, old.y};
 #pragma unroll
@@ -207,62 +255,66 @@ __global__ void __launch_bounds__(kWarps * 32) quantize_cache_kernel(const Quant
     }
 }
 
-// A thread takes units of 16 neighbouring elements, four at a time so that their chains of slot,
-// code and store run beside each other.
+// A thread takes units of 8 neighbouring elements of a token's key and the same of its value, two at a
+// time, so that their chains of slot, codes and stores run beside each other.  (With 16, whose results
+// are two stores a thread, each fills half of every sector that a warp's store touches: 200001 tokens of 2
+// heads of 256 took 107 us.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256) dequantize_cache_kernel(const DequantizeParams p)
 {
-    constexpr int kUnits = 4;
+    constexpr int kUnits = 2;
     dep_launch();
     dep_wait();
     const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.at_once;
     const int here = static_cast<int>(min(static_cast<int64_t>(p.at_once), p.tokens - t0)) * p.units;
     for (int u0 = threadIdx.x; u0 < here; u0 += 256 * kUnits) {
-        uint4 codes[kUnits];
-        int e[kUnits];
-        uint16_t* to[kUnits];
+        uint2 codes[kUnits][2];
+        int e[kUnits][2], token[kUnits], rest[kUnits];
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
             const int u = u0 + i * 256;
-            to[i] = nullptr;
+            token[i] = -1;
             if (u >= here) continue;
-            const int t = p.at_once == 1 ? 0 : static_cast<int>(__umulhi(u, p.magic));
-            int rest = u - t * p.units;
-            const int kv = rest >= p.units / 2;
-            rest -= kv * (p.units / 2);
-            const int head = rest / (D / 16), ch = rest % (D / 16);
-            const int slot = p.slots[t0 + t];
-            to[i] = p.y[kv] + (t0 + t) * p.y_stride[kv][0] + head * p.y_stride[kv][1] + ch * 16;
-            codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            e[i] = 127;
+            token[i] = p.at_once == 1 ? 0 : static_cast<int>(__umulhi(u, p.magic));
+            rest[i] = u - token[i] * p.units;
+            const int slot = p.slots[t0 + token[i]], head = rest[i] / (D / 8), ch = rest[i] % (D / 8);
             if (slot >= 0 && slot < p.places) {
                 const int page = divide(slot, p.page_size, p.page_shift);
                 const int offset = slot - page * p.page_size;
-                codes[i] = *reinterpret_cast<const uint4*>(
-                    p.codes[kv] + page * p.code_stride[kv][0] + offset * p.code_stride[kv][1] +
-                    head * p.code_stride[kv][2] + ch * 16);
-                e[i] = p.scales[kv][page * p.scale_stride[kv][0] +
-                                    divide(offset, p.block, p.block_shift) * p.scale_stride[kv][1] +
-                                    head * p.scale_stride[kv][2]];
-            } else if (slot != -1 && kv == 0 && rest == 0) {
-                atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+                const int block = divide(offset, p.block, p.block_shift);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    codes[i][kv] = *reinterpret_cast<const uint2*>(
+                        p.codes[kv] + page * p.code_stride[kv][0] + offset * p.code_stride[kv][1] +
+                        head * p.code_stride[kv][2] + ch * 8);
+                    e[i][kv] = p.scales[kv][page * p.scale_stride[kv][0] + block * p.scale_stride[kv][1] +
+                                            head * p.scale_stride[kv][2]];
+                }
+            } else {
+                if (slot != -1 && rest[i] == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+                codes[i][0] = codes[i][1] = make_uint2(0u, 0u);
+                e[i][0] = e[i][1] = 127;
             }
         }
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) {
-            if (to[i] == nullptr) continue;
-            const float by = scale_of(e[i]);
-            const uint32_t in[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
-            uint32_t out[8];
+            if (token[i] < 0) continue;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
-                const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
-                out[2 * h] = Half2<T>::pack(a.x * by, a.y * by);
-                out[2 * h + 1] = Half2<T>::pack(b.x * by, b.y * by);
+            for (int kv = 0; kv < 2; ++kv) {
+                const float by = scale_of(e[i][kv]);
+                const uint32_t in[2] = {codes[i][kv].x, codes[i][kv].y};
+                uint32_t out[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
+                    const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
+                    out[2 * h] = Half2<T>::pack(a.x * by, a.y * by);
+                    out[2 * h + 1] = Half2<T>::pack(b.x * by, b.y * by);
+                }
+                *reinterpret_cast<uint4*>(p.y[kv] + (t0 + token[i]) * p.y_stride[kv][0] +
+                                          rest[i] / (D / 8) * p.y_stride[kv][1] + rest[i] % (D / 8) * 8) =
+                    make_uint4(out[0], out[1], out[2], out[3]);
             }
-            reinterpret_cast<uint4*>(to[i])[0] = make_uint4(out[0], out[1], out[2], out[3]);
-            reinterpret_cast<uint4*>(to[i])[1] = make_uint4(out[4], out[5], out[6], out[7]);
         }
     }
 }
@@ -271,7 +323,7 @@ template <typename T, int D>
 int quantize(const QuantizeParams& p, cudaStream_t stream)
 {
     const int64_t windows = (static_cast<int64_t>(p.tokens) + p.window - 1) / p.window;
-    const int groups = (2 * p.heads + p.per - 1) / p.per;
+    const int groups = (2 / kKinds<D> * p.heads + p.per - 1) / p.per;
     const cudaError_t e = launch(quantize_cache_kernel<T, D>, dim3(static_cast<uint32_t>(windows), groups),
                                  dim3(kWarps * 32), 0, stream, p);
     if (e != cudaSuccess)
@@ -360,9 +412,10 @@ int decode_quantize_cache(const decode_quantize_cache_args* a, cudaStream_t stre
     if (sms == 0 || p.status == nullptr) return DECODE_ERR_CUDA;
     p.x[0] = static_cast<const uint16_t*>(a->k);
     p.x[1] = static_cast<const uint16_t*>(a->v);
-    p.per = 2 * p.heads < kWarps ? 2 * p.heads : kWarps;
+    const int each = d == 256 ? 2 * p.heads : p.heads;      // warps' work of a token
+    p.per = each < kWarps ? each : kWarps;
     // few tokens: each may be a block's only one, and has warps of its own
-    p.window = static_cast<int64_t>(p.tokens) * 2 * p.heads <= sms * 64 ? 1 : kWindow;
+    p.window = static_cast<int64_t>(p.tokens) * each <= sms * 64 ? 1 : kWindow;
     const bool bf16 = a->dtype == DECODE_BF16;
     if (d == 64) return bf16 ? quantize<__nv_bfloat16, 64>(p, stream) : quantize<__half, 64>(p, stream);
     if (d == 128)
@@ -392,8 +445,8 @@ int decode_dequantize_cache(const decode_dequantize_cache_args* a, cudaStream_t 
     if (p.status == nullptr) return DECODE_ERR_CUDA;
     p.y[0] = static_cast<uint16_t*>(a->k);
     p.y[1] = static_cast<uint16_t*>(a->v);
-    p.units = static_cast<int32_t>(2 * a->h_k * d / 16);
-    p.at_once = p.units < 1024 ? 1024 / p.units : 1;
+    p.units = static_cast<int32_t>(a->h_k * d / 8);
+    p.at_once = p.units < 512 ? 512 / p.units : 1;
     p.magic = static_cast<uint32_t>(((uint64_t(1) << 32) + p.units - 1) / p.units);
     const bool bf16 = a->dtype == DECODE_BF16;
     if (d == 64)
