@@ -132,6 +132,7 @@ struct Cfg {
     template <typename T>
     static constexpr int kShift = kWeightShift<T>;
     static constexpr bool kRowPairs = false;
+    static constexpr int kEndTiles = 0, kAloneTiles = 0;
     static constexpr int kResident = 2;                       // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;

@@ -101,7 +101,8 @@ struct Fp8Cfg {
     template <typename T>
     static constexpr int kShift = 0;                          // (the sums carry no factor)
     static constexpr bool kRowPairs = true;
-    static constexpr int kResident = D <= 128 && kTiles == 1 ? 3 : 2;   // blocks of an SM
+    static constexpr int kEndTiles = 1, kAloneTiles = 8;
+    static constexpr int kResident = kTiles == 1 ? 3 : 2;   // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice
     static constexpr int kTile = kWarps * kSlice;
     static constexpr int kPer = kSlice > 32 ? kSlice / 32 : 1;     // tokens of a slice by lane
@@ -113,7 +114,7 @@ struct Fp8Cfg {
     static constexpr bool kMergeInRing = kHeads * D * 4 <= kCodeBytes;
     static constexpr int kSmallBytes = 2 * kWarps * kHeads * 4 + 256;
     // the queries stay in registers, but for the one shape whose sums leave no room for them
-    static constexpr bool kQueriesShared = D == 256 && kTiles == 2;
+    static constexpr bool kQueriesShared = D == 256;
     static constexpr int kQueryRow = D + 16;                  // elements
     static constexpr int kQueryBytes = kQueriesShared ? kHeads * kQueryRow * 2 + kHeads * 4 : 0;
     static constexpr int kMergeBytes = kMergeInRing ? 0 : kWarps * kHeads * (D + 4) * 4;
@@ -274,10 +275,12 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                 }
             }
             ++pre_t;
-            if constexpr (kCluster)
+            if constexpr (kCluster) {
                 ++pre.tile;
-            else
-                advance<kTile>(pre, p);
+            } else {
+                if (pre.tile + 1 == pre.tiles) pre_t += C::kEndTiles;
+                if (pre_t < t1) advance<kTile>(pre, p);
+            }
         }
         cp_commit();
         look_up();
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             for (int x = 0; x < kHeadTiles; ++x) load_queries(of, x, qf[x]);
     };
     load_all_queries(cur);
-    for (int t = t0; t < t1; ++t) {
+    for (int t = t0, stage = 0; t < t1;) {
         if (fresh) {
             fresh = false;
             begin_item();
@@ -377,7 +380,6 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                 l[x][0] = l[x][1] = 0.f;
             }
         }
-        const int stage = (t - t0) % C::kStages;
         __syncwarp();
         load((stage + C::kStages - 1) % C::kStages);
         cp_wait<C::kStages - 1>();
@@ -500,8 +502,8 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             // product cuts its sum's last bits off, which would add up over a long axis
 #pragma unroll
             for (int d = 0; d < D / 16; d += 2) {
-                // (two pieces of 16 elements beside each other, but for the shape with the most sums)
-                constexpr int kBeside = C::kQueriesShared ? 1 : 2;
+                // (two pieces of 16 elements beside each other, but for the shapes with the most sums)
+                constexpr int kBeside = D == 256 ? 1 : 2;
                 float o[kBeside][kHeadTiles][4];
                 uint32_t two[4];                   // tokens 0 .. 7 and 8 .. 15 of elements d, of d + 1
 #pragma unroll
@@ -550,23 +552,26 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
         // The stage just done is free until the next load; a cluster's blocks, which have nothing more
         // to load, use the first.
         const bool item_ends = cur.tile + 1 == cur.tiles;
+        const int then = t + 1 + (!kCluster && item_ends ? C::kEndTiles : 0);      // the next tile
         [[maybe_unused]] Cursor<Fp8Rows> next = cur;
         if constexpr (!kCluster && !C::kQueriesShared) {
-            if (t + 1 < t1) advance<kTile>(next, p);
-            if (item_ends && t + 1 < t1) load_all_queries(next);
+            if (then < t1) advance<kTile>(next, p);
+            if (item_ends && then < t1) load_all_queries(next);
         }
-        if (item_ends || t + 1 == t1) {
+        if (item_ends || then >= t1) {
             float* const to = merge + (C::kMergeInRing && !kCluster ? stage * (C::kCodeBytes / 4) : 0);
             join_warps<T, C, kCluster>(p, cur, r, t, acc, m, l, to, sm_m, sm_l, sm_i);
             fresh = true;
         }
         if constexpr (kCluster) {
-            if (t + 1 < t1) ++cur.tile;
+            if (then < t1) ++cur.tile;
         } else if constexpr (C::kQueriesShared) {
-            if (t + 1 < t1) advance<kTile>(cur, p);
+            if (then < t1) advance<kTile>(cur, p);
         } else {
             cur = next;
         }
+        t = then;
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
     if constexpr (kCluster) join_cluster<T, C>(p, cur, merge, sm_i);
 }

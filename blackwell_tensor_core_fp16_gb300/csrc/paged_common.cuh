@@ -113,7 +113,8 @@ __device__ __forceinline__ void advance(Cursor<Span>& c, const P& p)
     } while (c.tiles == 0);
 }
 
-// A block's tiles [t0, t1), of `total` in `blocks` blocks.
+// A block's share [t0, t1) of what is dealt, `total` of it in `blocks` blocks: an item's tiles in order and
+// kEndTiles more for its end, at which the warps are joined and nothing is on its way.
 struct Range {
     int t0, t1, total = 0, blocks = 0;
 };
@@ -163,8 +164,13 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     const int items_per_seq = p.h_kv * p.head_items;
     const int chunk = (p.n + C::kThreads - 1) / C::kThreads;
     const int i_lo = min(p.n, tid * chunk), i_hi = min(p.n, i_lo + chunk);
+    // what a sequence's items are dealt as
+    auto dealt = [&](int i) {
+        const int tiles = tiles_of<kTile>(Span::of(p, i));
+        return (tiles + (tiles > 0 ? C::kEndTiles : 0)) * items_per_seq;
+    };
     int mine = 0;
-    for (int i = i_lo; i < i_hi; ++i) mine += tiles_of<kTile>(Span::of(p, i)) * items_per_seq;
+    for (int i = i_lo; i < i_hi; ++i) mine += dealt(i);
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -184,7 +190,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     if (r.t0 >= upto - mine && r.t0 < upto) {          // one thread: its sequences hold tile r.t0
         int at = upto - mine;
         for (int i = i_lo; i < i_hi; ++i) {
-            const int tiles = tiles_of<kTile>(Span::of(p, i)) * items_per_seq;
+            const int tiles = dealt(i);
             if (r.t0 < at + tiles) {
                 sm_i[32] = i;
                 sm_i[33] = r.t0 - at;
@@ -214,9 +220,14 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     cur.i = sm_i[32];
     cur.span = Span::of(p, cur.i);
     cur.tiles = tiles_of<kTile>(cur.span);
-    cur.item = sm_i[33] / cur.tiles;
-    cur.tile = sm_i[33] % cur.tiles;
-    return true;
+    cur.item = sm_i[33] / (cur.tiles + C::kEndTiles);
+    cur.tile = sm_i[33] % (cur.tiles + C::kEndTiles);
+    if (cur.tile >= cur.tiles) {                   // an end, which the block before has: the next item
+        r.t0 += cur.tiles + C::kEndTiles - cur.tile;
+        cur.tile = cur.tiles - 1;
+        if (r.t0 < r.t1) advance<kTile>(cur, p);
+    }
+    return r.t0 < r.t1;
 }
 
 // An item's end at tile t, or the range's: joins the warps' sums of their own tiles, through kMergeWarp
@@ -271,7 +282,7 @@ __device__ __forceinline__ void join_warps(const P& p, const Cursor<Span>& cur, 
             }
         }
     __syncthreads();
-    const int begin = t - cur.tile;                   // the item's tiles [begin, end)
+    const int begin = t - cur.tile;                   // the item's tiles are dealt as [begin, end)
     const int end = begin + cur.tiles;
     const bool whole = begin >= r.t0 && end <= r.t1;
     const int slot = 2 * c + (begin >= r.t0 ? 1 : 0);
@@ -495,9 +506,9 @@ int launch_attention(P p, int64_t most_tokens, int sms, cudaStream_t stream)
 {
     const int64_t per_item = (most_tokens + C::kTile - 1) / C::kTile;
     const int64_t items = static_cast<int64_t>(p.n) * p.h_kv * p.head_items;
-    if (per_item > 0 && items >= (int64_t(1) << 31) / per_item)
+    if (per_item > 0 && items >= (int64_t(1) << 31) / (per_item + C::kEndTiles))
         return fail(DECODE_ERR_UNSUPPORTED, "too many tiles of the cache for one call");
-    const int64_t tiles = per_item * items;
+    const int64_t tiles = (per_item + (per_item > 0 ? C::kEndTiles : 0)) * items;
     const int64_t most = static_cast<int64_t>(sms) * C::kResident;
     const int blocks = static_cast<int>(tiles < 1 ? 1 : tiles < most ? tiles : most);
     p.by_item = items <= kListedItems;
@@ -510,7 +521,9 @@ int launch_attention(P p, int64_t most_tokens, int sms, cudaStream_t stream)
     // long ones take the second kernel.
     int ranks = 1;
     while (ranks < kClusterMost && ranks < per_item && items * ranks * 2 <= most) ranks *= 2;
-    const bool cluster = ranks > 1 && per_item <= ranks * kClusterTiles;
+    // A block an item, as a cluster of one, where the items just fill the GPU and none has many tiles.
+    const bool alone = ranks == 1 && per_item <= C::kAloneTiles && items <= most && 4 * items >= 3 * most;
+    const bool cluster = alone || (ranks > 1 && per_item <= ranks * kClusterTiles);
     auto* kernel = cluster ? kClusters : kFlat;
     static thread_local bool set[2][kMaxDevices] = {};
     int dev = 0;
