@@ -53,13 +53,14 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t mag
 }
 
 // A row's zero point, as the differences need it, and the differences of a word's 8 columns: pairs
-// (c, c + 4) for c = 0 .. 3.
+// (c, c + 4) for c = 0 .. 3, or, for half an instruction a pair more, neighbours.
 template <typename T>
 struct Differences;
 template <>
 struct Differences<__nv_bfloat16> {
+    static constexpr uint32_t kMagic = 0x43004300u;                // twice 2^7
     uint32_t zero;                               // twice 2^7 + z
-    __device__ __forceinline__ void set(uint32_t z) { zero = (z & 15u) * 0x10001u | 0x43004300u; }
+    __device__ __forceinline__ void set(uint32_t z) { zero = (z & 15u) * 0x10001u | kMagic; }
     __device__ __forceinline__ uint32_t less(uint32_t x) const
     {
         uint32_t r;
@@ -69,32 +70,47 @@ struct Differences<__nv_bfloat16> {
     __device__ __forceinline__ void of(uint32_t word, uint32_t (&to)[4]) const
     {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) to[c] = less(pick(word >> 4 * c, 0x000f000fu, 0x43004300u));
+        for (int c = 0; c < 4; ++c) to[c] = less(pick(word >> 4 * c, 0x000f000fu, kMagic));
     }
 };
 template <>
 struct Differences<__half> {
+    static constexpr uint32_t kMagic = 0x64006400u;                // twice 2^10
     uint32_t zero, above;                        // twice 2^10 + z; twice -(2^6 + z)
     __device__ __forceinline__ void set(uint32_t z)
     {
-        zero = (z & 15u) * 0x10001u | 0x64006400u;
+        zero = (z & 15u) * 0x10001u | kMagic;
         above = (z & 15u) * 0x00100010u | 0xd400d400u;
+    }
+    __device__ __forceinline__ uint32_t less(uint32_t x) const
+    {
+        uint32_t r;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(zero));
+        return r;
     }
     __device__ __forceinline__ void of(uint32_t word, uint32_t (&to)[4]) const
     {
 #pragma unroll
         for (int c = 0; c < 4; c += 2) {
             const uint32_t x = word >> 4 * c;
-            const uint32_t lo = pick(x, 0x000f000fu, 0x64006400u);
             // the next column's bits stand four higher: 2^10 + 16 code, a sixteenth of which is 2^6 + code
-            const uint32_t hi = pick(x, 0x00f000f0u, 0x64006400u);
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(to[c]) : "r"(lo), "r"(zero));
+            const uint32_t hi = pick(x, 0x00f000f0u, kMagic);
+            to[c] = less(pick(x, 0x000f000fu, kMagic));
             asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(to[c + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(above));
         }
     }
 };
 
-// A token's 8 columns in the order of the differences: pairs (c, c + 4).
+template <typename T>
+__device__ __forceinline__ void neighbours(const Differences<T>& diff, uint32_t word, uint32_t* to)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c)                  // a byte's halves, the upper one from the shifted word
+        to[c] = diff.less(pick(__byte_perm(word, word >> 4, c | (4 + c) << 8), 0x000f000fu,
+                               Differences<T>::kMagic));
+}
+
+// A token's 8 columns in the order of the pairs: pairs (c, c + 4).
 __device__ __forceinline__ uint4 sorted(const uint4& x)
 {
     return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
@@ -439,56 +455,58 @@ bool few_with_words(const LinearParams& p, int sms, cudaStream_t stream, int& rc
 // ---- more tokens -------------------------------------------------------------------------------------
 //
 // A block takes 128 outputs and up to 64 tokens, over all columns or, in a cluster, a part of them, 128 at
-// a time (a chunk).  Sixteen warps make the chunk's operands in shared memory, 128-byte swizzled: the
-// codes' differences, a lane 32 columns of a row, and the tokens' elements, both of which each thread
-// copies for itself several chunks ahead.  One thread issues the tcgen05.mma (128 x tokens x 16), a scale's
-// columns into sums of their own in tensor memory, and four or eight warps read those, multiply them by
-// the scales and add them to the running sums in registers, while the next chunks are on their way: two or
-// three stages of operands, two of sums.
+// a time (a chunk).  The matrix instruction (tcgen05.mma, 128 x tokens x 16) takes the codes' differences
+// from tensor memory and the tokens' elements from shared memory.  Four groups of four warps take a chunk
+// each in turn: a lane makes a row's differences of what its warp has copied chunks ahead and stores them
+// into tensor memory.  Two warps copy the tokens' elements.  One thread issues the matrix instructions, a
+// scale's columns into sums of their own, and four or eight warps read those, multiply them by the scales
+// and add them to the running sums in registers.  So four chunks are made at once, while the sums of two
+// are on their way.
 
-constexpr int kMakers = 16;                      // warps that make operands
+constexpr int kGroups = 4, kMakers = 4 * kGroups, kLoaders = 2;    // warps
+constexpr int kAhead = 4;                        // chunks that a warp of makers has on their way, with its own
 
-template <int kTokens>
+template <int kTokens, int kParts>
 struct TileCfg {
     static constexpr int kReaders = kTokens > 32 ? 8 : 4;          // warps; four have 32 tokens
-    static constexpr int kThreads = (kReaders + kMakers + 1) * 32;
-    static constexpr int kABytes = kRows * 256, kBBytes = kTokens * 256;   // two swizzled 64-column halves
-    static constexpr int kStage = kABytes + kBBytes;
-    static constexpr int kStages = kTokens > 32 ? 2 : 3;
-    static constexpr int kAhead = kTokens > 32 ? 5 : 6;            // chunks on their way
-    static constexpr int kUnits = (kTokens * 16 + kMakers * 32 - 1) / (kMakers * 32);   // of a maker's x
-    static constexpr int kAhead0 = kStages * kStage;               // where they are, 16 bytes a thread
-    static constexpr int kAheadBytes = kMakers * 512 * (1 + kUnits);
-    static constexpr int kBarriers = kAhead0 + kAhead * kAheadBytes;
+    static constexpr int kMma = kReaders + kMakers;                // the warp that issues
+    static constexpr int kThreads = (kMma + 1 + kLoaders) * 32;
+    static constexpr int kSums = kParts * kTokens > 128 ? 1 : 2;   // chunks whose sums tensor memory holds
+    static constexpr int kACols = 64, kSumCols = kSums * kParts * kTokens;
+    static constexpr int kColumns = kSumCols + kGroups * kACols;
+    static constexpr int kAlloc = 512;
+    static_assert(kColumns > kAlloc / 2 && kColumns <= kAlloc, "allocations are powers of two");
+    static constexpr int kBBytes = kTokens * 256;                  // two swizzled 64-column halves
+    static constexpr int kCodes = kGroups * kBBytes;               // where the codes are
+    static constexpr int kBarriers = kCodes + kMakers * kAhead * 2048;
     static constexpr int kSmem = kBarriers + 128 + 1024;           // (the base is rounded up to 1024)
     static_assert(kSmem <= 232448, "more than an SM has");
     static_assert(kSmem > 233472 / 2, "one block an SM, so that a cluster's never wait for tensor memory");
-    static_assert(kTokens * kSumRow * 4 <= kAhead0, "no room for the sums");
+    static_assert(kTokens * kSumRow * 4 <= kCodes, "no room for the sums");
 };
 
 // kParts: sums of a chunk, each of the columns of one scale.
 template <typename T, int kTokens, int kParts>
-__global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_kernel(const LinearParams p)
+__global__ void __launch_bounds__(TileCfg<kTokens, kParts>::kThreads, 1)
+linear_w4_tile_kernel(const LinearParams p)
 {
-    using C = TileCfg<kTokens>;
-    constexpr int kColumns = 2 * kParts * kTokens;                 // of tensor memory
-    constexpr int kAlloc = kColumns <= 32 ? 32 : kColumns <= 64 ? 64 : kColumns <= 128 ? 128
-                           : kColumns <= 256 ? 256 : 512;
+    using C = TileCfg<kTokens, kParts>;
+    constexpr int kSums = C::kSums;
     extern __shared__ uint8_t dynamic[];
     uint8_t* const smem = dynamic + (-smem_addr(dynamic) & 1023u);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::kBarriers);
     // operands made; operands read; sums made; sums read
-    const uint32_t full = smem_addr(bars), empty = full + C::kStages * 8, made = empty + C::kStages * 8,
+    const uint32_t full = smem_addr(bars), empty = full + kGroups * 8, made = empty + kGroups * 8,
                    taken = made + 16;
-    uint32_t* const slot = reinterpret_cast<uint32_t*>(bars + 2 * C::kStages + 4);
+    uint32_t* const slot = reinterpret_cast<uint32_t*>(bars + 2 * kGroups + 4);
     volatile uint32_t* const gave_up = slot + 1;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int part = cluster_rank(), j0 = cluster_id() * kRows, i0 = blockIdx.y * kTokens;
     const int c0 = part * p.pieces_each + min(part, p.pieces_more);
     const int chunks = p.pieces_each + (part < p.pieces_more);
     if (tid == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
-            gf16::mbar_init(full + s * 8, kMakers);
+        for (int s = 0; s < kGroups; ++s) {
+            gf16::mbar_init(full + s * 8, kMakers / kGroups + 1);
             gf16::mbar_init(empty + s * 8, 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -499,13 +517,13 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
         gf16::fence_mbarrier_init();
     }
     if (w == 0) {
-        gf16::tmem_alloc<1>(smem_addr(slot), kAlloc);
+        gf16::tmem_alloc<1>(smem_addr(slot), C::kAlloc);
         gf16::tmem_relinquish<1>();
     }
     gf16::tcgen05_fence_before();
     __syncthreads();
     gf16::tcgen05_fence_after();
-    const uint32_t tmem = *slot;
+    const uint32_t tmem = *slot, operands = tmem + C::kSumCols;
     dep_launch();
     dep_wait();
 
@@ -531,7 +549,8 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
                 const int column = (c0 + c) * 128 + x * (128 / kParts);
                 scale[x] = column < p.k ? scales[divide(column / 32, p.group, p.group_shift)] : 0;
             }
-            wait(made + (c & 1) * 8, c >> 1 & 1);
+            const int at = c % kSums;
+            wait(made + at * 8, c / kSums & 1);
             gf16::tcgen05_fence_after();
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
@@ -543,7 +562,7 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
                     if (t0 + t >= kTokens) break;
                     uint32_t got[kAtOnce];
                     gf16::tmem_ld_32x32b(tmem + (static_cast<uint32_t>(w % 4 * 32) << 16) +
-                                                 ((c & 1) * kParts + x) * kTokens + t0 + t, got);
+                                                 (at * kParts + x) * kTokens + t0 + t, got);
                     gf16::tmem_ld_wait();
                     if (there)
 #pragma unroll
@@ -553,144 +572,131 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
             }
             gf16::tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) gf16::mbar_arrive_local(taken + (c & 1) * 8);
+            if (lane == 0) gf16::mbar_arrive_local(taken + at * 8);
         }
-        // [token][output], where the operands were: all of them have been read
+        // [token][output], where the elements were: all of them have been read
 #pragma unroll
         for (int t = 0; t < kMine; ++t)
             if (t0 + t < kTokens) sums[(t0 + t) * kSumRow + tid % kRows] = sum[t];
-    } else if (w < C::kReaders + kMakers) {
-        // ---- the operands: a lane has 32 columns of a row, and 8 of some tokens
-        const int m = tid - C::kReaders * 32, q = lane & 3, r = (w - C::kReaders) * 8 + (lane >> 2);
-        const uint32_t row = min(j0 + r, p.n - 1);
-        // what is left of the columns from the lane's first on
-        const int mine = p.k - c0 * 128 - q * 32;
-        const uint8_t* code = p.codes + (row * static_cast<uint32_t>(p.code_stride) + c0 * 64 + q * 16);
-        const uint8_t* const zeros = p.zeros + row * static_cast<uint32_t>(p.zero_stride);
-        // 16 bytes of codes and of each unit of elements.  Each thread reads what it has copied itself, so
-        // nothing but its own copies is waited for.
-        constexpr int kUnits = C::kUnits, kAhead = C::kAhead;
-        const uint16_t* x_from[kUnits];
-        int x_left[kUnits];                      // columns from the first on, 0 without a token
-        uint32_t x_to[kUnits];
+    } else if (w < C::kMma) {
+        // ---- the codes: a warp has 32 rows of every fourth chunk, those of its lanes of tensor memory.  It
+        // copies them four lanes a row, and a lane reads its row back: nothing but the warp's own copies is
+        // waited for.
+        const int group = (w - C::kReaders) / 4, quarter = w % 4;
+        const int piece = lane & 3;
+        uint32_t from[4];
 #pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int u = m + i * kMakers * 32, token = u / 16, piece = u % 16;
-            const bool there = u < kTokens * 16 && i0 + token < p.m;
-            x_from[i] = p.x + (there ? (i0 + token) * p.x_stride : 0) + c0 * 128 + piece * 8;
-            x_left[i] = there ? p.k - c0 * 128 - piece * 8 : 0;
-            x_to[i] = smem_addr(smem) + C::kABytes + piece / 8 * (kTokens * 128) + token * 128 +
-                      ((piece % 8 ^ (token & 7)) << 4);
-        }
-        const uint32_t ahead = smem_addr(smem) + C::kAhead0 + m * 16;
-        uint32_t copy_to = ahead, read_from = ahead;
-        auto next = [&](uint32_t& at) {
-            at += C::kAheadBytes;
-            if (at == ahead + kAhead * C::kAheadBytes) at = ahead;
-        };
+        for (int i = 0; i < 4; ++i)
+            from[i] = min(j0 + quarter * 32 + i * 8 + (lane >> 2), p.n - 1) *
+                      static_cast<uint32_t>(p.code_stride);
+        const int mine = p.k - c0 * 128 - piece * 32;              // columns from the lane's first on
+        const uint8_t* const codes = p.codes + (static_cast<int64_t>(c0) * 64 + piece * 16);
+        const uint8_t* const zeros =
+            p.zeros + min(j0 + quarter * 32 + lane, p.n - 1) * static_cast<uint32_t>(p.zero_stride);
+        // (a row's pieces are turned, so that lanes that read different rows' meet in no bank)
+        const uint32_t ring = smem_addr(smem) + C::kCodes + (w - C::kReaders) * (kAhead * 2048);
+        const uint32_t put = (lane >> 2) * 64 + ((piece ^ (lane >> 3)) << 4);
+        uint32_t copy_to = 0, read_from = 0;
         auto copy = [&](int c) {
             if (c < chunks) {
-                if (c * 128 < mine) cp_async16(copy_to, code + c * 64);
+                if (c * 128 < mine)
 #pragma unroll
-                for (int i = 0; i < kUnits; ++i) {
-                    const bool there = c * 128 < x_left[i];
-                    cp_async16(copy_to + (1 + i) * (kMakers * 512), there ? x_from[i] + c * 128 : p.x,
-                               there ? 16u : 0u);
-                }
-                next(copy_to);
+                    for (int i = 0; i < 4; ++i) cp_async16(ring + copy_to + put + i * 512, codes + from[i] + c * 64);
+                copy_to = (copy_to + 2048) % (kAhead * 2048);
             }
             cp_commit();
         };
-        uint32_t zero[2];
-        auto load_zero = [&](int c) {
-            if (p.zeros == nullptr || c >= chunks || c * 128 >= mine) return 8u;
-            return static_cast<uint32_t>(zeros[divide((c0 + c) * 4 + q, p.group, p.group_shift)]);
+        uint32_t zero[kParts];
+        auto load_zeros = [&](int c) {
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) {
+                const int column = (c0 + c) * 128 + x * (128 / kParts);
+                zero[x] = p.zeros == nullptr || c >= chunks || column >= p.k
+                              ? 8u : zeros[divide(column / 32, p.group, p.group_shift)];
+            }
         };
 #pragma unroll
-        for (int a = 0; a < kAhead - 1; ++a) copy(a);
-        zero[0] = load_zero(0), zero[1] = load_zero(1);
-        // Where the lane's pieces go.  Lanes 2 and 3 of four write theirs in another order, so that no two of
-        // eight lanes meet in a bank: their columns lie 16 KB behind the others'.
-        const uint32_t back = q >> 1;
-        uint32_t to[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-            to[y] = smem_addr(smem) + back * (kRows * 128) + r * 128 +
-                    ((((q & 1) * 4 + (back * 2 ^ y)) ^ (r & 7)) << 4);
-        uint32_t at = 0, parity = 1;             // the stage's place; the first pass waits for nothing
-        uint32_t bar = 0;
+        for (int a = 0; a < kAhead - 1; ++a) copy(group + a * kGroups);
+        load_zeros(group);
+        const uint32_t to = operands + (static_cast<uint32_t>(quarter * 32) << 16) + group * C::kACols;
+        uint32_t parity = 1;                     // the first pass waits for nothing
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            copy(c + kAhead - 1);
-            cp_wait<kAhead - 1>();
-            uint32_t words[4];
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(words[0]), "=r"(words[1]) : "r"(read_from + back * 8) : "memory");
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                         : "=r"(words[2]), "=r"(words[3]) : "r"(read_from + 8 - back * 8) : "memory");
-            uint4 x[kUnits];
+        for (int c = group; c < chunks; c += kGroups) {
+            copy(c + (kAhead - 1) * kGroups);
+            Differences<T> diff[kParts];
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i)
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
-                             : "r"(read_from + (1 + i) * (kMakers * 512)) : "memory");
-            next(read_from);
-            Differences<T> diff;
-            diff.set(zero[0]);
-            zero[0] = zero[1];
-            zero[1] = load_zero(c + 2);
-            wait(empty + bar, parity);
+            for (int x = 0; x < kParts; ++x) diff[x].set(zero[x]);
+            load_zeros(c + kGroups);
+            cp_wait<kAhead - 1>();
+            __syncwarp();
+            wait(empty + group * 8, parity);
+            parity ^= 1;
+            gf16::tcgen05_fence_after();
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                uint32_t d[4];
-                diff.of(words[y], d);
-                gf16::st_shared_v4(to[y] + at, d[0], d[1], d[2], d[3]);
-            }
+                uint32_t words[4], d[16];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(words[0]), "=r"(words[1]), "=r"(words[2]), "=r"(words[3])
+                             : "r"(ring + read_from + lane * 64 + ((y ^ (lane >> 1 & 3)) << 4)) : "memory");
 #pragma unroll
-            for (int i = 0; i < kUnits; ++i) {
-                const uint4 s = sorted(x[i]);
-                if (kTokens * 16 % (kMakers * 32) == 0 || m < kTokens * 16)
-                    gf16::st_shared_v4(x_to[i] + at, s.x, s.y, s.z, s.w);
+                for (int e = 0; e < 4; ++e) neighbours(diff[y * kParts / 4], words[e], d + 4 * e);
+                gf16::tmem_st_32x32b(to + y * 16, d);
             }
-            gf16::fence_proxy_async_smem();
+            read_from = (read_from + 2048) % (kAhead * 2048);
+            gf16::tmem_st_wait();
+            gf16::tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0) gf16::mbar_arrive_local(full + bar);
-            at += C::kStage, bar += 8;
-            if (bar == C::kStages * 8) {
-                at = bar = 0;
-                parity ^= 1;
-            }
+            if (lane == 0) gf16::mbar_arrive_local(full + group * 8);
         }
         cp_wait<0>();
+    } else if (w > C::kMma) {
+        // ---- the tokens' elements, 16 bytes a copy: a warp has every other chunk
+        constexpr int kCopies = kTokens / 2;     // of a lane, two tokens apart
+        const int piece = lane % 16, first = lane / 16;
+        const uint16_t* const x = p.x + (i0 + first) * p.x_stride + c0 * 128 + piece * 8;
+        const int left = p.k - c0 * 128 - piece * 8, tokens = p.m - i0 - first;
+        const uint32_t to = smem_addr(smem) + piece / 8 * (kTokens * 128) + first * 128;
+        uint32_t turned[4];                      // the swizzle: a token's pieces in an order of its own
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turned[i] = (piece % 8 ^ (first + 2 * i)) << 4;
+#pragma unroll 1
+        for (int c = w - C::kMma - 1; c < chunks; c += kLoaders) {
+            const int stage = c % kGroups;
+            wait(empty + stage * 8, (c / kGroups & 1) ^ 1);
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const bool there = c * 128 < left && 2 * i < tokens;
+                cp_async16(to + stage * C::kBBytes + i * 256 + turned[i % 4],
+                           there ? x + 2 * i * p.x_stride + c * 128 : p.x, there ? 16u : 0u);
+            }
+            cp_commit();
+            cp_wait<0>();
+            gf16::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) gf16::mbar_arrive_local(full + stage * 8);
+        }
     } else if (gf16::elect_one_sync()) {
         // ---- the products
         constexpr uint32_t idesc = gf16::make_idesc_f16(kRows, kTokens, std::is_same<T, __half>::value ? 0 : 1);
-        int stage = 0;
-        uint32_t parity = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            wait(full + stage * 8, parity);
-            if (c >= 2) wait(taken + (c & 1) * 8, (c >> 1) - 1 & 1);
+            const int stage = c % kGroups, at = c % kSums;
+            wait(full + stage * 8, c / kGroups & 1);
+            if (c >= kSums) wait(taken + at * 8, (c / kSums & 1) ^ 1);
             gf16::tcgen05_fence_after();
-            const uint32_t base = smem_addr(smem) + stage * C::kStage;
+            const uint32_t base = smem_addr(smem) + stage * C::kBBytes;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint64_t a = gf16::make_smem_desc_sw128(base + k / 4 * (kRows * 128), 1024) + 2 * (k % 4);
-                const uint64_t b = gf16::make_smem_desc_sw128(
-                                       base + C::kABytes + k / 4 * (kTokens * 128), 1024) + 2 * (k % 4);
-                gf16::mma_f16<1>(tmem + ((c & 1) * kParts + k * kParts / 8) * kTokens, a, b, idesc,
-                                 k % (8 / kParts) != 0);
-            }
+            for (int k = 0; k < 8; ++k)
+                gf16::mma_f16_tmem(tmem + (at * kParts + k * kParts / 8) * kTokens,
+                                   operands + stage * C::kACols + k * 8,
+                                   gf16::make_smem_desc_sw128(base + k / 4 * (kTokens * 128), 1024) + 2 * (k % 4),
+                                   idesc, k % (8 / kParts) != 0);
             gf16::mma_commit(empty + stage * 8);
-            gf16::mma_commit(made + (c & 1) * 8);
-            if (++stage == C::kStages) {
-                stage = 0;
-                parity ^= 1;
-            }
+            gf16::mma_commit(made + at * 8);
         }
         // (the last sums' reader waits for them; after a wait that ran out nothing else would)
         if (*gave_up && chunks > 0)
-            gf16::mbar_wait(made + (chunks - 1 & 1) * 8, chunks - 1 >> 1 & 1, nullptr, kTimeout);
+            gf16::mbar_wait(made + (chunks - 1) % kSums * 8, (chunks - 1) / kSums & 1, nullptr, kTimeout);
     }
     __syncwarp();
 
@@ -698,7 +704,7 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
     gf16::tcgen05_fence_before();
     __syncthreads();
     gf16::tcgen05_fence_after();
-    if (w == 0) gf16::tmem_dealloc<1>(tmem, kAlloc);
+    if (w == 0) gf16::tmem_dealloc<1>(tmem, C::kAlloc);
     if (p.split > 1) cluster_barrier();
     const int tokens = min(kTokens, p.m - i0);
     for (int at = part * C::kThreads + tid; at < tokens * kRows; at += p.split * C::kThreads) {
@@ -726,17 +732,13 @@ __global__ void __launch_bounds__(TileCfg<kTokens>::kThreads, 1) linear_w4_tile_
 template <typename T, int kTokens, int kParts>
 int run_tile(LinearParams p, int sms, cudaStream_t stream)
 {
-    using C = TileCfg<kTokens>;
+    using C = TileCfg<kTokens, kParts>;
     const int64_t blocks = (p.n + kRows - 1) / kRows, tokens = (p.m + kTokens - 1) / kTokens;
     const int64_t chunks = (p.k + 127) / 128;
-    // the columns' parts: so many that the fullest SM has the least to do, a block's beginning and end
-    // counted as six chunks
-    int64_t best = -1;
-    for (int split = 1; split <= kMostSplit && (split == 1 || split <= chunks); split *= 2) {
-        const int64_t cost = (blocks * tokens * split + sms - 1) / sms * ((chunks + split - 1) / split + 6);
-        if (best >= 0 && cost >= best) continue;
-        best = cost, p.split = split;
-    }
+    // the columns' parts: as many as leave every block an SM of its own and some chunks to do
+    p.split = 1;
+    while (p.split < kMostSplit && blocks * tokens * p.split * 2 <= sms && chunks >= p.split * 2 * kGroups)
+        p.split *= 2;
     p.pieces_each = static_cast<int>(chunks / p.split), p.pieces_more = static_cast<int>(chunks % p.split);
     if (blocks * p.split > (int64_t(1) << 31) - 1 || tokens > 65535)
         return fail(DECODE_ERR_UNSUPPORTED, "too many outputs or tokens for one call");
