@@ -2,23 +2,20 @@
 //
 //     y[i][j] = act(bias[j] + sum_g s[j][g] sum_{c in g} x[i][c] (code[j][c] - z[j][g]))
 //
-// A weight is half a byte and takes part in 2 m operations, so for a few tokens HBM bounds the time,
-// and what a weight costs in instructions on its way to the matrix units decides whether it does: the
-// SMs have to take 47 of them a clock each.
+// A weight is half a byte and takes part in 2 m operations, so for a few tokens HBM bounds the time, and what
+// a weight costs in instructions on its way to the matrix units decides whether it does: to keep up with HBM,
+// the SMs have to take 47 weights a clock each.
 //
-// Work split.  A block takes 128 outputs (rows of the weights), 16 a warp, and 8 kTiles tokens, over a
-// part of the columns; the blocks of a cluster share the columns out and add their sums through
-// distributed shared memory, in a fixed order.  The rows' codes come through a ring of shared-memory
-// stages of 256 columns (16-byte cp.async), and beside them the tokens' elements, which all warps read.
+// From a code to an operand.  A 32-bit word holds 8 neighbouring columns.  A mask leaves two of its codes, 16
+// bits apart, as the last bits of two 16-bit numbers whose upper bits an `or` makes 2^7 (bfloat16) or 2^10
+// (float16); the zero point, lifted the same way, is subtracted.  That is exact, both being whole numbers of at
+// most 5 bits, and takes about three instructions for two weights.  The scale is left out of the product: the
+// sums of a scale's columns, of exact products in fp32, are multiplied by it and added to the running ones in
+// fp32.  So no weight is ever rounded, and the only rounding to 16 bits is the output's.
 //
-// The codes are the matrix instructions' first operand (m16n8k16, the rows its 16 rows, the tokens its
-// 8 columns).  A lane's 32-bit word holds 8 neighbouring columns; a mask leaves two of them, 16 bits
-// apart, as the last bits of two 16-bit numbers whose upper bits an `or` makes 2^7 (bfloat16) or 2^10
-// (float16), from which the zero point, lifted the same way, is subtracted: exact, both being whole
-// numbers of at most 5 bits.  So columns c and c + 4 are a step's neighbours, and the tokens' elements
-// are put into that order once, in their stage, by the threads that loaded them.  The scale is left out of the product:
-// each group's sums, of exact products in fp32, are multiplied by it and added to the running ones in
-// fp32, so no weight is ever rounded.
+// Two kernels.  One for up to 8 tokens with few elements streams the codes from global memory to the warps that
+// use them; mma.sync is enough there, for the tensor cores have next to nothing to do.  The other, for more,
+// spares the instructions: tcgen05.mma takes 128 outputs and up to 64 tokens at a time.
 #include "decode_mma.cuh"
 #include "desc.h"
 #include "ptx.cuh"
@@ -28,7 +25,6 @@ namespace {
 using namespace decode;
 
 constexpr int kRows = 128;                       // outputs of a block for more tokens
-constexpr int kMostSplit = 8;
 constexpr int kSumRow = kRows + 4;               // floats of a token's sums; the pad spreads the banks
 
 struct LinearParams {
@@ -124,15 +120,58 @@ __device__ __forceinline__ float activated(float y, int activation)
     return y;
 }
 
+// How many clusters of 1, 2, 4 and 8 blocks the GPU runs at once, asked for once per thread and device, when
+// the kernel is also allowed its shared memory.  Some SMs take part in no cluster of 4 or 8: of the 304
+// blocks of the kernel for few tokens 296 and 288 run at once, of the other one's 152 144 and 120.  The
+// clusters left over would begin when the others end: one token, 8192 x 28672, in 76 clusters of 4 took 72 us,
+// not in parts 43.
+constexpr int kMostSplit = 8, kSplits = 4;
+struct Clusters {
+    bool known;
+    int at_once[kSplits];
+};
+template <auto kKernel>
+cudaError_t clusters_of(int threads, int smem, const Clusters*& of)
+{
+    static thread_local Clusters held[kMaxDevices + 1] = {};       // (the last is asked for at every call)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Clusters& c = held[dev < kMaxDevices ? dev : kMaxDevices];
+    of = &c;
+    if (c.known) return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    for (int s = 0; s < kSplits && e == cudaSuccess; ++s) {
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1 << s;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(1 << s);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&c.at_once[s], kKernel, &cfg);
+    }
+    c.known = e == cudaSuccess && dev < kMaxDevices;
+    return e;
+}
+
 // ---- few tokens ------------------------------------------------------------------------------------
 //
-// Up to 8 tokens.  The tokens' elements fit shared memory, all of a block's columns, so nothing but the
-// codes streams.  A block takes 16 outputs at a time (an item) and 2048 of their columns (a stage): their
-// 16 rows come by bulk copies, a row each, into a ring of stages, with none of the SM's threads busy on the
-// way.  Of a stage's 16 pieces of 128 columns each of eight warps takes two; its sums of an item go to
-// shared memory, where the warps' are added after several items.  Two blocks an SM stay and take equal
-// shares of the items; the blocks of a cluster share the columns out where there are few items, or where
-// the tokens' elements would not fit.
+// Up to 8 tokens (m16n8k16: the codes' differences are the first operand, the tokens its 8 columns).  The
+// tokens' elements of all of a block's columns fit shared memory, so nothing but the codes streams.  A block
+// takes 16 outputs at a time (an item) and 2048 of their columns (a stage): their 16 rows come by bulk
+// copies, a row each, into a ring of stages, with none of the SM's threads busy on the way.  Of a stage's 16
+// pieces of 128 columns each of eight warps takes two; its sums of an item go to shared memory, where the
+// warps' are added after several items.  Two blocks an SM stay and take equal shares of the items; the
+// blocks of a cluster share the columns out where there are few items, and add their sums through
+// distributed shared memory, in a fixed order.  The differences come as pairs (c, c + 4), a shift and a mask
+// away, and the tokens' elements are put into that order once.
+//
+// One token, 14336 x 4096: 12.4 us (floor 4.5); 4096 x 4096: 5.8 (1.3); 256 x 256: 2.8, a launch and the way
+// there and back.  7 tokens, 5000 x 1024, groups of 32: 5.6 (0.5).
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 constexpr int kItem = 16;                        // outputs
@@ -400,56 +439,63 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
             gf16::mbar_wait(full + step % p.stages * 8, step / p.stages & 1, nullptr, kTimeout);
 }
 
-// The kernel for few tokens; false if their elements do not fit it.
+// The kernel for few tokens; false if they have too many elements for it.  Each block brings its columns of
+// all tokens into shared memory before it begins: its time grows with the tokens, the other kernel's does
+// not.  Measured, us, this kernel and the other: 4096 x 4096, 1 token 5.8 and 7.4, 4 7.3 and 7.6, 6 8.2 and
+// 7.7, 8 9.3 and 7.8; 14336 x 4096, 1 12.4 and 14.9, 4 13.9 and 15.0, 6 15.4 and 15.1; 8192 x 8192, 1 15.6
+// and 16.0, 2 17.0 and 16.1; 1024 x 14336, split by 8, 8 9.7 and 9.7; 5000 x 1024, 8 5.7 and 6.0.  More
+// parts than are best without regard to this lose more: 8192 x 8192, 8 tokens, 28.3.
+constexpr int kFewMostElements = 16384;
 template <typename T, int kWords>
-bool run_few(LinearParams p, int sms, cudaStream_t stream, int& rc)
+bool run_few(LinearParams p, cudaStream_t stream, int& rc)
 {
+    constexpr int kMost = 233472 / 2 - 1024;    // bytes of one of two blocks
+    const Clusters* clusters = nullptr;
+    cudaError_t e = clusters_of<linear_w4_few_kernel<T, kWords>>(kFewThreads, kMost, clusters);
+    if (e != cudaSuccess) {
+        rc = fail(DECODE_ERR_CUDA, "linear_w4_few_kernel: %s", cudaGetErrorString(e));
+        return true;
+    }
     const int64_t items = (p.n + kItem - 1) / kItem, pieces = (p.k + 127) / 128;
     // The columns' parts: those with which the block with the most to do has the least, a block's beginning
     // and end counted as two stages, a cluster's as four.  What shared memory the elements and two stages
     // leave holds the sums of as many items as a block has, and more stages.
     int64_t best = -1, smem = 0, shares = 0;
-    for (int split = 1; split <= kMostSplit && (split == 1 || split <= pieces); split *= 2) {
+    bool fits = false;
+    for (int s = 0; s < kSplits && (s == 0 || 1 << s <= pieces) && clusters->at_once[s] > 0; ++s) {
+        const int split = 1 << s;
         const int64_t mine = (pieces + split - 1) / split;
-        const int64_t most = 2 * sms / split < items ? 2 * sms / split : items, each = (items + most - 1) / most;
+        const int64_t most = clusters->at_once[s] < items ? clusters->at_once[s] : items,
+                      each = (items + most - 1) / most;
         const int64_t bytes = p.m * (mine * 256 + 64), sums = kFewWarps * p.m * kItem * 4;
         const int64_t stages = 2, room = kFewMost - bytes - stages * kFewStage;
-        if (room < sums) continue;
         const int64_t cost = each * mine + (split > 1 ? 4 : 2) * kPieces;
         if (best >= 0 && cost >= best) continue;
         best = cost, p.split = split, shares = most;
+        fits = room >= sums && p.m * mine <= kFewMostElements / 128;
+        if (!fits) continue;
         const int64_t waiting = room / sums < each ? room / sums : each;
         const int64_t more = (room - waiting * sums) / kFewStage;
         p.waiting = static_cast<int>(waiting);
         p.stages = static_cast<int>(stages + more < kMostStages ? stages + more : kMostStages);
         smem = bytes + waiting * sums + p.stages * kFewStage + 2 * kMostStages * 8 + 16;
     }
-    if (best < 0) return false;
+    if (!fits) return false;
     p.items_each = static_cast<int>(items / shares), p.items_more = static_cast<int>(items % shares);
     p.pieces_each = static_cast<int>(pieces / p.split), p.pieces_more = static_cast<int>(pieces % p.split);
-    static thread_local bool set[kMaxDevices] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && !(dev < kMaxDevices && set[dev])) {
-        e = cudaFuncSetAttribute(linear_w4_few_kernel<T, kWords>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, 233472 / 2 - 1024);
-        if (e == cudaSuccess && dev < kMaxDevices) set[dev] = true;
-    }
-    if (e == cudaSuccess)
-        e = launch_cluster(linear_w4_few_kernel<T, kWords>,
-                           dim3(static_cast<uint32_t>(shares * p.split)), dim3(kFewThreads), smem, stream,
-                           p.split, p);
+    e = launch_cluster(linear_w4_few_kernel<T, kWords>, dim3(static_cast<uint32_t>(shares * p.split)),
+                       dim3(kFewThreads), smem, stream, p.split, p);
     rc = e == cudaSuccess ? DECODE_OK
                           : fail(DECODE_ERR_CUDA, "linear_w4_few_kernel: %s", cudaGetErrorString(e));
     return true;
 }
 
 template <typename T>
-bool few_with_words(const LinearParams& p, int sms, cudaStream_t stream, int& rc)
+bool few_with_words(const LinearParams& p, cudaStream_t stream, int& rc)
 {
-    if (p.group % 4 == 0) return run_few<T, 4>(p, sms, stream, rc);
-    if (p.group % 2 == 0) return run_few<T, 2>(p, sms, stream, rc);
-    return run_few<T, 1>(p, sms, stream, rc);
+    if (p.group % 4 == 0) return run_few<T, 4>(p, stream, rc);
+    if (p.group % 2 == 0) return run_few<T, 2>(p, stream, rc);
+    return run_few<T, 1>(p, stream, rc);
 }
 
 // ---- more tokens -------------------------------------------------------------------------------------
@@ -457,27 +503,35 @@ bool few_with_words(const LinearParams& p, int sms, cudaStream_t stream, int& rc
 // A block takes 128 outputs and up to 64 tokens, over all columns or, in a cluster, a part of them, 128 at
 // a time (a chunk).  The matrix instruction (tcgen05.mma, 128 x tokens x 16) takes the codes' differences
 // from tensor memory and the tokens' elements from shared memory.  Four groups of four warps take a chunk
-// each in turn: a lane makes a row's differences of what its warp has copied chunks ahead and stores them
-// into tensor memory.  Two warps copy the tokens' elements.  One thread issues the matrix instructions, a
+// each in turn: a lane makes a row's differences of the codes that its warp has copied and stores them into
+// tensor memory; the elements are copied to where the matrix instruction takes them, a chunk of the group
+// ahead.  One thread issues the matrix instructions, a
 // scale's columns into sums of their own, and four or eight warps read those, multiply them by the scales
 // and add them to the running sums in registers.  So four chunks are made at once, while the sums of two
 // are on their way.
+//
+// 48 tokens, 14336 x 4096: 18.3 us (floor 4.8), 0.43 us a chunk; 16 tokens 15.4; 200 tokens, 4096 x 4096: 18.3
+// (3.5).  The instructions that make the operands bound it, on 112 of 152 SMs, a block's 128 rows being
+// indivisible.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory
+// alone, written and read twice a chunk, was more than half.  The elements by warps of their own, into one
+// place a group: 20.5.  Scales loaded when their sums are awaited: 19.0.
 
-constexpr int kGroups = 4, kMakers = 4 * kGroups, kLoaders = 2;    // warps
-constexpr int kAhead = 4;                        // chunks that a warp of makers has on their way, with its own
+constexpr int kGroups = 4, kMakers = 4 * kGroups;                  // warps
+constexpr int kAhead = 3;                        // chunks of a warp whose codes are there or on their way
 
 template <int kTokens, int kParts>
 struct TileCfg {
     static constexpr int kReaders = kTokens > 32 ? 8 : 4;          // warps; four have 32 tokens
     static constexpr int kMma = kReaders + kMakers;                // the warp that issues
-    static constexpr int kThreads = (kMma + 1 + kLoaders) * 32;
+    static constexpr int kThreads = (kMma + 1) * 32;
     static constexpr int kSums = kParts * kTokens > 128 ? 1 : 2;   // chunks whose sums tensor memory holds
     static constexpr int kACols = 64, kSumCols = kSums * kParts * kTokens;
     static constexpr int kColumns = kSumCols + kGroups * kACols;
     static constexpr int kAlloc = 512;
     static_assert(kColumns > kAlloc / 2 && kColumns <= kAlloc, "allocations are powers of two");
     static constexpr int kBBytes = kTokens * 256;                  // two swizzled 64-column halves
-    static constexpr int kCodes = kGroups * kBBytes;               // where the codes are
+    static constexpr int kCodes = 2 * kGroups * kBBytes;           // where the codes are: behind two chunks'
+                                                                   // elements of each group
     static constexpr int kBarriers = kCodes + kMakers * kAhead * 2048;
     static constexpr int kSmem = kBarriers + 128 + 1024;           // (the base is rounded up to 1024)
     static_assert(kSmem <= 232448, "more than an SM has");
@@ -504,9 +558,13 @@ linear_w4_tile_kernel(const LinearParams p)
     const int part = cluster_rank(), j0 = cluster_id() * kRows, i0 = blockIdx.y * kTokens;
     const int c0 = part * p.pieces_each + min(part, p.pieces_more);
     const int chunks = p.pieces_each + (part < p.pieces_more);
+    // Every block begins elsewhere among its columns: were they all at the same ones, the few lines of L2
+    // with those of the tokens would be asked for by all SMs at once.
+    const int turn = chunks > 0 ? cluster_id() * 5 % chunks : 0;
+    auto column_of = [&](int c) { return (c0 + (c + turn < chunks ? c + turn : c + turn - chunks)) * 128; };
     if (tid == 0) {
         for (int s = 0; s < kGroups; ++s) {
-            gf16::mbar_init(full + s * 8, kMakers / kGroups + 1);
+            gf16::mbar_init(full + s * 8, kMakers / kGroups);
             gf16::mbar_init(empty + s * 8, 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -535,27 +593,34 @@ linear_w4_tile_kernel(const LinearParams p)
     float* const sums = reinterpret_cast<float*>(smem);
     if (w < C::kReaders) {
         // ---- the sums: a thread has an output and up to 32 tokens
-        constexpr int kMine = kTokens < 32 ? kTokens : 32, kAtOnce = kParts == 4 ? 16 : 8;
+        constexpr int kMine = kTokens < 32 ? kTokens : 32, kAtOnce = kParts == 4 && kTokens < 64 ? 16 : 8;
         const int t0 = w / 4 * 32;
         float sum[kMine] = {};
         const uint32_t row = min(j0 + tid % kRows, p.n - 1);
         const uint16_t* const scales = p.scales + row * static_cast<uint32_t>(p.scale_stride);
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            // (on their way while the sums are made)
-            uint32_t scale[kParts];
+        uint32_t next[kParts];                   // a chunk ahead
+        auto load_scales = [&](int c) {
+            const int begin = column_of(c);
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
-                const int column = (c0 + c) * 128 + x * (128 / kParts);
-                scale[x] = column < p.k ? scales[divide(column / 32, p.group, p.group_shift)] : 0;
+                const int column = begin + x * (128 / kParts);
+                next[x] = c < chunks && column < p.k ? scales[divide(column / 32, p.group, p.group_shift)] : 0;
             }
-            const int at = c % kSums;
+        };
+        load_scales(0);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            uint32_t scale[kParts];
+            const int begin = column_of(c), at = c % kSums;
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) scale[x] = next[x];
+            load_scales(c + 1);
             wait(made + at * 8, c / kSums & 1);
             gf16::tcgen05_fence_after();
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
                 // (no part where there is no column: its scale stands for nothing)
-                const bool there = x == 0 || (c0 + c) * 128 + x * (128 / kParts) < p.k;
+                const bool there = x == 0 || begin + x * (128 / kParts) < p.k;
                 const float by = Half2<T>::unpack(scale[x]).x;
 #pragma unroll
                 for (int t = 0; t < kMine; t += kAtOnce) {
@@ -579,9 +644,9 @@ linear_w4_tile_kernel(const LinearParams p)
         for (int t = 0; t < kMine; ++t)
             if (t0 + t < kTokens) sums[(t0 + t) * kSumRow + tid % kRows] = sum[t];
     } else if (w < C::kMma) {
-        // ---- the codes: a warp has 32 rows of every fourth chunk, those of its lanes of tensor memory.  It
-        // copies them four lanes a row, and a lane reads its row back: nothing but the warp's own copies is
-        // waited for.
+        // ---- the operands.  The codes: a warp has 32 rows of every fourth chunk, those of its lanes of tensor
+        // memory.  It copies them four lanes a row, and a lane reads its row back: nothing but the warp's
+        // own copies is waited for.
         const int group = (w - C::kReaders) / 4, quarter = w % 4;
         const int piece = lane & 3;
         uint32_t from[4];
@@ -589,49 +654,73 @@ linear_w4_tile_kernel(const LinearParams p)
         for (int i = 0; i < 4; ++i)
             from[i] = min(j0 + quarter * 32 + i * 8 + (lane >> 2), p.n - 1) *
                       static_cast<uint32_t>(p.code_stride);
-        const int mine = p.k - c0 * 128 - piece * 32;              // columns from the lane's first on
-        const uint8_t* const codes = p.codes + (static_cast<int64_t>(c0) * 64 + piece * 16);
+        const uint8_t* const codes = p.codes + piece * 16;
         const uint8_t* const zeros =
             p.zeros + min(j0 + quarter * 32 + lane, p.n - 1) * static_cast<uint32_t>(p.zero_stride);
         // (a row's pieces are turned, so that lanes that read different rows' meet in no bank)
         const uint32_t ring = smem_addr(smem) + C::kCodes + (w - C::kReaders) * (kAhead * 2048);
         const uint32_t put = (lane >> 2) * 64 + ((piece ^ (lane >> 3)) << 4);
         uint32_t copy_to = 0, read_from = 0;
-        auto copy = [&](int c) {
-            if (c < chunks) {
-                if (c * 128 < mine)
+        auto copy_codes = [&](int c) {
+            if (c >= chunks) return;
+            const int begin = column_of(c);
+            if (begin + piece * 32 < p.k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async16(ring + copy_to + put + i * 512, codes + from[i] + c * 64);
-                copy_to = (copy_to + 2048) % (kAhead * 2048);
+                for (int i = 0; i < 4; ++i)
+                    cp_async16(ring + copy_to + put + i * 512, codes + from[i] + begin / 2);
+            copy_to = copy_to == (kAhead - 1) * 2048 ? 0 : copy_to + 2048;
+        };
+        // The elements: a thread of a group's 128 has 8 columns of every eighth token.  What stands at tokens
+        // that are not there is multiplied into sums of theirs, which nobody writes.
+        const int first = quarter * 2 + lane / 16;
+        const int there = (p.m - i0 - first + 7) >> 3;             // tokens
+        const uint16_t* const x = p.x + (i0 + first) * p.x_stride + lane % 16 * 8;
+        const int64_t step = 8 * p.x_stride;
+        const uint32_t x_to = smem_addr(smem) + group * C::kBBytes + lane % 16 / 8 * (kTokens * 128) +
+                              first * 128 + ((lane % 8 ^ first) << 4);
+        auto copy_x = [&](int c, uint32_t half) {
+            if (c >= chunks) return;
+            const int begin = column_of(c);
+            const bool column = begin + lane % 16 * 8 < p.k;       // (zeros behind the last)
+            const uint16_t* at = column ? x + begin : p.x;
+#pragma unroll
+            for (int i = 0; i < kTokens / 8; ++i) {
+                if (i < there)
+                    cp_async16(x_to + half * (kGroups * C::kBBytes) + i * 1024, at, column ? 16u : 0u);
+                if (column) at += step;
             }
-            cp_commit();
         };
         uint32_t zero[kParts];
         auto load_zeros = [&](int c) {
+            const int begin = column_of(c);
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
-                const int column = (c0 + c) * 128 + x * (128 / kParts);
+                const int column = begin + x * (128 / kParts);
                 zero[x] = p.zeros == nullptr || c >= chunks || column >= p.k
                               ? 8u : zeros[divide(column / 32, p.group, p.group_shift)];
             }
         };
-#pragma unroll
-        for (int a = 0; a < kAhead - 1; ++a) copy(group + a * kGroups);
+        copy_codes(group);
+        cp_commit();
+        copy_codes(group + kGroups);
+        copy_x(group, 0);
+        cp_commit();
         load_zeros(group);
+        cp_wait<1>();
+        __syncwarp();
         const uint32_t to = operands + (static_cast<uint32_t>(quarter * 32) << 16) + group * C::kACols;
-        uint32_t parity = 1;                     // the first pass waits for nothing
+        uint32_t turn_of = 0;                    // the group's chunks so far, modulo 2
 #pragma unroll 1
-        for (int c = group; c < chunks; c += kGroups) {
-            copy(c + (kAhead - 1) * kGroups);
+        for (int c = group; c < chunks; c += kGroups, turn_of ^= 1) {
             Differences<T> diff[kParts];
 #pragma unroll
             for (int x = 0; x < kParts; ++x) diff[x].set(zero[x]);
             load_zeros(c + kGroups);
-            cp_wait<kAhead - 1>();
-            __syncwarp();
-            wait(empty + group * 8, parity);
-            parity ^= 1;
+            wait(empty + group * 8, turn_of ^ 1);                  // (the first waits for nothing)
             gf16::tcgen05_fence_after();
+            copy_codes(c + 2 * kGroups);
+            copy_x(c + kGroups, turn_of ^ 1);
+            cp_commit();
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 uint32_t words[4], d[16];
@@ -642,39 +731,16 @@ linear_w4_tile_kernel(const LinearParams p)
                 for (int e = 0; e < 4; ++e) neighbours(diff[y * kParts / 4], words[e], d + 4 * e);
                 gf16::tmem_st_32x32b(to + y * 16, d);
             }
-            read_from = (read_from + 2048) % (kAhead * 2048);
+            read_from = read_from == (kAhead - 1) * 2048 ? 0 : read_from + 2048;
+            // this chunk's elements and the codes of the group's next
+            cp_wait<1>();
+            gf16::fence_proxy_async_smem();
             gf16::tmem_st_wait();
             gf16::tcgen05_fence_before();
             __syncwarp();
             if (lane == 0) gf16::mbar_arrive_local(full + group * 8);
         }
         cp_wait<0>();
-    } else if (w > C::kMma) {
-        // ---- the tokens' elements, 16 bytes a copy: a warp has every other chunk
-        constexpr int kCopies = kTokens / 2;     // of a lane, two tokens apart
-        const int piece = lane % 16, first = lane / 16;
-        const uint16_t* const x = p.x + (i0 + first) * p.x_stride + c0 * 128 + piece * 8;
-        const int left = p.k - c0 * 128 - piece * 8, tokens = p.m - i0 - first;
-        const uint32_t to = smem_addr(smem) + piece / 8 * (kTokens * 128) + first * 128;
-        uint32_t turned[4];                      // the swizzle: a token's pieces in an order of its own
-#pragma unroll
-        for (int i = 0; i < 4; ++i) turned[i] = (piece % 8 ^ (first + 2 * i)) << 4;
-#pragma unroll 1
-        for (int c = w - C::kMma - 1; c < chunks; c += kLoaders) {
-            const int stage = c % kGroups;
-            wait(empty + stage * 8, (c / kGroups & 1) ^ 1);
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const bool there = c * 128 < left && 2 * i < tokens;
-                cp_async16(to + stage * C::kBBytes + i * 256 + turned[i % 4],
-                           there ? x + 2 * i * p.x_stride + c * 128 : p.x, there ? 16u : 0u);
-            }
-            cp_commit();
-            cp_wait<0>();
-            gf16::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) gf16::mbar_arrive_local(full + stage * 8);
-        }
     } else if (gf16::elect_one_sync()) {
         // ---- the products
         constexpr uint32_t idesc = gf16::make_idesc_f16(kRows, kTokens, std::is_same<T, __half>::value ? 0 : 1);
@@ -684,13 +750,13 @@ linear_w4_tile_kernel(const LinearParams p)
             wait(full + stage * 8, c / kGroups & 1);
             if (c >= kSums) wait(taken + at * 8, (c / kSums & 1) ^ 1);
             gf16::tcgen05_fence_after();
-            const uint32_t base = smem_addr(smem) + stage * C::kBBytes;
+            const uint32_t base = smem_addr(smem) + c % (2 * kGroups) * C::kBBytes;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 8; ++k) {
+                const uint64_t b = gf16::make_smem_desc_sw128(base + k / 4 * (kTokens * 128), 1024) + 2 * (k % 4);
                 gf16::mma_f16_tmem(tmem + (at * kParts + k * kParts / 8) * kTokens,
-                                   operands + stage * C::kACols + k * 8,
-                                   gf16::make_smem_desc_sw128(base + k / 4 * (kTokens * 128), 1024) + 2 * (k % 4),
-                                   idesc, k % (8 / kParts) != 0);
+                                   operands + stage * C::kACols + k * 8, b, idesc, k % (8 / kParts) != 0);
+            }
             gf16::mma_commit(empty + stage * 8);
             gf16::mma_commit(made + at * 8);
         }
@@ -730,26 +796,20 @@ linear_w4_tile_kernel(const LinearParams p)
 }
 
 template <typename T, int kTokens, int kParts>
-int run_tile(LinearParams p, int sms, cudaStream_t stream)
+int run_tile(LinearParams p, cudaStream_t stream)
 {
     using C = TileCfg<kTokens, kParts>;
     const int64_t blocks = (p.n + kRows - 1) / kRows, tokens = (p.m + kTokens - 1) / kTokens;
     const int64_t chunks = (p.k + 127) / 128;
-    // the columns' parts: as many as leave every block an SM of its own and some chunks to do
+    const Clusters* clusters = nullptr;
+    cudaError_t e = clusters_of<linear_w4_tile_kernel<T, kTokens, kParts>>(C::kThreads, C::kSmem, clusters);
+    // the columns' parts: as many as leave all blocks running at once, with some chunks each
     p.split = 1;
-    while (p.split < kMostSplit && blocks * tokens * p.split * 2 <= sms && chunks >= p.split * 2 * kGroups)
-        p.split *= 2;
+    for (int s = 1; s < kSplits && e == cudaSuccess; ++s)
+        if (blocks * tokens <= clusters->at_once[s] && chunks >= kGroups << s) p.split = 1 << s;
     p.pieces_each = static_cast<int>(chunks / p.split), p.pieces_more = static_cast<int>(chunks % p.split);
     if (blocks * p.split > (int64_t(1) << 31) - 1 || tokens > 65535)
         return fail(DECODE_ERR_UNSUPPORTED, "too many outputs or tokens for one call");
-    static thread_local bool set[kMaxDevices] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && !(dev < kMaxDevices && set[dev])) {
-        e = cudaFuncSetAttribute(linear_w4_tile_kernel<T, kTokens, kParts>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e == cudaSuccess && dev < kMaxDevices) set[dev] = true;
-    }
     if (e == cudaSuccess)
         e = launch_cluster(linear_w4_tile_kernel<T, kTokens, kParts>,
                            dim3(static_cast<uint32_t>(blocks * p.split), static_cast<uint32_t>(tokens)),
@@ -760,21 +820,21 @@ int run_tile(LinearParams p, int sms, cudaStream_t stream)
 }
 
 template <typename T, int kTokens>
-int tile_with_parts(const LinearParams& p, int sms, cudaStream_t stream)
+int tile_with_parts(const LinearParams& p, cudaStream_t stream)
 {
-    if (p.group % 4 == 0) return run_tile<T, kTokens, 1>(p, sms, stream);
-    if (p.group % 2 == 0) return run_tile<T, kTokens, 2>(p, sms, stream);
-    return run_tile<T, kTokens, 4>(p, sms, stream);
+    if (p.group % 4 == 0) return run_tile<T, kTokens, 1>(p, stream);
+    if (p.group % 2 == 0) return run_tile<T, kTokens, 2>(p, stream);
+    return run_tile<T, kTokens, 4>(p, stream);
 }
 
 template <typename T>
-int dispatch(const LinearParams& p, int sms, cudaStream_t stream)
+int dispatch(const LinearParams& p, cudaStream_t stream)
 {
     int rc = DECODE_OK;
-    if (p.m <= 8 && few_with_words<T>(p, sms, stream, rc)) return rc;
-    if (p.m <= 16) return tile_with_parts<T, 16>(p, sms, stream);
-    if (p.m <= 32) return tile_with_parts<T, 32>(p, sms, stream);
-    return tile_with_parts<T, 64>(p, sms, stream);
+    if (p.m <= 8 && few_with_words<T>(p, stream, rc)) return rc;
+    if (p.m <= 16) return tile_with_parts<T, 16>(p, stream);
+    if (p.m <= 32) return tile_with_parts<T, 32>(p, stream);
+    return tile_with_parts<T, 64>(p, stream);
 }
 
 }  // namespace
@@ -825,9 +885,8 @@ int decode_linear_w4(const decode_linear_w4_args* a, cudaStream_t stream)
                                       {"zeros", a->zeros, 1, groups, {a->n}, zero_stride},
                                       {"bias", a->bias, 2, a->n}});
     if (shared != DECODE_OK) return shared;
-    const int sms = sm_count();
     p.status = status_word();
-    if (sms == 0 || p.status == nullptr) return DECODE_ERR_CUDA;
+    if (p.status == nullptr) return DECODE_ERR_CUDA;
     p.x = static_cast<const uint16_t*>(a->x);
     p.codes = static_cast<const uint8_t*>(a->codes);
     p.scales = static_cast<const uint16_t*>(a->scales);
@@ -843,8 +902,8 @@ int decode_linear_w4(const decode_linear_w4_args* a, cudaStream_t stream)
     p.group = static_cast<int32_t>((a->group < a->k ? a->group : a->k > 0 ? a->k : 32) / 32);
     p.group_shift = shift_of(p.group);
     p.activation = a->activation;
-    return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, sms, stream)
-                                   : dispatch<__half>(p, sms, stream);
+    return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, stream)
+                                   : dispatch<__half>(p, stream);
 }
 
 }  // extern "C"
