@@ -21,6 +21,7 @@ using namespace decode;
 
 constexpr int kWarps = 8;
 constexpr int kWindow = 16;           // most tokens of a block of threads; half the lanes that see slots
+constexpr int kBack = 5;              // times 32 tokens before the window, looked through for its blocks
 
 // A cache's two tensors (keys, values), and where its places are.
 struct CacheParams {
@@ -77,7 +78,7 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
 }
 
 // (A warp that takes the keys' block and the values' has twice the rows on their way: 32768 tokens of 8
-// heads of 128 40 us, 46 with a warp for each.  At 256 there are no registers for both.)
+// heads of 128 41 us, 46 with a warp for each.  At 256 there are no registers for both.)
 template <int D>
 constexpr int kKinds = D == 256 ? 1 : 2;
 
@@ -103,11 +104,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quantize_cache_kernel(const Qu
     const bool mine = lane > 0 && lane <= p.window;
     const bool valid = slot >= 0 && slot < p.places;
     const bool after_one = lane > 0 && before >= 0 && before < p.places;
+    int earlier[kBack];
+#pragma unroll
+    for (int y = 0; y < kBack; ++y)
+        earlier[y] = t0 - lane - y * 32 >= 0 ? p.slots[t0 - lane - y * 32] : -1;
     const int in_block = valid ? slot - divide(slot, p.block, p.block_shift) * p.block : 0;
     const bool goes_on = valid && after_one && slot == before + 1 && in_block > 0;
-    const bool disordered = valid && after_one && !goes_on &&
-                            divide(slot, p.block, p.block_shift) ==
-                                divide(before, p.block, p.block_shift);
+    auto within = [&](int s, int begin) {        // of the block that begins there
+        return static_cast<uint32_t>(s - begin) < static_cast<uint32_t>(p.block);
+    };
+    const bool disordered = valid && after_one && !goes_on && within(before, slot - in_block);
     if (combo == 0 && phase == 0 && mine && (disordered || (!valid && slot != -1)))
         atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
     uint32_t leaders = __ballot_sync(kAll, mine && valid && !goes_on && !disordered);
@@ -116,6 +122,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) quantize_cache_kernel(const Qu
         if (nth % phases != phase) continue;
         const int lead = __ffs(leaders) - 1;
         const int place = __shfl_sync(kAll, slot, lead), first = __shfl_sync(kAll, in_block, lead);
+        // (another run of the same block, a little before: this one is refused)
+        bool again = lane < lead && within(slot, place - first);
+#pragma unroll
+        for (int y = 0; y < kBack; ++y) again = again || within(earlier[y], place - first);
+        if (__any_sync(kAll, again)) {
+            if (combo == 0 && lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+            continue;
+        }
         const int most = p.block - first;
         const int64_t token = t0 + lead;
         // the run: how many tokens of the block follow

@@ -216,9 +216,9 @@ def quantize_cache(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream=None)
 
     A block's tokens fill it from its first place on, over any number of calls: what lies below a
     call's first place in a block are older tokens, what lies above is nothing.  In a call they follow
-    one another in the order of their places, without a gap; neighbours that do not are refused
-    (``check_decode_status``), and tokens of one block that are apart leave it undefined.  An infinity
-    or NaN is held as NaN."""
+    one another in the order of their places, without a gap; one that comes up to 160 tokens after
+    another of its block and does not continue it is refused (``check_decode_status``), and tokens of one
+    block that are further apart leave it undefined.  An infinity or NaN is held as NaN."""
     _decode.quantize_cache(k, v, k_cache, v_cache, k_scale, v_scale, slots, stream)
 
 

@@ -246,15 +246,16 @@ int decode_paged_attention_workspace_bytes(int64_t h_q, int64_t h_kv, int64_t he
  *
  * so a token that is larger than those before it costs them at most the codes below E4M3's
  * smallest normal number.  Where a block's new tokens begin says what it holds: the places below
- * hold older tokens, those above nothing (a block whose first place is written begins anew).  An infinity or NaN becomes the code NaN, counts for no
- * scale and touches no other element.
+ * hold older tokens, those above nothing (a block whose first place is written begins anew).  An
+ * infinity or NaN becomes the code NaN, counts for no scale and touches no other element.
  *
  *   k, v          [tokens][h_k][head_dim], strides of the first two dimensions
  *   slots         int32 [tokens]: the token's place, page * page_size + offset, or -1 for none.  A
  *                 block's tokens follow one another in the call, in the order of their places without
- *                 a gap; one that is next to a token of its block and not in that order is refused
- *                 with those that continue it and reported, as is a slot outside the cache: neither is
- *                 written.  Tokens of one block that are apart leave its contents undefined.
+ *                 a gap.  One that comes after a token of its block, at most 160 tokens before, and
+ *                 does not continue it is refused with those that continue it and reported, as is a
+ *                 slot outside the cache: neither is written.  Tokens of one block that are further
+ *                 apart leave its contents undefined.
  *
  * decode_dequantize_cache gathers tokens: k and v [tokens][h_k][head_dim] receive c * 2^(e - 127), rounded
  * once to 16 bits.  Slot -1 gives zeros, and so does one outside the cache, which is reported.

@@ -183,6 +183,30 @@ def test_write_refusals(bad, kept, many):
             g.check_decode_status()
 
 
+@pytest.mark.parametrize("apart", [2, 3, 15, 16, 17, 31, 32, 33, 64, 100, 127, 128])
+@pytest.mark.parametrize("again", [[0, 1], [1, 2], [3], [-1, 1]])
+@pytest.mark.parametrize("lead,many", [(0, False), (0, True), (11, True)])
+def test_write_of_a_block_in_two_runs(apart, again, lead, many):
+    """A block's tokens that are `apart` tokens behind its first ones and do not continue them, the same
+    place among them: refused, as are those that continue them.  What lies between and behind is written."""
+    gen = generator(apart)
+    others = iter(range(8, 8 * 400, 8))
+    slots = [next(others) for _ in range(lead)] + [0]
+    slots += [next(others) for _ in range(apart - 1)]
+    first = len(slots)
+    slots += again + [next(others) + 5]
+    last = len(slots) - 1
+    slots = torch.tensor(slots + [-1] * (3000 if many else 0), dtype=torch.int32)
+    kept = list(range(first)) + [last]
+    c = caches(gen, 200, 16, 8, 2, 64)
+    before = {a: b.clone() for a, b in c.items()}
+    x = {kind: normal(gen, len(slots), 2, 64).half().cuda() for kind in "kv"}
+    write(c, x, slots.cuda())
+    check_cache(c, before, {kind: y[kept] for kind, y in x.items()}, slots[kept], "kept")
+    with pytest.raises(g.GemmError, match="cache slot"):
+        g.check_decode_status()
+
+
 def test_write_and_read_on_another_stream_and_in_a_graph():
     gen = generator(8)
     slots, pages = places(gen, 4, 30, 16)
