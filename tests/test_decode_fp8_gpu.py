@@ -513,6 +513,34 @@ def test_recorded_attention_follows_lengths_and_tables():
         ref.assert_close(lse, lse_ref, lb, f"{now}: lse")
 
 
+def test_graphs_that_share_a_workspace():
+    """Two recorded calls with one workspace between them, replayed in turn, and a third on its own on
+    another stream at the same time."""
+    gen = generator(22)
+    first = attention_inputs(gen, [900, 0, 77], 8, 2, 128, 16, 16, torch.bfloat16)
+    second = attention_inputs(gen, [5, 4000], 8, 2, 128, 20, 10, torch.bfloat16)
+    want = [attend(*x) for x in (first, second)]
+    ws = g.paged_attention_fp8_workspace(8, 2, 128)
+    graphs, outs = [], []
+    for x in (first, second):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(attend(*x, workspace=ws))
+        graphs.append(graph)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        for graph in graphs:
+            graph.replay()
+        with torch.cuda.stream(stream):
+            other = attend(*second)
+        torch.cuda.synchronize()
+        for o, w in zip(outs + [other], want + want[1:]):
+            assert torch.equal(o, w)
+
+
 def test_cache_past_32_bits():
     """Pages whose bytes lie past 2^32 of the cache's first."""
     gen = generator(21)
@@ -590,6 +618,57 @@ def test_linear_shapes(n, k):
     gen = generator(n)
     x = (0.1 * normal(gen, 3, k)).bfloat16().cuda()
     check_linear(x, weights(gen, n, k, 128, torch.bfloat16, True, False), f"{n} x {k}")
+
+
+@DTYPES
+@pytest.mark.parametrize("n,k,group", [(128, 8192, 128), (1000, 14336, 64), (20000, 512, 32), (130, 4128, 96),
+                                       (2500, 2080, 128)])
+@pytest.mark.parametrize("m", [7, 16, 31, 64, 129])
+def test_linear_shapes_of_more_tokens(m, n, k, group, dtype):
+    """Columns shared out by two, four and eight, more blocks than the GPU holds, and last chunks of 32 and
+    64 columns."""
+    gen = generator(n + m)
+    x = (0.1 * normal(gen, m, k)).to(dtype).cuda()
+    check_linear(x, weights(gen, n, k, group, dtype, True, False), f"{m} x {n} x {k}")
+
+
+@pytest.mark.parametrize("m", [9, 40, 100])
+def test_linear_of_strided_tokens(m):
+    """Tokens between others, and the same one for all; what other calls left on the chip (NaN) reaches
+    no result."""
+    gen = generator(m)
+    n, k = 200, 352
+    s = weights(gen, n, k, 96, torch.float16, True, True)
+    nothing = torch.full((128, k), math.nan, dtype=torch.float16, device="cuda")
+    packed = (0.3 * normal(gen, m, 3, k)).half().cuda()
+    out = torch.full((m, 2, n + 3), 7.0, dtype=torch.float16, device="cuda")
+    g.linear_w4(nothing, **s)
+    check_linear(packed[:, 1], s, "strided", out=out[:, 1, :n])
+    assert bool((out[:, 0] == 7).all()) and bool((out[:, 1, n:] == 7).all())
+    g.linear_w4(nothing, **s)
+    check_linear(packed[:1, 2].expand(m, k), s, "broadcast")
+
+
+def test_linear_beside_other_work():
+    """The same results from calls on two streams at once, beside a matrix product on a third."""
+    gen = generator(36)
+    cases = [((0.2 * normal(gen, m, k)).half().cuda(), weights(gen, n, k, 128, torch.float16, True, False))
+             for m, n, k in ((3, 1024, 4096), (16, 4096, 4096), (64, 1024, 4096), (48, 5000, 1024))]
+    want = [g.linear_w4(x, **s) for x, s in cases]
+    A, B = (torch.randn(1024, 2048, dtype=torch.float16, device="cuda") for _ in range(2))
+    product = g.linear(A, B)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        got += [(j, g.linear_w4(cases[j][0], **cases[j][1], stream=streams[i % 2]))
+                for j in ((i + 1) % 4, (i // 2) % 4)]
+        if i % 3 == 0:
+            got.append((-1, g.linear(A, B, stream=streams[2])))
+    torch.cuda.synchronize()
+    for j, y in got:
+        assert torch.equal(y, want[j] if j >= 0 else product), j
+    g.check_decode_status()
 
 
 def test_linear_of_strided_operands():

@@ -104,6 +104,28 @@ def test_linear_refusals(change, code, match):
     assert re.search(match, g.decode_last_error())
 
 
+@pytest.mark.parametrize("change", [
+    dict(k_stride=(1 << 33, 256, 128)), dict(v_stride=(8192, 1 << 32, 128)), dict(k_stride=(-8192, 256, 128)),
+    dict(k_scale_stride=(1 << 32, 2, 1)), dict(v_scale_stride=(4, 1 << 40, 1)),
+])
+def test_attention_refuses_strides_past_32_bits(change):
+    at = {x: (y + 1) << 20 for y, x in enumerate(("q", "k_cache", "v_cache", "k_scale", "v_scale", "page_table",
+                                                  "lens", "o", "workspace"))}
+    base = dict(ATTN, **at, q_stride=(512, 128), k_stride=(8192, 256, 128), v_stride=(8192, 256, 128),
+                k_scale_stride=(4, 2, 1), v_scale_stride=(4, 2, 1))
+    assert g.decode_paged_attention_fp8(pack("decode_paged_attention_fp8_args", **{**base, **change})) == NOT
+    assert "below 2^32" in g.decode_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(n=1 << 20, code_stride=4096), dict(n=3, scale_stride=1 << 31), dict(zero_stride=1 << 40),
+    dict(n=2, code_stride=1 << 31), dict(code_stride=-32),
+])
+def test_linear_refuses_weights_past_32_bits(change):
+    assert g.decode_linear_w4(pack("decode_linear_w4_args", **{**W4, **change})) == NOT
+    assert "2^32" in g.decode_last_error()
+
+
 def test_empty_problems_do_nothing():
     for name, values, size in (("quantize_cache", CACHE, "tokens"), ("dequantize_cache", CACHE, "tokens"),
                                ("paged_attention_fp8", ATTN, "n"), ("linear_w4", W4, "m"),
