@@ -6,12 +6,11 @@
 // a weight costs in instructions on its way to the matrix units decides whether it does: to keep up with HBM,
 // the SMs have to take 47 weights a clock each.
 //
-// From a code to an operand.  A 32-bit word holds 8 neighbouring columns.  A mask leaves two of its codes, 16
-// bits apart, as the last bits of two 16-bit numbers whose upper bits an `or` makes 2^7 (bfloat16) or 2^10
-// (float16); the zero point, lifted the same way, is subtracted.  That is exact, both being whole numbers of at
-// most 5 bits, and takes about three instructions for two weights.  The scale is left out of the product: the
-// sums of a scale's columns, of exact products in fp32, are multiplied by it and added to the running ones in
-// fp32.  So no weight is ever rounded, and the only rounding to 16 bits is the output's.
+// From a code to an operand.  The difference of a code and its zero point is exact in 16 bits, being a whole
+// number of at most 5 bits, and takes ten instructions for the 8 columns of a 32-bit word (below).  The scale
+// is left out of the product: the sums of a scale's columns, of exact products in fp32, are multiplied by it
+// and added to the running ones in fp32.  So no weight is ever rounded, and the only rounding to 16 bits is
+// the output's.
 //
 // Two kernels.  One for up to 8 tokens with few elements streams the codes from global memory to the warps that
 // use them; mma.sync is enough there, for the tensor cores have next to nothing to do.  The other, for more,
@@ -40,78 +39,64 @@ struct LinearParams {
     int32_t items_each, items_more, pieces_each, pieces_more, stages, waiting;    // for few tokens
 };
 
-// (x & mask) | magic in one instruction
-__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t magic)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(x), "r"(mask), "r"(magic));
-    return r;
-}
-
-// A row's zero point, as the differences need it, and the differences of a word's 8 columns: pairs
-// (c, c + 4) for c = 0 .. 3, or, for half an instruction a pair more, neighbours.
+// How codes become 16-bit numbers.  Two masks split a word's bytes, a permutation deals a byte of each to the
+// two halves of a register, and an fma makes them numbers.  (Masks that leave codes below the upper bits of
+// 2^7 or 2^10, from which the lifted zero point is subtracted, take 13 for neighbours, and 11 for columns
+// four apart, in whose order the tokens' elements have to be brought: 48 tokens, 14336 x 4096, 18.3 us for
+// 17.3, one token 12.4 for 12.0; the pipe of the integer operations was 67% busy.)
+//
+// A half of 16 bits that holds a whole number v < 256 and no more is v times the type's least number (bfloat16
+// has 7 bits behind the point and the exponents 0 and 1 the same unit, so this holds to 255): one fma brings it
+// to its size and takes the zero point from it.  kUp: the factors of a code in the lower half and of 16 times a
+// code in the upper one; kBack: what is left to be multiplied into the sums, for the least number's inverse is
+// no number of the type.
 template <typename T>
-struct Differences;
+struct Half;
 template <>
-struct Differences<__nv_bfloat16> {
-    static constexpr uint32_t kMagic = 0x43004300u;                // twice 2^7
-    uint32_t zero;                               // twice 2^7 + z
-    __device__ __forceinline__ void set(uint32_t z) { zero = (z & 15u) * 0x10001u | kMagic; }
-    __device__ __forceinline__ uint32_t less(uint32_t x) const
+struct Half<__nv_bfloat16> {
+    static constexpr uint32_t kUp = 0x7d007f00u, kDown = 0xff00ff00u;      // 2^127, 2^123; twice -2^127
+    static constexpr float kBack = 64.f;                                   // 2^133 / 2^127
+    __device__ __forceinline__ static uint32_t fma(uint32_t x, uint32_t y, uint32_t z)
     {
         uint32_t r;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(zero));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
         return r;
-    }
-    __device__ __forceinline__ void of(uint32_t word, uint32_t (&to)[4]) const
-    {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) to[c] = less(pick(word >> 4 * c, 0x000f000fu, kMagic));
     }
 };
 template <>
-struct Differences<__half> {
-    static constexpr uint32_t kMagic = 0x64006400u;                // twice 2^10
-    uint32_t zero, above;                        // twice 2^10 + z; twice -(2^6 + z)
-    __device__ __forceinline__ void set(uint32_t z)
-    {
-        zero = (z & 15u) * 0x10001u | kMagic;
-        above = (z & 15u) * 0x00100010u | 0xd400d400u;
-    }
-    __device__ __forceinline__ uint32_t less(uint32_t x) const
+struct Half<__half> {
+    static constexpr uint32_t kUp = 0x68007800u, kDown = 0xf800f800u;      // 2^15, 2^11; twice -2^15
+    static constexpr float kBack = 512.f;                                  // 2^24 / 2^15
+    __device__ __forceinline__ static uint32_t fma(uint32_t x, uint32_t y, uint32_t z)
     {
         uint32_t r;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(zero));
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
         return r;
     }
-    __device__ __forceinline__ void of(uint32_t word, uint32_t (&to)[4]) const
+};
+
+// A row's zero point as the differences need it, and the differences of a word's 8 columns, neighbours in
+// pairs, each over kBack.
+template <typename T>
+struct Differences {
+    static constexpr float kBack = Half<T>::kBack;
+    uint32_t zero;                               // twice -z / kBack
+    __device__ __forceinline__ void set(uint32_t z)
     {
+        zero = Half<T>::fma((z & 15u) * 0x10001u, Half<T>::kDown, 0u);
+    }
+    __device__ __forceinline__ void of(uint32_t word, uint32_t* to) const
+    {
+        const uint32_t even = word & 0x0f0f0f0fu, odd = word & 0xf0f0f0f0u;
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-            const uint32_t x = word >> 4 * c;
-            // the next column's bits stand four higher: 2^10 + 16 code, a sixteenth of which is 2^6 + code
-            const uint32_t hi = pick(x, 0x00f000f0u, kMagic);
-            to[c] = less(pick(x, 0x000f000fu, kMagic));
-            asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(to[c + 1]) : "r"(hi), "r"(0x2c002c00u), "r"(above));
+        for (int c = 0; c < 4; ++c) {            // byte c of each, and as upper bytes an even one's sign: 0
+            uint32_t two;
+            asm("prmt.b32 %0, %1, %2, %3;"
+                : "=r"(two) : "r"(even), "r"(odd), "r"(c | (4 + c) << 8 | (8 + c) * 0x1010));
+            to[c] = Half<T>::fma(two, Half<T>::kUp, zero);
         }
     }
 };
-
-template <typename T>
-__device__ __forceinline__ void neighbours(const Differences<T>& diff, uint32_t word, uint32_t* to)
-{
-#pragma unroll
-    for (int c = 0; c < 4; ++c)                  // a byte's halves, the upper one from the shifted word
-        to[c] = diff.less(pick(__byte_perm(word, word >> 4, c | (4 + c) << 8), 0x000f000fu,
-                               Differences<T>::kMagic));
-}
-
-// A token's 8 columns in the order of the pairs: pairs (c, c + 4).
-__device__ __forceinline__ uint4 sorted(const uint4& x)
-{
-    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                      __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-}
 
 __device__ __forceinline__ float activated(float y, int activation)
 {
@@ -167,10 +152,9 @@ cudaError_t clusters_of(int threads, int smem, const Clusters*& of)
 // pieces of 128 columns each of eight warps takes two; its sums of an item go to shared memory, where the
 // warps' are added after several items.  Two blocks an SM stay and take equal shares of the items; the
 // blocks of a cluster share the columns out where there are few items, and add their sums through
-// distributed shared memory, in a fixed order.  The differences come as pairs (c, c + 4), a shift and a mask
-// away, and the tokens' elements are put into that order once.
+// distributed shared memory, in a fixed order.
 //
-// One token, 14336 x 4096: 12.4 us (floor 4.5); 4096 x 4096: 5.8 (1.3); 256 x 256: 2.8, a launch and the way
+// One token, 14336 x 4096: 12.0 us (floor 4.5); 4096 x 4096: 5.6 (1.3); 256 x 256: 2.8, a launch and the way
 // there and back.  7 tokens, 5000 x 1024, groups of 32: 5.6 (0.5).
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
@@ -283,7 +267,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
     };
     load_scales();
 
-    // ---- the tokens' elements, 8 columns at a time in the codes' order; of a scale's columns the lanes'
+    // ---- the tokens' elements, 8 columns at a time; of a scale's columns the lanes'
     // first 8, then their second ones and so on.  Zeros past the last column, whatever the codes there.
     const int units = (piece1 - piece0) * 16;
     constexpr int kBatch = 4;
@@ -303,7 +287,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-            if (to[b] != nullptr) *reinterpret_cast<uint4*>(to[b]) = sorted(x[b]);
+            if (to[b] != nullptr) *reinterpret_cast<uint4*>(to[b]) = x[b];
     }
     __syncthreads();
     // (lanes without a token of their own read the last one's and have no result)
@@ -354,7 +338,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t got = __shfl_sync(0xffffffffu, sz[z], y * 16 + r + 8 * e);
-                        by[e] = Half2<T>::unpack(got & 0xffffu).x;
+                        by[e] = Half2<T>::unpack(got & 0xffffu).x * Differences<T>::kBack;
                         diff[e].set(got >> 16);
                     }
 #pragma unroll
@@ -441,10 +425,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 
 // The kernel for few tokens; false if they have too many elements for it.  Each block brings its columns of
 // all tokens into shared memory before it begins: its time grows with the tokens, the other kernel's does
-// not.  Measured, us, this kernel and the other: 4096 x 4096, 1 token 5.8 and 7.4, 4 7.3 and 7.6, 6 8.2 and
-// 7.7, 8 9.3 and 7.8; 14336 x 4096, 1 12.4 and 14.9, 4 13.9 and 15.0, 6 15.4 and 15.1; 8192 x 8192, 1 15.6
-// and 16.0, 2 17.0 and 16.1; 1024 x 14336, split by 8, 8 9.7 and 9.7; 5000 x 1024, 8 5.7 and 6.0.  More
-// parts than are best without regard to this lose more: 8192 x 8192, 8 tokens, 28.3.
+// not.  Measured, us, this kernel and the other: 4096 x 4096, 1 token 5.6 and 7.0, 4 7.0 and 7.2, 8 9.3 and
+// 7.4; 14336 x 4096, 1 12.0 and 13.6, 4 13.6 and 13.6, 8 16.7 and 13.8; 8192 x 8192, 1 15.0 and 14.7, 2 16.4
+// and 14.8; 28672 x 8192, 1 40.3 and 46.1, 2 41.4 and 46.1; 1024 x 14336, split by 8, 4 7.5 and 8.7; 5000 x
+// 1024, 8 5.7 and 5.8.  More parts than are best without regard to this lose more: 8192 x 8192, 8 tokens, 28.3.
 constexpr int kFewMostElements = 16384;
 template <typename T, int kWords>
 bool run_few(LinearParams p, cudaStream_t stream, int& rc)
@@ -510,12 +494,11 @@ bool few_with_words(const LinearParams& p, cudaStream_t stream, int& rc)
 // and add them to the running sums in registers.  So four chunks are made at once, while the sums of two
 // are on their way.
 //
-// 48 tokens, 14336 x 4096: 18.3 us (floor 4.8), 0.43 us a chunk; 16 tokens 15.4; 200 tokens, 4096 x 4096: 18.3
-// (3.5).  The instructions that make the operands bound it, on 112 of 152 SMs, a block's 128 rows being
-// indivisible.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory
-// alone, written and read twice a chunk, was more than half.  The elements by warps of their own, into one
-// place a group: 20.5.  Scales loaded when their sums are awaited: 19.0.
-
+// 48 tokens, 14336 x 4096: 17.3 us (floor 4.8), 0.4 us a chunk; 16 tokens 14.2; 200 tokens, 4096 x 4096: 17.3
+// (3.5).  The integer instructions that make the operands bound it, on 112 of 152 SMs, a block's 128 rows being
+// indivisible.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory alone,
+// written and read twice a chunk, was more than half.  The elements by warps of their own, into one place a
+// group: 20.5.  Scales loaded when their sums are awaited: 19.0.
 constexpr int kGroups = 4, kMakers = 4 * kGroups;                  // warps
 constexpr int kAhead = 3;                        // chunks of a warp whose codes are there or on their way
 
@@ -621,7 +604,7 @@ linear_w4_tile_kernel(const LinearParams p)
             for (int x = 0; x < kParts; ++x) {
                 // (no part where there is no column: its scale stands for nothing)
                 const bool there = x == 0 || begin + x * (128 / kParts) < p.k;
-                const float by = Half2<T>::unpack(scale[x]).x;
+                const float by = Half2<T>::unpack(scale[x]).x * Differences<T>::kBack;
 #pragma unroll
                 for (int t = 0; t < kMine; t += kAtOnce) {
                     if (t0 + t >= kTokens) break;
@@ -728,7 +711,7 @@ linear_w4_tile_kernel(const LinearParams p)
                              : "=r"(words[0]), "=r"(words[1]), "=r"(words[2]), "=r"(words[3])
                              : "r"(ring + read_from + lane * 64 + ((y ^ (lane >> 1 & 3)) << 4)) : "memory");
 #pragma unroll
-                for (int e = 0; e < 4; ++e) neighbours(diff[y * kParts / 4], words[e], d + 4 * e);
+                for (int e = 0; e < 4; ++e) diff[y * kParts / 4].of(words[e], d + 4 * e);
                 gf16::tmem_st_32x32b(to + y * 16, d);
             }
             read_from = read_from == (kAhead - 1) * 2048 ? 0 : read_from + 2048;
