@@ -705,6 +705,15 @@ def test_linear_of_what_is_no_number():
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("m", [3, 20])
+@pytest.mark.parametrize("exponent", [-118, -100, 100, 112])
+def test_linear_of_small_and_large_tokens(m, exponent):
+    """Elements near the ends of bfloat16's range: nothing is flushed to zero or overflows on the way."""
+    gen = generator(m)
+    x = (normal(gen, m, 256).double() * 2.0 ** exponent).bfloat16().cuda()
+    check_linear(x, weights(gen, 200, 256, 128, torch.bfloat16, True, False), f"2^{exponent}")
+
+
 def test_linear_without_columns_and_refusals():
     gen = generator(33)
     s = weights(gen, 5, 0, 32, torch.float16, False, True)
