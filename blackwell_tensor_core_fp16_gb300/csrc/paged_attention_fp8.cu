@@ -26,6 +26,11 @@
 // element between 2^14 and 2^15: no bit is lost of elements above 2^-31 of the largest, and of smaller
 // ones less than 2^-38 of it.
 //
+// Measured: 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, 97 to 110 us by their lengths (5.3 TB/s,
+// floor 79); 200001 tokens, 16 heads over 2 of 256, 49 (floor 30); 37 windows of 1000 and 4 first tokens, 12
+// heads of 64, 17 to 19 (floor 7.4).  The issue slots are half busy, with conversions, products and the
+// softmax of twelve warps an SM, while the codes come.
+//
 // With a window the seen tokens are two ranges.  They are laid one after the other on one axis of rows,
 // the first tokens' range rounded up and the window's start down to 16, so that 16 rows lie in one
 // range, and the axis is cut into tiles as any other.
@@ -101,6 +106,10 @@ struct Fp8Cfg {
     template <typename T>
     static constexpr int kShift = 0;                          // (the sums carry no factor)
     static constexpr bool kRowPairs = true;
+    // An item's end takes about as long as a tile; counted as nothing, blocks with many ends are the last:
+    // 64 sequences of up to 2000 tokens, 32 heads over 8 of 128, 42.0 us and 35.7 so, of up to 8192 100.8 and 97.1.
+    // A block an item spares the join's launch: 56 sequences of 1000 tokens 29.3 us and 26.3 so, 220 of 500 with
+    // 2 heads of 256 31.8 and 26.3; where lengths differ it may lose, 37 of up to 1000 with 12 heads 21.2 and 22.9.
     static constexpr int kEndTiles = 1, kAloneTiles = 8;
     static constexpr int kResident = kTiles == 1 ? 3 : 2;   // blocks of an SM
     static constexpr int kSlice = kSubs * kSub;               // tokens of a warp's slice

@@ -516,9 +516,9 @@ int launch_attention(P p, int64_t most_tokens, int sms, cudaStream_t stream)
     // Few items of few tiles: a cluster an item, which joins its blocks' parts itself, as large as
     // the GPU holds for all items, up to three tiles a block (8 key heads: one sequence of 500
     // tokens 5.7 us, 8.1 with the second kernel; 16 of up to 250 tokens 7.2 and 8.6; one of 1500
-    // 7.5 and 8.8; with four tiles a block, one of 2000 took as long either way).  The lengths being on the device, the page table's width
-    // stands for the longest (with a window, the window): short sequences under a table made for
-    // long ones take the second kernel.
+    // 7.5 and 8.8; with four tiles a block, one of 2000 took as long either way).  The lengths being
+    // on the device, the page table's width stands for the longest (with a window, the window): short
+    // sequences under a table made for long ones take the second kernel.
     int ranks = 1;
     while (ranks < kClusterMost && ranks < per_item && items * ranks * 2 <= most) ranks *= 2;
     // A block an item, as a cluster of one, where the items just fill the GPU and none has many tiles.
