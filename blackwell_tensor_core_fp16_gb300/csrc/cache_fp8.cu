@@ -2,13 +2,13 @@
 // its reading back (C ABI and formulas in include/decode.h).
 //
 // Both move every element once, 3 bytes of it, and do a dozen operations on it: HBM bounds them.  32768 tokens
-// of 8 heads of 128 are written in 41 us (5.0 TB/s; floor 29.7), 200001 of 2 heads of 256 read back in 101
+// of 8 heads of 128 are written in 39 us (5.2 TB/s; floor 29.7), 200001 of 2 heads of 256 read back in 101
 // (6.1 TB/s, 90% of the copy rate; floor 90.6).
 //
 // Write.  A block's scale needs the largest of its new elements before the first code is known, and
 // its other codes may have to follow, so one warp takes a block, of one head of the keys or of the
 // values, as a whole: the block's first new token in the call (its leader, found from the slots
-// beside it) stands for it.  The rows wait in registers while the maximum is taken (16 or 32 tokens;
+// beside it) stands for it.  The rows wait in registers while the maximum is taken (8 or 16 tokens;
 // of larger blocks the rest is read again, from a cache), nothing else is shared between warps, and no
 // order of blocks matters.  A scale being a power of two, x * 2^(127 - e) is exact and only the
 // conversion rounds, and codes that follow keep their bits but for those that become subnormal.
@@ -80,16 +80,23 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
 }
 
 // (A warp that takes the keys' block and the values' has twice the rows on their way: 32768 tokens of 8
-// heads of 128 41 us, 46 with a warp for each.  At 256 there are no registers for both.)
+// heads of 128 40 us, 46 with a warp for each.  At 256 there are no registers for both.)
 template <int D>
 constexpr int kKinds = D == 256 ? 1 : 2;
+// Blocks of an SM, by the loads that wait in registers, of keys and values.
+template <int D, int kHold>
+constexpr int kResident = kHold * kKinds<D> > 8 ? 2 : 3;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) quantize_cache_kernel(const QuantizeParams p)
+// kHold: loads of a warp (512 bytes) that wait in registers.  Rows that do not fit are read again from a cache,
+// but with fewer of them in registers three blocks fit an SM instead of two.  us, blocks of 8, 16, 32 and 64
+// tokens: 65536 tokens of 8 heads of 64, with 16 rows in registers 57, 42, 41, 44, with 32 80, 57, 45, 47; 32768
+// of 128, with 8 rows 38.3, 38.6, 41.9, 53.8, with 16 49.6, 40.7, 41.7, 46.0; 16384 of 256, with 8 rows 44.5, 44.7, -,
+// 62.9, with 16 46.3, 37.4, -, 44.8.
+template <typename T, int D, int kHold>
+__global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_cache_kernel(const QuantizeParams p)
 {
     constexpr int kBoth = kKinds<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;     // a row's lanes; rows of one load
-    constexpr int kHold = D == 256 ? 16 : 8;               // loads that wait in registers
     constexpr uint32_t kAll = 0xffffffffu;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int combo = blockIdx.y * p.per + w % p.per, phase = w / p.per, phases = kWarps / p.per;
@@ -335,12 +342,12 @@ __global__ void __launch_bounds__(256) dequantize_cache_kernel(const DequantizeP
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int kHold>
 int quantize(const QuantizeParams& p, cudaStream_t stream)
 {
     const int64_t windows = (static_cast<int64_t>(p.tokens) + p.window - 1) / p.window;
     const int groups = (2 / kKinds<D> * p.heads + p.per - 1) / p.per;
-    const cudaError_t e = launch(quantize_cache_kernel<T, D>, dim3(static_cast<uint32_t>(windows), groups),
+    const cudaError_t e = launch(quantize_cache_kernel<T, D, kHold>, dim3(static_cast<uint32_t>(windows), groups),
                                  dim3(kWarps * 32), 0, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "quantize_cache_kernel: %s", cudaGetErrorString(e));
@@ -439,10 +446,14 @@ int decode_quantize_cache(const decode_quantize_cache_args* a, cudaStream_t stre
     while (p.window < kWindow && static_cast<int64_t>(p.tokens) * each > static_cast<int64_t>(sms) * 24 * p.window)
         p.window *= 2;
     const bool bf16 = a->dtype == DECODE_BF16;
-    if (d == 64) return bf16 ? quantize<__nv_bfloat16, 64>(p, stream) : quantize<__half, 64>(p, stream);
-    if (d == 128)
-        return bf16 ? quantize<__nv_bfloat16, 128>(p, stream) : quantize<__half, 128>(p, stream);
-    return bf16 ? quantize<__nv_bfloat16, 256>(p, stream) : quantize<__half, 256>(p, stream);
+    if (d == 64) return bf16 ? quantize<__nv_bfloat16, 64, 4>(p, stream) : quantize<__half, 64, 4>(p, stream);
+    // (8 rows do for blocks of 8.  16 are two rounds of reads: worth it where the GPU is filled several times,
+    // 20000 tokens of 8 heads 24.6 us for 25.7, not before, 4800 6.5 for 4.9, 400 4.9 for 4.6.)
+    if (d == 128 && (p.block <= 8 ||
+                     (p.block <= 16 && static_cast<int64_t>(p.tokens) * each >= static_cast<int64_t>(sms) * 1024)))
+        return bf16 ? quantize<__nv_bfloat16, 128, 4>(p, stream) : quantize<__half, 128, 4>(p, stream);
+    if (d == 128) return bf16 ? quantize<__nv_bfloat16, 128, 8>(p, stream) : quantize<__half, 128, 8>(p, stream);
+    return bf16 ? quantize<__nv_bfloat16, 256, 16>(p, stream) : quantize<__half, 256, 16>(p, stream);
 }
 
 int decode_dequantize_cache(const decode_dequantize_cache_args* a, cudaStream_t stream)
