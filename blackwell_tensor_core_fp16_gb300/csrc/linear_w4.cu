@@ -35,6 +35,7 @@ struct LinearParams {
     uint16_t* y;
     int64_t x_stride, code_stride, scale_stride, zero_stride, y_stride;
     int32_t m, n, k, group, group_shift, split, activation;
+    int32_t wide;                                // a chunk's scales, and its zero points, are one word
     uint32_t* status;
     int32_t items_each, items_more, pieces_each, pieces_more, stages, waiting;    // for few tokens
 };
@@ -97,6 +98,35 @@ struct Differences {
         }
     }
 };
+
+// kParts neighbouring scales or zero points, as one word.
+template <int kParts>
+__device__ __forceinline__ void load_together(const uint16_t* from, uint32_t (&to)[kParts])
+{
+    if constexpr (kParts == 4) {
+        const uint2 b = *reinterpret_cast<const uint2*>(from);
+        to[0] = b.x & 0xffffu, to[1] = b.x >> 16, to[2] = b.y & 0xffffu, to[3] = b.y >> 16;
+    } else if constexpr (kParts == 2) {
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(from);
+        to[0] = b & 0xffffu, to[1] = b >> 16;
+    } else {
+        to[0] = *from;
+    }
+}
+template <int kParts>
+__device__ __forceinline__ void load_together(const uint8_t* from, uint32_t (&to)[kParts])
+{
+    if constexpr (kParts == 4) {
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(from);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) to[x] = b >> 8 * x & 0xffu;
+    } else if constexpr (kParts == 2) {
+        const uint32_t b = *reinterpret_cast<const uint16_t*>(from);
+        to[0] = b & 0xffu, to[1] = b >> 8;
+    } else {
+        to[0] = *from;
+    }
+}
 
 __device__ __forceinline__ float activated(float y, int activation)
 {
@@ -250,14 +280,25 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
     auto load_scales = [&]() {
         const int piece = piece0 + scale_round * kPieces + w + kFewWarps * (lane >> 4);
         const uint32_t row = min(scale_item * kItem + (lane & 15), p.n - 1);
+        const uint16_t* const scales = p.scales + row * static_cast<uint32_t>(p.scale_stride);
+        const uint8_t* const zeros = p.zeros + row * static_cast<uint32_t>(p.zero_stride);
+        if (kParts > 1 && p.wide) {
 #pragma unroll
-        for (int x = 0; x < kParts; ++x) {
-            const int column = piece * 128 + x * (32 * kWords);
-            scale[x] = 0, zero[x] = 0;
-            if (scale_item < item1 && piece < piece1 && column < p.k) {
-                const uint32_t g = divide(column / 32, p.group, p.group_shift);
-                scale[x] = p.scales[row * static_cast<uint32_t>(p.scale_stride) + g];
-                zero[x] = p.zeros != nullptr ? p.zeros[row * static_cast<uint32_t>(p.zero_stride) + g] : 8u;
+            for (int x = 0; x < kParts; ++x) scale[x] = 0, zero[x] = p.zeros != nullptr ? 0u : 8u;
+            if (scale_item < item1 && piece < piece1) {
+                load_together(scales + piece * kParts, scale);
+                if (p.zeros != nullptr) load_together(zeros + piece * kParts, zero);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < kParts; ++x) {
+                const int column = piece * 128 + x * (32 * kWords);
+                scale[x] = 0, zero[x] = 0;
+                if (scale_item < item1 && piece < piece1 && column < p.k) {
+                    const uint32_t g = divide(column / 32, p.group, p.group_shift);
+                    scale[x] = scales[g];
+                    zero[x] = p.zeros != nullptr ? zeros[g] : 8u;
+                }
             }
         }
         if (++scale_round == rounds) {
@@ -576,28 +617,35 @@ linear_w4_tile_kernel(const LinearParams p)
     float* const sums = reinterpret_cast<float*>(smem);
     if (w < C::kReaders) {
         // ---- the sums: a thread has an output and up to 32 tokens
-        constexpr int kMine = kTokens < 32 ? kTokens : 32, kAtOnce = kParts == 4 && kTokens < 64 ? 16 : 8;
+        constexpr int kMine = kTokens < 32 ? kTokens : 32, kAtOnce = kParts == 4 ? 16 : 8;
         const int t0 = w / 4 * 32;
         float sum[kMine] = {};
         const uint32_t row = min(j0 + tid % kRows, p.n - 1);
         const uint16_t* const scales = p.scales + row * static_cast<uint32_t>(p.scale_stride);
+        // (with four scales and 64 tokens there are no registers for scales ahead)
+        constexpr bool kPrefetch = kSums == 2;
         uint32_t next[kParts];                   // a chunk ahead
         auto load_scales = [&](int c) {
             const int begin = column_of(c);
+            if (kParts > 1 && p.wide) {
+                if (c < chunks) load_together(scales + begin / (128 / kParts), next);
+                return;
+            }
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
                 const int column = begin + x * (128 / kParts);
                 next[x] = c < chunks && column < p.k ? scales[divide(column / 32, p.group, p.group_shift)] : 0;
             }
         };
-        load_scales(0);
+        if constexpr (kPrefetch) load_scales(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             uint32_t scale[kParts];
             const int begin = column_of(c), at = c % kSums;
+            if constexpr (!kPrefetch) load_scales(c);
 #pragma unroll
             for (int x = 0; x < kParts; ++x) scale[x] = next[x];
-            load_scales(c + 1);
+            if constexpr (kPrefetch) load_scales(c + 1);
             wait(made + at * 8, c / kSums & 1);
             gf16::tcgen05_fence_after();
 #pragma unroll
@@ -676,6 +724,10 @@ linear_w4_tile_kernel(const LinearParams p)
         uint32_t zero[kParts];
         auto load_zeros = [&](int c) {
             const int begin = column_of(c);
+            if (kParts > 1 && p.wide && p.zeros != nullptr) {
+                if (c < chunks) load_together(zeros + begin / (128 / kParts), zero);
+                return;
+            }
 #pragma unroll
             for (int x = 0; x < kParts; ++x) {
                 const int column = begin + x * (128 / kParts);
@@ -885,6 +937,13 @@ int decode_linear_w4(const decode_linear_w4_args* a, cudaStream_t stream)
     p.group = static_cast<int32_t>((a->group < a->k ? a->group : a->k > 0 ? a->k : 32) / 32);
     p.group_shift = shift_of(p.group);
     p.activation = a->activation;
+    // Groups of 32 and 64: a lane's scales of 128 columns by one load, if a row's are aligned so.  Each lane has a
+    // row, so a load costs as many cycles as it touches lines: 64 tokens, 14336 x 4096, groups of 32 42.0 us with
+    // one for each, 16 tokens 27.9.
+    const int parts = p.group <= 2 ? 4 / p.group : 1;
+    p.wide = parts > 1 && a->k % 128 == 0 && scale_stride[0] % parts == 0 &&
+             reinterpret_cast<uintptr_t>(a->scales) % (2 * parts) == 0 &&
+             (!a->zeros || (zero_stride[0] % parts == 0 && reinterpret_cast<uintptr_t>(a->zeros) % parts == 0));
     return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, stream)
                                    : dispatch<__half>(p, stream);
 }
