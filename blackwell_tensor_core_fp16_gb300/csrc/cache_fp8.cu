@@ -71,6 +71,13 @@ __device__ __forceinline__ uint32_t largest(uint32_t top)
 {
     return __reduce_max_sync(0xffffffffu, max(top & 0x7fffu, top >> 16 & 0x7fffu));
 }
+// The least scale for a largest magnitude: 448 = 1.75 * 2^8.
+template <typename T>
+__device__ __forceinline__ int needed(uint32_t top)
+{
+    const uint32_t bits = __float_as_uint(from_bits<T>(top));
+    return max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u));
+}
 // x with zeros for infinities and NaN.
 template <typename T>
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
@@ -83,17 +90,19 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t x)
 // heads of 128 40 us, 46 with a warp for each.  At 256 there are no registers for both.)
 template <int D>
 constexpr int kKinds = D == 256 ? 1 : 2;
-// Blocks of an SM, by the loads that wait in registers, of keys and values.
-template <int D, int kHold>
-constexpr int kResident = kHold * kKinds<D> > 8 ? 2 : 3;
+// Blocks of an SM, by the loads that wait in registers, of keys and values.  (Calls of few tokens do not fill
+// three.)
+template <int D, int kHold, bool kSeveral>
+constexpr int kResident = kHold * kKinds<D> > 8 || !kSeveral ? 2 : 3;
 
 // kHold: loads of a warp (512 bytes) that wait in registers.  Rows that do not fit are read again from a cache,
 // but with fewer of them in registers three blocks fit an SM instead of two.  us, blocks of 8, 16, 32 and 64
 // tokens: 65536 tokens of 8 heads of 64, with 16 rows in registers 57, 42, 41, 44, with 32 80, 57, 45, 47; 32768
 // of 128, with 8 rows 38.3, 38.6, 41.9, 53.8, with 16 49.6, 40.7, 41.7, 46.0; 16384 of 256, with 8 rows 44.5, 44.7, -,
 // 62.9, with 16 46.3, 37.4, -, 44.8.
-template <typename T, int D, int kHold>
-__global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_cache_kernel(const QuantizeParams p)
+// kSeveral: windows of more than one token.
+template <typename T, int D, int kHold, bool kSeveral>
+__global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold, kSeveral>)) quantize_cache_kernel(const QuantizeParams p)
 {
     constexpr int kBoth = kKinds<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;     // a row's lanes; rows of one load
@@ -126,19 +135,138 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_c
     if (combo == 0 && phase == 0 && mine && (disordered || (!valid && slot != -1)))
         atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
     uint32_t leaders = __ballot_sync(kAll, mine && valid && !goes_on && !disordered);
+    // (one that begins another run of a block, a little behind the first, is refused)
+    for (uint32_t left = leaders; left != 0; left &= left - 1) {
+        const int lead = __ffs(left) - 1, begin = __shfl_sync(kAll, slot - in_block, lead);
+        bool again = lane < lead && within(slot, begin);
+#pragma unroll
+        for (int y = 0; y < kBack; ++y) again = again || within(earlier[y], begin);
+        if (!__any_sync(kAll, again)) continue;
+        if (combo == 0 && phase == 0 && lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
+        leaders &= ~(1u << lead);
+    }
+
+    const int ch = lane % kLanes, sub = lane / kLanes;
+    // a place, its scale and its codes (the lane's 8 of them)
+    struct Place {
+        int page, offset, block;
+    };
+    auto find = [&](int place) {
+        const int page = divide(place, p.page_size, p.page_shift), offset = place - page * p.page_size;
+        return Place{page, offset, divide(offset, p.block, p.block_shift)};
+    };
+    auto scale_at = [&](int kv, const Place& at) {
+        return p.scales[kv] + at.page * p.scale_stride[kv][0] + at.block * p.scale_stride[kv][1] +
+               head * p.scale_stride[kv][2];
+    };
+    auto codes_at = [&](int kv, const Place& at) {
+        return p.codes[kv] + at.page * p.code_stride[kv][0] + at.offset * p.code_stride[kv][1] +
+               head * p.code_stride[kv][2] + ch * 8;
+    };
+    // 8 elements' codes, and a block's other codes after its scale grew (from places `begin` on, all but the new
+    // tokens; a factor below 2^-126 takes any to 0, as 0 does)
+    auto convert = [&](const uint4& row, float by, bool odd) {
+        uint32_t out[2];
+        const uint32_t in[4] = {row.x, row.y, row.z, row.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float2 a = Half2<T>::unpack(in[2 * h]), b = Half2<T>::unpack(in[2 * h + 1]);
+            if (odd) {                             // x * 0: NaN for an infinity
+                a.x = fmaf(a.x, by, a.x * 0.f), a.y = fmaf(a.y, by, a.y * 0.f);
+                b.x = fmaf(b.x, by, b.x * 0.f), b.y = fmaf(b.y, by, b.y * 0.f);
+            } else {
+                a = halves(mul2(pair(a.x, a.y), pair(by, by)));
+                b = halves(mul2(pair(b.x, b.y), pair(by, by)));
+            }
+            out[h] = codes_of(a.x, a.y) | codes_of(b.x, b.y) << 16;
+        }
+        return make_uint2(out[0], out[1]);
+    };
+    auto follow = [&](int kv, uint8_t* codes, int from, int to, int run, int older, int e) {
+        const float down = e - older < 127 ? power_of(127 + older - e) : 0.f;
+        for (int r = from + sub; r < to; r += kRows) {
+            if (r >= 0 && r < run) continue;
+            uint2* const at = reinterpret_cast<uint2*>(codes + r * p.code_stride[kv][1]);
+            const uint2 old = *at;
+            uint32_t in[2] = {old.x, old.y};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
+                const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
+                in[h] = codes_of(a.x * down, a.y * down) | codes_of(b.x * down, b.y * down) << 16;
+            }
+            *at = make_uint2(in[0], in[1]);
+        }
+    };
+
+    // ---- blocks of which the call has one token, as a decode step's: where a window has several, as many at a
+    // time as there are rows in registers, a row's lanes finding its maximum between them (one after the other
+    // they take 1.3 us each: 8192 sequences' tokens 60 us, 26 so)
+    const uint32_t single = kSeveral ? leaders & ~(__ballot_sync(kAll, goes_on) >> 1) : 0;
+    if (kSeveral && (single & (single - 1)) != 0) {
+        leaders &= ~single;
+        for (int l0 = 1; l0 <= p.window; l0 += kHold * kRows) {
+            uint4 row[kBoth][kHold];
+            int e[kBoth][kHold];
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int l = l0 + i * kRows + sub;
+                const int place = __shfl_sync(kAll, slot, l & 31), first = __shfl_sync(kAll, in_block, l & 31);
+                const bool here = l < 32 && (single >> l & 1) != 0 && l % phases == phase;
+                const Place at = find(place);
+#pragma unroll
+                for (int y = 0; y < kBoth; ++y) {
+                    row[y][i] = make_uint4(0u, 0u, 0u, 0u);
+                    e[y][i] = 0;
+                    if (!here) continue;
+                    row[y][i] = *reinterpret_cast<const uint4*>(p.x[kv0 + y] + (t0 + l) * p.x_stride[kv0 + y][0] +
+                                                                head * p.x_stride[kv0 + y][1] + ch * 8);
+                    if (first > 0) e[y][i] = *scale_at(kv0 + y, at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                const int l = l0 + i * kRows + sub;
+                const int place = __shfl_sync(kAll, slot, l & 31), first = __shfl_sync(kAll, in_block, l & 31);
+                const bool here = l < 32 && (single >> l & 1) != 0 && l % phases == phase;
+                if (!__any_sync(kAll, here)) continue;
+                const Place at = find(place);
+#pragma unroll
+                for (int y = 0; y < kBoth; ++y) {
+                    const uint4& b = row[y][i];
+                    auto top_of = [&](uint32_t x, uint32_t u, uint32_t v, uint32_t z) {
+                        uint32_t top = larger<T>(larger<T>(x, u), larger<T>(v, z));
+                        top = max(top & 0x7fffu, top >> 16 & 0x7fffu);
+#pragma unroll
+                        for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(kAll, top, d));
+                        return top;
+                    };
+                    uint32_t top = top_of(b.x, b.y, b.z, b.w);
+                    const bool odd = __any_sync(kAll, top >= kInfinity<T>);
+                    if (odd)
+                        top = top_of(finite_or_zero<T>(b.x), finite_or_zero<T>(b.y), finite_or_zero<T>(b.z),
+                                     finite_or_zero<T>(b.w));
+                    const int older = e[y][i], now = max(needed<T>(top), older);
+                    if (here) {
+                        *reinterpret_cast<uint2*>(codes_at(kv0 + y, at)) = convert(b, power_of(254 - now), odd);
+                        if (ch == 0) *scale_at(kv0 + y, at) = static_cast<uint8_t>(now);
+                    }
+                    // (all of the warp for each row whose scale grew)
+                    for (uint32_t grown = __ballot_sync(kAll, here && first > 0 && now > older && ch == 0); grown != 0;
+                         grown &= grown - 1) {
+                        const int of = __ffs(grown) - 1, its = __shfl_sync(kAll, first, of);
+                        follow(kv0 + y, codes_at(kv0 + y, find(__shfl_sync(kAll, place, of))), -its, p.block - its, 1,
+                               __shfl_sync(kAll, older, of), __shfl_sync(kAll, now, of));
+                    }
+                }
+            }
+        }
+    }
 
     for (int nth = 0; leaders != 0; ++nth, leaders &= leaders - 1) {
         if (nth % phases != phase) continue;
         const int lead = __ffs(leaders) - 1;
         const int place = __shfl_sync(kAll, slot, lead), first = __shfl_sync(kAll, in_block, lead);
-        // (another run of the same block, a little before: this one is refused)
-        bool again = lane < lead && within(slot, place - first);
-#pragma unroll
-        for (int y = 0; y < kBack; ++y) again = again || within(earlier[y], place - first);
-        if (__any_sync(kAll, again)) {
-            if (combo == 0 && lane == 0) atomicOr(p.status, DECODE_BAD_CACHE_SLOT);
-            continue;
-        }
         const int most = p.block - first;
         const int64_t token = t0 + lead;
         // the run: how many tokens of the block follow
@@ -152,9 +280,7 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_c
             run += apart != 0 ? __ffs(apart) - 1 : 32;
         }
 
-        const int page = divide(place, p.page_size, p.page_shift), offset = place - page * p.page_size;
-        const int block = divide(offset, p.block, p.block_shift);
-        const int ch = lane % kLanes, sub = lane / kLanes;
+        const Place at = find(place);
         uint8_t* scale[kBoth];
         const uint16_t* x[kBoth];
         uint8_t* codes[kBoth];
@@ -162,12 +288,10 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_c
 #pragma unroll
         for (int y = 0; y < kBoth; ++y) {
             const int kv = kv0 + y;
-            scale[y] = p.scales[kv] + page * p.scale_stride[kv][0] + block * p.scale_stride[kv][1] +
-                       head * p.scale_stride[kv][2];
+            scale[y] = scale_at(kv, at);
             older[y] = first > 0 ? *scale[y] : 0;
             x[y] = p.x[kv] + token * p.x_stride[kv][0] + head * p.x_stride[kv][1] + ch * 8;
-            codes[y] = p.codes[kv] + page * p.code_stride[kv][0] + offset * p.code_stride[kv][1] +
-                       head * p.code_stride[kv][2] + ch * 8;
+            codes[y] = codes_at(kv, at);
         }
         uint4 row[kBoth][kHold];
         auto load = [&](int from) {
@@ -220,11 +344,7 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_c
         int e[kBoth];
 #pragma unroll
         for (int y = 0; y < kBoth; ++y) {
-            // 448 = 1.75 * 2^8
-            const uint32_t bits = __float_as_uint(from_bits<T>(top[y]));
-            const int need =
-                max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u));
-            e[y] = max(need, older[y]);
+            e[y] = max(needed<T>(top[y]), older[y]);
             if (lane == 0) *scale[y] = static_cast<uint8_t>(e[y]);
         }
         for (int from = last; from >= 0; from -= kChunk) {
@@ -236,45 +356,16 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold>)) quantize_c
                 for (int i = 0; i < kHold; ++i) {
                     if (from + i * kRows >= run) break;    // (for all lanes)
                     const int r = from + i * kRows + sub;
-                    uint32_t out[2];
-                    const uint32_t in[4] = {row[y][i].x, row[y][i].y, row[y][i].z, row[y][i].w};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float2 a = Half2<T>::unpack(in[2 * h]), b = Half2<T>::unpack(in[2 * h + 1]);
-                        if (odd) {                         // x * 0: NaN for an infinity
-                            a.x = fmaf(a.x, by, a.x * 0.f), a.y = fmaf(a.y, by, a.y * 0.f);
-                            b.x = fmaf(b.x, by, b.x * 0.f), b.y = fmaf(b.y, by, b.y * 0.f);
-                        } else {
-                            a = halves(mul2(pair(a.x, a.y), pair(by, by)));
-                            b = halves(mul2(pair(b.x, b.y), pair(by, by)));
-                        }
-                        out[h] = codes_of(a.x, a.y) | codes_of(b.x, b.y) << 16;
-                    }
                     if (r < run)
                         *reinterpret_cast<uint2*>(codes[y] + r * p.code_stride[kv0 + y][1]) =
-                            make_uint2(out[0], out[1]);
+                            convert(row[y][i], by, odd);
                 }
             }
         }
-        // the block's other codes follow a scale that grew (a factor below 2^-126 takes any to 0, as 0 does)
+        // the block's other codes follow a scale that grew
 #pragma unroll
-        for (int y = 0; y < kBoth; ++y) {
-            if (e[y] <= older[y] || first == 0) continue;
-            const float down = e[y] - older[y] < 127 ? power_of(127 + older[y] - e[y]) : 0.f;
-            for (int r = sub - first; r < most; r += kRows) {
-                if (r >= 0 && r < run) continue;
-                uint2* const at = reinterpret_cast<uint2*>(codes[y] + r * p.code_stride[kv0 + y][1]);
-                const uint2 old = *at;
-                uint32_t in[2] = {old.x, old.y};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float2 a = Half2<__half>::unpack(codes_to_half2(in[h]));
-                    const float2 b = Half2<__half>::unpack(codes_to_half2(in[h] >> 16));
-                    in[h] = codes_of(a.x * down, a.y * down) | codes_of(b.x * down, b.y * down) << 16;
-                }
-                *at = make_uint2(in[0], in[1]);
-            }
-        }
+        for (int y = 0; y < kBoth; ++y)
+            if (e[y] > older[y] && first > 0) follow(kv0 + y, codes[y], -first, most, run, older[y], e[y]);
     }
 }
 
@@ -347,8 +438,9 @@ int quantize(const QuantizeParams& p, cudaStream_t stream)
 {
     const int64_t windows = (static_cast<int64_t>(p.tokens) + p.window - 1) / p.window;
     const int groups = (2 / kKinds<D> * p.heads + p.per - 1) / p.per;
-    const cudaError_t e = launch(quantize_cache_kernel<T, D, kHold>, dim3(static_cast<uint32_t>(windows), groups),
-                                 dim3(kWarps * 32), 0, stream, p);
+    const cudaError_t e = launch(p.window > 1 ? quantize_cache_kernel<T, D, kHold, true>
+                                              : quantize_cache_kernel<T, D, kHold, false>,
+                                 dim3(static_cast<uint32_t>(windows), groups), dim3(kWarps * 32), 0, stream, p);
     if (e != cudaSuccess)
         return fail(DECODE_ERR_CUDA, "quantize_cache_kernel: %s", cudaGetErrorString(e));
     return DECODE_OK;
@@ -437,11 +529,11 @@ int decode_quantize_cache(const decode_quantize_cache_args* a, cudaStream_t stre
     p.x[1] = static_cast<const uint16_t*>(a->v);
     const int each = d == 256 ? 2 * p.heads : p.heads;      // warps' work of a token
     p.per = each < kWarps ? each : kWarps;
-    // A warp takes the blocks that begin in its window of tokens one after the other, 1.3 us each: of few
-    // tokens, each of which may be a block's only one, a window holds one; of more as many as leave the GPU 12
-    // to 24 warps an SM, for windows in which no block begins cost a warp all the same.  8 heads of 128, tokens
-    // of one sequence / of as many sequences, us with windows of 1, of 4, of 16: 200 4.0 / 3.1, 3.8 / 6.6,
-    // 3.7 / 22.6; 1200 6.7 / 10.7, 4.5 / 8.8, 3.9 / 23.8; 4800 16.8 / 38.7, 8.8 / 32.4, 4.9 / 31.5.
+    // A warp takes the blocks that begin in its window of tokens: of few tokens, each of which may be a block's
+    // only one, a window holds one; of more as many as leave the GPU 12 to 24 warps an SM, for windows in which
+    // no block begins cost a warp all the same.  8 heads of 128, tokens of one sequence / of as many sequences, us:
+    // 400 with windows of 1, 2, 4 4.8 / 4.8, 4.4 / 4.8, 4.2 / 6.0; 1200 of 4, 8 4.7 / 6.3, 4.6 / 8.4; 2400 of
+    // 8, 16 4.8 / 8.7, 4.9 / 13.1.
     p.window = 1;
     while (p.window < kWindow && static_cast<int64_t>(p.tokens) * each > static_cast<int64_t>(sms) * 24 * p.window)
         p.window *= 2;

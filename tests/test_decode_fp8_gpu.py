@@ -93,6 +93,46 @@ def test_write_many_tokens():
     check_cache(c, before, x, slots, "many")
 
 
+@pytest.mark.parametrize("tokens,h,page,block,d,dtype", [
+    (700, 8, 16, 16, 128, torch.bfloat16), (1900, 8, 8, 8, 128, torch.float16), (4000, 8, 16, 16, 128, torch.bfloat16),
+    (2600, 12, 6, 3, 64, torch.float16), (1900, 8, 4, 1, 256, torch.bfloat16), (15500, 2, 16, 16, 64, torch.bfloat16),
+    (31000, 1, 8, 4, 128, torch.float16), (8000, 2, 32, 16, 256, torch.float16)])
+def test_write_of_many_sequences_tokens(tokens, h, page, block, d, dtype):
+    """A token each of many sequences, at any place of its block, between some longer runs, inactive and
+    refused tokens; scales that grow and that do not, infinities and NaN."""
+    gen = generator(tokens + d + block)
+    per = page // block
+    where = torch.randperm(tokens + 64, generator=gen)[:tokens]          # blocks
+    slots = where * block + torch.randint(0, block, (tokens,), generator=gen)
+    slots[torch.rand(tokens, generator=gen) < 0.1] = -1
+    slots[::97] = -1                              # (so that the next one, of the same block, begins a run)
+    if block > 1:
+        for at in range(1, tokens - 1, 97):       # runs of two
+            slots[at] = where[at] * block
+            slots[at + 1] = where[at] * block + 1
+    wrong = torch.zeros(tokens, dtype=torch.bool)
+    again = torch.arange(50, tokens, 331)         # the place of a token a little before
+    for at in again.tolist():
+        if slots[at - 20] >= 0 and slots[at] >= 0 and (at - 20) % 97 > 2 and at % 97 > 2:
+            slots[at] = slots[at - 20]
+            wrong[at] = True
+    slots = slots.to(torch.int32)
+    pages = -(-(tokens + 64) // per)
+    c = caches(gen, pages, page, block, h, d)
+    before = {a: b.clone() for a, b in c.items()}
+    x = {kind: (normal(gen, tokens, h, d) * torch.exp2(4 * normal(gen, tokens, 1, 1))).to(dtype) for kind in "kv"}
+    x["k"][5::41, 0, 3] = math.inf
+    x["v"][7::53, -1, :] = math.nan
+    x["v"][9::59] = 0
+    x = {kind: y.cuda() for kind, y in x.items()}
+    write(c, x, slots.cuda())
+    kept = ((slots >= 0) & ~wrong).nonzero().flatten()
+    check_cache(c, before, {kind: y[kept.cuda()] for kind, y in x.items()}, slots[kept], "tokens")
+    if wrong.any():
+        with pytest.raises(g.GemmError, match="cache slot"):
+            g.check_decode_status()
+
+
 def test_write_token_by_token():
     """A block filled one token a call, each larger than the last: every growth of the scale."""
     gen = generator(4)
