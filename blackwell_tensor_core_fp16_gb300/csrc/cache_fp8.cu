@@ -98,11 +98,12 @@ constexpr int kResident = kHold * kKinds<D> > 8 || !kSeveral ? 2 : 3;
 // kHold: loads of a warp (512 bytes) that wait in registers.  Rows that do not fit are read again from a cache,
 // but with fewer of them in registers three blocks fit an SM instead of two.  us, blocks of 8, 16, 32 and 64
 // tokens: 65536 tokens of 8 heads of 64, with 16 rows in registers 57, 42, 41, 44, with 32 80, 57, 45, 47; 32768
-// of 128, with 8 rows 38.3, 38.6, 41.9, 53.8, with 16 49.6, 40.7, 41.7, 46.0; 16384 of 256, with 8 rows 44.5, 44.7, -,
-// 62.9, with 16 46.3, 37.4, -, 44.8.
+// of 128, with 8 rows 38.3, 38.6, 41.9, 53.8, with 16 49.6, 40.7, 41.7, 46.0; 16384 of 256, blocks of 8, 16 and 64,
+// with 8 rows 44.5, 44.7, 62.9, with 16 46.3, 37.4, 44.8.
 // kSeveral: windows of more than one token.
 template <typename T, int D, int kHold, bool kSeveral>
-__global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold, kSeveral>)) quantize_cache_kernel(const QuantizeParams p)
+__global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold, kSeveral>))
+quantize_cache_kernel(const QuantizeParams p)
 {
     constexpr int kBoth = kKinds<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;     // a row's lanes; rows of one load
@@ -252,8 +253,8 @@ __global__ void __launch_bounds__(kWarps * 32, (kResident<D, kHold, kSeveral>)) 
                         if (ch == 0) *scale_at(kv0 + y, at) = static_cast<uint8_t>(now);
                     }
                     // (all of the warp for each row whose scale grew)
-                    for (uint32_t grown = __ballot_sync(kAll, here && first > 0 && now > older && ch == 0); grown != 0;
-                         grown &= grown - 1) {
+                    uint32_t grown = __ballot_sync(kAll, here && first > 0 && now > older && ch == 0);
+                    for (; grown != 0; grown &= grown - 1) {
                         const int of = __ffs(grown) - 1, its = __shfl_sync(kAll, first, of);
                         follow(kv0 + y, codes_at(kv0 + y, find(__shfl_sync(kAll, place, of))), -its, p.block - its, 1,
                                __shfl_sync(kAll, older, of), __shfl_sync(kAll, now, of));
