@@ -257,21 +257,25 @@ def quantize_weight_w4(W, group: int = 128, zeros: bool = True):
     """The operands of ``linear_w4`` nearest to W [N, K] float16 or bfloat16, K even, each group of
     ``group`` neighbouring columns of a row (the last may be shorter) on its own: (codes, scales,
     zeros).  With ``zeros`` a group's range, stretched to hold 0, is dealt to the codes 0 .. 15;
-    without, its largest magnitude to 7 either side of 8, and None takes the zeros' place."""
+    without, its largest magnitude to 7 either side of 8, and None takes the zeros' place.  W is finite."""
     if W.dim() != 2 or W.dtype not in (torch.float16, torch.bfloat16) or W.shape[1] % 2 or group < 1:
         raise ValueError("W must be a float16 or bfloat16 matrix with an even number of columns")
     n, k = W.shape
     groups = -(-k // group)
     w = torch.nn.functional.pad(W.float(), (0, groups * group - k)).view(n, groups, group)
+    # (in 64 bits: a range of bfloat16 may pass fp32's)
     if zeros:
-        low, high = w.amin(-1).clamp(max=0), w.amax(-1).clamp(min=0)
-        scale = ((high - low) / 15).to(W.dtype)
-        by = scale.float().clamp(min=torch.finfo(W.dtype).tiny)
-        zero = torch.round(-low / by).clamp(0, 15)
+        low, high = w.amin(-1).clamp(max=0).double(), w.amax(-1).clamp(min=0).double()
+        scale = (high - low) / 15
     else:
-        scale = (w.abs().amax(-1) / 7).to(W.dtype)
-        by = scale.float().clamp(min=torch.finfo(W.dtype).tiny)
-        zero = torch.full_like(by, 8)
+        scale = w.abs().amax(-1).double() / 7
+    # a scale that is a subnormal number is rounded up: down, it could leave the largest weights out of the
+    # codes' reach by half of theirs
+    info = torch.finfo(W.dtype)
+    least = info.tiny * info.eps
+    scale = torch.where(scale < info.tiny, torch.ceil(scale / least) * least, scale).to(W.dtype)
+    by = torch.where(scale > 0, scale.float(), 1.0)
+    zero = torch.round(-low / by).clamp(0, 15).float() if zeros else torch.full_like(by, 8)
     code = torch.round(w / by[..., None] + zero[..., None]).clamp(0, 15).to(torch.uint8)
     code = code.view(n, groups * group)[:, :k]
     return (code[:, 0::2] | code[:, 1::2] << 4).contiguous(), scale, \

@@ -186,3 +186,29 @@ def test_weights_that_are_refused():
     for W in (torch.zeros(3, 5).half(), torch.zeros(4, 4), torch.zeros(4).half()):
         with pytest.raises(ValueError, match="matrix"):
             g.quantize_weight_w4(W)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("zeros", [True, False])
+def test_nearest_weights_at_the_ends_of_the_range(zeros, dtype):
+    """The bound of test_nearest_weights where a scale is a subnormal number, which is rounded up, so that
+    no code is cut off for it, and where a group's range passes fp32's: a code's step is the scale that
+    comes back, whatever its size."""
+    gen = torch.Generator().manual_seed(int(zeros))
+    sizes = (1e-4, 1e-5, 1e-6, 1e-7) if dtype == torch.float16 else (1e-37, 1e-38, 1e-39, 1e-40)
+    normal = torch.randn(len(sizes) + 2, 256, generator=gen, dtype=torch.float64)
+    W = (normal * torch.tensor(sizes + (0.0, 0.0), dtype=torch.float64)[:, None]).to(dtype)
+    W[-2] = torch.finfo(dtype).max * torch.sign(normal[-2])                # one after the other, either sign
+    W[-1, 3] = W[-1, 200] = torch.finfo(dtype).tiny * torch.finfo(dtype).eps      # the least number alone
+    codes, scales, z = g.quantize_weight_w4(W, 128, zeros)
+    assert bool(scales.isfinite().all()) and bool((scales > 0).all())
+    back, _ = ref.linear_w4(torch.eye(256, dtype=torch.float64), codes, scales, 128, z)
+    step = scales.double().repeat_interleave(128, 1)
+    err = (back.T - W.double()).abs()
+    half = 0.5 + (0.5 if zeros else 0.0) + 15 * ref.U[dtype]
+    assert bool((err <= half * step).all())
+    # no scale is larger than its group asks for by more than its own rounding
+    top = W.double().view(len(W), 2, 128)
+    need = (top.amax(-1).clamp(min=0) - top.amin(-1).clamp(max=0)) / 15 if zeros else top.abs().amax(-1) / 7
+    least = torch.finfo(dtype).tiny * torch.finfo(dtype).eps
+    assert bool((scales.double() <= need * (1 + ref.U[dtype]) + least).all())
