@@ -261,6 +261,7 @@ def quantize_weight_w4(W, group: int = 128, zeros: bool = True):
     if W.dim() != 2 or W.dtype not in (torch.float16, torch.bfloat16) or W.shape[1] % 2 or group < 1:
         raise ValueError("W must be a float16 or bfloat16 matrix with an even number of columns")
     n, k = W.shape
+    group = min(group, max(k, 1))
     groups = -(-k // group)
     w = torch.nn.functional.pad(W.float(), (0, groups * group - k)).view(n, groups, group)
     # (in 64 bits: a range of bfloat16 may pass fp32's)

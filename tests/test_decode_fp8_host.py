@@ -212,3 +212,11 @@ def test_nearest_weights_at_the_ends_of_the_range(zeros, dtype):
     need = (top.amax(-1).clamp(min=0) - top.amin(-1).clamp(max=0)) / 15 if zeros else top.abs().amax(-1) / 7
     least = torch.finfo(dtype).tiny * torch.finfo(dtype).eps
     assert bool((scales.double() <= need * (1 + ref.U[dtype]) + least).all())
+
+
+def test_weights_of_a_group_wider_than_the_matrix():
+    """A group may be wider than K, as in linear_w4, by any amount."""
+    W = torch.randn(3, 64, generator=torch.Generator().manual_seed(1)).half()
+    for zeros in (True, False):
+        for one, other in zip(g.quantize_weight_w4(W, 1 << 50, zeros), g.quantize_weight_w4(W, 64, zeros)):
+            assert (one is None and other is None) or torch.equal(one, other)
