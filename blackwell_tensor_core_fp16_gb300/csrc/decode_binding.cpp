@@ -473,6 +473,7 @@ struct Cache {
             refuse("the caches must be [pages, page_size, heads, d], the scales [pages, blocks, heads]");
         pages = kc.size(0), page_size = kc.size(1);
         const int64_t blocks = ks.size(1);
+        if (page_size < 1) refuse("pages must hold a token at least");
         if (blocks < 1 || page_size % blocks != 0 || page_size / blocks > INT32_MAX)
             refuse(std::to_string(blocks) + " scales do not share pages of " + std::to_string(page_size) +
                    " tokens out");

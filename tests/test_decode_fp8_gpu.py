@@ -812,3 +812,17 @@ def test_quantised_weights_through_the_layer(dtype):
     for zeros in (True, False):
         codes, scales, z = g.quantize_weight_w4(W, 64, zeros)
         check_linear(x, dict(codes=codes, scales=scales, zeros=z, group=64), f"zeros {zeros}")
+
+
+def test_pages_without_tokens_are_refused():
+    """(their blocks of no token divide by 0)"""
+    x = torch.zeros(2, 1, 64, dtype=torch.float16, device="cuda")
+    codes = torch.zeros(3, 0, 1, 64, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(3, 1, 1, dtype=torch.uint8, device="cuda")
+    at = torch.zeros(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="hold a token"):
+        g.quantize_cache(x, x, codes, codes, scale, scale, at)
+    with pytest.raises(ValueError, match="hold a token"):
+        g.dequantize_cache(codes, codes, scale, scale, at)
+    with pytest.raises(ValueError, match="hold a token"):
+        g.paged_attention_fp8(x, codes, codes, scale, scale, at[:, None], at)
