@@ -17,24 +17,28 @@
 //
 // Scales are read for each token of a slice (a byte each of keys and values) with its rows and wait
 // beside its stage, so blocks may have any size.  A key's scale multiplies its scores.  A
-// value's goes into its weight: times 2^15 over the slice's largest scale, by which the slice's sums
-// are multiplied when they are added to the running ones, so a weight fits float16 whatever the scales.
-// It is carried as two float16 pieces, 22 bits, which leave out less than 2^-22 of it or 2^-40 of the
-// slice's largest.
+// value's goes into its weight: times 2^15 over the slice's largest scale, so that a weight fits float16
+// whatever the scales.  Weights are taken against the slice's own largest score, and where its scales are
+// further apart than 2^8, against its largest product of weight and scale; what that leaves out multiplies the
+// slice's sums when they are added to the running ones.  So the two float16 pieces of a weight leave out less
+// than 2^-22 of it, or 2^-32 of the slice's largest product of weight and scale, however large the scale of a
+// token that has no weight and however small all of a slice's weights.  (Against the running maximum and the
+// largest scale alone, as they were, tokens whose scale is below 2^-40 of their slice's largest were lost.)
 //
 // bfloat16 queries become float16 too, each head's divided by a power of two that brings its largest
 // element between 2^14 and 2^15: no bit is lost of elements above 2^-31 of the largest, and of smaller
 // ones less than 2^-38 of it.
 //
-// Measured: 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, 97 to 110 us by their lengths (5.3 TB/s,
-// floor 79); 200001 tokens, 16 heads over 2 of 256, 49 (floor 30); 37 windows of 1000 and 4 first tokens, 12
-// heads of 64, 17 to 19 (floor 7.4).  The issue slots are half busy, with conversions, products and the
+// Measured: 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, 91 to 97 us by their lengths (5.7 TB/s,
+// floor 79); 200001 tokens, 16 heads over 2 of 256, 47 (floor 30); 37 windows of 1000 and 4 first tokens, 12
+// heads of 64, 19 (floor 7.4).  The issue slots are half busy, with conversions, products and the
 // softmax of twelve warps an SM, while the codes come.
 //
 // With a window the seen tokens are two ranges.  They are laid one after the other on one axis of rows,
 // the first tokens' range rounded up and the window's start down to 16, so that 16 rows lie in one
 // range, and the axis is cut into tiles as any other.
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -45,6 +49,10 @@ namespace {
 using namespace decode;
 
 constexpr int kMostResident = 3;     // of Fp8Cfg::kResident
+constexpr int kFar = 8;              // powers of two between scales, to which weights keep to the slice's largest
+// The scales of a token that is not seen: a key's that no write leaves (a finite one: its codes are zeros), and
+// a value's below all others.
+constexpr uint32_t kUnseen = 250;
 
 struct Fp8Params : SplitParams {
     const uint16_t* q;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             bool all = true;
 #pragma unroll
             for (int y = 0; y < kPer; ++y) {
-                scale_byte[0][y] = scale_byte[1][y] = 0;
+                scale_byte[0][y] = kUnseen, scale_byte[1][y] = 0;
                 if (there[y] && static_cast<uint32_t>(page[y]) >= static_cast<uint32_t>(p.pages)) {
                     atomicOr(p.status, DECODE_BAD_PAGE);
                     there[y] = false;
@@ -430,6 +438,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
             }
             // the scales of the lane's token, and of its rows, row0 + 8 j + lane / 4
             float k_scale[2 * kSubs], v_scale[2 * kSubs], slice_scale;
+            bool far;                              // the values' scales are far apart (for the warp)
             {
                 uint32_t two[kPer], largest = 0;
                 float kf[kPer], vf[kPer];
@@ -440,12 +449,15 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                 }
                 largest = __reduce_max_sync(kAll, largest);
                 slice_scale = power_of(static_cast<int>(largest) - 15);
+                far = false;
 #pragma unroll
                 for (int y = 0; y < kPer; ++y) {
                     const int e = two[y] >> 8, below = static_cast<int>(largest) - e;
+                    far = far || (below > kFar && two[y] != kUnseen);
                     kf[y] = scale_of(two[y] & 0xffu) * p.scale_log2;
                     vf[y] = e == 255 ? NAN : below < 142 ? power_of(142 - below) : 0.f;
                 }
+                far = __any_sync(kAll, far);
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
                     k_scale[j] = __shfl_sync(kAll, kf[j / 4 % kPer], (j * 8 + (lane >> 2)) & 31);
@@ -469,7 +481,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                     }
             }
             uint32_t pb[kHeadTiles][kSubs][2][2];  // [piece][rows 0 .. 7, 8 .. 15]
-            float corr[kHeadTiles][2];
+            float corr[kHeadTiles][2], back[kHeadTiles][2];        // factors of the running sums, of the slice's
 #pragma unroll
             for (int x = 0; x < kHeadTiles; ++x) {
 #pragma unroll
@@ -477,27 +489,49 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                     const float by = !C::kQueriesShared               ? q_scale[C::kQueriesShared ? 0 : x][e]
                                      : std::is_same<T, H>::value      ? 1.f
                                                                       : sm_q_scale[x * 8 + (lane & 3) * 2 + e];
-                    float top = -INFINITY;
+                    float own = -INFINITY;         // the slice's largest
 #pragma unroll
-                    for (int j = 0; j < 2 * kSubs; ++j) top = fmaxf(top, s[x][j / 2][j % 2 * 2 + e]);
-                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 16));
-                    top = fmaxf(top * by, m[x][e]);
+                    for (int j = 0; j < 2 * kSubs; ++j) own = fmaxf(own, s[x][j / 2][j % 2 * 2 + e]);
+                    own = fmaxf(own, __shfl_xor_sync(kAll, own, 4));
+                    own = fmaxf(own, __shfl_xor_sync(kAll, own, 8));
+                    own = fmaxf(own, __shfl_xor_sync(kAll, own, 16)) * by;
+                    const float top = fmaxf(own, m[x][e]);
                     // scores of -infinity only: any finite reference leaves their weights 0
-                    const float ref = top == -INFINITY ? 0.f : top;
+                    const float ref = fmaxf(top, -FLT_MAX), base = fmaxf(own, -FLT_MAX);
+                    const float share = exp2_fast(own - ref);
                     corr[x][e] = exp2_fast(m[x][e] - ref);
                     m[x][e] = top;
                     float sum = 0.f;
 #pragma unroll
                     for (int j = 0; j < 2 * kSubs; ++j) {
                         float& v = s[x][j / 2][j % 2 * 2 + e];
-                        v = exp2_fast(fmaf(v, by, -ref));
+                        v = exp2_fast(fmaf(v, by, -base));
                         sum += v;
                         v *= v_scale[j];
                     }
-                    l[x][e] = fmaf(l[x][e], corr[x][e], sum);
+                    l[x][e] = fmaf(l[x][e], corr[x][e], sum * share);
+                    back[x][e] = slice_scale * share;
                 }
+            }
+            if (far) {                             // each head's largest to 2^14 .. 2^15
+#pragma unroll
+                for (int x = 0; x < kHeadTiles; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float most = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 2 * kSubs; ++j) most = fmaxf(most, s[x][j / 2][j % 2 * 2 + e]);
+                        most = fmaxf(most, __shfl_xor_sync(kAll, most, 4));
+                        most = fmaxf(most, __shfl_xor_sync(kAll, most, 8));
+                        most = fmaxf(most, __shfl_xor_sync(kAll, most, 16));
+                        const int up = min(max(141 - static_cast<int>(__float_as_uint(most) >> 23), 0), 127);
+#pragma unroll
+                        for (int j = 0; j < 2 * kSubs; ++j) s[x][j / 2][j % 2 * 2 + e] *= power_of(127 + up);
+                        back[x][e] *= power_of(127 - up);
+                    }
+            }
+#pragma unroll
+            for (int x = 0; x < kHeadTiles; ++x) {
 #pragma unroll
                 for (int j = 0; j < 2 * kSubs; ++j) {
                     const float v0 = s[x][j / 2][j % 2 * 2], v1 = s[x][j / 2][j % 2 * 2 + 1];
@@ -550,7 +584,7 @@ __global__ void __launch_bounds__(Fp8Cfg<D, kHeadTiles>::kThreads, Fp8Cfg<D, kHe
                                 const uint64_t old =
                                     mul2(pair(sum[0], sum[1]), pair(corr[x][0], corr[x][1]));
                                 const float2 f = halves(fma2(pair(o[z][x][e], o[z][x][e + 1]),
-                                                             pair(slice_scale, slice_scale), old));
+                                                             pair(back[x][0], back[x][1]), old));
                                 sum[0] = f.x, sum[1] = f.y;
                             }
                 }

@@ -246,9 +246,9 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens,
                         scale: float | None = None, window: int | None = None, sinks: int = 0,
                         return_lse: bool = False, out=None, workspace=None, stream=None):
     """``paged_attention`` over a cache of ``quantize_cache``: the same operands, results and refusals,
-    with the values that the codes stand for.  With a ``window`` the first ``sinks`` tokens stay
-    visible beside the last ``window``.  ``workspace``: from ``paged_attention_fp8_workspace``; None takes
-    one from torch's allocator for the call."""
+    with the values that the codes stand for (the C header says to what precision, and for which scales).
+    With a ``window`` the first ``sinks`` tokens stay visible beside the last ``window``.  ``workspace``:
+    from ``paged_attention_fp8_workspace``; None takes one from torch's allocator for the call."""
     return _decode.paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, lens, scale,
                                        window, sinks, return_lse, out, workspace, stream)
 

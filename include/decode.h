@@ -300,6 +300,13 @@ int decode_dequantize_cache(const decode_dequantize_cache_args* args, cudaStream
  * scale or code that stands for NaN reaches the results of its block's or token's head; those of
  * unseen tokens reach none.  Strides of pages, offsets and blocks are below 2^32.  The workspace is its
  * own: decode_paged_attention_fp8_workspace_bytes().
+ *
+ * What the results hold to: a token's weight is taken to 2^-22 of itself, or to 2^-32 of the largest product of
+ * weight and value scale among 16 to 64 neighbours.  A weight below 2^-126 of the sequence's largest counts as
+ * 0, and so does a value whose scale is below 2^-140 of its neighbours' largest.  Elements of a bfloat16 query
+ * are taken to 2^-38 of its largest.  Parts of a sequence are summed in fp32 each by itself: the sum of the
+ * magnitudes of any part's values must be a number of fp32, and scale * 2^(e - 127) of a seen key's block must
+ * be below 2^94 (and above 2^-126, below which a score loses bits).
  */
 typedef struct {
     const void* q;

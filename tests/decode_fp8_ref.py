@@ -124,3 +124,39 @@ def linear_w4(x, codes, scales, group, zeros=None, bias=None, activation="none")
         y = y * torch.special.ndtr(y)
         bound = 1.13 * bound + 2.0 ** -20 * y.abs()
     return y, bound
+
+
+def paged_attention_by_weight(q, c, table, lens, scale):
+    """(o, lse, o's bound, lse's bound) as paged_attention gives them for all of a sequence's tokens, but that
+    what the pieces of a weight leave out is held to the weights: they keep 2^-25 where the slice's largest
+    product of weight and scale stands for 2^7 at least (2^15, but that scales up to 2^8 apart are left as they
+    are), so a token's part is off by 2^-32 of the largest such product, times its code.  (c: the four tensors of
+    a cache.)"""
+    dt = q.dtype
+    q = q.double().cpu()
+    k, v = values(c["k_cache"], c["k_scale"]), values(c["v_cache"], c["v_scale"])
+    page, h_kv = k.shape[1], k.shape[2]
+    block = page // c["v_scale"].shape[1]
+    o = torch.zeros_like(q)
+    lse = torch.zeros(q.shape[:2], dtype=torch.float64)
+    ob, lb = torch.zeros_like(o), torch.zeros_like(lse)
+    for i, length in enumerate(lens.tolist()):
+        at = torch.arange(length)
+        rows = table[i].cpu().long()[at // page]
+        for m in range(q.shape[1]):
+            kv = m // (q.shape[1] // h_kv)
+            K, V = k[rows, at % page, kv], v[rows, at % page, kv]
+            by = torch.ldexp(torch.ones(length, dtype=torch.float64),
+                             c["v_scale"].cpu().long()[rows, at % page // block, kv] - 127)
+            x = scale * (K @ q[i, m])
+            es = float((abs(scale) * (K.abs() @ q[i, m].abs())).max()) * (q.shape[2] + 4) * 4 * E + \
+                8 * E * float(x.abs().max())
+            if dt == torch.bfloat16:
+                es += abs(scale) * 2.0 ** -38 * float(q[i, m].abs().max()) * float(K.abs().sum(1).max())
+            lse[i, m] = torch.logsumexp(x, 0)
+            p = torch.exp(x - lse[i, m])
+            o[i, m] = p @ V
+            rel = 2 * es + 2.0 ** -18 + length / 16 * E
+            ob[i, m] = rel * (p @ V.abs()) + 2.0 ** -32 * 448 * length * float((p * by).max())
+            lb[i, m] = es + 2.0 ** -18 + length / 16 * E + 4 * E * abs(float(lse[i, m]))
+    return o, lse, ob, lb

@@ -826,3 +826,40 @@ def test_pages_without_tokens_are_refused():
         g.dequantize_cache(codes, codes, scale, scale, at)
     with pytest.raises(ValueError, match="hold a token"):
         g.paged_attention_fp8(x, codes, codes, scale, scale, at[:, None], at)
+
+
+@DTYPES
+@pytest.mark.parametrize("h_q,h_kv,d", [(4, 2, 64), (9, 1, 64), (4, 2, 128), (12, 1, 128), (4, 2, 256), (16, 1, 256)])
+@pytest.mark.parametrize("whole", [False, True], ids=["blocks", "stretch"])
+@pytest.mark.parametrize("apart,weight", [(5, 0), (12, -40), (30, 0), (60, 0), (60, -40), (100, 0), (100, -60),
+                                          (110, -100)])
+def test_large_values_of_little_weight(apart, weight, whole, h_q, h_kv, d, dtype):
+    """Blocks whose values are 2^apart larger, with weights 2^(weight - apart) of the others', so that they
+    matter as much or not at all: among the others' blocks, and as the first 1000 tokens of 1500.  (2^110 times
+    codes to 448, over 1000 tokens, stays a number of fp32, in which a part of a sequence is summed by itself.)"""
+    gen = generator(apart + d + h_q)
+    q, c, table, lens = attention_inputs(gen, [40, 1500, 9], h_q, h_kv, d, 16, 8, dtype)
+    c = {x: y.cpu() for x, y in c.items()}
+    q = (torch.rand(3, h_q, d, generator=gen) + 0.5).to(dtype).cuda()
+    k = 0.1 * normal(gen, *c["k_cache"].shape)
+    large = torch.rand(c["k_cache"].shape[0], 2, generator=gen) < 0.3                  # pages, blocks
+    if whole:
+        large[:] = False
+        large[table[1, :1000 // 16].cpu().long()] = True
+    score = (apart - weight) * math.log(2)                                             # of which e^-score is left
+    k[large.repeat_interleave(8, 1)] = -score / d ** 0.5                               # (queries are 1 on average)
+    e = torch.where(large, 127 - 4, 127 - 8)[..., None].expand(-1, -1, h_kv)
+    c["k_scale"] = e.to(torch.uint8).contiguous()
+    c["k_cache"] = (k * torch.exp2(127.0 - e)[:, :, None, :, None].expand(-1, -1, 8, -1, -1).flatten(1, 2)).to(E4M3)
+    c["v_scale"] = (c["v_scale"].int() + apart * large[..., None].int()).to(torch.uint8)
+    c = {x: y.cuda() for x, y in c.items()}
+    o, lse = attend(q, c, table, lens, return_lse=True)
+    o_ref, lse_ref, ob, lb = ref.paged_attention_by_weight(q, c, table, lens, d ** -0.5)
+    # (a short sequence may have large values alone: from half a step past the type's largest number on, what a
+    # value within the bound is rounded to is infinity)
+    most = torch.finfo(dtype).max
+    most += ref.U[dtype] * 2.0 ** math.floor(math.log2(most))
+    past = o.cpu().double() == o_ref.sign() * math.inf
+    assert bool((o_ref.abs() + ob >= most)[past].all()) and bool(past[o_ref.abs() - ob >= most].all())
+    ref.assert_close(o.cpu().masked_fill(past, 0), o_ref.masked_fill(past, 0), ob.masked_fill(past, 0), "o")
+    ref.assert_close(lse, lse_ref, lb, "lse")
