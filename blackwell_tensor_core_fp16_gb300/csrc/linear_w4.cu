@@ -49,8 +49,8 @@ struct LinearParams {
 // A half of 16 bits that holds a whole number v < 256 and no more is v times the type's least number (bfloat16
 // has 7 bits behind the point and the exponents 0 and 1 the same unit, so this holds to 255): one fma brings it
 // to its size and takes the zero point from it.  kUp: the factors of a code in the lower half and of 16 times a
-// code in the upper one; kBack: what is left to be multiplied into the sums, for the least number's inverse is
-// no number of the type.
+// code in the upper one; kBack: what is left to be multiplied into the sums at the end, for the least number's inverse is
+// no number of the type.  (Not into the scales, which may be the type's largest.)
 template <typename T>
 struct Half;
 template <>
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t got = __shfl_sync(0xffffffffu, sz[z], y * 16 + r + 8 * e);
-                        by[e] = Half2<T>::unpack(got & 0xffffu).x * Differences<T>::kBack;
+                        by[e] = Half2<T>::unpack(got & 0xffffu).x;
                         diff[e].set(got >> 16);
                     }
 #pragma unroll
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int token = q * 2 + (e & 1);
-            if (token < p.m) to[token * kItem + r + 8 * (e >> 1)] = sum[e];
+            if (token < p.m) to[token * kItem + r + 8 * (e >> 1)] = sum[e] * Differences<T>::kBack;
             sum[e] = 0.f;
         }
         ++item;
@@ -652,7 +652,7 @@ linear_w4_tile_kernel(const LinearParams p)
             for (int x = 0; x < kParts; ++x) {
                 // (no part where there is no column: its scale stands for nothing)
                 const bool there = x == 0 || begin + x * (128 / kParts) < p.k;
-                const float by = Half2<T>::unpack(scale[x]).x * Differences<T>::kBack;
+                const float by = Half2<T>::unpack(scale[x]).x;
 #pragma unroll
                 for (int t = 0; t < kMine; t += kAtOnce) {
                     if (t0 + t >= kTokens) break;
@@ -673,7 +673,7 @@ linear_w4_tile_kernel(const LinearParams p)
         // [token][output], where the elements were: all of them have been read
 #pragma unroll
         for (int t = 0; t < kMine; ++t)
-            if (t0 + t < kTokens) sums[(t0 + t) * kSumRow + tid % kRows] = sum[t];
+            if (t0 + t < kTokens) sums[(t0 + t) * kSumRow + tid % kRows] = sum[t] * Differences<T>::kBack;
     } else if (w < C::kMma) {
         // ---- the operands.  The codes: a warp has 32 rows of every fourth chunk, those of its lanes of tensor
         // memory.  It copies them four lanes a row, and a lane reads its row back: nothing but the warp's

@@ -340,7 +340,8 @@ int decode_paged_attention_fp8_workspace_bytes(int64_t h_q, int64_t h_kv, int64_
  *
  * with g over the groups of `group` neighbouring columns (the last may be shorter).  Differences of
  * codes are exact in the tensor cores' 16 bits, sums are fp32 and so are the scales' products: y is
- * rounded once.  Made for few tokens, whose time is that of reading the weights.
+ * rounded once.  Made for few tokens, whose time is that of reading the weights.  The sums of a group are
+ * taken before its scale: with bfloat16 they must be below 2^134 in magnitude, however small the scale.
  *
  *   x             [m][k], 16 bits, x_stride (a multiple of 8) between rows
  *   codes         [n][k / 2] bytes, code_stride (a multiple of 16) between rows: byte c holds column

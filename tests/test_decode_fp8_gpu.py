@@ -863,3 +863,17 @@ def test_large_values_of_little_weight(apart, weight, whole, h_q, h_kv, d, dtype
     assert bool((o_ref.abs() + ob >= most)[past].all()) and bool(past[o_ref.abs() - ob >= most].all())
     ref.assert_close(o.cpu().masked_fill(past, 0), o_ref.masked_fill(past, 0), ob.masked_fill(past, 0), "o")
     ref.assert_close(lse, lse_ref, lb, "lse")
+
+
+@pytest.mark.parametrize("m", [1, 6, 12, 40])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("scale,token", [(122, -122), (126, -126), (127, -133), (-110, 110), (-126, 118), (-66, -60),
+                                         (0, -133), (0, -126), (0, 118)])
+def test_linear_of_small_and_large_scales(scale, token, group, m):
+    """Scales and elements at either end of bfloat16's range, subnormal elements among them: a sum of 128
+    products of elements below 2^121 stays below 2^134."""
+    gen = generator(m + scale)
+    x = (normal(gen, m, 384).double() * 2.0 ** token).bfloat16().cuda()
+    s = weights(gen, 150, 384, group, torch.bfloat16, True, False)
+    s["scales"] = (0.9 * s["scales"].double() * 2.0 ** scale).bfloat16()
+    check_linear(x, s, f"2^{scale} x 2^{token}")
