@@ -188,6 +188,10 @@ def load():
             getattr(lib, name).restype = i32
         lib.decode_last_error.argtypes = []
         lib.decode_last_error.restype = ctypes.c_char_p
+        lib.decode_set_wait_timeout_ms.argtypes = [u32]
+        lib.decode_set_wait_timeout_ms.restype = i32
+        lib.decode_set_fault_injection.argtypes = [i32]
+        lib.decode_set_fault_injection.restype = i32
         lib.decode_check_status.argtypes = [vp, u32p]
         lib.decode_check_status.restype = i32
         _lib = lib
@@ -754,7 +758,8 @@ _DECODE_NAMES = frozenset((
     "check_decode_status", "decode_check_status", "decode_dequantize_cache", "decode_gdn_step",
     "decode_last_error", "decode_linear_w4", "decode_paged_attention", "decode_paged_attention_fp8",
     "decode_paged_attention_fp8_workspace_bytes", "decode_paged_attention_workspace_bytes",
-    "decode_qk_norm_rope", "decode_quantize_cache", "dequantize_cache", "gated_delta_step",
+    "decode_qk_norm_rope", "decode_quantize_cache", "decode_set_fault_injection",
+    "decode_set_wait_timeout_ms", "dequantize_cache", "gated_delta_step",
     "linear_w4", "paged_attention", "paged_attention_fp8", "paged_attention_fp8_workspace",
     "paged_attention_workspace", "qk_norm_rope", "quantize_cache", "quantize_weight_w4",
     "rotary_table"))

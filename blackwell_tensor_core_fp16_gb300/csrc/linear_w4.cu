@@ -15,6 +15,8 @@
 // Two kernels.  One for up to 8 tokens with few elements streams the codes from global memory to the warps that
 // use them; mma.sync is enough there, for the tensor cores have next to nothing to do.  The other, for more,
 // spares the instructions: tcgen05.mma takes 128 outputs and up to 64 tokens at a time.
+#include <atomic>
+
 #include "decode_mma.cuh"
 #include "desc.h"
 #include "ptx.cuh"
@@ -38,7 +40,17 @@ struct LinearParams {
     int32_t wide;                                // a chunk's scales, and its zero points, are one word
     uint32_t* status;
     int32_t items_each, items_more, pieces_each, pieces_more, stages, waiting;    // for few tokens
+    int32_t fault;                               // for the tests: full[1] waits for one arrival too many
+    uint32_t wait_ms;                            // that one wait may take
 };
+
+__device__ __forceinline__ uint64_t limit_ns(const LinearParams& p)
+{
+    return static_cast<uint64_t>(p.wait_ms) * 1000000;
+}
+
+std::atomic<uint32_t> g_wait_ms{2000};
+std::atomic<int32_t> g_fault{0};
 
 // How codes become 16-bit numbers.  Two masks split a word's bytes, a permutation deals a byte of each to the
 // two halves of a register, and an fma makes them numbers.  (Masks that leave codes below the upper bits of
@@ -49,8 +61,8 @@ struct LinearParams {
 // A half of 16 bits that holds a whole number v < 256 and no more is v times the type's least number (bfloat16
 // has 7 bits behind the point and the exponents 0 and 1 the same unit, so this holds to 255): one fma brings it
 // to its size and takes the zero point from it.  kUp: the factors of a code in the lower half and of 16 times a
-// code in the upper one; kBack: what is left to be multiplied into the sums at the end, for the least number's inverse is
-// no number of the type.  (Not into the scales, which may be the type's largest.)
+// code in the upper one; kBack: what is left to be multiplied into the sums at the end, for the least number's
+// inverse is no number of the type.  (Not into the scales, which may be the type's largest.)
 template <typename T>
 struct Half;
 template <>
@@ -195,7 +207,6 @@ constexpr int kFewRow = kPieces * 64 + 64;       // bytes of a stage's row; two 
 constexpr int kFewStage = kItem * kFewRow;
 constexpr int kMostStages = 5;
 constexpr int kFewMost = 233472 / 2 - 1024 - 2 * kMostStages * 8 - 16;   // bytes for elements, sums, stages
-constexpr uint64_t kTimeout = 2000000000;        // ns that a copy may take
 
 __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t barrier)
 {
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
     volatile uint32_t* const gave_up = reinterpret_cast<uint32_t*>(bars + 2 * kMostStages);
     if (tid == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            gf16::mbar_init(full + s * 8, 1);
+            gf16::mbar_init(full + s * 8, p.fault == 1 && s == 1 ? 2 : 1);
             gf16::mbar_init(empty + s * 8, kFewWarps);
         }
         *gave_up = 0;
@@ -243,17 +254,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
     dep_wait();
 
     auto wait = [&](uint32_t barrier, uint32_t parity) {
-        if (gf16::mbar_wait(barrier, parity, gave_up, kTimeout)) return;
+        if (gf16::mbar_wait(barrier, parity, gave_up, limit_ns(p))) return true;
         *gave_up = 1;                            // nothing waits any more; the results are no results
         atomicOr(p.status, DECODE_TIMED_OUT);
+        return false;                            // (whoever gets this announces nothing)
     };
     // the copies of a step, by the first warp: rows past the last output are the last one's
+    // (none any more once a stage is not given back: it may still be on its way)
     int next_item = item0, next_round = 0;
     auto fetch = [&](int stage, bool again, uint32_t parity) {
-        if (next_item >= item1) return;
+        if (next_item >= item1) return true;
         const int first = piece0 + next_round * kPieces;
         const int columns = min(p.k, min(piece1, first + kPieces) * 128) - first * 128;
-        if (again) wait(empty + stage * 8, parity);
+        if (again && !__all_sync(0xffffffffu, wait(empty + stage * 8, parity))) {
+            next_item = item1;
+            return false;
+        }
         if (columns > 0) {
             if (lane == 0) gf16::mbar_arrive_expect_tx(full + stage * 8, kItem * (columns / 2));
             __syncwarp();
@@ -269,6 +285,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
             next_round = 0;
             ++next_item;
         }
+        return true;
     };
     if (w == 0)
         for (int s = 0; s < p.stages; ++s) fetch(s, false, 0);
@@ -336,13 +353,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 
     float sum[4] = {};
     int item = item0, round = 0, stage = 0, slot = 0;
+    int fetched = steps;                         // steps whose copies have begun, at the end
     uint32_t parity = 0;
     for (int step = 0; step < steps; ++step) {
         uint32_t sz[kParts];
 #pragma unroll
         for (int x = 0; x < kParts; ++x) sz[x] = scale[x] | zero[x] << 16;
         load_scales();
-        wait(full + stage * 8, parity);
+        const bool come = wait(full + stage * 8, parity);
         const uint8_t* const from = smem + stage * kFewStage + r * kFewRow + w * 64;
         // the warp's pieces of the stage: kCount of them at once
         auto take = [&](auto count) {
@@ -369,7 +387,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
                     }
                 }
             __syncwarp();
-            if (lane == 0) gf16::mbar_arrive_local(empty + stage * 8);
+            if (lane == 0 && come) gf16::mbar_arrive_local(empty + stage * 8);
 #pragma unroll
             for (int y = 0; y < kCount; ++y)
 #pragma unroll
@@ -406,9 +424,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
             take(std::integral_constant<int, 2>());
         else if (last > 0)
             take(std::integral_constant<int, 1>());
-        else if (lane == 0)
+        else if (lane == 0 && come)
             gf16::mbar_arrive_local(empty + stage * 8);
-        if (w == 0) fetch(stage, true, parity);
+        if (w == 0 && !fetch(stage, true, parity)) fetched = step + p.stages;
         if (++stage == p.stages) {
             stage = 0;
             parity ^= 1;
@@ -458,10 +476,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
         else if (item < item1)
             __syncthreads();
     }
-    // after a wait that ran out: the copies in flight are waited for, once more
+    // after a wait that ran out: the copies in flight are waited for, once more.  (A stage's former copies had
+    // come before it was filled again, so a parity stands for the last ones.)
     if (*gave_up && w == 0)
-        for (int step = max(0, steps - p.stages); step < steps; ++step)
-            gf16::mbar_wait(full + step % p.stages * 8, step / p.stages & 1, nullptr, kTimeout);
+        for (int step = max(0, fetched - p.stages); step < fetched; ++step)
+            gf16::mbar_wait(full + step % p.stages * 8, step / p.stages & 1, nullptr, limit_ns(p));
 }
 
 // The kernel for few tokens; false if they have too many elements for it.  Each block brings its columns of
@@ -573,10 +592,10 @@ linear_w4_tile_kernel(const LinearParams p)
     extern __shared__ uint8_t dynamic[];
     uint8_t* const smem = dynamic + (-smem_addr(dynamic) & 1023u);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + C::kBarriers);
-    // operands made; operands read; sums made; sums read
+    // operands made; operands read; sums made; sums read; all products done
     const uint32_t full = smem_addr(bars), empty = full + kGroups * 8, made = empty + kGroups * 8,
-                   taken = made + 16;
-    uint32_t* const slot = reinterpret_cast<uint32_t*>(bars + 2 * kGroups + 4);
+                   taken = made + 16, done = taken + 16;
+    uint32_t* const slot = reinterpret_cast<uint32_t*>(bars + 2 * kGroups + 5);
     volatile uint32_t* const gave_up = slot + 1;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     const int part = cluster_rank(), j0 = cluster_id() * kRows, i0 = blockIdx.y * kTokens;
@@ -588,13 +607,14 @@ linear_w4_tile_kernel(const LinearParams p)
     auto column_of = [&](int c) { return (c0 + (c + turn < chunks ? c + turn : c + turn - chunks)) * 128; };
     if (tid == 0) {
         for (int s = 0; s < kGroups; ++s) {
-            gf16::mbar_init(full + s * 8, kMakers / kGroups);
+            gf16::mbar_init(full + s * 8, kMakers / kGroups + (p.fault == 1 && s == 1 ? 1 : 0));
             gf16::mbar_init(empty + s * 8, 1);
         }
         for (int s = 0; s < 2; ++s) {
             gf16::mbar_init(made + s * 8, 1);
             gf16::mbar_init(taken + s * 8, C::kReaders);
         }
+        gf16::mbar_init(done, 1);
         *gave_up = 0;
         gf16::fence_mbarrier_init();
     }
@@ -610,7 +630,7 @@ linear_w4_tile_kernel(const LinearParams p)
     dep_wait();
 
     auto wait = [&](uint32_t barrier, uint32_t parity) {
-        if (gf16::mbar_wait(barrier, parity, gave_up, kTimeout)) return;
+        if (gf16::mbar_wait(barrier, parity, gave_up, limit_ns(p))) return;
         *gave_up = 1;                            // nothing waits any more; the results are no results
         atomicOr(p.status, DECODE_TIMED_OUT);
     };
@@ -795,9 +815,10 @@ linear_w4_tile_kernel(const LinearParams p)
             gf16::mma_commit(empty + stage * 8);
             gf16::mma_commit(made + at * 8);
         }
-        // (the last sums' reader waits for them; after a wait that ran out nothing else would)
-        if (*gave_up && chunks > 0)
-            gf16::mbar_wait(made + (chunks - 1) % kSums * 8, (chunks - 1) / kSums & 1, nullptr, kTimeout);
+        // All of them are waited for, on a barrier of their own, whoever has given up: tensor memory and the
+        // elements go with the block.  (After a wait that ran out the others' parities stand for nothing.)
+        gf16::mma_commit(done);
+        if (!gf16::mbar_wait(done, 0, nullptr, limit_ns(p))) atomicOr(p.status, DECODE_TIMED_OUT);
     }
     __syncwarp();
 
@@ -937,6 +958,7 @@ int decode_linear_w4(const decode_linear_w4_args* a, cudaStream_t stream)
     p.group = static_cast<int32_t>((a->group < a->k ? a->group : a->k > 0 ? a->k : 32) / 32);
     p.group_shift = shift_of(p.group);
     p.activation = a->activation;
+    p.fault = g_fault.load(), p.wait_ms = g_wait_ms.load();
     // Groups of 32 and 64: a lane's scales of 128 columns by one load, if a row's are aligned so.  Each lane has a
     // row, so a load costs as many cycles as it touches lines: 64 tokens, 14336 x 4096, groups of 32 42.0 us with
     // one for each, 16 tokens 27.9.
@@ -946,6 +968,22 @@ int decode_linear_w4(const decode_linear_w4_args* a, cudaStream_t stream)
              (!a->zeros || (zero_stride[0] % parts == 0 && reinterpret_cast<uintptr_t>(a->zeros) % parts == 0));
     return a->dtype == DECODE_BF16 ? dispatch<__nv_bfloat16>(p, stream)
                                    : dispatch<__half>(p, stream);
+}
+
+int decode_set_wait_timeout_ms(uint32_t ms)
+{
+    clear_error();
+    if (ms == 0) return fail(DECODE_ERR_INVALID_ARG, "timeout must be at least 1 ms");
+    g_wait_ms.store(ms);
+    return DECODE_OK;
+}
+
+int decode_set_fault_injection(int mode)
+{
+    clear_error();
+    if (mode < 0 || mode > 1) return fail(DECODE_ERR_INVALID_ARG, "unknown fault mode %d", mode);
+    g_fault.store(mode);
+    return DECODE_OK;
 }
 
 }  // extern "C"

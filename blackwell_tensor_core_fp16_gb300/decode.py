@@ -31,7 +31,7 @@ DECODE_STATUS = {1: "a state slot outside the pool",
                  2: "a cache slot outside the cache, or out of its block's order",
                  4: "a position outside the rotary table",
                  8: "a sequence length its page table cannot hold",
-                 16: "a page number outside the cache", 32: "a copy that took too long"}
+                 16: "a page number outside the cache", 32: "a copy or product that took too long"}
 
 # The argument structs of include/decode.h, field by field (no padding on either side).
 GDN_STEP_ARGS = struct.Struct("=8Q7q9q4qqif")
@@ -98,6 +98,14 @@ def decode_check_status(stream: int = 0):
     bits = ctypes.c_uint32(0)
     rc = load().decode_check_status(stream, ctypes.byref(bits))
     return rc, bits.value
+
+
+def decode_set_wait_timeout_ms(ms: int) -> int:
+    return load().decode_set_wait_timeout_ms(ms)
+
+
+def decode_set_fault_injection(mode: int) -> int:
+    return load().decode_set_fault_injection(mode)
 
 
 # ---- torch entry points ---------------------------------------------------------------------------

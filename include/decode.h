@@ -64,8 +64,8 @@ extern "C" {
 #define DECODE_BAD_POSITION 4u    /* decode_qk_norm_rope: a position outside the table */
 #define DECODE_BAD_LENGTH 8u      /* an attention: a length its page table cannot hold */
 #define DECODE_BAD_PAGE 16u       /* an attention: a page outside the cache */
-#define DECODE_TIMED_OUT 32u      /* decode_linear_w4: a copy took longer than two seconds, and the call's
-                                     results are undefined */
+#define DECODE_TIMED_OUT 32u      /* decode_linear_w4: a copy or product took longer than the limit, and the
+                                     call's results are undefined */
 
 /* ---- the gated delta rule, token by token ------------------------------------------------------
  *
@@ -383,6 +383,16 @@ const char* decode_last_error(void);
  * a refusal is reported to whichever check comes first after it.  Returns DECODE_OK, or
  * DECODE_ERR_CUDA if the stream reported an error. */
 int decode_check_status(cudaStream_t stream, uint32_t* bits);
+
+/* Limit of one wait of decode_linear_w4's kernels, for later calls of this process (ms >= 1; default 2000).
+ * After one that runs out a block waits for what it has in flight, up to the limit again, writes results
+ * that are none and sets DECODE_TIMED_OUT. */
+int decode_set_wait_timeout_ms(uint32_t ms);
+
+/* Testing hook, 0 = off (default).  1: decode_linear_w4's kernels never learn that the codes of a block's second
+ * stage have come, or that the operands of its second chunk of 128 columns are made, so the wait for them runs
+ * out.  For failure-detection tests only. */
+int decode_set_fault_injection(int mode);
 
 #ifdef __cplusplus
 }

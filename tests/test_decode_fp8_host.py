@@ -220,3 +220,11 @@ def test_weights_of_a_group_wider_than_the_matrix():
     for zeros in (True, False):
         for one, other in zip(g.quantize_weight_w4(W, 1 << 50, zeros), g.quantize_weight_w4(W, 64, zeros)):
             assert (one is None and other is None) or torch.equal(one, other)
+
+
+def test_wait_limit_and_testing_hook_refuse_what_they_do_not_have():
+    assert g.decode_set_wait_timeout_ms(0) == BAD and "1 ms" in g.decode_last_error()
+    assert g.decode_set_wait_timeout_ms(2000) == 0
+    for mode in (-1, 2):
+        assert g.decode_set_fault_injection(mode) == BAD and "fault mode" in g.decode_last_error()
+    assert g.decode_set_fault_injection(0) == 0
