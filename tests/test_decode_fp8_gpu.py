@@ -877,3 +877,27 @@ def test_linear_of_small_and_large_scales(scale, token, group, m):
     s = weights(gen, 150, 384, group, torch.bfloat16, True, False)
     s["scales"] = (0.9 * s["scales"].double() * 2.0 ** scale).bfloat16()
     check_linear(x, s, f"2^{scale} x 2^{token}")
+
+
+@pytest.mark.parametrize("apart", [129, 143, 144, 145, 159, 160])
+@pytest.mark.parametrize("again", [[0, 1], [3], [-1, 1]])
+@pytest.mark.parametrize("many", [0, 3000, 9000, 17000])
+@pytest.mark.parametrize("last_of_window", [False, True])
+def test_write_of_a_block_in_two_runs_far_apart(last_of_window, many, again, apart):
+    """The farthest second runs that are refused, at the first and at the last token of a window, with windows of
+    1, 2, 8 and 16 tokens."""
+    gen = generator(apart + many)
+    lead = ((15 if last_of_window else 0) - apart) % 16
+    others = iter(range(8, 8 * 400, 8))
+    between = apart - 1 - (again[0] == -1)       # (inactive, and the run behind it is `apart` behind)
+    slots = [next(others) for _ in range(lead)] + [0] + [next(others) for _ in range(between)]
+    kept = list(range(len(slots)))
+    slots += again
+    slots = torch.tensor(slots + [-1] * many, dtype=torch.int32)
+    c = caches(gen, 200, 16, 8, 2, 64)
+    before = {a: b.clone() for a, b in c.items()}
+    x = {kind: normal(gen, len(slots), 2, 64).half().cuda() for kind in "kv"}
+    write(c, x, slots.cuda())
+    check_cache(c, before, {kind: y[kept] for kind, y in x.items()}, slots[kept], "kept")
+    with pytest.raises(g.GemmError, match="cache slot"):
+        g.check_decode_status()
