@@ -196,8 +196,9 @@ cudaError_t clusters_of(int threads, int smem, const Clusters*& of)
 // blocks of a cluster share the columns out where there are few items, and add their sums through
 // distributed shared memory, in a fixed order.
 //
-// One token, 14336 x 4096: 12.0 us (floor 4.5); 4096 x 4096: 5.6 (1.3); 256 x 256: 2.8, a launch and the way
-// there and back.  7 tokens, 5000 x 1024, groups of 32: 5.6 (0.5).
+// One token, 14336 x 4096: 12.0 us (floor 4.5); 28672 x 8192: 40 (18), so large layers run at 3.1 TB/s, with
+// 160 KB an SM on their way (why no faster is not shown: one warp computes and issues the copies of 16 rows, one
+// after another); 4096 x 4096: 5.6 (1.3); 256 x 256: 2.8, a launch and the way there and back.  7 tokens, 5000 x 1024, groups of 32: 5.6 (0.5).
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 constexpr int kItem = 16;                        // outputs
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_w4_few_kernel(const Lin
 // 7.4; 14336 x 4096, 1 12.0 and 13.6, 4 13.6 and 13.6, 8 16.7 and 13.8; 8192 x 8192, 1 15.0 and 14.7, 2 16.4
 // and 14.8; 28672 x 8192, 1 40.3 and 46.1, 2 41.4 and 46.1; 1024 x 14336, split by 8, 4 7.5 and 8.7; 5000 x
 // 1024, 8 5.7 and 5.8.  More parts than are best without regard to this lose more: 8192 x 8192, 8 tokens, 28.3.
+// (The rule goes by elements alone, so 2 tokens of 8192 x 8192 stay with this kernel, which loses a tenth there.)
 constexpr int kFewMostElements = 16384;
 template <typename T, int kWords>
 bool run_few(LinearParams p, cudaStream_t stream, int& rc)
@@ -555,8 +557,10 @@ bool few_with_words(const LinearParams& p, cudaStream_t stream, int& rc)
 // are on their way.
 //
 // 48 tokens, 14336 x 4096: 17.3 us (floor 4.8), 0.4 us a chunk; 16 tokens 14.2; 200 tokens, 4096 x 4096: 17.3
-// (3.5).  The integer instructions that make the operands bound it, on 112 of 152 SMs, a block's 128 rows being
-// indivisible.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory alone,
+// (3.5).  A block's 128 rows being indivisible, 112 of 152 SMs have one, and on those nothing is full: a
+// scheduler issues for 600 of a chunk's 850 to 1000 cycles, the pipe of the integer operations, which make the
+// operands, is 59% busy, and the warps wait for one another's chunks meanwhile.  Every 64 tokens convert the
+// codes anew: 512 tokens, 14336 x 4096, take 115, 2048 take 419.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory alone,
 // written and read twice a chunk, was more than half.  The elements by warps of their own, into one place a
 // group: 20.5.  Scales loaded when their sums are awaited: 19.0.
 constexpr int kGroups = 4, kMakers = 4 * kGroups;                  // warps

@@ -31,8 +31,11 @@
 //
 // Measured: 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, 91 to 97 us by their lengths (5.7 TB/s,
 // floor 79); 200001 tokens, 16 heads over 2 of 256, 47 (floor 30); 37 windows of 1000 and 4 first tokens, 12
-// heads of 64, 19 (floor 7.4).  The issue slots are half busy, with conversions, products and the
-// softmax of twelve warps an SM, while the codes come.
+// heads of 64, 19 (floor 7.4).  Twelve warps an SM, each a chain of
+// dependent conversions, products and a softmax, keep half of the issue slots busy while the codes come, and no
+// pipe above 44%: what bounds the time is how little of the chains' latency and the memory's overlap.  With 16
+// query heads a key head there are eight warps an SM, for 256 four: 64 sequences of 4096 tokens, launch included,
+// 8 key heads of 64 83 us with 8 query heads each and 123 with 16, of 128 130 and 172, 4 of 256 119 and 247.
 //
 // With a window the seen tokens are two ranges.  They are laid one after the other on one axis of rows,
 // the first tokens' range rounded up and the window's start down to 16, so that 16 rows lie in one

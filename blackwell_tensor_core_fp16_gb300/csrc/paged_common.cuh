@@ -184,7 +184,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
         if (x == w) upto += r.total;
         r.total += sm_i[x];
     }
-    r.blocks = min(static_cast<int>(gridDim.x), r.total);   // with a tile each at least
+    r.blocks = min(static_cast<int>(gridDim.x), r.total);   // with a tile, or an item's end, each at least
     r.t0 = c < r.blocks ? first_tile(c, r.total, r.blocks) : r.total;
     r.t1 = c < r.blocks ? first_tile(c + 1, r.total, r.blocks) : r.total;
     if (r.t0 >= upto - mine && r.t0 < upto) {          // one thread: its sequences hold tile r.t0
@@ -223,7 +223,7 @@ __device__ __forceinline__ bool block_range(const P& p, Cursor<Span>& cur, Range
     cur.item = sm_i[33] / (cur.tiles + C::kEndTiles);
     cur.tile = sm_i[33] % (cur.tiles + C::kEndTiles);
     if (cur.tile >= cur.tiles) {                   // an end, which the block before has: the next item
-        r.t0 += cur.tiles + C::kEndTiles - cur.tile;
+        r.t0 += cur.tiles + C::kEndTiles - cur.tile;       // (of which there may be none in the share)
         cur.tile = cur.tiles - 1;
         if (r.t0 < r.t1) advance<kTile>(cur, p);
     }
