@@ -198,7 +198,8 @@ cudaError_t clusters_of(int threads, int smem, const Clusters*& of)
 //
 // One token, 14336 x 4096: 12.0 us (floor 4.5); 28672 x 8192: 40 (18), so large layers run at 3.1 TB/s, with
 // 160 KB an SM on their way (why no faster is not shown: one warp computes and issues the copies of 16 rows, one
-// after another); 4096 x 4096: 5.6 (1.3); 256 x 256: 2.8, a launch and the way there and back.  7 tokens, 5000 x 1024, groups of 32: 5.6 (0.5).
+// after another); 4096 x 4096: 5.6 (1.3); 256 x 256: 2.8, a launch and the way there and back.
+// 7 tokens, 5000 x 1024, groups of 32: 5.8 (0.5).
 
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 constexpr int kItem = 16;                        // outputs
@@ -560,9 +561,10 @@ bool few_with_words(const LinearParams& p, cudaStream_t stream, int& rc)
 // (3.5).  A block's 128 rows being indivisible, 112 of 152 SMs have one, and on those nothing is full: a
 // scheduler issues for 600 of a chunk's 850 to 1000 cycles, the pipe of the integer operations, which make the
 // operands, is 59% busy, and the warps wait for one another's chunks meanwhile.  Every 64 tokens convert the
-// codes anew: 512 tokens, 14336 x 4096, take 115, 2048 take 419.  Differences through shared memory, all makers at one chunk: 27.9, of which shared memory alone,
-// written and read twice a chunk, was more than half.  The elements by warps of their own, into one place a
-// group: 20.5.  Scales loaded when their sums are awaited: 19.0.
+// codes anew: 512 tokens, 14336 x 4096, take 115, 2048 take 419.  Differences through shared
+// memory, all makers at one chunk: 27.9, of which shared memory alone, written and read twice a chunk, was more
+// than half.  The elements by warps of their own, into one place a group: 20.5.  Scales loaded when their sums are
+// awaited: 19.0.
 constexpr int kGroups = 4, kMakers = 4 * kGroups;                  // warps
 constexpr int kAhead = 3;                        // chunks of a warp whose codes are there or on their way
 
